@@ -24,38 +24,38 @@ BYTES = {"bf16": 2, "f16": 2, "f32": 4}
 def listed():
     return [
         # one user's next token: 16 key heads shared by 32 value heads; 4 MiB of state move, so latency counts
-        dict(name="step, one sequence", kind="step", n=1, t=1, hk=16, hv=32, k=128, v=128, dtype="bf16", spare=3),
+        dict(name="step: one sequence", kind="step", n=1, t=1, hk=16, hv=32, k=128, v=128, dtype="bf16", spare=3),
         # the next token of a full serving batch: over 1 GB of state move
-        dict(name="step, full batch", kind="step", n=256, t=1, hk=16, hv=32, k=128, v=128, dtype="bf16", spare=8),
+        dict(name="step: full batch", kind="step", n=256, t=1, hk=16, hv=32, k=128, v=128, dtype="bf16", spare=8),
         # prompts of very different lengths in one packed batch, as a server takes them in
-        dict(name="prompt, ragged batch", kind="prompt", n=48, tokens=12345, spread=7, hk=16, hv=32, k=128, v=128,
+        dict(name="prompt: ragged batch", kind="prompt", n=48, tokens=12345, spread=7, hk=16, hv=32, k=128, v=128,
              dtype="bf16", fused=True),
         # one long document and few heads: little to do at a time, a long way to go
-        dict(name="prompt, one long", kind="prompt", n=1, tokens=32768, spread=0, hk=4, hv=8, k=128, v=128,
+        dict(name="prompt: one long", kind="prompt", n=1, tokens=32768, spread=0, hk=4, hv=8, k=128, v=128,
              dtype="bf16", fused=True),
         # a small model in 32 bits with odd head sizes, as in an experiment or a check
-        dict(name="prompt, f32 odd sizes", kind="prompt", n=3, tokens=1111, spread=3, hk=3, hv=3, k=80, v=56,
+        dict(name="prompt: f32 odd sizes", kind="prompt", n=3, tokens=1111, spread=3, hk=3, hv=3, k=80, v=56,
              dtype="f32", fused=False),
         # an ordinary training batch
-        dict(name="train, batch", kind="train", n=4, tokens=16384, spread=0, hk=16, hv=16, k=128, v=128, dtype="bf16",
+        dict(name="train: batch", kind="train", n=4, tokens=16384, spread=0, hk=16, hv=16, k=128, v=128, dtype="bf16",
              fused=True, h0=False),
         # a long training context with few heads and shared key heads
-        dict(name="train, long", kind="train", n=1, tokens=16384, spread=0, hk=4, hv=8, k=128, v=128, dtype="bf16",
+        dict(name="train: long", kind="train", n=1, tokens=16384, spread=0, hk=4, hv=8, k=128, v=128, dtype="bf16",
              fused=True, h0=False),
         # packed documents, states carried in and gradients carried out, small heads in 16-bit floats
-        dict(name="train, ragged f16", kind="train", n=9, tokens=3001, spread=5, hk=4, hv=4, k=64, v=64, dtype="f16",
+        dict(name="train: ragged f16", kind="train", n=9, tokens=3001, spread=5, hk=4, hv=4, k=64, v=64, dtype="f16",
              fused=False, h0=True),
         # four candidates branch off one sequence's recurrent state and are dropped: latency
-        dict(name="branch, four states", kind="branch", seqs=8, rows=4, pages=64, width=1, page_tokens=1 << 30,
+        dict(name="branch: four states", kind="branch", seqs=8, rows=4, pages=64, width=1, page_tokens=1 << 30,
              elems=32 * 64 * 64, pools=1, dtype="f32", draft=0),
         # a batch of candidates branches off key and value pages, grows by draft tokens and is dropped
-        dict(name="branch, wide", kind="branch", seqs=128, rows=512, pages=16384, width=160, page_tokens=16,
+        dict(name="branch: wide", kind="branch", seqs=128, rows=512, pages=16384, width=160, page_tokens=16,
              elems=16 * 8 * 128, pools=2, dtype="bf16", draft=5),
         # a cache of key and value pages after many sequences have ended: the rest moves to the front
-        dict(name="compact, large cache", kind="compact", seqs=192, pages=16384, width=128, elems=16 * 8 * 128, pools=2,
+        dict(name="compact: large cache", kind="compact", seqs=192, pages=16384, width=128, elems=16 * 8 * 128, pools=2,
              dtype="bf16", drop=3),
         # pages of a few sequences copied elsewhere in the cache, as before they are written to
-        dict(name="copy, few pages", kind="copy", pages=2048, moves=37, elems=16 * 8 * 128, pools=2, dtype="bf16"),
+        dict(name="copy: few pages", kind="copy", pages=2048, moves=37, elems=16 * 8 * 128, pools=2, dtype="bf16"),
     ]
 
 
