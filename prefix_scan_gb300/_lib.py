@@ -61,6 +61,24 @@ SIGNATURES["ps_reduce_by_key"] = (_int, [_int, _int, _vp, _vp, _vp, _vp, _vp, _s
 SIGNATURES["ps_run_length_encode"] = (_int, [_int, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp])
 PS_NOALLOC_MAX_ELEMENTS = 1 << 29
 
+PS_REAL_F32, PS_REAL_BF16, PS_REAL_F16 = 0, 1, 2
+
+
+class DeltaTensor(ctypes.Structure):   # ps_delta_tensor
+    _fields_ = [("data", _vp), ("seq_stride", _i64), ("tok_stride", _i64), ("head_stride", _i64)]
+
+
+class DeltaShape(ctypes.Structure):    # ps_delta_shape
+    _fields_ = [("num_seqs", _i64), ("tokens", _i64), ("cu_seqlens", _vp), ("heads_k", ctypes.c_int32),
+                ("heads_v", ctypes.c_int32), ("dim_k", ctypes.c_int32), ("dim_v", ctypes.c_int32), ("type", _int),
+                ("beta_type", _int), ("scale", ctypes.c_float)]
+
+
+_dt, _ds = ctypes.POINTER(DeltaTensor), ctypes.POINTER(DeltaShape)
+SIGNATURES["ps_delta_workspace_size"] = (_sz, [_ds, _int])
+SIGNATURES["ps_delta_forward"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _vp, _vp, _int, _vp, _sz, _vp])
+SIGNATURES["ps_delta_step"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _i64, _vp, _vp, _vp, _vp])
+
 for _kind in ("inclusive", "exclusive"):
     for _t in ("i32", "i64", "f32"):
         SIGNATURES[f"ps_scan_{_kind}_{_t}"] = (_int, [_vp, _vp, _sz, _vp, _sz, _vp])

@@ -1,0 +1,104 @@
+// delta_internal.h -- host-side pieces shared by the gated delta rule's
+// translation units: arguments, workspace layout, launcher declarations.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "prefix_scan_delta.h"
+
+namespace ps {
+
+constexpr int kChunk = 64;        // tokens of a chunk
+constexpr int kMaxDimK = 128;     // largest key size
+
+struct DeltaTensor {              // element strides; the innermost dimension is contiguous
+    const void *p;
+    long long seq, tok, head;
+};
+struct DeltaShape {
+    long long seqs, tokens;       // tokens of each sequence, or of all with cu
+    const int32_t *cu;
+    int hk, hv, k, v;
+    float scale;
+};
+
+// What the forward kernels leave for each (chunk, value head), in this order; all
+// images are swizzled as in delta_common.cuh and kept as pairs hi, lo of bf16.
+//   scal   6 x 64 f32: exp(G), exp(G_C - G), beta, G as a sum of two floats, and how many
+//          tokens up to here have forgotten the state
+//   T      2 x 64 x 64       row i, column j
+//   P      2 x 64 x 64
+//   N      2 x 64 x 64       (kept for the backward pass only)
+//   S      2 x V x K         row v, column k: the state at the chunk's start (backward only)
+//   U      2 x V x 64        row v, column token (backward only)
+// and the backward chain adds dS (as S: the gradient of the state at the chunk's end) and
+// dR (as U).
+struct ChunkLayout {
+    size_t scal, t, p, n, s, u, ds, dr, stride;
+};
+constexpr size_t kSquare = (size_t)kChunk * kChunk * 2;   // bytes of one 64 x 64 plane
+constexpr int pad_k(int k) { return k <= 64 ? 64 : 128; }
+constexpr int pad_v(int v) { return (v + 15) / 16 * 16; }
+constexpr ChunkLayout chunk_layout(int k, int v, bool train) {
+    ChunkLayout l{};
+    const size_t sp = (size_t)pad_v(v) * pad_k(k) * 2, up = (size_t)pad_v(v) * kChunk * 2;
+    size_t at = 0;
+    l.scal = at; at += 6 * kChunk * 4;
+    l.t = at; at += 2 * kSquare;
+    l.p = at; at += 2 * kSquare;
+    if (train) {
+        l.n = at; at += 2 * kSquare;
+        l.s = at; at += 2 * sp;
+        l.u = at; at += 2 * up;
+        l.ds = at; at += 2 * sp;
+        l.dr = at; at += 2 * up;
+    }
+    l.stride = (at + 255) / 256 * 256;
+    return l;
+}
+constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
+    return packed ? tokens / kChunk + seqs : seqs * ((tokens + kChunk - 1) / kChunk);
+}
+
+struct DeltaArgs {
+    DeltaShape s;
+    DeltaTensor q, k, v, g, beta;
+    int beta_f32;                 // beta holds f32 and not the inputs' type
+    int vec_qk, vec_v;            // rows 16-byte aligned, sizes a multiple of 8
+    const float *h0;              // [seqs, hv, k, v] or null
+    float *ht;                    // the same, or null
+    void *o;                      // contiguous [tokens, hv, v]
+    unsigned char *ws;
+    long long slots;
+    int train;                    // keep what the backward pass reads
+    // backward
+    DeltaTensor dout;
+    int vec_do;
+    const float *dht;
+    float *dh0, *dg;
+    void *dq, *dk, *dv, *dbeta;
+    float *part;                  // [slots, hv, v blocks, 2, 64]: sums over v blocks of dbeta and of b_j
+};
+
+// Type codes: PS_REAL_F32, PS_REAL_BF16, PS_REAL_F16.
+cudaError_t launch_delta_prepare(const DeltaArgs &a, int type, cudaStream_t s);
+cudaError_t launch_delta_chain(const DeltaArgs &a, int type, cudaStream_t s);
+cudaError_t launch_delta_chain_backward(const DeltaArgs &a, int type, cudaStream_t s);
+cudaError_t launch_delta_gradients(const DeltaArgs &a, int type, cudaStream_t s);
+
+struct DeltaStepArgs {
+    long long seqs, pages;
+    int t, hk, hv, k, v;
+    float scale;
+    DeltaTensor q, kk, vv, g, beta;
+    int beta_f32;
+    float *state;                 // [pages, hv, k, v]
+    const int32_t *slots, *lengths;   // [seqs] or null
+    void *o;                      // contiguous [seqs, t, hv, v]
+};
+cudaError_t launch_delta_step(const DeltaStepArgs &a, int type, cudaStream_t s);
+
+}  // namespace ps

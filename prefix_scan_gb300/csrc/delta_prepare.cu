@@ -1,0 +1,230 @@
+// delta_prepare.cu -- what the chunks of the gated delta rule need before
+// their states are known: decays, the masked products P and N, and the
+// triangular inverse T (notation in delta_common.cuh).  One CTA per chunk and
+// key head, all chunks at once; it keeps k and q and their products for all
+// value heads that share the key head.
+#include "delta_common.cuh"
+
+namespace ps {
+
+namespace {
+
+constexpr int kPrepThreads = 128;   // four warps: 16 rows of a 64 x 64 product each
+
+template <int NP, int KP>
+struct PrepSmem {
+    static constexpr int kPlane = kChunk * KP * 2;
+    static constexpr int kK = 0, kQ = NP * kPlane;
+    static constexpr int kL = 2 * NP * kPlane;               // f32 64 x 64
+    static constexpr int kT = kL + kChunk * kChunk * 4;      // images hi, lo
+    static constexpr int kP = kT + 2 * (int)kSquare;
+    static constexpr int kN = kP + 2 * (int)kSquare;
+    static constexpr int kScal = kN + 2 * (int)kSquare;
+    static constexpr int kBytes = kScal + 6 * kChunk * 4;
+};
+
+// exp(x) leaves f32's normal range below this: the state is forgotten.
+constexpr float kForget = -87.f;
+
+}  // namespace
+
+template <typename T, int KP>
+__global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const DeltaArgs a) {
+    constexpr int NP = Planes<T>::NP;
+    using M = PrepSmem<NP, KP>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = smem_addr(smem);
+    float *L = reinterpret_cast<float *>(smem + M::kL);
+    float *scal = reinterpret_cast<float *>(smem + M::kScal);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long slot = blockIdx.x;
+    const int head_k = blockIdx.y, rep = a.s.hv / a.s.hk;
+
+    const long long seq = seq_of_slot(a.s, slot);
+    if (seq < 0) return;
+    const Span sp = span_of(a.s, seq);
+    const long long t0 = (slot - sp.slot) * kChunk;
+    const int rows = (int)min((long long)kChunk, sp.len - t0);
+
+    load_tile<T, KP>(base + M::kK, M::kPlane, row_ptr<T>(a.k, sp, seq, t0, head_k), a.k.tok, rows, a.s.k, a.vec_qk != 0,
+                     tid, kPrepThreads);
+    load_tile<T, KP>(base + M::kQ, M::kPlane, row_ptr<T>(a.q, sp, seq, t0, head_k), a.q.tok, rows, a.s.k, a.vec_qk != 0,
+                     tid, kPrepThreads);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+
+    // rows 16 warp .. of k k^T and q k^T, columns j <= i only
+    float kk[8][4], qk[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < KP / 16; ++kt) {
+        uint32_t ak[NP][4], aq[NP][4];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            load_a<KP * 2>(ak[p], base + M::kK + p * M::kPlane, 16 * warp, 16 * kt, lane);
+            load_a<KP * 2>(aq[p], base + M::kQ + p * M::kPlane, 16 * warp, 16 * kt, lane);
+        }
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            if (np <= warp) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    uint32_t b[4];
+                    load_b<KP * 2>(b, base + M::kK + p * M::kPlane, 16 * np, 16 * kt, lane);
+#pragma unroll
+                    for (int f = 0; f + p < NP; ++f) {   // lo lo is left out
+                        mma_bf16(kk[2 * np], ak[f], b[0], b[1]);
+                        mma_bf16(kk[2 * np + 1], ak[f], b[2], b[3]);
+                        mma_bf16(qk[2 * np], aq[f], b[0], b[1]);
+                        mma_bf16(qk[2 * np + 1], aq[f], b[2], b[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
+    for (int hr = 0; hr < rep; ++hr) {
+        const int head = head_k * rep + hr;
+        if (warp == 0) {
+            // running sums of g in 64 bits, kept as two floats: differences of far sums stay exact to
+            // f32.  Tokens that forget the state start a new count r; sums go on without them.
+            const float *gp = row_ptr<float>(a.g, sp, seq, t0, head);
+            float g0 = 2 * lane < rows ? gp[(2 * lane) * a.g.tok] : 0.f;
+            float g1 = 2 * lane + 1 < rows ? gp[(2 * lane + 1) * a.g.tok] : 0.f;
+            const bool f0 = g0 <= kForget, f1 = g1 <= kForget;
+            if (f0) g0 = 0.f;
+            if (f1) g1 = 0.f;
+            double sum = (double)g0 + (double)g1;
+            int cnt = (int)f0 + (int)f1;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const double s2 = __shfl_up_sync(0xffffffffu, sum, d);
+                const int c2 = __shfl_up_sync(0xffffffffu, cnt, d);
+                if (lane >= d) { sum += s2; cnt += c2; }
+            }
+            const double last = __shfl_sync(0xffffffffu, sum, 31);
+            const int rlast = __shfl_sync(0xffffffffu, cnt, 31);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                const double G = e ? sum : sum - (double)g1;
+                const int r = e ? cnt : cnt - (int)f1;
+                const float hi = (float)G;
+                scal[i] = r == 0 ? expf((float)G) : 0.f;
+                scal[64 + i] = i < rows && r == rlast ? expf((float)(last - G)) : 0.f;
+                scal[192 + i] = hi;
+                scal[256 + i] = (float)(G - (double)hi);
+                scal[320 + i] = (float)r;
+            }
+        } else if (warp < 3) {
+            const int i = tid - 32;
+            float b = 0.f;
+            if (i < rows)
+                b = a.beta_f32 ? row_ptr<float>(a.beta, sp, seq, t0, head)[i * a.beta.tok]
+                               : to_f32<T>(row_ptr<T>(a.beta, sp, seq, t0, head)[i * a.beta.tok]);
+            // the backward pass divides u by beta; 2^-60 in the place of 0 changes no result by more than that
+            if (fabsf(b) < 0x1p-60f) b = 0x1p-60f;
+            scal[128 + i] = b;
+        }
+        __syncthreads();
+
+        {   // L = diag(beta) N in f32, P and N as pairs
+            const int i0 = 16 * warp + (lane >> 2);
+            const float gh0 = scal[192 + i0], gl0 = scal[256 + i0], r0 = scal[320 + i0], b0 = scal[128 + i0];
+            const float gh1 = scal[200 + i0], gl1 = scal[264 + i0], r1 = scal[328 + i0], b1 = scal[136 + i0];
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0}, nh[4] = {0, 0, 0, 0}, nl[4] = {0, 0, 0, 0};
+                if (np <= warp) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {   // register q of the block's fragment: tile q >> 1, rows +8 for odd q
+                        const int n = 2 * np + (q >> 1), row = q & 1, i = i0 + 8 * row, j = 8 * n + 2 * (lane & 3);
+                        float pv[2], nv[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = j + e;
+                            const float dx = ((row ? gh1 : gh0) - scal[192 + c]) + ((row ? gl1 : gl0) - scal[256 + c]);
+                            const float D = i >= c && (row ? r1 : r0) == scal[320 + c] ? expf(dx) : 0.f;
+                            nv[e] = i > c ? D * kk[n][2 * row + e] : 0.f;
+                            pv[e] = i >= c ? a.s.scale * D * qk[n][2 * row + e] : 0.f;
+                        }
+                        *reinterpret_cast<float2 *>(L + i * kChunk + j) =
+                            make_float2((row ? b1 : b0) * nv[0], (row ? b1 : b0) * nv[1]);
+                        split2(pv[0], pv[1], ph[q], pl[q]);
+                        split2(nv[0], nv[1], nh[q], nl[q]);
+                    }
+                }
+                const uint32_t at = img<128>(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
+                stsm4(base + M::kP + at, ph[0], ph[1], ph[2], ph[3]);
+                stsm4(base + M::kP + (uint32_t)kSquare + at, pl[0], pl[1], pl[2], pl[3]);
+                if (a.train) {
+                    stsm4(base + M::kN + at, nh[0], nh[1], nh[2], nh[3]);
+                    stsm4(base + M::kN + (uint32_t)kSquare + at, nl[0], nl[1], nl[2], nl[3]);
+                }
+            }
+        }
+        __syncthreads();
+
+        if (tid < kChunk) {
+            // column tid of T by forward substitution: T_ij = delta_ij - sum_{l < i} L_il T_lj
+            float x[kChunk];
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                float s0 = i == tid ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                for (int l = 0; l + 3 < i; l += 4) {
+                    const float4 c = *reinterpret_cast<const float4 *>(L + i * kChunk + l);
+                    s0 -= c.x * x[l]; s1 -= c.y * x[l + 1]; s2 -= c.z * x[l + 2]; s3 -= c.w * x[l + 3];
+                }
+#pragma unroll
+                for (int l = i & ~3; l < i; ++l) s0 -= L[i * kChunk + l] * x[l];
+                x[i] = (s0 + s1) + (s2 + s3);
+            }
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
+                const __nv_bfloat16 l = __float2bfloat16_rn(split_rest(x[i], __bfloat162float(h)));
+                const int at = (int)img<128>(0, i, tid >> 3) + (tid & 7) * 2;
+                *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + at) = h;
+                *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + kSquare + at) = l;
+            }
+        }
+        __syncthreads();
+
+        unsigned char *out = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
+        const int imgs = (a.train ? 6 : 4) * (int)kSquare / 16;   // T, P, N follow one another on both sides
+        for (int i = tid; i < imgs; i += kPrepThreads)
+            reinterpret_cast<uint4 *>(out + lay.t)[i] = reinterpret_cast<const uint4 *>(smem + M::kT)[i];
+        for (int i = tid; i < 6 * kChunk; i += kPrepThreads) reinterpret_cast<float *>(out + lay.scal)[i] = scal[i];
+        __syncthreads();
+    }
+}
+
+namespace {
+
+template <typename T, int KP>
+cudaError_t prepare(const DeltaArgs &a, cudaStream_t s) {
+    constexpr int bytes = PrepSmem<Planes<T>::NP, KP>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    delta_prepare_kernel<T, KP><<<dim3((unsigned)a.slots, (unsigned)a.s.hk), kPrepThreads, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_prepare(const DeltaArgs &a, int type, cudaStream_t s) {
+    const bool small = a.s.k <= 64;
+    switch (type) {
+    case PS_REAL_BF16: return small ? prepare<__nv_bfloat16, 64>(a, s) : prepare<__nv_bfloat16, 128>(a, s);
+    case PS_REAL_F16: return small ? prepare<__half, 64>(a, s) : prepare<__half, 128>(a, s);
+    default: return small ? prepare<float, 64>(a, s) : prepare<float, 128>(a, s);
+    }
+}
+
+}  // namespace ps

@@ -1,0 +1,195 @@
+"""PyTorch-facing wrappers of the gated delta rule (``include/prefix_scan_delta.h``).
+
+The recurrence, for each value head of each sequence, of a K x V state S::
+
+    S <- exp(g) S;   u = beta (v - k^T S);   S <- S + k u^T;   o = scale q^T S
+
+Tensors are passed as raw device pointers with their strides and the current
+(or given) CUDA stream; every step runs in ``libprefixscan.so``.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+
+REAL_CODES = {torch.float32: _lib.PS_REAL_F32, torch.bfloat16: _lib.PS_REAL_BF16, torch.float16: _lib.PS_REAL_F16}
+
+
+def _on(device, stream):
+    """The stream to use, and a context in which new tensors belong to it."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    ctx.enter_context(torch.cuda.stream(s))
+    return s, ctx
+
+
+def _check_inputs(fn, q, k, v, g, beta, cu_seqlens):
+    dims = 4 if cu_seqlens is None else 3
+    lead = "[sequences, tokens" if cu_seqlens is None else "for packed sequences [tokens"
+    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{fn}: {name} must be a CUDA tensor on q's device (there is no CPU path)")
+        if t.dim() != dims - (name in ("g", "beta")):
+            raise ValueError(f"{fn}: q, k, v are {lead}, heads, size], g and beta the same without size")
+        if name in "qkv" and t.shape[-1] > 1 and t.numel() > 0 and t.stride(-1) != 1:
+            raise ValueError(f"{fn}: {name} must be contiguous in its last dimension")
+    if q.dtype not in REAL_CODES or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError(f"{fn} supports q, k and v of one type, float32, bfloat16 or float16, not {q.dtype}, {k.dtype}, {v.dtype}")
+    if g.dtype != torch.float32 or beta.dtype not in (torch.float32, q.dtype):
+        raise TypeError(f"{fn}: g is float32, and beta float32 or q's type")
+    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2] or g.shape != v.shape[:-1] or beta.shape != v.shape[:-1]:
+        raise ValueError(f"{fn}: shapes of q, k, v, g and beta do not go together")
+    hk, hv = q.shape[-2], v.shape[-2]
+    if hk < 1 or hv < 1 or hv % hk:
+        raise ValueError(f"{fn}: the value heads ({hv}) must be a multiple of the key heads ({hk})")
+    if not 1 <= q.shape[-1] <= 128 or not 1 <= v.shape[-1] <= 1024:
+        raise ValueError(f"{fn}: key sizes up to 128 and value sizes up to 1024 are supported")
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 \
+                or cu_seqlens.device != q.device or not cu_seqlens.is_contiguous():
+            raise ValueError(f"{fn}: cu_seqlens must be a contiguous 1-D int32 CUDA tensor of one offset more than sequences")
+
+
+def _tensor(t: torch.Tensor, packed: bool, inner: bool) -> _lib.DeltaTensor:
+    """The strides of a [sequences,] tokens, heads[, size] tensor."""
+    st = t.stride()
+    head = -2 if inner else -1
+    return _lib.DeltaTensor(t.data_ptr() if t.numel() else None, 0 if packed else st[0], st[head - 1], st[head])
+
+
+def _shape(q, v, beta, cu_seqlens, scale) -> _lib.DeltaShape:
+    packed = cu_seqlens is not None
+    return _lib.DeltaShape(cu_seqlens.numel() - 1 if packed else q.shape[0], q.shape[0] if packed else q.shape[1],
+                           cu_seqlens.data_ptr() if packed else None, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
+                           REAL_CODES[q.dtype], REAL_CODES[beta.dtype],
+                           q.shape[-1] ** -0.5 if scale is None else float(scale))
+
+
+def _check_state(fn, name, t, shape, device):
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
+
+
+def _workspace(fn, workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if workspace.numel() * workspace.element_size() < need or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace needs {need} contiguous bytes on {device}")
+    return workspace
+
+
+def delta_rule_workspace_size(q: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor | None = None, *,
+                              train: bool = False) -> int:
+    """Bytes of workspace :func:`delta_rule` needs for such inputs (``train``: the buffer that
+    :func:`delta_rule_forward` leaves for the backward pass)."""
+    shape = _shape(q, v, q, cu_seqlens, 1.0)
+    return int(_lib.load().ps_delta_workspace_size(ctypes.byref(shape), int(train)))
+
+
+@dataclass
+class DeltaRuleSaved:
+    """What :func:`delta_rule_forward` keeps for :func:`delta_rule_backward`."""
+    q: torch.Tensor
+    k: torch.Tensor
+    v_shape: torch.Size
+    beta_dtype: torch.dtype
+    cu_seqlens: torch.Tensor | None
+    shape: object
+    has_initial_state: bool
+    workspace: torch.Tensor
+
+
+def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state, workspace,
+             stream, train):
+    _check_inputs(fn, q, k, v, g, beta, cu_seqlens)
+    shape = _shape(q, v, beta, cu_seqlens, scale)
+    states = (int(shape.num_seqs), v.shape[-2], q.shape[-1], v.shape[-1])
+    if initial_state is not None:
+        _check_state(fn, "initial_state", initial_state, states, q.device)
+    if final_state is not None:
+        _check_state(fn, "final_state", final_state, states, q.device)
+    if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != q.device or not out.is_contiguous()):
+        raise ValueError(f"{fn}: `out` must be contiguous and match v's shape, type and device")
+    packed = cu_seqlens is not None
+    lib = _lib.load()
+    s, ctx = _on(q.device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty(states, dtype=torch.float32, device=q.device)
+        need = int(lib.ps_delta_workspace_size(ctypes.byref(shape), int(train)))
+        workspace = _workspace(fn, workspace, need, q.device)
+        ts = [_tensor(t, packed, inner) for t, inner in ((q, True), (k, True), (v, True), (g, False), (beta, False))]
+        st = lib.ps_delta_forward(ctypes.byref(shape), *(ctypes.byref(t) for t in ts),
+                                  initial_state.data_ptr() if initial_state is not None else None,
+                                  final_state.data_ptr() if final_state is not None else None,
+                                  out.data_ptr() if out.numel() else None, int(train), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
+    _lib.check("ps_delta_forward", st)
+    return out, final_state, shape, workspace
+
+
+def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, *,
+               scale: float | None = None, cu_seqlens: torch.Tensor | None = None,
+               initial_state: torch.Tensor | None = None, output_final_state: bool = False,
+               out: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """The gated delta rule over whole sequences: ``(o, final_state)``.
+
+    ``q``, ``k``: [sequences, tokens, key heads, K]; ``v``: [sequences, tokens, value heads, V]; ``g`` (log decays,
+    float32) and ``beta`` (gates, float32 or q's type): [sequences, tokens, value heads].  With ``cu_seqlens``
+    (int32, on the device, one offset more than sequences) the first two dimensions are one that packs all
+    sequences' tokens.  Any strides go, as long as the last dimension is contiguous.  ``initial_state``:
+    [sequences, value heads, K, V] float32 (0 if not given); the states at the end are written to
+    ``final_state`` (which may be ``initial_state``), or returned in a new tensor with ``output_final_state``.
+    ``scale`` is K ** -0.5 if not given.  Asynchronous on ``stream`` (default: the current stream).  With
+    ``cu_seqlens``, outputs of tokens that no sequence holds are not written.  For gradients see
+    :func:`delta_rule_forward`.
+    """
+    out, final_state, _, _ = _forward("delta_rule", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
+                                      out, final_state, workspace, stream, False)
+    return out, final_state
+
+
+def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                    state: torch.Tensor, *, slots: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                    scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The next token (or few) of many sequences: the outputs, with ``state`` advanced in place.
+
+    ``q`` .. ``beta`` as for :func:`delta_rule` without ``cu_seqlens``.  ``state``: a pool of pages, [pages, value
+    heads, K, V] float32.  ``slots`` (int32, one per sequence, all different): the page of each sequence's state, -1
+    for one that takes no part; page i for sequence i if not given.  ``lengths`` (int32, one per sequence): how many
+    of the tokens count.  Outputs of tokens that do not count are 0.
+    """
+    fn = "delta_rule_step"
+    _check_inputs(fn, q, k, v, g, beta, None)
+    shape = _shape(q, v, beta, None, scale)
+    if state.dim() != 4:
+        raise ValueError(f"{fn}: state must be [pages, value heads, K, V]")
+    _check_state(fn, "state", state, (state.shape[0], v.shape[-2], q.shape[-1], v.shape[-1]), q.device)
+    for name, t in (("slots", slots), ("lengths", lengths)):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (q.shape[0],) or t.device != q.device
+                              or not t.is_contiguous()):
+            raise ValueError(f"{fn}: {name} must be a contiguous int32 CUDA tensor with one entry per sequence")
+    if slots is None and state.shape[0] < q.shape[0]:
+        raise ValueError(f"{fn}: fewer pages than sequences")
+    if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != q.device or not out.is_contiguous()):
+        raise ValueError(f"{fn}: `out` must be contiguous and match v's shape, type and device")
+    s, ctx = _on(q.device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        ts = [_tensor(t, False, inner) for t, inner in ((q, True), (k, True), (v, True), (g, False), (beta, False))]
+        st = _lib.load().ps_delta_step(ctypes.byref(shape), *(ctypes.byref(t) for t in ts), state.data_ptr(),
+                                       state.shape[0], slots.data_ptr() if slots is not None else None,
+                                       lengths.data_ptr() if lengths is not None else None,
+                                       out.data_ptr() if out.numel() else None, ctypes.c_void_p(s.cuda_stream))
+    _lib.check("ps_delta_step", st)
+    return out
