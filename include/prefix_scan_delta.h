@@ -99,6 +99,21 @@ ps_status ps_delta_forward(const ps_delta_shape *shape, const ps_delta_tensor *q
                            ps_stream_t stream);
 
 /*
+ * Backward of one ps_delta_forward(train != 0) call with the same shape, q,
+ * k and beta; `ws` is that call's workspace, which one backward call may use
+ * any number of times but which must not change otherwise.
+ *   d_o   gradient of o;  d_ht  gradient of ht or NULL (0)
+ *   dq, dk [.., heads_k, dim_k], dv [.., heads_v, dim_v], dbeta, dg
+ *         [.., heads_v]: contiguous; dq and dk are summed over the value
+ *         heads that share a key head, in a fixed order
+ *   dh0   gradient of h0, or NULL
+ * Results are bitwise reproducible from call to call (no atomics).
+ */
+ps_status ps_delta_backward(const ps_delta_shape *shape, const ps_delta_tensor *q, const ps_delta_tensor *k,
+                            const ps_delta_tensor *d_o, const float *d_ht, void *dq, void *dk, void *dv,
+                            float *dg, void *dbeta, float *dh0, void *ws, size_t ws_bytes, ps_stream_t stream);
+
+/*
  * The recurrence for the next token or few of many sequences, on states that
  * lie in pages of a pool.
  *   tokens    t >= 0 tokens of each sequence (shape->cu_seqlens must be NULL)

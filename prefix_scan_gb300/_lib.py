@@ -77,6 +77,7 @@ class DeltaShape(ctypes.Structure):    # ps_delta_shape
 _dt, _ds = ctypes.POINTER(DeltaTensor), ctypes.POINTER(DeltaShape)
 SIGNATURES["ps_delta_workspace_size"] = (_sz, [_ds, _int])
 SIGNATURES["ps_delta_forward"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _vp, _vp, _int, _vp, _sz, _vp])
+SIGNATURES["ps_delta_backward"] = (_int, [_ds, _dt, _dt, _dt, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_delta_step"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _i64, _vp, _vp, _vp, _vp])
 
 for _kind in ("inclusive", "exclusive"):

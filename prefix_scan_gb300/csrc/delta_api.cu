@@ -149,6 +149,64 @@ extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_te
     return done(ps::launch_delta_chain(a, d->type, s));
 }
 
+extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_tensor *q, const ps_delta_tensor *k,
+                                       const ps_delta_tensor *d_o, const float *d_ht, void *dq, void *dk, void *dv,
+                                       float *dg, void *dbeta, float *dh0, void *ws, size_t ws_bytes,
+                                       ps_stream_t stream) {
+    if (!valid(d)) return PS_ERR_INVALID_ARG;
+    if (d->num_seqs == 0) return PS_OK;
+    const size_t es = real_bytes(d->type), bs = real_bytes(d->beta_type), need = ps_delta_workspace_size(d, 1);
+    const bool packed = d->cu_seqlens != nullptr;
+    const size_t state = (size_t)d->num_seqs * d->heads_v * d->dim_k * d->dim_v * 4;
+    const size_t tokens = (size_t)total_tokens(d);
+    if (reinterpret_cast<uintptr_t>(d_ht) % 4 != 0 || reinterpret_cast<uintptr_t>(dh0) % 4 != 0) return PS_ERR_INVALID_ARG;
+    ps::DeltaArgs a{};
+    a.s = shape_of(d);
+    a.dht = d_ht;
+    a.dh0 = dh0;
+    if (d->tokens > 0) {
+        if (!tensor_ok(q, es) || !tensor_ok(k, es) || !tensor_ok(d_o, es)) return PS_ERR_INVALID_ARG;
+        if (!dq || !dk || !dv || !dg || !dbeta || !ws) return PS_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(dq) | reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) % es != 0 ||
+            reinterpret_cast<uintptr_t>(dg) % 4 != 0 || reinterpret_cast<uintptr_t>(dbeta) % bs != 0 ||
+            reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+            return PS_ERR_INVALID_ARG;
+        if (ws_bytes < need) return PS_ERR_WORKSPACE_TOO_SMALL;
+        const Range in[] = {range(d, q, d->heads_k, d->dim_k, es), range(d, k, d->heads_k, d->dim_k, es),
+                            range(d, d_o, d->heads_v, d->dim_v, es), range(d_ht == dh0 ? nullptr : d_ht, state),
+                            range(d->cu_seqlens, ((size_t)d->num_seqs + 1) * 4)};
+        const Range out[] = {range(dq, tokens * d->heads_k * d->dim_k * es), range(dk, tokens * d->heads_k * d->dim_k * es),
+                             range(dv, tokens * d->heads_v * d->dim_v * es), range(dg, tokens * d->heads_v * 4),
+                             range(dbeta, tokens * d->heads_v * bs), range(dh0, state), range(ws, need)};
+        if (outputs_meet(out, in)) return PS_ERR_OVERLAP;
+        a.q = tensor(q, packed);
+        a.k = tensor(k, packed);
+        a.dout = tensor(d_o, packed);
+        a.beta_f32 = d->beta_type == PS_REAL_F32;
+        a.vec_qk = vectors(*q, d->dim_k, es, packed) && vectors(*k, d->dim_k, es, packed);
+        a.vec_do = vectors(*d_o, d->dim_v, es, packed);
+        a.dq = dq;
+        a.dk = dk;
+        a.dv = dv;
+        a.dg = dg;
+        a.dbeta = dbeta;
+        a.ws = static_cast<unsigned char *>(ws);
+        a.part = reinterpret_cast<float *>(a.ws + chunks_bytes(d, 1));
+        a.slots = ps::delta_slots(d->num_seqs, d->tokens, packed);
+        a.train = 1;
+    } else {
+        const Range in[] = {range(d_ht == dh0 ? nullptr : d_ht, state)};
+        const Range out[] = {range(dh0, state)};
+        if (outputs_meet(out, in)) return PS_ERR_OVERLAP;
+        if (dh0 == nullptr) return PS_OK;
+        a.s.cu = nullptr;
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = ps::launch_delta_chain_backward(a, d->type, s);
+    if (e == cudaSuccess && a.slots > 0) e = ps::launch_delta_gradients(a, d->type, s);
+    return done(e);
+}
+
 extern "C" ps_status ps_delta_step(const ps_delta_shape *d, const ps_delta_tensor *q, const ps_delta_tensor *k,
                                    const ps_delta_tensor *v, const ps_delta_tensor *g, const ps_delta_tensor *beta,
                                    float *state, int64_t pages, const int32_t *slots, const int32_t *lengths, void *o,

@@ -100,7 +100,7 @@ class DeltaRuleSaved:
     v_shape: torch.Size
     beta_dtype: torch.dtype
     cu_seqlens: torch.Tensor | None
-    shape: object
+    shape: _lib.DeltaShape
     has_initial_state: bool
     workspace: torch.Tensor
 
@@ -156,6 +156,60 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     out, final_state, _, _ = _forward("delta_rule", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
                                       out, final_state, workspace, stream, False)
     return out, final_state
+
+
+def delta_rule_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, *,
+                       scale: float | None = None, cu_seqlens: torch.Tensor | None = None,
+                       initial_state: torch.Tensor | None = None, output_final_state: bool = False,
+                       out: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None
+                       ) -> tuple[torch.Tensor, torch.Tensor | None, DeltaRuleSaved]:
+    """:func:`delta_rule` for training: ``(o, final_state, saved)``.
+
+    ``saved`` goes to :func:`delta_rule_backward`; it holds q and k (which must not change until then) and a workspace of
+    ``delta_rule_workspace_size(q, v, cu_seqlens, train=True)`` bytes.
+    """
+    out, final_state, shape, workspace = _forward("delta_rule_forward", q, k, v, g, beta, scale, cu_seqlens, initial_state,
+                                                  output_final_state, out, final_state, workspace, stream, True)
+    return out, final_state, DeltaRuleSaved(q, k, v.shape, beta.dtype, cu_seqlens, shape, initial_state is not None, workspace)
+
+
+def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_state: torch.Tensor | None = None, stream=None
+                        ) -> tuple[torch.Tensor, ...]:
+    """Gradients ``(dq, dk, dv, dg, dbeta, d_initial_state)`` of one :func:`delta_rule_forward` call.
+
+    ``d_o``: the gradient of ``o``, of its shape and type (any strides with a contiguous last dimension);
+    ``d_final_state``: that of the final states (0 if not given).  dq and dk are summed over the value heads that share a
+    key head; ``d_initial_state`` is None where the forward call had no initial state.  Bitwise reproducible.  Gradients
+    of tokens that no sequence holds are 0.
+    """
+    fn = "delta_rule_backward"
+    q, k, packed = saved.q, saved.k, saved.cu_seqlens is not None
+    if d_o.shape != saved.v_shape or d_o.dtype != q.dtype or d_o.device != q.device:
+        raise ValueError(f"{fn}: d_o must match o's shape, type and device")
+    if d_o.numel() and d_o.shape[-1] > 1 and d_o.stride(-1) != 1:
+        d_o = d_o.contiguous()
+    hv, dv_size = saved.v_shape[-2:]
+    states = (int(saved.shape.num_seqs), hv, q.shape[-1], dv_size)
+    if d_final_state is not None:
+        _check_state(fn, "d_final_state", d_final_state, states, q.device)
+    lib = _lib.load()
+    s, ctx = _on(q.device, stream)
+    with ctx:
+        new = torch.zeros if packed else torch.empty
+        heads = saved.v_shape[:-1]
+        dq, dk = (new(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+        dv = new(saved.v_shape, dtype=q.dtype, device=q.device)
+        dg = new(heads, dtype=torch.float32, device=q.device)
+        dbeta = new(heads, dtype=saved.beta_dtype, device=q.device)
+        dh0 = torch.empty(states, dtype=torch.float32, device=q.device) if saved.has_initial_state else None
+        ts = [_tensor(t, packed, True) for t in (q, k, d_o)]
+        ptr = lambda t: t.data_ptr() if t is not None and t.numel() else None  # noqa: E731
+        st = lib.ps_delta_backward(ctypes.byref(saved.shape), *(ctypes.byref(t) for t in ts), ptr(d_final_state), ptr(dq),
+                                   ptr(dk), ptr(dv), ptr(dg), ptr(dbeta), ptr(dh0), saved.workspace.data_ptr(),
+                                   saved.workspace.numel() * saved.workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
+    _lib.check("ps_delta_backward", st)
+    return dq, dk, dv, dg, dbeta, dh0
 
 
 def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
