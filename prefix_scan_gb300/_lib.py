@@ -80,6 +80,21 @@ SIGNATURES["ps_delta_forward"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _vp,
 SIGNATURES["ps_delta_backward"] = (_int, [_ds, _dt, _dt, _dt, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_delta_step"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _i64, _vp, _vp, _vp, _vp])
 
+PS_PAGES_MAX_POOLS = 128
+
+
+class PagePool(ctypes.Structure):      # ps_page_pool
+    _fields_ = [("data", _vp), ("page_bytes", _i64)]
+
+
+_pp, _i32 = ctypes.POINTER(PagePool), ctypes.c_int32
+SIGNATURES["ps_pages_workspace_size"] = (_sz, [_i64, _i64])
+SIGNATURES["ps_pages_copy"] = (_int, [_pp, _int, _i64, _vp, _vp, _i64, _vp])
+SIGNATURES["ps_pages_fork"] = (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _pp, _int, _i64, _vp, _vp, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_pages_grow"] = (_int, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_pages_free"] = (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp])
+SIGNATURES["ps_pages_compact"] = (_int, [_vp, _i64, _i64, _vp, _pp, _int, _i64, _vp, _vp, _sz, _vp])
+
 for _kind in ("inclusive", "exclusive"):
     for _t in ("i32", "i64", "f32"):
         SIGNATURES[f"ps_scan_{_kind}_{_t}"] = (_int, [_vp, _vp, _sz, _vp, _sz, _vp])

@@ -1,0 +1,20 @@
+"""Which stream a call runs on, and whose new tensors are."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+_HERE = contextlib.nullcontext()
+
+
+def enter(device: torch.device, stream):
+    """The CUDA stream handle to enqueue on, and a context for the call: inside it ``device`` is the current device and
+    new tensors belong to the stream (the given one, or the device's current one)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return torch.cuda.current_stream().cuda_stream, _HERE
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    ctx.enter_context(torch.cuda.stream(s))
+    return s.cuda_stream, ctx

@@ -9,24 +9,15 @@ Tensors are passed as raw device pointers with their strides and the current
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
 import torch
 
 from . import _lib
+from ._streams import enter
 
 REAL_CODES = {torch.float32: _lib.PS_REAL_F32, torch.bfloat16: _lib.PS_REAL_BF16, torch.float16: _lib.PS_REAL_F16}
-
-
-def _on(device, stream):
-    """The stream to use, and a context in which new tensors belong to it."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(device))
-    ctx.enter_context(torch.cuda.stream(s))
-    return s, ctx
 
 
 def _check_inputs(fn, q, k, v, g, beta, cu_seqlens):
@@ -118,7 +109,7 @@ def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_fina
         raise ValueError(f"{fn}: `out` must be contiguous and match v's shape, type and device")
     packed = cu_seqlens is not None
     lib = _lib.load()
-    s, ctx = _on(q.device, stream)
+    s, ctx = enter(q.device, stream)
     with ctx:
         if out is None:
             out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
@@ -131,7 +122,7 @@ def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_fina
                                   initial_state.data_ptr() if initial_state is not None else None,
                                   final_state.data_ptr() if final_state is not None else None,
                                   out.data_ptr() if out.numel() else None, int(train), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
+                                  workspace.numel() * workspace.element_size(), s)
     _lib.check("ps_delta_forward", st)
     return out, final_state, shape, workspace
 
@@ -194,7 +185,7 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
     if d_final_state is not None:
         _check_state(fn, "d_final_state", d_final_state, states, q.device)
     lib = _lib.load()
-    s, ctx = _on(q.device, stream)
+    s, ctx = enter(q.device, stream)
     with ctx:
         new = torch.zeros if packed else torch.empty
         heads = saved.v_shape[:-1]
@@ -207,7 +198,7 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
         ptr = lambda t: t.data_ptr() if t is not None and t.numel() else None  # noqa: E731
         st = lib.ps_delta_backward(ctypes.byref(saved.shape), *(ctypes.byref(t) for t in ts), ptr(d_final_state), ptr(dq),
                                    ptr(dk), ptr(dv), ptr(dg), ptr(dbeta), ptr(dh0), saved.workspace.data_ptr(),
-                                   saved.workspace.numel() * saved.workspace.element_size(), ctypes.c_void_p(s.cuda_stream))
+                                   saved.workspace.numel() * saved.workspace.element_size(), s)
     _lib.check("ps_delta_backward", st)
     return dq, dk, dv, dg, dbeta, dh0
 
@@ -236,7 +227,7 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
         raise ValueError(f"{fn}: fewer pages than sequences")
     if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != q.device or not out.is_contiguous()):
         raise ValueError(f"{fn}: `out` must be contiguous and match v's shape, type and device")
-    s, ctx = _on(q.device, stream)
+    s, ctx = enter(q.device, stream)
     with ctx:
         if out is None:
             out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
@@ -244,6 +235,6 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
         st = _lib.load().ps_delta_step(ctypes.byref(shape), *(ctypes.byref(t) for t in ts), state.data_ptr(),
                                        state.shape[0], slots.data_ptr() if slots is not None else None,
                                        lengths.data_ptr() if lengths is not None else None,
-                                       out.data_ptr() if out.numel() else None, ctypes.c_void_p(s.cuda_stream))
+                                       out.data_ptr() if out.numel() else None, s)
     _lib.check("ps_delta_step", st)
     return out
