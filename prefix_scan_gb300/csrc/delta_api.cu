@@ -81,16 +81,16 @@ size_t chunks_bytes(const ps_delta_shape *d, int train) {
     const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
     return (size_t)slots * d->heads_v * ps::chunk_layout(d->dim_k, d->dim_v, train != 0).stride;
 }
-size_t part_bytes(const ps_delta_shape *d) {
+size_t kq_bytes(const ps_delta_shape *d) {
     const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
-    return (size_t)slots * d->heads_v * ((d->dim_v + 15) / 16) * 2 * ps::kChunk * 4;
+    return (size_t)slots * d->heads_k * ps::kq_stride(d->dim_k, d->type == PS_REAL_BF16 ? 1 : 2);
 }
 
 }  // namespace
 
 extern "C" size_t ps_delta_workspace_size(const ps_delta_shape *d, int train) {
     if (!valid(d)) return 0;
-    return chunks_bytes(d, train) + (train ? part_bytes(d) : 0);
+    return chunks_bytes(d, train) + kq_bytes(d);
 }
 
 extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_tensor *q, const ps_delta_tensor *k,
@@ -132,6 +132,7 @@ extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_te
         a.vec_v = vectors(*v, d->dim_v, es, packed);
         a.o = o;
         a.ws = static_cast<unsigned char *>(ws);
+        a.kq = a.ws + chunks_bytes(d, train);
         a.slots = ps::delta_slots(d->num_seqs, d->tokens, packed);
         a.train = train != 0;
     } else {
@@ -191,7 +192,7 @@ extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_t
         a.dg = dg;
         a.dbeta = dbeta;
         a.ws = static_cast<unsigned char *>(ws);
-        a.part = reinterpret_cast<float *>(a.ws + chunks_bytes(d, 1));
+        a.kq = a.ws + chunks_bytes(d, 1);
         a.slots = ps::delta_slots(d->num_seqs, d->tokens, packed);
         a.train = 1;
     } else {

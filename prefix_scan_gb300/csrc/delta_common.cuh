@@ -71,14 +71,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo_half, float hi_half) {
 __device__ __forceinline__ float bf16_low(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 // (x, y) as a pair of packed bf16x2: x ~ low halves of hi + lo, y ~ high halves.
-// An infinite or NaN x keeps its value in hi and leaves 0 in lo (inf - inf
-// would make every infinity a NaN).
-__device__ __forceinline__ float split_rest(float x, float h) {
-    return fabsf(h) < __int_as_float(0x7f800000) ? x - h : 0.f;
-}
+// (An infinity becomes a NaN: its rest is inf - inf.)
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x, y);
-    lo = pack_bf16(split_rest(x, bf16_low(hi)), split_rest(y, bf16_high(hi)));
+    lo = pack_bf16(x - bf16_low(hi), y - bf16_high(hi));
+}
+// Two accumulator tiles of a 16-column block (columns 0-7 and 8-15) as a left operand.
+__device__ __forceinline__ void split_tiles(const float (&lo8)[4], const float (&hi8)[4], uint32_t (&f)[2][4]) {
+    split2(lo8[0], lo8[1], f[0][0], f[1][0]);
+    split2(lo8[2], lo8[3], f[0][1], f[1][1]);
+    split2(hi8[0], hi8[1], f[0][2], f[1][2]);
+    split2(hi8[2], hi8[3], f[0][3], f[1][3]);
 }
 
 // ---- swizzled images -----------------------------------------------------------
@@ -199,11 +202,32 @@ __device__ __forceinline__ void load_tile(uint32_t hi, uint32_t plane, const T *
     }
 }
 
-// Copies `bytes` (a multiple of 16) of an image as it stands in the workspace.
-__device__ __forceinline__ void load_image(uint32_t dst, const void *src, int bytes, int tid, int nthreads) {
-    for (int i = tid * 16; i < bytes; i += nthreads * 16)
-        cp_async16(dst + i, static_cast<const char *>(src) + i, true);
+// Copies BYTES (a multiple of 16) of an image as it stands in the workspace.
+template <int BYTES, int THREADS>
+__device__ __forceinline__ void load_image(uint32_t dst, const void *src, int tid) {
+    const char *s = static_cast<const char *>(src) + tid * 16;
+    dst += tid * 16;
+#pragma unroll
+    for (int i = 0; i < BYTES / (16 * THREADS); ++i) cp_async16(dst + i * THREADS * 16, s + i * THREADS * 16, true);
+    constexpr int DONE = BYTES / (16 * THREADS) * 16 * THREADS;
+    if (DONE < BYTES && DONE + tid * 16 < BYTES) cp_async16(dst + DONE, s + DONE, true);
 }
+// The same for the first `bytes` of an image of at most MOST.
+template <int MOST, int THREADS>
+__device__ __forceinline__ void load_part(uint32_t dst, const void *src, int bytes, int tid) {
+    if (bytes == MOST) return load_image<MOST, THREADS>(dst, src, tid);
+    for (int i = tid * 16; i < bytes; i += THREADS * 16) cp_async16(dst + i, static_cast<const char *>(src) + i, true);
+}
+// Stores BYTES of an image from shared memory by one warp.
+template <int BYTES>
+__device__ __forceinline__ void store_image(void *dst, const void *src, int lane) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 512; ++i)
+        static_cast<uint4 *>(dst)[i * 32 + lane] = static_cast<const uint4 *>(src)[i * 32 + lane];
+}
+// Named barriers between a pair of warps: one announces, the other waits.
+__device__ __forceinline__ void announce(int id) { asm volatile("bar.arrive %0, 64;" :: "r"(id) : "memory"); }
+__device__ __forceinline__ void await(int id) { asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory"); }
 
 // ---- sequences and chunks ----------------------------------------------------------
 

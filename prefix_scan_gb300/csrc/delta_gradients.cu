@@ -4,10 +4,10 @@
 // value head, with dP = dO U^T and dN = -dR U^T (j < i only):
 //     dQ = scale diag(exp(G)) dO S^T + (scale D dP) K
 //     dK = (scale D dP)^T Q + (D dN) K + (D dN)^T K - diag(exp(G)) dR S^T + diag(exp(G_C - G)) U dS'^T
-//     dbeta_j = (dU_j . U_j) / beta_j
+//     dbeta_j = (dU_j . U_j) / beta_j          (U = beta (what was missing))
 //     dg_t = sum_{j < t <= i} Z_ij + sum_{i >= t} a_i + sum_{j < t} b_j + exp(G_C) <S, dS'>
 // where Z = P dP + N dN (element by element), a_i = exp(G_i) (scale q_i . S dO_i -
-// k_i . S dR_i) and b_j = U_j . Y_j: every term that the decay of token t scales,
+// k_i . S dR_i) and b_j = exp(G_C - G_j) k_j . dS' U_j: every term that the decay of token t scales,
 // each counted once, so nothing cancels.
 //
 // One CTA per chunk and key head: gradients of a shared key head are sums over its
@@ -26,9 +26,9 @@ template <int NP, int KP>
 struct GradSmem {
     static constexpr int kKP = kChunk * KP * 2, kSP = kGradV * KP * 2, kUP = kGradV * kChunk * 2;
     static constexpr int kK = 0, kQ = NP * kKP;
-    static constexpr int kS = 2 * NP * kKP, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDR = kU + 2 * kUP;
-    static constexpr int kO = kDR + 2 * kUP, kScal = kO + NP * kUP, kMore = kScal + 6 * kChunk * 4;
-    static constexpr int kBytes = kMore + (2 * 2 * kChunk + 5 * kChunk + 8) * 4;
+    static constexpr int kS = 2 * NP * kKP, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDU = kU + 2 * kUP;
+    static constexpr int kO = kDU + 2 * kUP, kScal = kO + NP * kUP, kMore = kScal + 6 * kChunk * 4;
+    static constexpr int kBytes = kMore + (2 * kChunk + 2 * kChunk + 4 * kChunk + kChunk + 8) * 4;
     // F1, F2 and Z take the place of the blocks above once these are used up
     static constexpr int kF1 = kS, kF2 = kF1 + 2 * (int)kSquare, kZ = kF2 + 2 * (int)kSquare;
     static_assert(kZ + kChunk * kZStride * 4 <= kO, "the products fit where the blocks were");
@@ -46,8 +46,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     const float *scal = reinterpret_cast<const float *>(smem + M::kScal);
     float *Z = reinterpret_cast<float *>(smem + M::kZ);
     float *dots = reinterpret_cast<float *>(smem + M::kMore);   // [2 halves][64] of a_i
-    float *run = dots + 2 * kChunk;                             // [4 quarters][64] column sums of Z
-    float *inner = run + 4 * kChunk;                            // <S, dS'> by warps
+    float *dotb = dots + 2 * kChunk;                            // [2 halves][64] of b_j
+    float *run = dotb + 2 * kChunk;                             // [4 quarters][64] column sums of Z
+    float *diag = run + 4 * kChunk;                             // [64] dU_j . U_j
+    float *inner = diag + kChunk;                               // <S, dS'> by warps
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int strip = warp & 3, half = warp >> 2;   // rows 16 strip.., columns of half `half`
     const int r8 = lane >> 2, c2 = 2 * (lane & 3), i0 = 16 * strip + r8;
@@ -60,12 +62,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     const long long t0 = (slot - sp.slot) * kChunk;
     const int rows = (int)min((long long)kChunk, sp.len - t0);
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
-    const int vpad = pad_v(a.s.v), vparts = (a.s.v + 15) / 16;
+    const int vpad = pad_v(a.s.v);
 
-    load_tile<T, KP>(base + M::kK, M::kKP, row_ptr<T>(a.k, sp, seq, t0, head_k), a.k.tok, rows, a.s.k, a.vec_qk != 0,
-                     tid, kGradThreads);
-    load_tile<T, KP>(base + M::kQ, M::kKP, row_ptr<T>(a.q, sp, seq, t0, head_k), a.q.tok, rows, a.s.k, a.vec_qk != 0,
-                     tid, kGradThreads);
+    load_image<2 * NP * M::kKP, kGradThreads>(base + M::kK, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), tid);
 
     float dq[NH][4], dk[NH][4];   // rows i0 (+8), columns 8 (half NH + n) + c2 (+1)
 #pragma unroll
@@ -76,8 +75,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     for (int hr = 0; hr < rep; ++hr) {
         const int head = head_k * rep + hr;
         const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
-        float pa[4][4], na[4][4];                     // dP and -dN: columns 32 half + 8 n..
-        float x1[NH][4], x2[NH][4], x3[NH][4];        // dO S^T, dR S^T, U dS'^T
+        float pa[4][4], na[4][4];                     // dP and dU U^T: columns 32 half + 8 n..
+        float x1[NH][4], x2[NH][4], x3[NH][4];        // dO S^T, dU S^T, U dS'^T
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -90,13 +89,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 
         for (int v0 = 0; v0 < a.s.v; v0 += kGradV) {
             const int vr = min(kGradV, vpad - v0);
-            load_image(base + M::kScal, w + lay.scal, 6 * kChunk * 4, tid, kGradThreads);
+            load_image<6 * kChunk * 4, kGradThreads>(base + M::kScal, w + lay.scal, tid);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                load_image(base + M::kS + p * M::kSP, w + lay.s + ((size_t)p * vpad + v0) * KP * 2, vr * KP * 2, tid, kGradThreads);
-                load_image(base + M::kDS + p * M::kSP, w + lay.ds + ((size_t)p * vpad + v0) * KP * 2, vr * KP * 2, tid, kGradThreads);
-                load_image(base + M::kU + p * M::kUP, w + lay.u + ((size_t)p * vpad + v0) * kChunk * 2, vr * kChunk * 2, tid, kGradThreads);
-                load_image(base + M::kDR + p * M::kUP, w + lay.dr + ((size_t)p * vpad + v0) * kChunk * 2, vr * kChunk * 2, tid, kGradThreads);
+                const size_t row = (size_t)p * vpad + v0;
+                load_part<M::kSP, kGradThreads>(base + M::kS + p * M::kSP, w + lay.s + row * KP * 2, vr * KP * 2, tid);
+                load_part<M::kSP, kGradThreads>(base + M::kDS + p * M::kSP, w + lay.ds + row * KP * 2, vr * KP * 2, tid);
+                load_part<M::kUP, kGradThreads>(base + M::kU + p * M::kUP, w + lay.u + row * kChunk * 2, vr * kChunk * 2, tid);
+                load_part<M::kUP, kGradThreads>(base + M::kDU + p * M::kUP, w + lay.du + row * kChunk * 2, vr * kChunk * 2, tid);
             }
             load_tile<T, kGradV>(base + M::kO, M::kUP, row_ptr<T>(a.dout, sp, seq, t0, head) + v0, a.dout.tok, rows,
                                  a.s.v - v0, a.vec_do != 0, tid, kGradThreads);
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     load_a_t<128>(fu[p], base + M::kU + p * M::kUP, 16 * kt, 16 * strip, lane);
-                    load_a_t<128>(fr[p], base + M::kDR + p * M::kUP, 16 * kt, 16 * strip, lane);
+                    load_a_t<128>(fr[p], base + M::kDU + p * M::kUP, 16 * kt, 16 * strip, lane);
                 }
 #pragma unroll
                 for (int np = 0; np < 2; ++np)
@@ -164,11 +164,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             __syncthreads();
         }
 
-        // <S, dS'>, the parts of dQ and dK that go through the states, a_i
+        // <S, dS'>, the parts of dQ and dK that go through the states, a_i and b_j
 #pragma unroll
         for (int m = 16; m; m >>= 1) prod += __shfl_xor_sync(0xffffffffu, prod, m);
         if (lane == 0) inner[warp] = prod;
-        float dot[2] = {0.f, 0.f};
+        float dot[2] = {0.f, 0.f}, dob[2] = {0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             const int col = 8 * (half * NH + n) + c2;
@@ -184,21 +184,28 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                     qw = *reinterpret_cast<const uint32_t *>(smem + M::kQ + M::kKP + at);
                     k0 += bf16_low(kw); k1 += bf16_high(kw); q0 += bf16_low(qw); q1 += bf16_high(qw);
                 }
-                const float eg = scal[i], el = scal[64 + i], sc = a.s.scale * eg;
+                const float eg = scal[i], el = scal[64 + i], sc = a.s.scale * eg, eb = eg * scal[128 + i];
                 const float y0 = sc * x1[n][2 * e], y1 = sc * x1[n][2 * e + 1];
-                const float z0 = eg * x2[n][2 * e], z1 = eg * x2[n][2 * e + 1];
+                const float z0 = eb * x2[n][2 * e], z1 = eb * x2[n][2 * e + 1];
                 dot[e] += q0 * y0 + q1 * y1 - (k0 * z0 + k1 * z1);
+                const float u0 = el * x3[n][2 * e], u1 = el * x3[n][2 * e + 1];
+                dob[e] += k0 * u0 + k1 * u1;
                 dq[n][2 * e] += y0;
                 dq[n][2 * e + 1] += y1;
-                dk[n][2 * e] += el * x3[n][2 * e] - z0;
-                dk[n][2 * e + 1] += el * x3[n][2 * e + 1] - z1;
+                dk[n][2 * e] += u0 - z0;
+                dk[n][2 * e + 1] += u1 - z1;
             }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], 1);
             dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], 2);
-            if ((lane & 3) == 0) dots[half * kChunk + i0 + 8 * e] = dot[e];
+            dob[e] += __shfl_xor_sync(0xffffffffu, dob[e], 1);
+            dob[e] += __shfl_xor_sync(0xffffffffu, dob[e], 2);
+            if ((lane & 3) == 0) {
+                dots[half * kChunk + i0 + 8 * e] = dot[e];
+                dotb[half * kChunk + i0 + 8 * e] = dob[e];
+            }
         }
         // F1 = scale D dP, F2 = D dN as pairs, and Z
 #pragma unroll
@@ -221,7 +228,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                         const int c = j + e;
                         const float dx = (scal[192 + i] - scal[192 + c]) + (scal[256 + i] - scal[256 + c]);
                         const float D = i >= c && scal[320 + i] == scal[320 + c] ? expf(dx) : 0.f;
-                        const float dp = pa[n][2 * row + e], dn = -na[n][2 * row + e];
+                        const float dp = pa[n][2 * row + e], dn = -scal[128 + i] * na[n][2 * row + e];
+                        if (i == c) diag[i] = na[n][2 * row + e];
                         const float pv = e ? bf16_high(ph) + bf16_high(pl) : bf16_low(ph) + bf16_low(pl);
                         const float nv = e ? bf16_high(nh) + bf16_high(nl) : bf16_low(nh) + bf16_low(nl);
                         f1[e] = i >= c ? a.s.scale * D * dp : 0.f;
@@ -322,15 +330,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
         }
         __syncthreads();
         if (warp == 0) {   // tokens 2 lane, 2 lane + 1
-            const float *part = a.part + (size_t)(slot * a.s.hv + head) * vparts * 2 * kChunk;
-            float db[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, av[2];
-            for (int v = 0; v < vparts; ++v) {
-                const float2 x = *reinterpret_cast<const float2 *>(part + v * 2 * kChunk + 2 * lane);
-                const float2 y = *reinterpret_cast<const float2 *>(part + v * 2 * kChunk + kChunk + 2 * lane);
-                db[0] += x.x; db[1] += x.y; b[0] += y.x; b[1] += y.y;
-            }
+            float av[2], b[2];
             av[0] = dots[2 * lane] + dots[kChunk + 2 * lane];
             av[1] = dots[2 * lane + 1] + dots[kChunk + 2 * lane + 1];
+            b[0] = dotb[2 * lane] + dotb[kChunk + 2 * lane];
+            b[1] = dotb[2 * lane + 1] + dotb[kChunk + 2 * lane + 1];
             float below = av[0] + av[1], above = b[0] + b[1];   // sums over i >= 2 lane, over j <= 2 lane + 1
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                     const bool forgets = scal[320 + t] != (t ? scal[319 + t] : 0.f);
                     const float s = run[t] + (e ? after + av[1] : below) + (e ? before + b[0] : before) + c;
                     a.dg[at + (size_t)t * a.s.hv] = forgets ? 0.f : s;
-                    const float d = db[e] / scal[128 + t];
+                    const float d = diag[t] / scal[128 + t];
                     if (a.beta_f32) static_cast<float *>(a.dbeta)[at + (size_t)t * a.s.hv] = d;
                     else static_cast<T *>(a.dbeta)[at + (size_t)t * a.s.hv] = from_f32<T>(d);
                 }

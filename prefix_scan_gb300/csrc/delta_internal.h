@@ -35,9 +35,11 @@ struct DeltaShape {
 //   S      2 x V x K         row v, column k: the state at the chunk's start (backward only)
 //   U      2 x V x 64        row v, column token (backward only)
 // and the backward chain adds dS (as S: the gradient of the state at the chunk's end) and
-// dR (as U).
+// dU (as U).  After all of these come, for each (chunk, key head), the chunk's keys and then
+// its queries as images of 64 rows of K, one plane for bf16 and two for other types: rows past
+// the sequence's end and columns past K are 0.
 struct ChunkLayout {
-    size_t scal, t, p, n, s, u, ds, dr, stride;
+    size_t scal, t, p, n, s, u, ds, du, stride;
 };
 constexpr size_t kSquare = (size_t)kChunk * kChunk * 2;   // bytes of one 64 x 64 plane
 constexpr int pad_k(int k) { return k <= 64 ? 64 : 128; }
@@ -54,11 +56,12 @@ constexpr ChunkLayout chunk_layout(int k, int v, bool train) {
         l.s = at; at += 2 * sp;
         l.u = at; at += 2 * up;
         l.ds = at; at += 2 * sp;
-        l.dr = at; at += 2 * up;
+        l.du = at; at += 2 * up;
     }
     l.stride = (at + 255) / 256 * 256;
     return l;
 }
+constexpr size_t kq_stride(int k, int planes) { return (size_t)2 * planes * kChunk * pad_k(k) * 2; }
 constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
     return packed ? tokens / kChunk + seqs : seqs * ((tokens + kChunk - 1) / kChunk);
 }
@@ -71,7 +74,7 @@ struct DeltaArgs {
     const float *h0;              // [seqs, hv, k, v] or null
     float *ht;                    // the same, or null
     void *o;                      // contiguous [tokens, hv, v]
-    unsigned char *ws;
+    unsigned char *ws, *kq;
     long long slots;
     int train;                    // keep what the backward pass reads
     // backward
@@ -80,7 +83,6 @@ struct DeltaArgs {
     const float *dht;
     float *dh0, *dg;
     void *dq, *dk, *dv, *dbeta;
-    float *part;                  // [slots, hv, v blocks, 2, 64]: sums over v blocks of dbeta and of b_j
 };
 
 // Type codes: PS_REAL_F32, PS_REAL_BF16, PS_REAL_F16.

@@ -1,8 +1,14 @@
 // delta_prepare.cu -- what the chunks of the gated delta rule need before
-// their states are known: decays, the masked products P and N, and the
-// triangular inverse T (notation in delta_common.cuh).  One CTA per chunk and
-// key head, all chunks at once; it keeps k and q and their products for all
-// value heads that share the key head.
+// their states are known: decays, the masked products P and N, the triangular
+// inverse T (notation in delta_common.cuh), and the chunk's keys and queries as
+// images.  One CTA per chunk and key head, all chunks at once; the products
+// k k^T and q k^T stay in registers for all value heads that share the key head.
+//
+// T comes in blocks of 16: the four diagonal blocks by forward substitution in
+// f32 (one column per thread), the blocks below them a block column per warp,
+//     T_ij = -T_ii diag(beta) sum_{j <= l < i} N_il T_lj,
+// transposed, so that each product's left operand is the result before it in
+// the warp's registers.
 #include "delta_common.cuh"
 
 namespace ps {
@@ -10,21 +16,22 @@ namespace ps {
 namespace {
 
 constexpr int kPrepThreads = 128;   // four warps: 16 rows of a 64 x 64 product each
+constexpr int kDiag = 264;          // floats from one diagonal block to the next: 16 x 16, and 8 against bank conflicts
 
 template <int NP, int KP>
 struct PrepSmem {
     static constexpr int kPlane = kChunk * KP * 2;
     static constexpr int kK = 0, kQ = NP * kPlane;
-    static constexpr int kL = 2 * NP * kPlane;               // f32 64 x 64
-    static constexpr int kT = kL + kChunk * kChunk * 4;      // images hi, lo
-    static constexpr int kP = kT + 2 * (int)kSquare;
-    static constexpr int kN = kP + 2 * (int)kSquare;
-    static constexpr int kScal = kN + 2 * (int)kSquare;
-    static constexpr int kBytes = kScal + 6 * kChunk * 4;
+    static constexpr int kT = 0, kP = 2 * (int)kSquare, kN = 4 * (int)kSquare;   // in the place of K and Q
+    static constexpr int kScal = 2 * NP * kPlane > 6 * (int)kSquare ? 2 * NP * kPlane : 6 * (int)kSquare;
+    static constexpr int kL = kScal + 6 * kChunk * 4;                            // f32 diagonal blocks of diag(beta) N
+    static constexpr int kBytes = kL + 4 * kDiag * 4;
 };
 
 // exp(x) leaves f32's normal range below this: the state is forgotten.
 constexpr float kForget = -87.f;
+// In the place of smaller gates: the backward pass divides by beta.  No result changes by more than that.
+constexpr float kLeastBeta = 0x1p-60f;
 
 }  // namespace
 
@@ -86,6 +93,13 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
             }
         }
     }
+    {
+        uint4 *kq = reinterpret_cast<uint4 *>(a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP));
+#pragma unroll
+        for (int i = 0; i < 2 * NP * M::kPlane / (16 * kPrepThreads); ++i)
+            kq[i * kPrepThreads + tid] = reinterpret_cast<const uint4 *>(smem + M::kK)[i * kPrepThreads + tid];
+    }
+    __syncthreads();
 
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
     for (int hr = 0; hr < rep; ++hr) {
@@ -127,77 +141,125 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
             if (i < rows)
                 b = a.beta_f32 ? row_ptr<float>(a.beta, sp, seq, t0, head)[i * a.beta.tok]
                                : to_f32<T>(row_ptr<T>(a.beta, sp, seq, t0, head)[i * a.beta.tok]);
-            // the backward pass divides u by beta; 2^-60 in the place of 0 changes no result by more than that
-            if (fabsf(b) < 0x1p-60f) b = 0x1p-60f;
+            if (fabsf(b) < kLeastBeta) b = kLeastBeta;
             scal[128 + i] = b;
         }
         __syncthreads();
 
-        {   // L = diag(beta) N in f32, P and N as pairs
-            const int i0 = 16 * warp + (lane >> 2);
+        {   // P and N as pairs, the diagonal blocks of diag(beta) N in f32
+            const int r8 = lane >> 2, i0 = 16 * warp + r8;
             const float gh0 = scal[192 + i0], gl0 = scal[256 + i0], r0 = scal[320 + i0], b0 = scal[128 + i0];
             const float gh1 = scal[200 + i0], gl1 = scal[264 + i0], r1 = scal[328 + i0], b1 = scal[136 + i0];
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
-                uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0}, nh[4] = {0, 0, 0, 0}, nl[4] = {0, 0, 0, 0};
-                if (np <= warp) {
+                if (np > warp) continue;   // above the diagonal: nobody reads it
+                uint32_t ph[4], pl[4], nh[4], nl[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {   // register q of the block's fragment: tile q >> 1, rows +8 for odd q
-                        const int n = 2 * np + (q >> 1), row = q & 1, i = i0 + 8 * row, j = 8 * n + 2 * (lane & 3);
-                        float pv[2], nv[2];
+                for (int q = 0; q < 4; ++q) {   // register q of the block's fragment: tile q >> 1, rows +8 for odd q
+                    const int n = 2 * np + (q >> 1), row = q & 1, i = i0 + 8 * row, j = 8 * n + 2 * (lane & 3);
+                    float pv[2], nv[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int c = j + e;
-                            const float dx = ((row ? gh1 : gh0) - scal[192 + c]) + ((row ? gl1 : gl0) - scal[256 + c]);
-                            const float D = i >= c && (row ? r1 : r0) == scal[320 + c] ? expf(dx) : 0.f;
-                            nv[e] = i > c ? D * kk[n][2 * row + e] : 0.f;
-                            pv[e] = i >= c ? a.s.scale * D * qk[n][2 * row + e] : 0.f;
-                        }
-                        *reinterpret_cast<float2 *>(L + i * kChunk + j) =
-                            make_float2((row ? b1 : b0) * nv[0], (row ? b1 : b0) * nv[1]);
-                        split2(pv[0], pv[1], ph[q], pl[q]);
-                        split2(nv[0], nv[1], nh[q], nl[q]);
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = j + e;
+                        const float dx = ((row ? gh1 : gh0) - scal[192 + c]) + ((row ? gl1 : gl0) - scal[256 + c]);
+                        const float D = i >= c && (row ? r1 : r0) == scal[320 + c] ? expf(dx) : 0.f;
+                        nv[e] = i > c ? D * kk[n][2 * row + e] : 0.f;
+                        pv[e] = i >= c ? a.s.scale * D * qk[n][2 * row + e] : 0.f;
                     }
+                    if (np == warp)
+                        *reinterpret_cast<float2 *>(L + warp * kDiag + (r8 + 8 * row) * 16 + (j & 15)) =
+                            make_float2((row ? b1 : b0) * nv[0], (row ? b1 : b0) * nv[1]);
+                    split2(pv[0], pv[1], ph[q], pl[q]);
+                    split2(nv[0], nv[1], nh[q], nl[q]);
                 }
                 const uint32_t at = img<128>(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
                 stsm4(base + M::kP + at, ph[0], ph[1], ph[2], ph[3]);
                 stsm4(base + M::kP + (uint32_t)kSquare + at, pl[0], pl[1], pl[2], pl[3]);
-                if (a.train) {
-                    stsm4(base + M::kN + at, nh[0], nh[1], nh[2], nh[3]);
-                    stsm4(base + M::kN + (uint32_t)kSquare + at, nl[0], nl[1], nl[2], nl[3]);
-                }
+                stsm4(base + M::kN + at, nh[0], nh[1], nh[2], nh[3]);
+                stsm4(base + M::kN + (uint32_t)kSquare + at, nl[0], nl[1], nl[2], nl[3]);
             }
         }
         __syncthreads();
 
         if (tid < kChunk) {
-            // column tid of T by forward substitution: T_ij = delta_ij - sum_{l < i} L_il T_lj
-            float x[kChunk];
+            // column c of a diagonal block by forward substitution: x_i = delta_ic - sum_{l < i} L_il x_l
+            const int c = tid & 15;
+            const float *D = L + (tid >> 4) * kDiag;
+            float x[16];
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                float s0 = i == tid ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            for (int i = 0; i < 16; ++i) {
+                float s[4] = {i == c ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int l = 0; l + 3 < i; l += 4) {
-                    const float4 c = *reinterpret_cast<const float4 *>(L + i * kChunk + l);
-                    s0 -= c.x * x[l]; s1 -= c.y * x[l + 1]; s2 -= c.z * x[l + 2]; s3 -= c.w * x[l + 3];
+                for (int l = 0; l < i; l += 4) {
+                    const float4 d = *reinterpret_cast<const float4 *>(D + i * 16 + l);
+                    s[0] -= d.x * x[l];
+                    if (l + 1 < i) s[1] -= d.y * x[l + 1];
+                    if (l + 2 < i) s[2] -= d.z * x[l + 2];
+                    if (l + 3 < i) s[3] -= d.w * x[l + 3];
                 }
-#pragma unroll
-                for (int l = i & ~3; l < i; ++l) s0 -= L[i * kChunk + l] * x[l];
-                x[i] = (s0 + s1) + (s2 + s3);
+                x[i] = (s[0] + s[1]) + (s[2] + s[3]);
             }
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
-                const __nv_bfloat16 l = __float2bfloat16_rn(split_rest(x[i], __bfloat162float(h)));
-                const int at = (int)img<128>(0, i, tid >> 3) + (tid & 7) * 2;
+                const __nv_bfloat16 l = __float2bfloat16_rn(x[i] - __bfloat162float(h));
+                const int at = (int)img<128>(0, (tid & ~15) + i, tid >> 3) + (tid & 7) * 2;
                 *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + at) = h;
                 *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + kSquare + at) = l;
             }
         }
         __syncthreads();
 
+        {   // block column `warp` below its diagonal block
+            uint32_t x[4][2][4];   // T_lj^T as left operands
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                load_a_t<128>(x[0][p], base + M::kT + p * (uint32_t)kSquare, 16 * warp, 16 * warp, lane);
+#pragma unroll
+            for (int d = 1; d < 4; ++d) {
+                const int i = warp + d;
+                if (i > 3) continue;
+                float y[2][4], z[2][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[0][e] = y[1][e] = z[0][e] = z[1][e] = 0.f;
+#pragma unroll
+                for (int l = 0; l < d; ++l) {
+                    uint32_t bh[4], bl[4];
+                    load_b<128>(bh, base + M::kN, 16 * i, 16 * (warp + l), lane);
+                    load_b<128>(bl, base + M::kN + (uint32_t)kSquare, 16 * i, 16 * (warp + l), lane);
+                    mma_bf16(y[0], x[l][0], bh[0], bh[1]);
+                    mma_bf16(y[1], x[l][0], bh[2], bh[3]);
+                    mma_bf16(y[0], x[l][1], bh[0], bh[1]);
+                    mma_bf16(y[1], x[l][1], bh[2], bh[3]);
+                    mma_bf16(y[0], x[l][0], bl[0], bl[1]);
+                    mma_bf16(y[1], x[l][0], bl[2], bl[3]);
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float2 be = *reinterpret_cast<const float2 *>(scal + 128 + 16 * i + 8 * t + 2 * (lane & 3));
+                    y[t][0] *= -be.x; y[t][1] *= -be.y; y[t][2] *= -be.x; y[t][3] *= -be.y;
+                }
+                uint32_t f[2][4], bh[4], bl[4];
+                split_tiles(y[0], y[1], f);
+                load_b<128>(bh, base + M::kT, 16 * i, 16 * i, lane);
+                load_b<128>(bl, base + M::kT + (uint32_t)kSquare, 16 * i, 16 * i, lane);
+                mma_bf16(z[0], f[0], bh[0], bh[1]);
+                mma_bf16(z[1], f[0], bh[2], bh[3]);
+                mma_bf16(z[0], f[1], bh[0], bh[1]);
+                mma_bf16(z[1], f[1], bh[2], bh[3]);
+                mma_bf16(z[0], f[0], bl[0], bl[1]);
+                mma_bf16(z[1], f[0], bl[2], bl[3]);
+                split_tiles(z[0], z[1], x[d]);
+                const uint32_t at = img<128>(base + M::kT, 16 * i + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1));
+                stsm4_t(at, x[d][0][0], x[d][0][1], x[d][0][2], x[d][0][3]);
+                stsm4_t(at + (uint32_t)kSquare, x[d][1][0], x[d][1][1], x[d][1][2], x[d][1][3]);
+            }
+        }
+        __syncthreads();
+
         unsigned char *out = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
         const int imgs = (a.train ? 6 : 4) * (int)kSquare / 16;   // T, P, N follow one another on both sides
+#pragma unroll 4
         for (int i = tid; i < imgs; i += kPrepThreads)
             reinterpret_cast<uint4 *>(out + lay.t)[i] = reinterpret_cast<const uint4 *>(smem + M::kT)[i];
         for (int i = tid; i < 6 * kChunk; i += kPrepThreads) reinterpret_cast<float *>(out + lay.scal)[i] = scal[i];
