@@ -1,345 +1,475 @@
 // delta_chain.cu -- the gated delta rule's states, chunk after chunk, and its
 // outputs (notation in delta_common.cuh).
 //
-// A warp owns 16 of the V columns of one head's state, transposed: S^T is a
-// 16 x K accumulator in registers, and every product of a chunk,
-//     X^T = S^T K^T,  U^T = (beta R)^T T^T,  S'^T = exp(G_C) S^T + (exp(G_C - G) U)^T K,
-// has its left operand in this warp's registers (the result of the one before
-// it: an accumulator's registers are a left operand's) and its right operand
-// in shared memory, the same for all warps.  So the chain of dependent
-// products, which bounds the kernel, crosses no barrier and no memory.
+// One CTA per sequence, value head and block of 128 values.  Everything is held
+// transposed: values are the 128 rows of the tensor-memory accumulators, and the
+// left operand of each product is the result of the one before it, split into
+// pairs of bf16 and put back into tensor memory, while keys, queries, T and P are
+// right operands in shared memory:
+//     X^T = S^T K^T           U^T = (beta R)^T T^T
+//     S'^T = exp(G_C) S^T + (exp(G_C - G) U)^T K
+//     O^T = scale exp(G) (S^T Q^T) + U^T P^T
+// The state stays in tensor memory from the first chunk to the last.  T and P are
+// lower triangular.
 //
-// Each such warp has a partner on the same 16 columns that does what the chain
-// does not wait for: the loads of the next chunk, the outputs
-//     O^T = scale exp(G) S^T Q^T + U^T P^T
-// from the S and U that the chain left in shared memory, and in training their
-// way to memory for the backward pass.
-#include "delta_common.cuh"
+// A product of 128 rows, 16 inner and up to 128 columns takes 64 clocks however
+// few the columns (measured), so keys and queries are one operand of 128 columns,
+// and so are the two parts of T: U comes as two accumulators, added on their way out.
+//
+// Bounded by the chain S -> X -> U -> S' of each chunk: three products and, between
+// them, the way of 128 x 128 and twice 128 x 64 numbers through registers.  So the
+// warps have roles: one issues products, two load the next chunk (one its values),
+// one stores what training keeps, eight convert on the chain (row = lane, half of
+// the columns each), and four take the outputs, which the chain does not wait for:
+// U^T P^T of a chunk runs while the next one's X is on its way through registers.
+#include "delta_tmem.cuh"
 
 namespace ps {
 
 namespace {
 
-template <typename T, int KP, int NW>
+constexpr int kChainThreads = 16 * 32, kFirstConvert = 4, kFirstOut = 12;   // warps
+// Tensor-memory columns: S; its pair, later U's two accumulators; X and S^T Q^T; the pair of beta R,
+// later of U; the pair of exp(G_C - G) U, later U^T P^T.
+constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColU = 128, kColX = 256, kColQ = 320, kColR = 384, kColW = 448;
+constexpr uint32_t kColO = kColW;
+
+template <typename T, int KP>
 struct ChainSmem {
     static constexpr int NP = Planes<T>::NP;
-    static constexpr int VB = 16 * NW;
-    static constexpr int kKP = kChunk * KP * 2, kVP = kChunk * VB * 2;
-    // one stage
-    static constexpr int kK = 0, kQ = NP * kKP, kV = 2 * NP * kKP, kT = kV + NP * kVP;
-    static constexpr int kP = kT + 2 * (int)kSquare, kScal = kP + 2 * (int)kSquare;
-    static constexpr int kStage = kScal + 1024;   // exp(G), exp(G_C - G), beta; stages 1024 bytes apart
+    static constexpr int kKQ = NP * (KP / 64) * kHalf, kTP = 4 * (int)kSquare;
     static constexpr int kStages = NP == 1 ? 2 : 1;
-    // for each pair of warps: images of S and U, rows of outputs
-    static constexpr int kS = 0, kU = 2 * 16 * KP * 2, kOut = kU + 2 * 16 * kChunk * 2;
-    static constexpr int kWarp = kOut + (sizeof(T) == 2 ? kChunk * 16 * 2 : 0);
-    static constexpr int kBytes = kStages * kStage + NW * kWarp;
-    static_assert(kStage % 1024 == 0 && kWarp % 128 == 0 && kBytes <= 227 * 1024, "images are aligned and fit");
+    static constexpr int kScal = 256, kTiles = 2048, kStage = kKQ + kTP;   // barriers and scalars come first
+    static constexpr int kVRow = kBlockV * (int)sizeof(T), kVTile = kChunk * kVRow, kV = kTiles + kStages * kStage;
+    static constexpr int kOut = kV + kVTile, kSave = kOut + kVTile;   // outputs; what training keeps: S, later U
+    static constexpr int kBytes = kSave, kTrainBytes = kSave + 2 * (KP / 64 > 1 ? 2 : 1) * kHalf;
+    static_assert(kTrainBytes <= 227 * 1024, "too much shared memory");
 };
+struct ChainBars {
+    uint64_t full[2], empty[2], v_full, v_empty, s_ready[2], x_done, q_read, r_ready, u_done, w_ready, u_ready, s_done, o_done, o_read, s_free, u_free, drained;
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(ChainBars) <= 256, "barriers precede the scalars");
 
 }  // namespace
 
-template <typename T, int KP, int NW>
-__global__ void __launch_bounds__(NW * 64) delta_chain_kernel(const DeltaArgs a) {
-    using M = ChainSmem<T, KP, NW>;
-    constexpr int NP = M::NP, VB = M::VB, NT = NW * 32, KT = KP / 16;
+template <typename T, int KP>
+__global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const DeltaArgs a) {
+    using M = ChainSmem<T, KP>;
+    constexpr int NP = M::NP, KH = KP / 64;
     extern __shared__ __align__(1024) unsigned char smem[];
+    ChainBars &bar = *reinterpret_cast<ChainBars *>(smem);
+    volatile int *gave_up = &bar.gave_up;
     const uint32_t base = smem_addr(smem);
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW;
-    const bool helper = threadIdx.x >= NT;
-    const int blocks = (a.s.v + VB - 1) / VB, rep = a.s.hv / a.s.hk;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be uniform
+    const int blocks = blocks_v(a.s.v), rep = a.s.hv / a.s.hk;
     const int vb = (int)(blockIdx.x % blocks);
     const int head = (int)(blockIdx.x / blocks % a.s.hv);
     const long long seq = blockIdx.x / blocks / a.s.hv;
     const Span sp = span_of(a.s, seq);
-    const int v0 = vb * VB, vw = v0 + 16 * warp;   // this CTA's and this pair's first column
-    const bool idle = vw >= a.s.v;                 // no column of this pair exists
-    const int r8 = lane >> 2, c2 = 2 * (lane & 3);
+    const int v0 = vb * kBlockV;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
-    const long long chunks = (sp.len + kChunk - 1) / kChunk;
-    const uint32_t own = base + M::kStages * M::kStage + warp * M::kWarp;
-    const int s_ready = 1 + warp, u_ready = 1 + NW + warp;
+    const int chunks = (int)((sp.len + kChunk - 1) / kChunk);
+    const size_t state = (size_t)(seq * a.s.hv + head) * a.s.k * a.s.v;
+    auto chunk_ws = [&](int c) { return a.ws + (size_t)((sp.slot + c) * a.s.hv + head) * lay.stride; };
 
-    if (helper) {
-        const unsigned char *ownp = smem + M::kStages * M::kStage + warp * M::kWarp;
-        const int tid = threadIdx.x - NT;
-        auto load = [&](long long c, int stage) {
-            const uint32_t st = base + stage * M::kStage;
-            const int rows = (int)min((long long)kChunk, sp.len - c * kChunk);
-            const unsigned char *w = a.ws + (size_t)((sp.slot + c) * a.s.hv + head) * lay.stride;
-            const unsigned char *kq = a.kq + (size_t)((sp.slot + c) * a.s.hk + head / rep) * kq_stride(a.s.k, NP);
-            load_image<2 * NP * M::kKP, NT>(st + M::kK, kq, tid);
-            load_image<4 * (int)kSquare, NT>(st + M::kT, w + lay.t, tid);
-            load_image<3 * kChunk * 4, NT>(st + M::kScal, w + lay.scal, tid);
-            load_tile<T, VB>(st + M::kV, M::kVP, row_ptr<T>(a.v, sp, seq, c * kChunk, head) + v0, a.v.tok, rows,
-                             a.s.v - v0, a.vec_v != 0, tid, NT);
-            cp_async_commit();
-        };
-        if (chunks > 0) load(0, 0);
-        for (long long c = 0; c < chunks; ++c) {
-            const int stage = M::kStages == 2 ? (int)(c & 1) : 0;
-            cp_async_wait<0>();
-            __syncthreads();
-            if (M::kStages == 2 && c + 1 < chunks) load(c + 1, stage ^ 1);
-            const uint32_t st = base + stage * M::kStage;
-            const float *scal = reinterpret_cast<const float *>(smem + stage * M::kStage + M::kScal);
-            if (!idle) {
-                unsigned char *w = a.ws + (size_t)((sp.slot + c) * a.s.hv + head) * lay.stride;
-                const int rows = (int)min((long long)kChunk, sp.len - c * kChunk);
-                float o[8][4];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1 + 4);
+        }
+        mbar_init(&bar.v_full, 32);
+        mbar_init(&bar.v_empty, 8);
+        mbar_init(&bar.s_ready[0], 8);
+        mbar_init(&bar.s_ready[1], 8);
+        mbar_init(&bar.x_done, 1);
+        mbar_init(&bar.q_read, 4);
+        mbar_init(&bar.r_ready, 8);
+        mbar_init(&bar.u_done, 1);
+        mbar_init(&bar.w_ready, 8);
+        mbar_init(&bar.u_ready, 8);
+        mbar_init(&bar.s_done, 1);
+        mbar_init(&bar.o_done, 1);
+        mbar_init(&bar.o_read, 4);
+        mbar_init(&bar.s_free, 1);
+        mbar_init(&bar.u_free, 1);
+        mbar_init(&bar.drained, 1);
+        bar.gave_up = base & 1023 ? 1 : 0;   // images need their alignment
+        mbar_init_done();
+    }
+    if (warp == 0) tmem_alloc(smem_addr(&bar.tmem));
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    constexpr uint32_t tm = 0;   // all columns are this CTA's
+    if (threadIdx.x == 0 && bar.tmem != tm) bar.gave_up = 1;
+
+    if (warp == 0) {
+        const uint32_t one = elect_lane();
+        {
+            // operands: keys and queries by rows, keys by columns, T and P after it
+            const uint64_t kq0 = operand(base + M::kTiles, true, 0), kt0 = operand(base + M::kTiles, false, kHalf);
+            // U^T P^T: tokens 16 k.. of U reach tokens 16 k.. and later
+            auto outputs = [&](int c) {
+                const int st = c % M::kStages;
+                const uint64_t pp = further(kq0, st * M::kStage + M::kKQ + 2 * (uint32_t)kSquare);
+                wait_phase(&bar.u_ready, c & 1, gave_up);
+                tmem_fence_after();
 #pragma unroll
-                for (int n = 0; n < 8; ++n)
+                for (int t = 0; t < 3; ++t)   // hi hi, lo hi, hi lo
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-                await(s_ready);
+                    for (int k = 0; k < 4; ++k)
+                        mma_tmem(one, tm + kColO + 16 * k, tm + kColR + (t == 1 ? 32 : 0) + k * 8,
+                                 further(pp, (t == 2 ? (uint32_t)kSquare : 0) + k * (16 * 128 + 32)), shape(kChunk - 16 * k, true),
+                                 t + k > 0);
+                mma_commit(one, &bar.o_done);
+                mma_commit(one, &bar.empty[st]);
+            };
+#pragma unroll 1
+            for (int c = 0; c < chunks && !*gave_up; ++c) {
+                const int st = c % M::kStages;
+                const uint32_t at_stage = st * M::kStage;
+                const uint64_t kq = further(kq0, at_stage), kt = further(kt0, at_stage), tt = further(kq, M::kKQ);
+                if (M::kStages == 1 && c) outputs(c - 1);
+                wait_phase(&bar.full[st], (c / M::kStages) & 1, gave_up);
+                if (c) wait_phase(&bar.q_read, (c - 1) & 1, gave_up);
+                // S^T [K^T Q^T], by the columns of S that are ready together
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    uint32_t f[2][4];
+                for (int r = 0; r < KH; ++r) {
+                    wait_busy(&bar.s_ready[r], c & 1, gave_up);
+                    tmem_fence_after();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) load_a<KP * 2>(f[h], own + M::kS + h * 16 * KP * 2, 0, 16 * kt, lane);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint32_t b[4][4];
-#pragma unroll
-                        for (int np = 0; np < 4; ++np) load_b<KP * 2>(b[np], st + M::kQ + p * M::kKP, 16 * np, 16 * kt, lane);
+                    for (int p = 0; p < NP; ++p)
 #pragma unroll
                         for (int h = 0; h + p < 2; ++h)
 #pragma unroll
-                            for (int np = 0; np < 4; ++np) {
-                                mma_bf16(o[2 * np], f[h], b[np][0], b[np][1]);
-                                mma_bf16(o[2 * np + 1], f[h], b[np][2], b[np][3]);
+                            for (int i = 0; i < 4; ++i) {
+                                const int k = (i >> 1) * (KP / 32) + 2 * r + (i & 1);   // columns 16 k..
+                                mma_tmem(one, tm + kColX, tm + (h ? kColSLo : kColSHi) + k * 8,
+                                         further(kq, (p * KH + (k >> 2)) * kHalf + (k & 3) * 32), shape(2 * kChunk, true),
+                                         r + p + h + i > 0);
                             }
-                    }
                 }
-                const size_t srow = (size_t)pad_v(a.s.v) * KP * 2, urow = (size_t)pad_v(a.s.v) * kChunk * 2;
-                if (a.train)   // the state at the chunk's start
+                mma_commit(one, &bar.x_done);
+                if (M::kStages == 2 && c) outputs(c - 1);
+                wait_busy(&bar.r_ready, c & 1, gave_up);
+                tmem_fence_after();
+                // (beta R)^T T^T: the upper part of beta R with both of T's, the rest with T's upper one
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        store_image<16 * KP * 2>(w + lay.s + p * srow + (size_t)vw * KP * 2, ownp + M::kS + p * 16 * KP * 2, lane);
+                for (int k = 0; k < 4; ++k)
+                    mma_tmem(one, tm + kColU, tm + kColR + k * 8, further(tt, k * 32), shape(2 * kChunk, true), k > 0);
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float2 eg = *reinterpret_cast<const float2 *>(scal + 8 * n + c2);
-                    o[n][0] *= a.s.scale * eg.x; o[n][1] *= a.s.scale * eg.y;
-                    o[n][2] *= a.s.scale * eg.x; o[n][3] *= a.s.scale * eg.y;
-                }
-                await(u_ready);
+                for (int k = 0; k < 4; ++k)
+                    mma_tmem(one, tm + kColU, tm + kColR + 32 + k * 8, further(tt, k * 32), shape(kChunk, true), true);
+                mma_commit(one, &bar.u_done);
+                wait_busy(&bar.w_ready, c & 1, gave_up);
+                tmem_fence_after();
+                // S^T += (exp(G_C - G) U)^T K
 #pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {   // P is lower triangular
-                    uint32_t f[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) load_a<128>(f[h], own + M::kU + h * 16 * kChunk * 2, 0, 16 * kt, lane);
-#pragma unroll
-                    for (int np = kt; np < 4; ++np) {
-                        uint32_t ph[4], pl[4];
-                        load_b<128>(ph, st + M::kP, 16 * np, 16 * kt, lane);
-                        load_b<128>(pl, st + M::kP + (uint32_t)kSquare, 16 * np, 16 * kt, lane);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            mma_bf16(o[2 * np], f[h], ph[0], ph[1]);
-                            mma_bf16(o[2 * np + 1], f[h], ph[2], ph[3]);
-                        }
-                        mma_bf16(o[2 * np], f[0], pl[0], pl[1]);
-                        mma_bf16(o[2 * np + 1], f[0], pl[2], pl[3]);
-                    }
-                }
-                if (a.train)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        store_image<16 * kChunk * 2>(w + lay.u + p * urow + (size_t)vw * kChunk * 2,
-                                                     ownp + M::kU + p * 16 * kChunk * 2, lane);
-                // O^T in registers, rows of 16 columns in memory
-                T *out = static_cast<T *>(a.o) + ((size_t)(sp.first + c * kChunk) * a.s.hv + head) * a.s.v + vw;
-                const size_t ostride = (size_t)a.s.hv * a.s.v;
-                const bool whole = vw + 16 <= a.s.v && (a.s.v & 7) == 0 && (reinterpret_cast<uintptr_t>(a.o) & 15) == 0;
-                if (sizeof(T) == 2 && whole) {
-                    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                        for (int np = 0; np < 4; ++np) {
-                            const int row = 16 * np + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-                            stsm4_t(own + M::kOut + row * 32 + half * 16, pack2<T>(o[2 * np][0], o[2 * np][1]),
-                                    pack2<T>(o[2 * np][2], o[2 * np][3]), pack2<T>(o[2 * np + 1][0], o[2 * np + 1][1]),
-                                    pack2<T>(o[2 * np + 1][2], o[2 * np + 1][3]));
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = i * 16 + (lane >> 1);
-                            if (row < rows)
-                                *reinterpret_cast<uint4 *>(out + row * ostride + (lane & 1) * 8) =
-                                    *reinterpret_cast<const uint4 *>(ownp + M::kOut + row * 32 + (lane & 1) * 16);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = 8 * n + c2 + (e & 1), v = r8 + 8 * (e >> 1);
-                            if (tok < rows && vw + v < a.s.v) out[tok * ostride + v] = from_f32<T>(o[n][e]);
-                        }
-                }
-                __syncwarp();
-            }
-            if (M::kStages == 1) {
-                __syncthreads();
-                if (c + 1 < chunks) load(c + 1, 0);
-            }
-        }
-        return;
-    }
-
-    float s[2 * KT][4];   // S^T: rows vw + r8 (+8), columns 8 n + c2 (+1)
-    const size_t state = (size_t)(seq * a.s.hv + head) * a.s.k * a.s.v;
-#pragma unroll
-    for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int k = 8 * n + c2 + (e & 1), v = vw + r8 + 8 * (e >> 1);
-            s[n][e] = a.h0 != nullptr && k < a.s.k && v < a.s.v ? a.h0[state + (size_t)k * a.s.v + v] : 0.f;
-        }
-    for (long long c = 0; c < chunks; ++c) {
-        const int stage = M::kStages == 2 ? (int)(c & 1) : 0;
-        __syncthreads();
-        if (!idle) {
-            const uint32_t st = base + stage * M::kStage;
-            const float *scal = reinterpret_cast<const float *>(smem + stage * M::kStage + M::kScal);
-            // X^T = S^T K^T: tile n is tokens 8 n..
-            float x[8][4];
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                uint32_t f[2][4];
-                split_tiles(s[2 * kt], s[2 * kt + 1], f);
-                const uint32_t at = img<KP * 2>(own + M::kS, lane & 15, 2 * kt + (lane >> 4));
-                stsm4(at, f[0][0], f[0][1], f[0][2], f[0][3]);
-                stsm4(at + 16 * KP * 2, f[1][0], f[1][1], f[1][2], f[1][3]);
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    uint32_t b[4][4];
-#pragma unroll
-                    for (int np = 0; np < 4; ++np) load_b<KP * 2>(b[np], st + M::kK + p * M::kKP, 16 * np, 16 * kt, lane);
+                for (int p = 0; p < NP; ++p)
 #pragma unroll
                     for (int h = 0; h + p < 2; ++h)
 #pragma unroll
-                        for (int np = 0; np < 4; ++np) {
-                            mma_bf16(x[2 * np], f[h], b[np][0], b[np][1]);
-                            mma_bf16(x[2 * np + 1], f[h], b[np][2], b[np][3]);
-                        }
-                }
+                        for (int k = 0; k < 4; ++k)
+                            mma_tmem(one, tm + kColS, tm + kColW + h * 32 + k * 8,
+                                     further(kt, p * KH * kHalf + k * 16 * 128), shape(KP, false), true);
+                mma_commit(one, &bar.s_done);
             }
-            announce(s_ready);
-
-            // beta R as left operands, and U^T = (beta R)^T T^T; T is lower triangular
-            float u[8][4];
+            if (chunks > 0 && !*gave_up) outputs(chunks - 1);
+            mma_commit(one, &bar.drained);
+            wait_drained(&bar.drained, 0);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && a.train) {   // what training keeps
+            const int rows = min(kBlockV, (a.s.v - v0 + 15) / 16 * 16);
+            for (int c = 0; c < chunks; ++c) {
+                unsigned char *w = chunk_ws(c);
+                for (int r = 0; r < KH; ++r) wait_phase(&bar.s_ready[r], c & 1, gave_up);
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+                for (int p = 0; p < 2 * KH; ++p)
+                    bulk_store(w + lay.s + (size_t)(vb * 2 * KH + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(&bar.s_free);
+                wait_phase(&bar.u_ready, c & 1, gave_up);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[n][e] = 0.f;
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t f[NP][4], r[2][4];
-#pragma unroll
-                for (int p = 0; p < NP; ++p) load_a_t<VB * 2>(f[p], st + M::kV + p * M::kVP, 16 * kt, 16 * warp, lane);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = 2 * kt + (q >> 1), tok = 8 * n + c2;
-                    const float2 eg = *reinterpret_cast<const float2 *>(scal + tok);
-                    const float2 be = *reinterpret_cast<const float2 *>(scal + 128 + tok);
-                    float y0 = bf16_low(f[0][q]), y1 = bf16_high(f[0][q]);
-                    if constexpr (NP == 2) { y0 += bf16_low(f[1][q]); y1 += bf16_high(f[1][q]); }
-                    y0 = be.x * (y0 - eg.x * x[n][2 * (q & 1)]);
-                    y1 = be.y * (y1 - eg.y * x[n][2 * (q & 1) + 1]);
-                    split2(y0, y1, r[0][q], r[1][q]);
-                }
-                uint32_t th[4][4], tl[4][4];
-#pragma unroll
-                for (int np = kt; np < 4; ++np) {
-                    load_b<128>(th[np], st + M::kT, 16 * np, 16 * kt, lane);
-                    load_b<128>(tl[np], st + M::kT + (uint32_t)kSquare, 16 * np, 16 * kt, lane);
-                }
-#pragma unroll
-                for (int h = 0; h < 3; ++h)
-#pragma unroll
-                    for (int np = kt; np < 4; ++np) {
-                        const uint32_t(&b)[4] = h == 2 ? tl[np] : th[np];
-                        mma_bf16(u[2 * np], r[h & 1], b[0], b[1]);
-                        mma_bf16(u[2 * np + 1], r[h & 1], b[2], b[3]);
-                    }
+                for (int p = 0; p < 2; ++p)
+                    bulk_store(w + lay.u + (size_t)(vb * 2 + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(&bar.u_free);
             }
-
-            // the state: S^T = exp(G_C) S^T + (exp(G_C - G) U)^T K; exp(G_C) is the last token's
-            const float eall = scal[kChunk - 1];
-#pragma unroll
-            for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] *= eall;
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t f[2][4];
-                split_tiles(u[2 * kt], u[2 * kt + 1], f);
-                const uint32_t at = img<128>(own + M::kU, lane & 15, 2 * kt + (lane >> 4));
-                stsm4(at, f[0][0], f[0][1], f[0][2], f[0][3]);
-                stsm4(at + 16 * kChunk * 2, f[1][0], f[1][1], f[1][2], f[1][3]);
+            bulk_wait();
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int c = 0;
+            for (; c < chunks; ++c) {
+                const int st = c % M::kStages;
+                if (c >= M::kStages) wait_phase(&bar.empty[st], (c / M::kStages - 1) & 1, gave_up);
+                if (*gave_up) break;
+                unsigned char *w = chunk_ws(c), *to = smem + M::kTiles + st * M::kStage;
+                mbar_arrive_expect_tx(&bar.full[st], M::kStage + 3 * kChunk * 4);
+                bulk_load(to, a.kq + (size_t)((sp.slot + c) * a.s.hk + head / rep) * kq_stride(a.s.k, NP), M::kKQ, &bar.full[st]);
+                bulk_load(to + M::kKQ, w + lay.t, M::kTP, &bar.full[st]);
+                bulk_load(smem + M::kScal + st * 3 * kChunk * 4, w + lay.scal, 3 * kChunk * 4, &bar.full[st]);
             }
-            announce(u_ready);
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t f[2][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = 2 * kt + (q >> 1);
-                    const float2 el = *reinterpret_cast<const float2 *>(scal + 64 + 8 * n + c2);
-                    split2(el.x * u[n][2 * (q & 1)], el.y * u[n][2 * (q & 1) + 1], f[0][q], f[1][q]);
-                }
-#pragma unroll
-                for (int nb = 0; nb < KT; nb += 4)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint32_t b[4][4];
-#pragma unroll
-                        for (int np = 0; np < 4; ++np)
-                            load_b_t<KP * 2>(b[np], st + M::kK + p * M::kKP, 16 * kt, 16 * (nb + np), lane);
-#pragma unroll
-                        for (int h = 0; h + p < 2; ++h)
-#pragma unroll
-                            for (int np = 0; np < 4; ++np) {
-                                mma_bf16(s[2 * (nb + np)], f[h], b[np][0], b[np][1]);
-                                mma_bf16(s[2 * (nb + np) + 1], f[h], b[np][2], b[np][3]);
-                            }
-                    }
+            for (int i = c < M::kStages ? 0 : c - M::kStages; i < c; ++i)   // copies in flight
+                wait_drained(&bar.full[i % M::kStages], (i / M::kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        const int cols = min(kBlockV, a.s.v - v0);
+        int c = 0;
+        for (; c < chunks; ++c) {
+            const int n = (int)min((long long)kChunk, sp.len - (long long)c * kChunk);
+            if (c) wait_phase(&bar.v_empty, (c - 1) & 1, gave_up);
+            if (*gave_up) break;
+            const T *src = row_ptr<T>(a.v, sp, seq, (long long)c * kChunk, head) + v0;
+            unsigned char *dst = smem + M::kV;
+            if (a.vec_v) {
+                constexpr int PIECES = M::kVRow / 16;   // 16-byte pieces of a row
+                const int piece = lane % PIECES;
+                if (piece * 16 < cols * (int)sizeof(T))
+                    for (int i = lane / PIECES; i < n; i += 32 / PIECES)
+                        cp_async16(smem_addr(dst) + i * M::kVRow + piece * 16, reinterpret_cast<const char *>(src + i * a.v.tok) + piece * 16, true);
+                mbar_arrive_after_copies(&bar.v_full);
+            } else {
+                for (int i = lane; i < n * kBlockV; i += 32)
+                    if (i % kBlockV < cols) reinterpret_cast<T *>(dst)[i] = src[(i / kBlockV) * a.v.tok + i % kBlockV];
+                mbar_arrive(&bar.v_full);
             }
         }
-        if (M::kStages == 1) __syncthreads();
-    }
-
-    if (a.ht != nullptr) {
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+    } else if (warp >= kFirstConvert && warp < kFirstOut) {
+        const int row = 32 * (warp & 3) + lane, half = (warp - kFirstConvert) >> 2, v = v0 + row;   // this thread's value, its half
+        const uint32_t at = (uint32_t)(warp & 3) << 21;                                             // lane 32 (warp % 4)
+        float x[2][16], y[2][16];
+        uint32_t hi[8], lo[8];
+#pragma unroll 1
+        for (int b = 0; b < KP / 32; ++b) {   // 16 columns of the state at a time
+            const int k0 = half * (KP / 2) + 16 * b;
 #pragma unroll
-        for (int n = 0; n < 2 * KT; ++n)
+            for (int i = 0; i < 16; ++i)
+                x[0][i] = a.h0 != nullptr && k0 + i < a.s.k && v < a.s.v ? a.h0[state + (size_t)(k0 + i) * a.s.v + v] : 0.f;
+            tmem_st16(at + kColS + k0, x[0]);
+        }
+        tmem_wait_st();
+        // this half's values of a chunk; rows past the sequence's end and values past V hold anything and count as 0
+        auto values = [&](int c) {
+            const T *vp = reinterpret_cast<const T *>(smem + M::kV) + 32 * half * kBlockV + row;
+            const int n = v < a.s.v ? (int)min((long long)kChunk, sp.len - (long long)c * kChunk) - 32 * half : 0;
+            wait_phase(&bar.v_full, c & 1, gave_up);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 8 * n + c2 + (e & 1), v = vw + r8 + 8 * (e >> 1);
-                if (k < a.s.k && v < a.s.v) a.ht[state + (size_t)k * a.s.v + v] = s[n][e];
+            for (int i = 0; i < 32; ++i) y[i >> 4][i & 15] = to_f32<T>(vp[i * kBlockV]);
+            if (n < 32)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i >= n) y[i >> 4][i & 15] = 0.f;
+            warp_arrive(&bar.v_empty, lane);
+        };
+        if (chunks > 0) values(0);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c % M::kStages;
+            const float *scal = reinterpret_cast<const float *>(smem + M::kScal + st * 3 * kChunk * 4) + 32 * half;
+            wait_phase(&bar.full[st], (c / M::kStages) & 1, gave_up);
+            const float eall = scal[kChunk - 1 - 32 * half];
+            if (c > 0) {
+                if (a.train) wait_phase(&bar.u_free, (c - 1) & 1, gave_up);
+                wait_phase(&bar.s_done, (c - 1) & 1, gave_up);
+                tmem_fence_after();
             }
+#pragma unroll 1
+            for (int r = 0; r < KH; ++r) {
+                const int k16 = half * (KP / 32) + 2 * r;
+                tmem_ld16(x[0], at + kColS + 16 * k16, x[1], at + kColS + 16 * k16 + 16);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    split16(x[b], hi, lo);
+                    tmem_st8(at + kColSHi + 8 * (k16 + b), hi);
+                    tmem_st8(at + kColSLo + 8 * (k16 + b), lo);
+                    scale16(x[b], eall);
+                    tmem_st16(at + kColS + 16 * (k16 + b), x[b]);
+                    if (a.train) keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
+                }
+                if (a.train) fence_async();
+                tmem_wait_st();
+                tmem_fence_before();
+                warp_arrive(&bar.s_ready[r], lane);
+            }
+
+            wait_phase(&bar.x_done, c & 1, gave_up);
+            tmem_fence_after();
+            tmem_ld16(x[0], at + kColX + 32 * half, x[1], at + kColX + 32 * half + 16);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {   // beta R = beta (V - exp(G) X)
+                    const float4 eg = *reinterpret_cast<const float4 *>(scal + 16 * b + i);
+                    const float4 be = *reinterpret_cast<const float4 *>(scal + 128 + 16 * b + i);
+                    const float2 r0 = fma2(make_float2(-eg.x, -eg.y), make_float2(x[b][i], x[b][i + 1]), make_float2(y[b][i], y[b][i + 1]));
+                    const float2 r1 = fma2(make_float2(-eg.z, -eg.w), make_float2(x[b][i + 2], x[b][i + 3]), make_float2(y[b][i + 2], y[b][i + 3]));
+                    const float2 y0 = mul2(make_float2(be.x, be.y), r0), y1 = mul2(make_float2(be.z, be.w), r1);
+                    x[b][i] = y0.x; x[b][i + 1] = y0.y; x[b][i + 2] = y1.x; x[b][i + 3] = y1.y;
+                }
+            if (c > 0) wait_phase(&bar.o_done, (c - 1) & 1, gave_up);   // the last chunk's U was there
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                split16(x[b], hi, lo);
+                tmem_st8(at + kColR + 16 * half + 8 * b, hi);
+                tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            warp_arrive(&bar.r_ready, lane);
+            if (c + 1 < chunks) values(c + 1);
+
+            if (c > 0) wait_phase(&bar.o_read, (c - 1) & 1, gave_up);   // the last outputs were where the next pair goes
+            wait_phase(&bar.u_done, c & 1, gave_up);
+            tmem_fence_after();
+            {
+                float z[2][16];
+                tmem_ld16(x[0], at + kColU + 32 * half, z[0], at + kColU + kChunk + 32 * half);
+                tmem_ld16(x[1], at + kColU + 32 * half + 16, z[1], at + kColU + kChunk + 32 * half + 16);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 u = fma2(make_float2(1.f, 1.f), make_float2(x[b][i], x[b][i + 1]), make_float2(z[b][i], z[b][i + 1]));
+                        z[b][i] = x[b][i] = u.x;
+                        z[b][i + 1] = x[b][i + 1] = u.y;
+                    }
+                    scale16(z[b], scal + 64 + 16 * b);
+                    split16(z[b], hi, lo);
+                    tmem_st8(at + kColW + 16 * half + 8 * b, hi);
+                    tmem_st8(at + kColW + 32 + 16 * half + 8 * b, lo);
+                }
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            warp_arrive(&bar.w_ready, lane);
+            if (a.train) wait_phase(&bar.s_free, c & 1, gave_up);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                split16(x[b], hi, lo);
+                tmem_st8(at + kColR + 16 * half + 8 * b, hi);
+                tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
+                if (a.train) keep16(base + M::kSave, kHalf, row, 2 * half + b, hi, lo);
+            }
+            if (a.train) fence_async();
+            tmem_wait_st();
+            tmem_fence_before();
+            warp_arrive(&bar.u_ready, lane);
+        }
+        if (a.ht != nullptr) {   // the state at the end
+            if (chunks > 0) wait_phase(&bar.s_done, (chunks - 1) & 1, gave_up);
+            tmem_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < KP / 32; ++b) {
+                const int k0 = half * (KP / 2) + 16 * b;
+                tmem_ld16(x[0], at + kColS + k0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (k0 + i < a.s.k && v < a.s.v)
+                        a.ht[state + (size_t)(k0 + i) * a.s.v + v] = *gave_up ? __int_as_float(0x7fffffff) : x[0][i];
+            }
+        }
+    } else if (warp >= kFirstOut) {
+        const int row = 32 * (warp & 3) + lane;   // this thread's value
+        const uint32_t at = (uint32_t)(warp & 3) << 21;
+        const size_t ostride = (size_t)a.s.hv * a.s.v;
+        const bool rows_out = (a.s.v * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 15) == 0;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c % M::kStages;
+            const float *scal = reinterpret_cast<const float *>(smem + M::kScal + st * 3 * kChunk * 4);
+            const int n = (int)min((long long)kChunk, sp.len - (long long)c * kChunk);
+            T *out = static_cast<T *>(a.o) + ((size_t)(sp.first + (long long)c * kChunk) * a.s.hv + head) * a.s.v + v0;
+            float x[4][16];   // scale exp(G) S^T Q^T
+            wait_phase(&bar.full[st], (c / M::kStages) & 1, gave_up);
+            wait_phase(&bar.x_done, c & 1, gave_up);
+            tmem_fence_after();
+            tmem_ld16(x[0], at + kColQ, x[1], at + kColQ + 16);
+            tmem_ld16(x[2], at + kColQ + 32, x[3], at + kColQ + 48);
+            tmem_fence_before();
+            warp_arrive(&bar.q_read, lane);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                scale16(x[b], scal + 16 * b);
+                scale16(x[b], a.s.scale);
+            }
+            wait_phase(&bar.o_done, c & 1, gave_up);
+            tmem_fence_after();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float y[16];
+                tmem_ld16(y, at + kColO + 16 * b);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 o = fma2(make_float2(1.f, 1.f), make_float2(x[b][i], x[b][i + 1]), make_float2(y[i], y[i + 1]));
+                    x[b][i] = o.x;
+                    x[b][i + 1] = o.y;
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.o_read);
+                mbar_arrive(&bar.empty[st]);
+            }
+            if (rows_out) {   // by way of shared memory, to store whole rows
+                T *stage = reinterpret_cast<T *>(smem + M::kOut);
+                asm volatile("bar.sync 1, 128;" ::: "memory");   // the last chunk's rows have been read
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) stage[(16 * b + i) * kBlockV + row] = from_f32<T>(x[b][i]);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                constexpr int PIECES = M::kVRow / 16;
+                const int piece = row % PIECES;
+                if (piece * 16 < (a.s.v - v0) * (int)sizeof(T))
+#pragma unroll 2
+                    for (int i = row / PIECES; i < n; i += 128 / PIECES)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(out + i * ostride) + piece * 16) =
+                            *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(stage) + i * M::kVRow + piece * 16);
+            } else if (v0 + row < a.s.v) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * b + i < n) out[(16 * b + i) * ostride + row] = from_f32<T>(x[b][i]);
+            }
+        }
     }
+    tmem_fence_before();
+    __syncthreads();
+    if (*gave_up && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the outputs are not what they should be: say so
+        for (long long t = 0; t < sp.len; ++t)
+            static_cast<T *>(a.o)[((size_t)(sp.first + t) * a.s.hv + head) * a.s.v + v0 + threadIdx.x] =
+                from_f32<T>(__int_as_float(0x7fffffff));
+    tmem_fence_after();
+    if (warp == 0) tmem_free(bar.tmem);
 }
 
 namespace {
 
-template <typename T, int KP, int NW>
+template <typename T, int KP>
 cudaError_t chain(const DeltaArgs &a, cudaStream_t s) {
-    using M = ChainSmem<T, KP, NW>;
-    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, KP, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kBytes);
+    using M = ChainSmem<T, KP>;
+    const int bytes = a.train ? M::kTrainBytes : M::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kTrainBytes);
     if (e != cudaSuccess) return e;
-    const long long ctas = a.s.seqs * a.s.hv * ((a.s.v + M::VB - 1) / M::VB);
-    delta_chain_kernel<T, KP, NW><<<(unsigned)ctas, NW * 64, M::kBytes, s>>>(a);
+    const long long ctas = a.s.seqs * a.s.hv * blocks_v(a.s.v);
+    delta_chain_kernel<T, KP><<<(unsigned)ctas, kChainThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T>
 cudaError_t chain_for(const DeltaArgs &a, cudaStream_t s) {
-    return a.s.k <= 64 ? chain<T, 64, 4>(a, s) : chain<T, 128, 4>(a, s);
+    return a.s.k <= 64 ? chain<T, 64>(a, s) : chain<T, 128>(a, s);
 }
 
 }  // namespace

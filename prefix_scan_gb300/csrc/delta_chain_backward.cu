@@ -7,369 +7,430 @@
 // and leaves dS' and dU for the gradients of the other inputs
 // (delta_gradients.cu).
 //
-// As in the forward chain, a warp owns 16 columns and keeps dS'^T and every
-// left operand of the dependent products in registers.  Its partner works one
-// chunk ahead on what does not depend on the states, P^T dO and scale (exp(G)
-// Q)^T dO, holds both in registers until the chain has taken the last ones from
-// shared memory, loads the next chunk, and takes dS', dU and dV to memory.
-#include "delta_common.cuh"
+// Laid out as the forward chain (delta_chain.cu): everything transposed, values
+// are the 128 rows of the accumulators, left operands go through registers back
+// into tensor memory, right operands are the images in shared memory.  P^T dO
+// runs while dS' is on its way through registers, scale (exp(G) Q)^T dO while Y
+// is; dO becomes a left operand while the state's product runs.
+#include "delta_tmem.cuh"
 
 namespace ps {
 
 namespace {
 
-template <typename T, int KP, int NW>
+constexpr int kBackThreads = 16 * 32, kFirstConvert = 4, kFirstOut = 12;   // warps
+// Tensor-memory columns: dS; its pair, later dU's two accumulators; dO, later K dS'; P^T dO; the
+// pair of Y, later of -exp(G) dR; the pair of scale exp(G) dO.
+constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColU = 128, kColY = 256, kColO = 256, kColP = 320;
+constexpr uint32_t kColR = 384, kColQ = 448;
+
+template <typename T, int KP>
 struct BackSmem {
     static constexpr int NP = Planes<T>::NP;
-    static constexpr int VB = 16 * NW;
-    static constexpr int kKP = kChunk * KP * 2, kVP = kChunk * VB * 2;
-    // a stage of what the chain reads; the partners' tiles; exp(G), exp(G_C - G), beta of two chunks
-    static constexpr int kK = 0, kT = NP * kKP, kStage = kT + 2 * (int)kSquare;
+    static constexpr int kKQ = NP * (KP / 64) * kHalf, kTP = 4 * (int)kSquare;
     static constexpr int kStages = NP == 1 ? 2 : 1;
-    static constexpr int kQ = kStages * kStage, kP = kQ + NP * kKP, kO = kP + 2 * (int)kSquare;
-    static constexpr int kScal = kO + NP * kVP, kPairs = kScal + 2 * 1024;
-    // for each pair of warps: P^T dO and (exp(G) Q)^T dO as accumulators, images of dS' and dU, rows of dV
-    static constexpr int kA1 = 0, kA2 = kA1 + 16 * kChunk * 4, kDS = kA2 + 16 * KP * 4, kDU = kDS + 2 * 16 * KP * 2;
-    static constexpr int kOut = kDU + 2 * 16 * kChunk * 2;
-    static constexpr int kWarp = kOut + (sizeof(T) == 2 ? kChunk * 16 * 2 : 0);
-    static constexpr int kBytes = kPairs + NW * kWarp;
-    static_assert(kStage % 1024 == 0 && kWarp % 128 == 0 && kBytes <= 227 * 1024, "images are aligned and fit");
+    static constexpr int kScal = 256, kTiles = 2048, kStage = kKQ + kTP;   // barriers and two chunks' scalars come first
+    static constexpr int kRow = kBlockV * (int)sizeof(T), kTile = kChunk * kRow;
+    static constexpr int kDO = kTiles + kStages * kStage, kOut = kDO + kTile, kSave = kOut + kTile;   // kSave: dS', later dU
+    static constexpr int kBytes = kSave + 2 * (KP / 64 > 1 ? 2 : 1) * kHalf;
 };
+struct BackBars {
+    uint64_t full[2], empty[2], o_full, o_empty, o_ready, s_ready[2], y_done, r_ready, u_done, w_ready, s_done, out_ready, out_free;
+    uint64_t s_free, u_free, drained;
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(BackBars) <= 256, "barriers precede the scalars");
 
 }  // namespace
 
-template <typename T, int KP, int NW>
-__global__ void __launch_bounds__(NW * 64) delta_chain_backward_kernel(const DeltaArgs a) {
-    using M = BackSmem<T, KP, NW>;
-    constexpr int NP = M::NP, VB = M::VB, NT = NW * 32, KT = KP / 16;
+template <typename T, int KP>
+__global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(const DeltaArgs a) {
+    using M = BackSmem<T, KP>;
+    constexpr int NP = M::NP, KH = KP / 64;
     extern __shared__ __align__(1024) unsigned char smem[];
+    BackBars &bar = *reinterpret_cast<BackBars *>(smem);
+    volatile int *gave_up = &bar.gave_up;
     const uint32_t base = smem_addr(smem);
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW;
-    const bool helper = threadIdx.x >= NT;
-    const int blocks = (a.s.v + VB - 1) / VB, rep = a.s.hv / a.s.hk;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be uniform
+    const int blocks = blocks_v(a.s.v), rep = a.s.hv / a.s.hk;
     const int vb = (int)(blockIdx.x % blocks);
     const int head = (int)(blockIdx.x / blocks % a.s.hv);
     const long long seq = blockIdx.x / blocks / a.s.hv;
     const Span sp = span_of(a.s, seq);
-    const int v0 = vb * VB, vw = v0 + 16 * warp;
-    const bool idle = vw >= a.s.v;
-    const int r8 = lane >> 2, c2 = 2 * (lane & 3);
+    const int v0 = vb * kBlockV;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
-    const long long chunks = (sp.len + kChunk - 1) / kChunk;
-    const uint32_t own = base + M::kPairs + warp * M::kWarp;
-    unsigned char *ownp = smem + M::kPairs + warp * M::kWarp;
-    float4 *a1p = reinterpret_cast<float4 *>(ownp + M::kA1) + lane, *a2p = reinterpret_cast<float4 *>(ownp + M::kA2) + lane;
-    const int s_ready = 1 + warp, r_ready = 1 + NW + warp, a_ready = 1 + 2 * NW + warp;
-
-    if (helper) {
-        const int tid = threadIdx.x - NT;
-        auto chunk_ws = [&](long long c) { return a.ws + (size_t)((sp.slot + c) * a.s.hv + head) * lay.stride; };
-        auto chunk_kq = [&](long long c) {
-            return a.kq + (size_t)((sp.slot + c) * a.s.hk + head / rep) * kq_stride(a.s.k, NP);
-        };
-        auto load_chain = [&](long long c, int stage) {
-            load_image<NP * M::kKP, NT>(base + stage * M::kStage + M::kK, chunk_kq(c), tid);
-            load_image<2 * (int)kSquare, NT>(base + stage * M::kStage + M::kT, chunk_ws(c) + lay.t, tid);
-        };
-        auto load_own = [&](long long c) {
-            const int rows = (int)min((long long)kChunk, sp.len - c * kChunk);
-            load_image<NP * M::kKP, NT>(base + M::kQ, chunk_kq(c) + NP * M::kKP, tid);
-            load_image<2 * (int)kSquare, NT>(base + M::kP, chunk_ws(c) + lay.p, tid);
-            load_image<3 * kChunk * 4, NT>(base + M::kScal + (uint32_t)(c & 1) * 1024, chunk_ws(c) + lay.scal, tid);
-            load_tile<T, VB>(base + M::kO, M::kVP, row_ptr<T>(a.dout, sp, seq, c * kChunk, head) + v0, a.dout.tok, rows,
-                             a.s.v - v0, a.vec_do != 0, tid, NT);
-        };
-        float a1[8][4], a2[2 * KT][4];
-        // the tiles of chunk c have been loaded by all partners: P^T dO and scale (exp(G) Q)^T dO, transposed
-        auto ahead = [&](long long c) {
-            const float *scal = reinterpret_cast<const float *>(smem + M::kScal + (c & 1) * 1024);
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a1[n][e] = 0.f;
-#pragma unroll
-            for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a2[n][e] = 0.f;
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t f[NP][4], g[2][4];
-#pragma unroll
-                for (int p = 0; p < NP; ++p) load_a_t<VB * 2>(f[p], base + M::kO + p * M::kVP, 16 * kt, 16 * warp, lane);
-#pragma unroll
-                for (int np = 0; np <= kt; ++np) {   // token kt at or after token np
-                    uint32_t ph[4], pl[4];
-                    load_b_t<128>(ph, base + M::kP, 16 * kt, 16 * np, lane);
-                    load_b_t<128>(pl, base + M::kP + (uint32_t)kSquare, 16 * kt, 16 * np, lane);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        mma_bf16(a1[2 * np], f[p], ph[0], ph[1]);
-                        mma_bf16(a1[2 * np + 1], f[p], ph[2], ph[3]);
-                    }
-                    mma_bf16(a1[2 * np], f[0], pl[0], pl[1]);
-                    mma_bf16(a1[2 * np + 1], f[0], pl[2], pl[3]);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 eg = *reinterpret_cast<const float2 *>(scal + 8 * (2 * kt + (q >> 1)) + c2);
-                    float x0 = bf16_low(f[0][q]), x1 = bf16_high(f[0][q]);
-                    if constexpr (NP == 2) { x0 += bf16_low(f[1][q]); x1 += bf16_high(f[1][q]); }
-                    split2(a.s.scale * eg.x * x0, a.s.scale * eg.y * x1, g[0][q], g[1][q]);
-                }
-#pragma unroll
-                for (int np = 0; np < KT; ++np)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint32_t b[4];
-                        load_b_t<KP * 2>(b, base + M::kQ + p * M::kKP, 16 * kt, 16 * np, lane);
-#pragma unroll
-                        for (int h = 0; h + p < 2; ++h) {
-                            mma_bf16(a2[2 * np], g[h], b[0], b[1]);
-                            mma_bf16(a2[2 * np + 1], g[h], b[2], b[3]);
-                        }
-                    }
-            }
-        };
-        auto partners = [&] { asm volatile("bar.sync %0, %1;" :: "r"(1 + 3 * NW), "n"(NT) : "memory"); };
-
-        if (chunks > 0) {
-            load_chain(chunks - 1, 0);
-            load_own(chunks - 1);
-            cp_async_commit();
-            cp_async_wait<0>();
-            partners();
-            ahead(chunks - 1);
-        }
-        for (long long c = chunks - 1; c >= 0; --c) {
-            const int stage = M::kStages == 2 ? (int)((chunks - 1 - c) & 1) : 0;
-            __syncthreads();   // the chain is done with chunk c + 1; this chunk's stage is loaded; all partners are done with theirs
-            if (!idle) {
-#pragma unroll
-                for (int n = 0; n < 8; ++n) a1p[n * 32] = make_float4(a1[n][0], a1[n][1], a1[n][2], a1[n][3]);
-#pragma unroll
-                for (int n = 0; n < 2 * KT; ++n) a2p[n * 32] = make_float4(a2[n][0], a2[n][1], a2[n][2], a2[n][3]);
-                announce(a_ready);
-            }
-            if (c > 0) {
-                if (M::kStages == 2) load_chain(c - 1, stage ^ 1);
-                load_own(c - 1);
-                cp_async_commit();
-            }
-            unsigned char *w = chunk_ws(c);
-            const int rows = (int)min((long long)kChunk, sp.len - c * kChunk), vpad = pad_v(a.s.v);
-            if (!idle) {
-                await(s_ready);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    store_image<16 * KP * 2>(w + lay.ds + ((size_t)p * vpad + vw) * KP * 2, ownp + M::kDS + p * 16 * KP * 2, lane);
-            }
-            if (c > 0) {
-                cp_async_wait<0>();
-                partners();
-                ahead(c - 1);
-            }
-            if (!idle) {
-                await(r_ready);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    store_image<16 * kChunk * 2>(w + lay.du + ((size_t)p * vpad + vw) * kChunk * 2,
-                                                 ownp + M::kDU + p * 16 * kChunk * 2, lane);
-                // dV = dR: rows of 16 columns (f32 rows go out from the chain)
-                T *out = static_cast<T *>(a.dv) + ((size_t)(sp.first + c * kChunk) * a.s.hv + head) * a.s.v + vw;
-                const size_t ostride = (size_t)a.s.hv * a.s.v;
-                if constexpr (sizeof(T) == 2) {
-                    if (vw + 16 <= a.s.v && (a.s.v & 7) == 0 && (reinterpret_cast<uintptr_t>(a.dv) & 15) == 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = i * 16 + (lane >> 1);
-                            if (row < rows)
-                                *reinterpret_cast<uint4 *>(out + row * ostride + (lane & 1) * 8) =
-                                    *reinterpret_cast<const uint4 *>(ownp + M::kOut + row * 32 + (lane & 1) * 16);
-                        }
-                    } else {
-                        for (int i = lane; i < rows * 16; i += 32)
-                            if (vw + (i & 15) < a.s.v)
-                                out[(i >> 4) * ostride + (i & 15)] = reinterpret_cast<const T *>(ownp + M::kOut)[i];
-                    }
-                }
-            }
-            if (M::kStages == 1) {
-                __syncthreads();
-                if (c > 0) {
-                    load_chain(c - 1, 0);
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                }
-            }
-        }
-        return;
-    }
-
-    float ds[2 * KT][4];   // dS'^T: rows vw + r8 (+8), columns 8 n + c2 (+1)
+    const int chunks = (int)((sp.len + kChunk - 1) / kChunk);
     const size_t state = (size_t)(seq * a.s.hv + head) * a.s.k * a.s.v;
-#pragma unroll
-    for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int k = 8 * n + c2 + (e & 1), v = vw + r8 + 8 * (e >> 1);
-            ds[n][e] = a.dht != nullptr && k < a.s.k && v < a.s.v ? a.dht[state + (size_t)k * a.s.v + v] : 0.f;
+    // chunks are taken last to first: i counts them as they come
+    auto chunk_ws = [&](int i) { return a.ws + (size_t)((sp.slot + chunks - 1 - i) * a.s.hv + head) * lay.stride; };
+    auto first_token = [&](int i) { return (long long)(chunks - 1 - i) * kChunk; };
+    auto rows_of = [&](int i) { return (int)min((long long)kChunk, sp.len - first_token(i)); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1);
+            mbar_init(&bar.s_ready[i], 8);
         }
-    for (long long c = chunks - 1; c >= 0; --c) {
-        const int stage = M::kStages == 2 ? (int)((chunks - 1 - c) & 1) : 0;
-        __syncthreads();
-        if (!idle) {
-            const uint32_t st = base + stage * M::kStage;
-            const float *scal = reinterpret_cast<const float *>(smem + M::kScal + (c & 1) * 1024);
-            // Y^T: first dS'^T K^T
-            float y[8][4];
+        mbar_init(&bar.o_full, 32);
+        mbar_init(&bar.o_empty, 8);
+        mbar_init(&bar.o_ready, 8);
+        mbar_init(&bar.y_done, 1);
+        mbar_init(&bar.r_ready, 8);
+        mbar_init(&bar.u_done, 1);
+        mbar_init(&bar.w_ready, 8);
+        mbar_init(&bar.s_done, 1);
+        mbar_init(&bar.out_ready, 8);
+        mbar_init(&bar.out_free, 4);
+        mbar_init(&bar.s_free, 1);
+        mbar_init(&bar.u_free, 1);
+        mbar_init(&bar.drained, 1);
+        bar.gave_up = base & 1023 ? 1 : 0;   // images need their alignment
+        mbar_init_done();
+    }
+    if (warp == 0) tmem_alloc(smem_addr(&bar.tmem));
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    constexpr uint32_t tm = 0;   // all columns are this CTA's
+    if (threadIdx.x == 0 && bar.tmem != tm) bar.gave_up = 1;
+
+    if (warp == 0) {
+        const uint32_t one = elect_lane();
+        // operands: keys by rows; keys, queries, T (both of its parts side by side) and P by columns
+        const uint64_t kq0 = operand(base + M::kTiles, true, 0), kt0 = operand(base + M::kTiles, false, kHalf);
+        const uint64_t tt0 = operand(base + M::kTiles + M::kKQ, false, (uint32_t)kSquare);
+#pragma unroll 1
+        for (int i = 0; i < chunks && !*gave_up; ++i) {
+            const int st = i % M::kStages;
+            const uint32_t at_stage = st * M::kStage;
+            const uint64_t kq = further(kq0, at_stage), kt = further(kt0, at_stage), tt = further(tt0, at_stage);
+            wait_phase(&bar.full[st], (i / M::kStages) & 1, gave_up);
+            wait_phase(&bar.o_ready, i & 1, gave_up);
+            tmem_fence_after();
+            // dO^T P
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[n][e] = 0.f;
+                for (int p = 0; p + t < (NP == 1 ? 1 + t : 2); ++p)   // dO's parts with P's upper, dO's upper with P's lower
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                uint32_t f[2][4];
-                split_tiles(ds[2 * kt], ds[2 * kt + 1], f);
-                const uint32_t at = img<KP * 2>(own + M::kDS, lane & 15, 2 * kt + (lane >> 4));
-                stsm4(at, f[0][0], f[0][1], f[0][2], f[0][3]);
-                stsm4(at + 16 * KP * 2, f[1][0], f[1][1], f[1][2], f[1][3]);
+                    for (int k = 0; k < 4; ++k)
+                        mma_tmem(one, tm + kColP, tm + kColO + p * 32 + k * 8,
+                                 further(tt, (2 + t) * (uint32_t)kSquare + k * 16 * 128), shape(kChunk, false), t + p + k > 0);
+            // dS'^T K^T, by the columns of dS' that are ready together
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    uint32_t b[4][4];
+            for (int r = 0; r < KH; ++r) {
+                wait_busy(&bar.s_ready[r], i & 1, gave_up);
+                tmem_fence_after();
 #pragma unroll
-                    for (int np = 0; np < 4; ++np) load_b<KP * 2>(b[np], st + M::kK + p * M::kKP, 16 * np, 16 * kt, lane);
+                for (int p = 0; p < NP; ++p)
 #pragma unroll
                     for (int h = 0; h + p < 2; ++h)
 #pragma unroll
-                        for (int np = 0; np < 4; ++np) {
-                            mma_bf16(y[2 * np], f[h], b[np][0], b[np][1]);
-                            mma_bf16(y[2 * np + 1], f[h], b[np][2], b[np][3]);
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = (j >> 1) * (KP / 32) + 2 * r + (j & 1);   // columns 16 k..
+                            mma_tmem(one, tm + kColY, tm + (h ? kColSLo : kColSHi) + k * 8,
+                                     further(kq, (p * KH + (k >> 2)) * kHalf + (k & 3) * 32), shape(kChunk, true), r + p + h + j > 0);
                         }
-                }
             }
-            announce(s_ready);
-            await(a_ready);
-            float du[8][4];
+            mma_commit(one, &bar.y_done);
+            // dS^T += scale (exp(G) dO)^T Q
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const float2 el = *reinterpret_cast<const float2 *>(scal + 64 + 8 * n + c2);
-                const float4 p = a1p[n * 32];
-                y[n][0] = el.x * y[n][0] + p.x; y[n][1] = el.y * y[n][1] + p.y;
-                y[n][2] = el.x * y[n][2] + p.z; y[n][3] = el.y * y[n][3] + p.w;
+            for (int p = 0; p < NP; ++p)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) du[n][e] = 0.f;
+                for (int h = 0; h + p < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_tmem(one, tm + kColS, tm + kColQ + h * 32 + k * 8,
+                                 further(kt, p * KH * kHalf + kChunk * 128 + k * 16 * 128), shape(KP, false), true);
+            wait_busy(&bar.r_ready, i & 1, gave_up);
+            tmem_fence_after();
+            // dU^T = Y^T T
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_tmem(one, tm + kColU, tm + kColR + k * 8, further(tt, k * 16 * 128), shape(2 * kChunk, false), k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_tmem(one, tm + kColU, tm + kColR + 32 + k * 8, further(tt, k * 16 * 128), shape(kChunk, false), true);
+            mma_commit(one, &bar.u_done);
+            wait_busy(&bar.w_ready, i & 1, gave_up);
+            tmem_fence_after();
+            // dS^T -= (exp(G) dR)^T K
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int h = 0; h + p < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_tmem(one, tm + kColS, tm + kColR + h * 32 + k * 8,
+                                 further(kt, p * KH * kHalf + k * 16 * 128), shape(KP, false), true);
+            mma_commit(one, &bar.s_done);
+            mma_commit(one, &bar.empty[st]);
+        }
+        mma_commit(one, &bar.drained);
+        wait_drained(&bar.drained, 0);
+    } else if (warp == 1) {
+        if (lane == 0) {   // dS' and dU for the gradients
+            const int rows = min(kBlockV, (a.s.v - v0 + 15) / 16 * 16);
+            for (int i = 0; i < chunks; ++i) {
+                unsigned char *w = chunk_ws(i);
+                for (int r = 0; r < KH; ++r) wait_phase(&bar.s_ready[r], i & 1, gave_up);
+#pragma unroll
+                for (int p = 0; p < 2 * KH; ++p)
+                    bulk_store(w + lay.ds + (size_t)(vb * 2 * KH + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(&bar.s_free);
+                wait_phase(&bar.out_ready, i & 1, gave_up);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    bulk_store(w + lay.du + (size_t)(vb * 2 + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(&bar.u_free);
             }
-            // dU^T = Y^T T: row kt at or after column np
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t f[2][4], th[4][4], tl[4][4];
-                split_tiles(y[2 * kt], y[2 * kt + 1], f);
-#pragma unroll
-                for (int np = 0; np <= kt; ++np) {
-                    load_b_t<128>(th[np], st + M::kT, 16 * kt, 16 * np, lane);
-                    load_b_t<128>(tl[np], st + M::kT + (uint32_t)kSquare, 16 * kt, 16 * np, lane);
-                }
-#pragma unroll
-                for (int h = 0; h < 3; ++h)
-#pragma unroll
-                    for (int np = 0; np <= kt; ++np) {
-                        const uint32_t(&b)[4] = h == 2 ? tl[np] : th[np];
-                        mma_bf16(du[2 * np], f[h & 1], b[0], b[1]);
-                        mma_bf16(du[2 * np + 1], f[h & 1], b[2], b[3]);
-                    }
+            bulk_wait();
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < chunks; ++i) {
+                const int st = i % M::kStages;
+                if (i >= M::kStages) wait_phase(&bar.empty[st], (i / M::kStages - 1) & 1, gave_up);
+                if (*gave_up) break;
+                unsigned char *w = chunk_ws(i), *to = smem + M::kTiles + st * M::kStage;
+                mbar_arrive_expect_tx(&bar.full[st], M::kStage + 3 * kChunk * 4);
+                bulk_load(to, a.kq + (size_t)((sp.slot + chunks - 1 - i) * a.s.hk + head / rep) * kq_stride(a.s.k, NP), M::kKQ, &bar.full[st]);
+                bulk_load(to + M::kKQ, w + lay.t, M::kTP, &bar.full[st]);
+                bulk_load(smem + M::kScal + (i & 1) * 3 * kChunk * 4, w + lay.scal, 3 * kChunk * 4, &bar.full[st]);
             }
-            // dU and dV = dR leave; the state's gradient at the chunk's start
-            const float eall = scal[kChunk - 1];
-#pragma unroll
-            for (int n = 0; n < 2 * KT; ++n) {
-                const float4 p = a2p[n * 32];
-                ds[n][0] = eall * ds[n][0] + p.x; ds[n][1] = eall * ds[n][1] + p.y;
-                ds[n][2] = eall * ds[n][2] + p.z; ds[n][3] = eall * ds[n][3] + p.w;
-            }
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t r[2][4];
-                split_tiles(du[2 * kt], du[2 * kt + 1], r);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {   // dU is now dR
-                    const int n = 2 * kt + t;
-                    const float2 be = *reinterpret_cast<const float2 *>(scal + 128 + 8 * n + c2);
-                    du[n][0] *= be.x; du[n][1] *= be.y; du[n][2] *= be.x; du[n][3] *= be.y;
-                }
-                const uint32_t at = img<128>(own + M::kDU, lane & 15, 2 * kt + (lane >> 4));
-                stsm4(at, r[0][0], r[0][1], r[0][2], r[0][3]);
-                stsm4(at + 16 * kChunk * 2, r[1][0], r[1][1], r[1][2], r[1][3]);
-                if constexpr (sizeof(T) == 2) {
-                    const int row = 16 * kt + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-                    stsm4_t(own + M::kOut + row * 32 + half * 16, pack2<T>(du[2 * kt][0], du[2 * kt][1]),
-                            pack2<T>(du[2 * kt][2], du[2 * kt][3]), pack2<T>(du[2 * kt + 1][0], du[2 * kt + 1][1]),
-                            pack2<T>(du[2 * kt + 1][2], du[2 * kt + 1][3]));
-                }
-            }
-            announce(r_ready);
-            if constexpr (sizeof(T) == 4) {
-                const int rows = (int)min((long long)kChunk, sp.len - c * kChunk);
-                T *out = static_cast<T *>(a.dv) + ((size_t)(sp.first + c * kChunk) * a.s.hv + head) * a.s.v + vw;
-                const size_t ostride = (size_t)a.s.hv * a.s.v;
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int tok = 8 * n + c2 + (e & 1), v = r8 + 8 * (e >> 1);
-                        if (tok < rows && vw + v < a.s.v) out[tok * ostride + v] = du[n][e];
-                    }
-            }
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                uint32_t g[2][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = 2 * kt + (q >> 1);
-                    const float2 eg = *reinterpret_cast<const float2 *>(scal + 8 * n + c2);
-                    split2(-eg.x * du[n][2 * (q & 1)], -eg.y * du[n][2 * (q & 1) + 1], g[0][q], g[1][q]);
-                }
-#pragma unroll
-                for (int nb = 0; nb < KT; nb += 4)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint32_t b[4][4];
-#pragma unroll
-                        for (int np = 0; np < 4; ++np)
-                            load_b_t<KP * 2>(b[np], st + M::kK + p * M::kKP, 16 * kt, 16 * (nb + np), lane);
-#pragma unroll
-                        for (int h = 0; h + p < 2; ++h)
-#pragma unroll
-                            for (int np = 0; np < 4; ++np) {
-                                mma_bf16(ds[2 * (nb + np)], g[h], b[np][0], b[np][1]);
-                                mma_bf16(ds[2 * (nb + np) + 1], g[h], b[np][2], b[np][3]);
-                            }
-                    }
+            for (int j = i < M::kStages ? 0 : i - M::kStages; j < i; ++j)   // copies in flight
+                wait_drained(&bar.full[j % M::kStages], (j / M::kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        const int cols = min(kBlockV, a.s.v - v0);
+        for (int i = 0; i < chunks; ++i) {
+            const int n = rows_of(i);
+            if (i) wait_phase(&bar.o_empty, (i - 1) & 1, gave_up);
+            if (*gave_up) break;
+            const T *src = row_ptr<T>(a.dout, sp, seq, first_token(i), head) + v0;
+            unsigned char *dst = smem + M::kDO;
+            if (a.vec_do) {
+                constexpr int PIECES = M::kRow / 16;   // 16-byte pieces of a row
+                const int piece = lane % PIECES;
+                if (piece * 16 < cols * (int)sizeof(T))
+                    for (int r = lane / PIECES; r < n; r += 32 / PIECES)
+                        cp_async16(smem_addr(dst) + r * M::kRow + piece * 16, reinterpret_cast<const char *>(src + r * a.dout.tok) + piece * 16, true);
+                mbar_arrive_after_copies(&bar.o_full);
+            } else {
+                for (int r = lane; r < n * kBlockV; r += 32)
+                    if (r % kBlockV < cols) reinterpret_cast<T *>(dst)[r] = src[(r / kBlockV) * a.dout.tok + r % kBlockV];
+                mbar_arrive(&bar.o_full);
             }
         }
-        if (M::kStages == 1) __syncthreads();
-    }
-
-    if (a.dh0 != nullptr) {
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+    } else if (warp < kFirstOut) {
+        const int row = 32 * (warp & 3) + lane, half = (warp - kFirstConvert) >> 2, v = v0 + row;   // this thread's value, its half
+        const uint32_t at = (uint32_t)(warp & 3) << 21;                                             // lane 32 (warp % 4)
+        float x[2][16];
+        uint32_t hi[8], lo[8];
+#pragma unroll 1
+        for (int b = 0; b < KP / 32; ++b) {   // 16 columns of the state at a time
+            const int k0 = half * (KP / 2) + 16 * b;
 #pragma unroll
-        for (int n = 0; n < 2 * KT; ++n)
+            for (int i = 0; i < 16; ++i)
+                x[0][i] = a.dht != nullptr && k0 + i < a.s.k && v < a.s.v ? a.dht[state + (size_t)(k0 + i) * a.s.v + v] : 0.f;
+            tmem_st16(at + kColS + k0, x[0]);
+        }
+        tmem_wait_st();
+        auto scalars = [&](int i) { return reinterpret_cast<const float *>(smem + M::kScal + (i & 1) * 3 * kChunk * 4) + 32 * half; };
+        // dO and scale exp(G) dO of a chunk as left operands; rows past the sequence's end and values past V hold
+        // anything and count as 0
+        auto outputs = [&](int i) {
+            const T *op = reinterpret_cast<const T *>(smem + M::kDO) + 32 * half * kBlockV + row;
+            const int n = v < a.s.v ? rows_of(i) - 32 * half : 0;
+            wait_phase(&bar.o_full, i & 1, gave_up);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 8 * n + c2 + (e & 1), v = vw + r8 + 8 * (e >> 1);
-                if (k < a.s.k && v < a.s.v) a.dh0[state + (size_t)k * a.s.v + v] = ds[n][e];
+            for (int j = 0; j < 32; ++j) x[j >> 4][j & 15] = to_f32<T>(op[j * kBlockV]);
+            if (n < 32)
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j >= n) x[j >> 4][j & 15] = 0.f;
+            warp_arrive(&bar.o_empty, lane);
+            wait_phase(&bar.full[i % M::kStages], (i / M::kStages) & 1, gave_up);
+            const float *scal = scalars(i);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                split16(x[b], hi, lo);
+                tmem_st8(at + kColO + 16 * half + 8 * b, hi);
+                if constexpr (NP == 2) tmem_st8(at + kColO + 32 + 16 * half + 8 * b, lo);
+                scale16(x[b], scal + 16 * b);
+                scale16(x[b], a.s.scale);
+                split16(x[b], hi, lo);
+                tmem_st8(at + kColQ + 16 * half + 8 * b, hi);
+                tmem_st8(at + kColQ + 32 + 16 * half + 8 * b, lo);
             }
+            tmem_wait_st();
+            tmem_fence_before();
+            warp_arrive(&bar.o_ready, lane);
+        };
+        if (chunks > 0) outputs(0);
+        for (int i = 0; i < chunks; ++i) {
+            const float *scal = scalars(i);
+            const float eall = scal[kChunk - 1 - 32 * half];
+            if (i > 0) {
+                wait_phase(&bar.u_free, (i - 1) & 1, gave_up);
+                wait_phase(&bar.s_done, (i - 1) & 1, gave_up);
+                tmem_fence_after();
+            }
+#pragma unroll 1
+            for (int r = 0; r < KH; ++r) {
+                const int k16 = half * (KP / 32) + 2 * r;
+                tmem_ld16(x[0], at + kColS + 16 * k16, x[1], at + kColS + 16 * k16 + 16);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    split16(x[b], hi, lo);
+                    tmem_st8(at + kColSHi + 8 * (k16 + b), hi);
+                    tmem_st8(at + kColSLo + 8 * (k16 + b), lo);
+                    scale16(x[b], eall);
+                    tmem_st16(at + kColS + 16 * (k16 + b), x[b]);
+                    keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
+                }
+                fence_async();
+                tmem_wait_st();
+                tmem_fence_before();
+                warp_arrive(&bar.s_ready[r], lane);
+            }
+
+            wait_phase(&bar.y_done, i & 1, gave_up);
+            tmem_fence_after();
+            {
+                float z[2][16];
+                tmem_ld16(x[0], at + kColY + 32 * half, z[0], at + kColP + 32 * half);
+                tmem_ld16(x[1], at + kColY + 32 * half + 16, z[1], at + kColP + 32 * half + 16);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 el = *reinterpret_cast<const float4 *>(scal + 64 + 16 * b + j);
+                        const float2 y0 = fma2(make_float2(el.x, el.y), make_float2(x[b][j], x[b][j + 1]), make_float2(z[b][j], z[b][j + 1]));
+                        const float2 y1 = fma2(make_float2(el.z, el.w), make_float2(x[b][j + 2], x[b][j + 3]), make_float2(z[b][j + 2], z[b][j + 3]));
+                        x[b][j] = y0.x; x[b][j + 1] = y0.y; x[b][j + 2] = y1.x; x[b][j + 3] = y1.y;
+                    }
+                    split16(x[b], hi, lo);
+                    tmem_st8(at + kColR + 16 * half + 8 * b, hi);
+                    tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
+                }
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            warp_arrive(&bar.r_ready, lane);
+
+            wait_phase(&bar.u_done, i & 1, gave_up);
+            tmem_fence_after();
+            {
+                float z[2][16];
+                tmem_ld16(x[0], at + kColU + 32 * half, z[0], at + kColU + kChunk + 32 * half);
+                tmem_ld16(x[1], at + kColU + 32 * half + 16, z[1], at + kColU + kChunk + 32 * half + 16);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {   // dU, and -exp(G) beta dU
+                        const float4 eg = *reinterpret_cast<const float4 *>(scal + 16 * b + j);
+                        const float4 be = *reinterpret_cast<const float4 *>(scal + 128 + 16 * b + j);
+                        const float2 u0 = fma2(make_float2(1.f, 1.f), make_float2(x[b][j], x[b][j + 1]), make_float2(z[b][j], z[b][j + 1]));
+                        const float2 u1 = fma2(make_float2(1.f, 1.f), make_float2(x[b][j + 2], x[b][j + 3]), make_float2(z[b][j + 2], z[b][j + 3]));
+                        const float2 g0 = mul2(mul2(make_float2(-eg.x, -eg.y), make_float2(be.x, be.y)), u0);
+                        const float2 g1 = mul2(mul2(make_float2(-eg.z, -eg.w), make_float2(be.z, be.w)), u1);
+                        x[b][j] = u0.x; x[b][j + 1] = u0.y; x[b][j + 2] = u1.x; x[b][j + 3] = u1.y;
+                        z[b][j] = g0.x; z[b][j + 1] = g0.y; z[b][j + 2] = g1.x; z[b][j + 3] = g1.y;
+                    }
+                    split16(z[b], hi, lo);
+                    tmem_st8(at + kColR + 16 * half + 8 * b, hi);
+                    tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
+                }
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            warp_arrive(&bar.w_ready, lane);
+            // dU, and dV = beta dU by rows
+            wait_phase(&bar.s_free, i & 1, gave_up);
+            if (i > 0) wait_phase(&bar.out_free, (i - 1) & 1, gave_up);
+            T *stage = reinterpret_cast<T *>(smem + M::kOut) + 32 * half * kBlockV + row;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                split16(x[b], hi, lo);
+                keep16(base + M::kSave, kHalf, row, 2 * half + b, hi, lo);
+                scale16(x[b], scal + 128 + 16 * b);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) stage[(16 * b + j) * kBlockV] = from_f32<T>(x[b][j]);
+            }
+            fence_async();
+            warp_arrive(&bar.out_ready, lane);
+            if (i + 1 < chunks) outputs(i + 1);
+        }
+        if (a.dh0 != nullptr) {
+            if (chunks > 0) wait_phase(&bar.s_done, (chunks - 1) & 1, gave_up);
+            tmem_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < KP / 32; ++b) {
+                const int k0 = half * (KP / 2) + 16 * b;
+                tmem_ld16(x[0], at + kColS + k0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (k0 + i < a.s.k && v < a.s.v)
+                        a.dh0[state + (size_t)(k0 + i) * a.s.v + v] = *gave_up ? __int_as_float(0x7fffffff) : x[0][i];
+            }
+        }
+    } else {
+        const int tid = threadIdx.x - 32 * kFirstOut;
+        const size_t ostride = (size_t)a.s.hv * a.s.v;
+        const int cols = min(kBlockV, a.s.v - v0);
+        const bool rows_out = (a.s.v * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dv) & 15) == 0;
+        for (int i = 0; i < chunks; ++i) {
+            const int n = rows_of(i);
+            T *out = static_cast<T *>(a.dv) + ((size_t)(sp.first + first_token(i)) * a.s.hv + head) * a.s.v + v0;
+            const T *stage = reinterpret_cast<const T *>(smem + M::kOut);
+            wait_phase(&bar.out_ready, i & 1, gave_up);
+            if (rows_out) {
+                constexpr int PIECES = M::kRow / 16;
+                const int piece = tid % PIECES;
+                if (piece * 16 < cols * (int)sizeof(T))
+#pragma unroll 4
+                    for (int r = tid / PIECES; r < n; r += 128 / PIECES)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(out + r * ostride) + piece * 16) =
+                            *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(stage) + r * M::kRow + piece * 16);
+            } else if (tid < cols) {
+                for (int r = 0; r < n; ++r) out[r * ostride + tid] = stage[r * kBlockV + tid];
+            }
+            warp_arrive(&bar.out_free, lane);
+        }
     }
+    tmem_fence_before();
+    __syncthreads();
+    if (*gave_up && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the gradients are not what they should be: say so
+        for (long long t = 0; t < sp.len; ++t)
+            static_cast<T *>(a.dv)[((size_t)(sp.first + t) * a.s.hv + head) * a.s.v + v0 + threadIdx.x] =
+                from_f32<T>(__int_as_float(0x7fffffff));
+    tmem_fence_after();
+    if (warp == 0) tmem_free(bar.tmem);
 }
 
 namespace {
 
 template <typename T, int KP>
 cudaError_t chain_back(const DeltaArgs &a, cudaStream_t s) {
-    using M = BackSmem<T, KP, 4>;
-    cudaError_t e = cudaFuncSetAttribute(delta_chain_backward_kernel<T, KP, 4>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, M::kBytes);
+    constexpr int bytes = BackSmem<T, KP>::kBytes;
+    static_assert(bytes <= 227 * 1024, "too much shared memory");
+    cudaError_t e = cudaFuncSetAttribute(delta_chain_backward_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const long long ctas = a.s.seqs * a.s.hv * ((a.s.v + M::VB - 1) / M::VB);
-    delta_chain_backward_kernel<T, KP, 4><<<(unsigned)ctas, 256, M::kBytes, s>>>(a);
+    const long long ctas = a.s.seqs * a.s.hv * blocks_v(a.s.v);
+    delta_chain_backward_kernel<T, KP><<<(unsigned)ctas, kBackThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 

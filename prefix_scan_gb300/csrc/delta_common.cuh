@@ -85,12 +85,15 @@ __device__ __forceinline__ void split_tiles(const float (&lo8)[4], const float (
 }
 
 // ---- swizzled images -----------------------------------------------------------
-// A tile of `rows` rows of ROWB bytes (128 or 256); the 16-byte piece p of row r
-// sits at piece p ^ (r & 7), so that the eight rows of an ldmatrix matrix fall
-// into eight different bank groups.
-template <int ROWB>
+// A tile of 16-bit numbers in rows of 64 (128 bytes); the 16-byte piece p of row r sits at
+// piece p ^ (r & 7), so that the eight rows of an ldmatrix matrix fall into eight different
+// bank groups.  It is also the 128-byte swizzle of the tensor-memory products' operands, for
+// which an image starts at a multiple of 1024 bytes.  Wider tiles are columns of such images:
+// numbers 64 h .. 64 h + 63 of all rows lie HALF bytes after the 64 before them.
+constexpr int kHalf = 128 * 128;   // 128 rows
+template <int HALF = kHalf>
 __device__ __forceinline__ uint32_t img(uint32_t base, int row, int piece) {
-    return base + (uint32_t)(row * ROWB + ((piece ^ (row & 7)) << 4));
+    return base + (uint32_t)((piece >> 3) * HALF + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 // Operands by ldmatrix from an image whose rows are `row`s and whose pieces hold
 // eight 16-bit columns.  r16, c16: the first row and the first column.
@@ -99,22 +102,22 @@ __device__ __forceinline__ uint32_t img(uint32_t base, int row, int piece) {
 //   load_b    B fragments of two 8-column tiles n = rows r16.., r16+8.. and k = columns
 //             c16..c16+15 (B column = image row): b[0], b[1] and b[2], b[3]
 //   load_b_t  the same with n = columns c16.., c16+8.. and k = rows r16..r16+15
-template <int ROWB>
+template <int HALF = kHalf>
 __device__ __forceinline__ void load_a(uint32_t (&a)[4], uint32_t base, int r16, int c16, int lane) {
-    ldsm4(a, img<ROWB>(base, r16 + (lane & 15), (c16 >> 3) + (lane >> 4)));
+    ldsm4(a, img<HALF>(base, r16 + (lane & 15), (c16 >> 3) + (lane >> 4)));
 }
-template <int ROWB>
+template <int HALF = kHalf>
 __device__ __forceinline__ void load_a_t(uint32_t (&a)[4], uint32_t base, int r16, int c16, int lane) {
     // matrices: (rows 0-7, cols 0-7), (rows 0-7, cols 8-15), (rows 8-15, cols 0-7), (rows 8-15, cols 8-15)
-    ldsm4_t(a, img<ROWB>(base, r16 + (lane & 7) + ((lane >> 4) << 3), (c16 >> 3) + ((lane >> 3) & 1)));
+    ldsm4_t(a, img<HALF>(base, r16 + (lane & 7) + ((lane >> 4) << 3), (c16 >> 3) + ((lane >> 3) & 1)));
 }
-template <int ROWB>
+template <int HALF = kHalf>
 __device__ __forceinline__ void load_b(uint32_t (&b)[4], uint32_t base, int r16, int c16, int lane) {
-    ldsm4(b, img<ROWB>(base, r16 + (lane & 7) + ((lane >> 4) << 3), (c16 >> 3) + ((lane >> 3) & 1)));
+    ldsm4(b, img<HALF>(base, r16 + (lane & 7) + ((lane >> 4) << 3), (c16 >> 3) + ((lane >> 3) & 1)));
 }
-template <int ROWB>
+template <int HALF = kHalf>
 __device__ __forceinline__ void load_b_t(uint32_t (&b)[4], uint32_t base, int r16, int c16, int lane) {
-    ldsm4_t(b, img<ROWB>(base, r16 + (lane & 15), (c16 >> 3) + (lane >> 4)));
+    ldsm4_t(b, img<HALF>(base, r16 + (lane & 15), (c16 >> 3) + (lane >> 4)));
 }
 
 // ---- tile loads ------------------------------------------------------------------
@@ -161,7 +164,7 @@ __device__ __forceinline__ void load_tile(uint32_t hi, uint32_t plane, const T *
     constexpr int PIECES = COLS / 8;
     for (int i = tid; i < kChunk * PIECES; i += nthreads) {
         const int r = i / PIECES, p = i % PIECES;
-        const uint32_t dst = img<COLS * 2>(hi, r, p);
+        const uint32_t dst = img(hi, r, p);
         const bool in = r < rows && p * 8 < cols;
         if constexpr (Planes<T>::NP == 1) {
             if (vec) {

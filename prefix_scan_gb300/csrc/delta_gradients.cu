@@ -20,13 +20,14 @@ namespace {
 
 constexpr int kGradThreads = 256;   // eight warps: 16 rows and half of the columns each
 constexpr int kGradV = 64;          // columns of the state taken at a time
+constexpr int kSlice = kGradV * 128;   // bytes of 64 columns of a block of the state
 constexpr int kZStride = kChunk + 1;
 
 template <int NP, int KP>
 struct GradSmem {
-    static constexpr int kKP = kChunk * KP * 2, kSP = kGradV * KP * 2, kUP = kGradV * kChunk * 2;
-    static constexpr int kK = 0, kQ = NP * kKP;
-    static constexpr int kS = 2 * NP * kKP, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDU = kU + 2 * kUP;
+    static constexpr int kKQ = (KP / 64) * kHalf, kSP = kGradV * KP * 2, kUP = kGradV * kChunk * 2;   // planes
+    static constexpr int kK = 0, kQ = kChunk * 128;
+    static constexpr int kS = NP * kKQ, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDU = kU + 2 * kUP;
     static constexpr int kO = kDU + 2 * kUP, kScal = kO + NP * kUP, kMore = kScal + 6 * kChunk * 4;
     static constexpr int kBytes = kMore + (2 * kChunk + 2 * kChunk + 4 * kChunk + kChunk + 8) * 4;
     // F1, F2 and Z take the place of the blocks above once these are used up
@@ -39,7 +40,7 @@ struct GradSmem {
 
 template <typename T, int KP>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const DeltaArgs a) {
-    constexpr int NP = Planes<T>::NP, NH = KP / 16;   // column tiles of half a row
+    constexpr int NP = Planes<T>::NP, NH = KP / 16, KH = KP / 64;   // NH: column tiles of half a row
     using M = GradSmem<NP, KP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
@@ -62,9 +63,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     const long long t0 = (slot - sp.slot) * kChunk;
     const int rows = (int)min((long long)kChunk, sp.len - t0);
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
-    const int vpad = pad_v(a.s.v);
+    const int vpad = (a.s.v + 15) / 16 * 16;
 
-    load_image<2 * NP * M::kKP, kGradThreads>(base + M::kK, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), tid);
+    load_image<NP * M::kKQ, kGradThreads>(base + M::kK, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), tid);
 
     float dq[NH][4], dk[NH][4];   // rows i0 (+8), columns 8 (half NH + n) + c2 (+1)
 #pragma unroll
@@ -92,11 +93,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             load_image<6 * kChunk * 4, kGradThreads>(base + M::kScal, w + lay.scal, tid);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const size_t row = (size_t)p * vpad + v0;
-                load_part<M::kSP, kGradThreads>(base + M::kS + p * M::kSP, w + lay.s + row * KP * 2, vr * KP * 2, tid);
-                load_part<M::kSP, kGradThreads>(base + M::kDS + p * M::kSP, w + lay.ds + row * KP * 2, vr * KP * 2, tid);
-                load_part<M::kUP, kGradThreads>(base + M::kU + p * M::kUP, w + lay.u + row * kChunk * 2, vr * kChunk * 2, tid);
-                load_part<M::kUP, kGradThreads>(base + M::kDU + p * M::kUP, w + lay.du + row * kChunk * 2, vr * kChunk * 2, tid);
+                const int vb = v0 / kBlockV, vi = v0 % kBlockV;
+#pragma unroll
+                for (int h = 0; h < KH; ++h) {
+                    const size_t from = ((size_t)(vb * 2 + p) * KH + h) * kHalf + vi * 128;
+                    load_part<kSlice, kGradThreads>(base + M::kS + p * M::kSP + h * kSlice, w + lay.s + from, vr * 128, tid);
+                    load_part<kSlice, kGradThreads>(base + M::kDS + p * M::kSP + h * kSlice, w + lay.ds + from, vr * 128, tid);
+                }
+                const size_t from = (size_t)(vb * 2 + p) * kHalf + vi * 128;
+                load_part<M::kUP, kGradThreads>(base + M::kU + p * M::kUP, w + lay.u + from, vr * 128, tid);
+                load_part<M::kUP, kGradThreads>(base + M::kDU + p * M::kUP, w + lay.du + from, vr * 128, tid);
             }
             load_tile<T, kGradV>(base + M::kO, M::kUP, row_ptr<T>(a.dout, sp, seq, t0, head) + v0, a.dout.tok, rows,
                                  a.s.v - v0, a.vec_do != 0, tid, kGradThreads);
@@ -104,7 +110,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             cp_async_wait<0>();
             __syncthreads();
 
-            for (int i = tid; i < vr * KP / 8; i += kGradThreads) {   // the same place in all four images
+            for (int i = tid; i < kGradV * KP / 8; i += kGradThreads) {   // the same place in all four images
+                if (i % (kGradV * 8) >= vr * 8) continue;   // not loaded
                 const uint4 *s = reinterpret_cast<const uint4 *>(smem + M::kS) + i;
                 const uint4 *d = reinterpret_cast<const uint4 *>(smem + M::kDS) + i;
                 const uint4 sh = s[0], sl = s[M::kSP / 16], dh = d[0], dl = d[M::kSP / 16];
@@ -118,11 +125,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             for (int kt = 0; kt < vr / 16; ++kt) {
                 uint32_t fo[NP][4], fu[2][4], fr[2][4];
 #pragma unroll
-                for (int p = 0; p < NP; ++p) load_a<128>(fo[p], base + M::kO + p * M::kUP, 16 * strip, 16 * kt, lane);
+                for (int p = 0; p < NP; ++p) load_a(fo[p], base + M::kO + p * M::kUP, 16 * strip, 16 * kt, lane);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    load_a_t<128>(fu[p], base + M::kU + p * M::kUP, 16 * kt, 16 * strip, lane);
-                    load_a_t<128>(fr[p], base + M::kDU + p * M::kUP, 16 * kt, 16 * strip, lane);
+                    load_a_t(fu[p], base + M::kU + p * M::kUP, 16 * kt, 16 * strip, lane);
+                    load_a_t(fr[p], base + M::kDU + p * M::kUP, 16 * kt, 16 * strip, lane);
                 }
 #pragma unroll
                 for (int np = 0; np < 2; ++np)
@@ -130,7 +137,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
                             uint32_t b[4];
-                            load_b_t<128>(b, base + M::kU + p * M::kUP, 16 * kt, 32 * half + 16 * np, lane);
+                            load_b_t(b, base + M::kU + p * M::kUP, 16 * kt, 32 * half + 16 * np, lane);
 #pragma unroll
                             for (int h = 0; h + p < 2; ++h) {
                                 if (h < NP) {
@@ -146,8 +153,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         uint32_t b[4], d[4];
-                        load_b_t<KP * 2>(b, base + M::kS + p * M::kSP, 16 * kt, 8 * half * NH + 16 * np, lane);
-                        load_b_t<KP * 2>(d, base + M::kDS + p * M::kSP, 16 * kt, 8 * half * NH + 16 * np, lane);
+                        load_b_t<kSlice>(b, base + M::kS + p * M::kSP, 16 * kt, 8 * half * NH + 16 * np, lane);
+                        load_b_t<kSlice>(d, base + M::kDS + p * M::kSP, 16 * kt, 8 * half * NH + 16 * np, lane);
 #pragma unroll
                         for (int h = 0; h + p < 2; ++h) {
                             if (h < NP) {
@@ -175,13 +182,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {   // rows i0, i0 + 8
                 const int i = i0 + 8 * e;
-                const uint32_t at = img<KP * 2>(0, i, col >> 3) + (col & 7) * 2;
+                const uint32_t at = img(0, i, col >> 3) + (col & 7) * 2;
                 uint32_t kw = *reinterpret_cast<const uint32_t *>(smem + M::kK + at);
                 uint32_t qw = *reinterpret_cast<const uint32_t *>(smem + M::kQ + at);
                 float k0 = bf16_low(kw), k1 = bf16_high(kw), q0 = bf16_low(qw), q1 = bf16_high(qw);
                 if constexpr (NP == 2) {
-                    kw = *reinterpret_cast<const uint32_t *>(smem + M::kK + M::kKP + at);
-                    qw = *reinterpret_cast<const uint32_t *>(smem + M::kQ + M::kKP + at);
+                    kw = *reinterpret_cast<const uint32_t *>(smem + M::kK + M::kKQ + at);
+                    qw = *reinterpret_cast<const uint32_t *>(smem + M::kQ + M::kKQ + at);
                     k0 += bf16_low(kw); k1 += bf16_high(kw); q0 += bf16_low(qw); q1 += bf16_high(qw);
                 }
                 const float eg = scal[i], el = scal[64 + i], sc = a.s.scale * eg, eb = eg * scal[128 + i];
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 const int n = 2 * np + (q >> 1), row = q & 1, i = i0 + 8 * row, j = cb + 8 * (q >> 1) + c2;
                 float z0 = 0.f, z1 = 0.f;
                 if (cb <= 16 * strip) {
-                    const uint32_t at = img<128>(0, i, j >> 3) + (j & 7) * 2;
+                    const uint32_t at = img(0, i, j >> 3) + (j & 7) * 2;
                     const uint32_t ph = *reinterpret_cast<const uint32_t *>(w + lay.p + at);
                     const uint32_t pl = *reinterpret_cast<const uint32_t *>(w + lay.p + kSquare + at);
                     const uint32_t nh = *reinterpret_cast<const uint32_t *>(w + lay.n + at);
@@ -244,7 +251,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 Z[i * kZStride + j] = z0;
                 Z[i * kZStride + j + 1] = z1;
             }
-            const uint32_t at = img<128>(0, 16 * strip + (lane & 15), (cb >> 3) + (lane >> 4));
+            const uint32_t at = img(0, 16 * strip + (lane & 15), (cb >> 3) + (lane >> 4));
             stsm4(base + M::kF1 + at, f1h[0], f1h[1], f1h[2], f1h[3]);
             stsm4(base + M::kF1 + (uint32_t)kSquare + at, f1l[0], f1l[1], f1l[2], f1l[3]);
             stsm4(base + M::kF2 + at, f2h[0], f2h[1], f2h[2], f2h[3]);
@@ -260,19 +267,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             if (down)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    load_a<128>(f1[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * strip, 16 * kt, lane);
-                    load_a<128>(f2[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * strip, 16 * kt, lane);
+                    load_a(f1[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * strip, 16 * kt, lane);
+                    load_a(f2[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * strip, 16 * kt, lane);
                 }
             if (up)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) load_a_t<128>(f1t[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
+                for (int p = 0; p < 2; ++p) load_a_t(f1t[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
 #pragma unroll
             for (int np = 0; np < NH / 2; ++np)
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     uint32_t bk[4], bq[4];
-                    load_b_t<KP * 2>(bk, base + M::kK + p * M::kKP, 16 * kt, 8 * half * NH + 16 * np, lane);
-                    load_b_t<KP * 2>(bq, base + M::kQ + p * M::kKP, 16 * kt, 8 * half * NH + 16 * np, lane);
+                    load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * half * NH + 16 * np, lane);
+                    load_b_t(bq, base + M::kQ + p * M::kKQ, 16 * kt, 8 * half * NH + 16 * np, lane);
 #pragma unroll
                     for (int h = 0; h + p < 2; ++h) {
                         if (down) {
@@ -289,13 +296,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 }
             if (up) {
 #pragma unroll
-                for (int p = 0; p < 2; ++p) load_a_t<128>(f1t[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
+                for (int p = 0; p < 2; ++p) load_a_t(f1t[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
 #pragma unroll
                 for (int np = 0; np < NH / 2; ++np)
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
                         uint32_t bk[4];
-                        load_b_t<KP * 2>(bk, base + M::kK + p * M::kKP, 16 * kt, 8 * half * NH + 16 * np, lane);
+                        load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * half * NH + 16 * np, lane);
 #pragma unroll
                         for (int h = 0; h + p < 2; ++h) {
                             mma_bf16(dk[2 * np], f1t[h], bk[0], bk[1]);

@@ -31,37 +31,43 @@ struct DeltaShape {
 //          tokens up to here have forgotten the state
 //   T      2 x 64 x 64       row i, column j
 //   P      2 x 64 x 64
-//   N      2 x 64 x 64       (kept for the backward pass only)
-//   S      2 x V x K         row v, column k: the state at the chunk's start (backward only)
-//   U      2 x V x 64        row v, column token (backward only)
-// and the backward chain adds dS (as S: the gradient of the state at the chunk's end) and
-// dU (as U).  After all of these come, for each (chunk, key head), the chunk's keys and then
-// its queries as images of 64 rows of K, one plane for bf16 and two for other types: rows past
-// the sequence's end and columns past K are 0.
+//   N      2 x 64 x 64       (blocks of 16 above the diagonal are not written; kept for the
+//                            backward pass only)
+// and for the backward pass, for each block of 128 values (rows past the values, to a multiple
+// of 16, are 0; further ones are not written)
+//   S      2 x 128 x K       row v, column k: the state at the chunk's start
+//   U      2 x 128 x 64      row v, column token
+// to which the backward chain adds dS (as S: the gradient of the state at the chunk's end) and
+// dU (as U).  After all of these come, for each (chunk, key head), the chunk's keys (rows 0-63)
+// and queries (rows 64-127) as one image of 128 rows of K, one plane for bf16 and two for other
+// types: rows past the sequence's end and columns past K are 0.
 struct ChunkLayout {
     size_t scal, t, p, n, s, u, ds, du, stride;
 };
 constexpr size_t kSquare = (size_t)kChunk * kChunk * 2;   // bytes of one 64 x 64 plane
+constexpr int kBlockV = 128;                              // values of a block
 constexpr int pad_k(int k) { return k <= 64 ? 64 : 128; }
-constexpr int pad_v(int v) { return (v + 15) / 16 * 16; }
+constexpr int blocks_v(int v) { return (v + kBlockV - 1) / kBlockV; }
+constexpr size_t s_plane(int k) { return (size_t)kBlockV * pad_k(k) * 2; }
+constexpr size_t kUPlane = (size_t)kBlockV * kChunk * 2;
 constexpr ChunkLayout chunk_layout(int k, int v, bool train) {
     ChunkLayout l{};
-    const size_t sp = (size_t)pad_v(v) * pad_k(k) * 2, up = (size_t)pad_v(v) * kChunk * 2;
+    const size_t sb = 2 * s_plane(k) * blocks_v(v), ub = 2 * kUPlane * blocks_v(v);
     size_t at = 0;
     l.scal = at; at += 6 * kChunk * 4;
     l.t = at; at += 2 * kSquare;
     l.p = at; at += 2 * kSquare;
     if (train) {
         l.n = at; at += 2 * kSquare;
-        l.s = at; at += 2 * sp;
-        l.u = at; at += 2 * up;
-        l.ds = at; at += 2 * sp;
-        l.du = at; at += 2 * up;
+        l.s = at; at += sb;
+        l.u = at; at += ub;
+        l.ds = at; at += sb;
+        l.du = at; at += ub;
     }
     l.stride = (at + 255) / 256 * 256;
     return l;
 }
-constexpr size_t kq_stride(int k, int planes) { return (size_t)2 * planes * kChunk * pad_k(k) * 2; }
+constexpr size_t kq_stride(int k, int planes) { return (size_t)planes * 2 * kChunk * pad_k(k) * 2; }
 constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
     return packed ? tokens / kChunk + seqs : seqs * ((tokens + kChunk - 1) / kChunk);
 }

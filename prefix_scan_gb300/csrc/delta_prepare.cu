@@ -20,10 +20,10 @@ constexpr int kDiag = 264;          // floats from one diagonal block to the nex
 
 template <int NP, int KP>
 struct PrepSmem {
-    static constexpr int kPlane = kChunk * KP * 2;
-    static constexpr int kK = 0, kQ = NP * kPlane;
+    static constexpr int kPlane = 2 * kChunk * KP * 2;                           // keys, then queries
+    static constexpr int kK = 0, kQ = kChunk * 128;
     static constexpr int kT = 0, kP = 2 * (int)kSquare, kN = 4 * (int)kSquare;   // in the place of K and Q
-    static constexpr int kScal = 2 * NP * kPlane > 6 * (int)kSquare ? 2 * NP * kPlane : 6 * (int)kSquare;
+    static constexpr int kScal = NP * kPlane > 6 * (int)kSquare ? NP * kPlane : 6 * (int)kSquare;
     static constexpr int kL = kScal + 6 * kChunk * 4;                            // f32 diagonal blocks of diag(beta) N
     static constexpr int kBytes = kL + 4 * kDiag * 4;
 };
@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
         uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            load_a<KP * 2>(ak[p], base + M::kK + p * M::kPlane, 16 * warp, 16 * kt, lane);
-            load_a<KP * 2>(aq[p], base + M::kQ + p * M::kPlane, 16 * warp, 16 * kt, lane);
+            load_a(ak[p], base + M::kK + p * M::kPlane, 16 * warp, 16 * kt, lane);
+            load_a(aq[p], base + M::kQ + p * M::kPlane, 16 * warp, 16 * kt, lane);
         }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     uint32_t b[4];
-                    load_b<KP * 2>(b, base + M::kK + p * M::kPlane, 16 * np, 16 * kt, lane);
+                    load_b(b, base + M::kK + p * M::kPlane, 16 * np, 16 * kt, lane);
 #pragma unroll
                     for (int f = 0; f + p < NP; ++f) {   // lo lo is left out
                         mma_bf16(kk[2 * np], ak[f], b[0], b[1]);
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
     {
         uint4 *kq = reinterpret_cast<uint4 *>(a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP));
 #pragma unroll
-        for (int i = 0; i < 2 * NP * M::kPlane / (16 * kPrepThreads); ++i)
+        for (int i = 0; i < NP * M::kPlane / (16 * kPrepThreads); ++i)
             kq[i * kPrepThreads + tid] = reinterpret_cast<const uint4 *>(smem + M::kK)[i * kPrepThreads + tid];
     }
     __syncthreads();
@@ -152,7 +152,12 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
             const float gh1 = scal[200 + i0], gl1 = scal[264 + i0], r1 = scal[328 + i0], b1 = scal[136 + i0];
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
-                if (np > warp) continue;   // above the diagonal: nobody reads it
+                if (np > warp) {   // above the diagonal: T and P are 0, N is not read
+                    const uint32_t at = img(base + M::kT, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) stsm4(at + m * (uint32_t)kSquare, 0, 0, 0, 0);
+                    continue;
+                }
                 uint32_t ph[4], pl[4], nh[4], nl[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {   // register q of the block's fragment: tile q >> 1, rows +8 for odd q
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
                     split2(pv[0], pv[1], ph[q], pl[q]);
                     split2(nv[0], nv[1], nh[q], nl[q]);
                 }
-                const uint32_t at = img<128>(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
+                const uint32_t at = img(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
                 stsm4(base + M::kP + at, ph[0], ph[1], ph[2], ph[3]);
                 stsm4(base + M::kP + (uint32_t)kSquare + at, pl[0], pl[1], pl[2], pl[3]);
                 stsm4(base + M::kN + at, nh[0], nh[1], nh[2], nh[3]);
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
             for (int i = 0; i < 16; ++i) {
                 const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
                 const __nv_bfloat16 l = __float2bfloat16_rn(x[i] - __bfloat162float(h));
-                const int at = (int)img<128>(0, (tid & ~15) + i, tid >> 3) + (tid & 7) * 2;
+                const int at = (int)img(0, (tid & ~15) + i, tid >> 3) + (tid & 7) * 2;
                 *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + at) = h;
                 *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + kSquare + at) = l;
             }
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
             uint32_t x[4][2][4];   // T_lj^T as left operands
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-                load_a_t<128>(x[0][p], base + M::kT + p * (uint32_t)kSquare, 16 * warp, 16 * warp, lane);
+                load_a_t(x[0][p], base + M::kT + p * (uint32_t)kSquare, 16 * warp, 16 * warp, lane);
 #pragma unroll
             for (int d = 1; d < 4; ++d) {
                 const int i = warp + d;
@@ -225,8 +230,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
 #pragma unroll
                 for (int l = 0; l < d; ++l) {
                     uint32_t bh[4], bl[4];
-                    load_b<128>(bh, base + M::kN, 16 * i, 16 * (warp + l), lane);
-                    load_b<128>(bl, base + M::kN + (uint32_t)kSquare, 16 * i, 16 * (warp + l), lane);
+                    load_b(bh, base + M::kN, 16 * i, 16 * (warp + l), lane);
+                    load_b(bl, base + M::kN + (uint32_t)kSquare, 16 * i, 16 * (warp + l), lane);
                     mma_bf16(y[0], x[l][0], bh[0], bh[1]);
                     mma_bf16(y[1], x[l][0], bh[2], bh[3]);
                     mma_bf16(y[0], x[l][1], bh[0], bh[1]);
@@ -241,8 +246,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
                 }
                 uint32_t f[2][4], bh[4], bl[4];
                 split_tiles(y[0], y[1], f);
-                load_b<128>(bh, base + M::kT, 16 * i, 16 * i, lane);
-                load_b<128>(bl, base + M::kT + (uint32_t)kSquare, 16 * i, 16 * i, lane);
+                load_b(bh, base + M::kT, 16 * i, 16 * i, lane);
+                load_b(bl, base + M::kT + (uint32_t)kSquare, 16 * i, 16 * i, lane);
                 mma_bf16(z[0], f[0], bh[0], bh[1]);
                 mma_bf16(z[1], f[0], bh[2], bh[3]);
                 mma_bf16(z[0], f[1], bh[0], bh[1]);
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
                 mma_bf16(z[0], f[0], bl[0], bl[1]);
                 mma_bf16(z[1], f[0], bl[2], bl[3]);
                 split_tiles(z[0], z[1], x[d]);
-                const uint32_t at = img<128>(base + M::kT, 16 * i + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1));
+                const uint32_t at = img(base + M::kT, 16 * i + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1));
                 stsm4_t(at, x[d][0][0], x[d][0][1], x[d][0][2], x[d][0][3]);
                 stsm4_t(at + (uint32_t)kSquare, x[d][1][0], x[d][1][1], x[d][1][2], x[d][1][3]);
             }
