@@ -18,21 +18,21 @@ namespace ps {
 
 namespace {
 
-constexpr int kGradThreads = 256;   // eight warps: 16 rows and half of the columns each
-constexpr int kGradV = 64;          // columns of the state taken at a time
+constexpr int kGradThreads = 512;   // sixteen warps: 16 rows and a quarter of the columns each
+constexpr int kGradV = 32;          // values taken at a time
 constexpr int kSlice = kGradV * 128;   // bytes of 64 columns of a block of the state
 constexpr int kZStride = kChunk + 1;
 
 template <int NP, int KP>
 struct GradSmem {
-    static constexpr int kKQ = (KP / 64) * kHalf, kSP = kGradV * KP * 2, kUP = kGradV * kChunk * 2;   // planes
+    static constexpr int kKQ = (KP / 64) * kHalf, kSP = kGradV * KP * 2, kUP = kGradV * kChunk * 2, kOP = kChunk * 128;   // planes
     static constexpr int kK = 0, kQ = kChunk * 128;
-    static constexpr int kS = NP * kKQ, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDU = kU + 2 * kUP;
-    static constexpr int kO = kDU + 2 * kUP, kScal = kO + NP * kUP, kMore = kScal + 6 * kChunk * 4;
-    static constexpr int kBytes = kMore + (2 * kChunk + 2 * kChunk + 4 * kChunk + kChunk + 8) * 4;
-    // F1, F2 and Z take the place of the blocks above once these are used up
-    static constexpr int kF1 = kS, kF2 = kF1 + 2 * (int)kSquare, kZ = kF2 + 2 * (int)kSquare;
-    static_assert(kZ + kChunk * kZStride * 4 <= kO, "the products fit where the blocks were");
+    // a stage: S, dS', U, dU, dO of the values taken at a time
+    static constexpr int kS = 0, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDU = kU + 2 * kUP, kO = kDU + 2 * kUP, kStage = kO + NP * kOP;
+    static constexpr int kStages = NP == 1 ? 2 : 1, kFirst = NP * kKQ;
+    static constexpr int kF1 = kFirst + kStages * kStage, kF2 = kF1 + 2 * (int)kSquare, kZ = kF2 + 2 * (int)kSquare;
+    static constexpr int kScal = kZ + kChunk * kZStride * 4, kMore = kScal + 2 * 6 * kChunk * 4;   // scalars of two heads
+    static constexpr int kBytes = kMore + (4 * kChunk + 4 * kChunk + 4 * kChunk + kChunk + 16) * 4;
     static_assert(kBytes <= 227 * 1024, "too much shared memory");
 };
 
@@ -40,19 +40,18 @@ struct GradSmem {
 
 template <typename T, int KP>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const DeltaArgs a) {
-    constexpr int NP = Planes<T>::NP, NH = KP / 16, KH = KP / 64;   // NH: column tiles of half a row
+    constexpr int NP = Planes<T>::NP, NQ = KP / 32, KH = KP / 64;   // NQ: column tiles of a quarter of a row
     using M = GradSmem<NP, KP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
-    const float *scal = reinterpret_cast<const float *>(smem + M::kScal);
     float *Z = reinterpret_cast<float *>(smem + M::kZ);
-    float *dots = reinterpret_cast<float *>(smem + M::kMore);   // [2 halves][64] of a_i
-    float *dotb = dots + 2 * kChunk;                            // [2 halves][64] of b_j
-    float *run = dotb + 2 * kChunk;                             // [4 quarters][64] column sums of Z
+    float *dots = reinterpret_cast<float *>(smem + M::kMore);   // [4 quarters of the columns][64] of a_i
+    float *dotb = dots + 4 * kChunk;                            // the same of b_j
+    float *run = dotb + 4 * kChunk;                             // [4 quarters of the rows][64] column sums of Z
     float *diag = run + 4 * kChunk;                             // [64] dU_j . U_j
     float *inner = diag + kChunk;                               // <S, dS'> by warps
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int strip = warp & 3, half = warp >> 2;   // rows 16 strip.., columns of half `half`
+    const int strip = warp & 3, quarter = warp >> 2;   // rows 16 strip.., this quarter of the columns
     const int r8 = lane >> 2, c2 = 2 * (lane & 3), i0 = 16 * strip + r8;
     const long long slot = blockIdx.x;
     const int head_k = blockIdx.y, rep = a.s.hv / a.s.hk;
@@ -67,54 +66,67 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 
     load_image<NP * M::kKQ, kGradThreads>(base + M::kK, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), tid);
 
-    float dq[NH][4], dk[NH][4];   // rows i0 (+8), columns 8 (half NH + n) + c2 (+1)
+    // all value heads' values, kGradV at a time, in one sequence of stages
+    const int slices = (vpad + kGradV - 1) / kGradV;
+    auto load = [&](int it) {
+        const int head = head_k * rep + it / slices, v0 = it % slices * kGradV, vr = min(kGradV, vpad - v0);
+        const int vb = v0 / kBlockV, vi = v0 % kBlockV;
+        const uint32_t st = base + M::kFirst + it % M::kStages * M::kStage;
+        const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
 #pragma unroll
-    for (int n = 0; n < NH; ++n)
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                const size_t from = ((size_t)(vb * 2 + p) * KH + h) * kHalf + vi * 128;
+                load_part<kSlice, kGradThreads>(st + M::kS + p * M::kSP + h * kSlice, w + lay.s + from, vr * 128, tid);
+                load_part<kSlice, kGradThreads>(st + M::kDS + p * M::kSP + h * kSlice, w + lay.ds + from, vr * 128, tid);
+            }
+            const size_t from = (size_t)(vb * 2 + p) * kHalf + vi * 128;
+            load_part<M::kUP, kGradThreads>(st + M::kU + p * M::kUP, w + lay.u + from, vr * 128, tid);
+            load_part<M::kUP, kGradThreads>(st + M::kDU + p * M::kUP, w + lay.du + from, vr * 128, tid);
+        }
+        load_tile<T, kGradV>(st + M::kO, M::kOP, row_ptr<T>(a.dout, sp, seq, t0, head) + v0, a.dout.tok, rows, a.s.v - v0,
+                             a.vec_do != 0, tid, kGradThreads);
+        if (v0 == 0) load_image<6 * kChunk * 4, kGradThreads>(base + M::kScal + (it / slices & 1) * 6 * kChunk * 4, w + lay.scal, tid);
+        cp_async_commit();
+    };
+    load(0);
+
+    float dq[NQ][4], dk[NQ][4];   // rows i0 (+8), columns 8 (quarter NQ + n) + c2 (+1)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
 
     for (int hr = 0; hr < rep; ++hr) {
         const int head = head_k * rep + hr;
         const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
-        float pa[4][4], na[4][4];                     // dP and dU U^T: columns 32 half + 8 n..
-        float x1[NH][4], x2[NH][4], x3[NH][4];        // dO S^T, dU S^T, U dS'^T
+        const float *scal = reinterpret_cast<const float *>(smem + M::kScal + (hr & 1) * 6 * kChunk * 4);
+        float pa[2][4], na[2][4];                     // dP and dU U^T: columns 16 quarter + 8 n..
+        float x1[NQ][4], x2[NQ][4], x3[NQ][4];        // dO S^T, dU S^T, U dS'^T
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) pa[n][e] = na[n][e] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NH; ++n)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x1[n][e] = x2[n][e] = x3[n][e] = 0.f;
         float prod = 0.f;   // this thread's part of <S, dS'>
 
-        for (int v0 = 0; v0 < a.s.v; v0 += kGradV) {
-            const int vr = min(kGradV, vpad - v0);
-            load_image<6 * kChunk * 4, kGradThreads>(base + M::kScal, w + lay.scal, tid);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int vb = v0 / kBlockV, vi = v0 % kBlockV;
-#pragma unroll
-                for (int h = 0; h < KH; ++h) {
-                    const size_t from = ((size_t)(vb * 2 + p) * KH + h) * kHalf + vi * 128;
-                    load_part<kSlice, kGradThreads>(base + M::kS + p * M::kSP + h * kSlice, w + lay.s + from, vr * 128, tid);
-                    load_part<kSlice, kGradThreads>(base + M::kDS + p * M::kSP + h * kSlice, w + lay.ds + from, vr * 128, tid);
-                }
-                const size_t from = (size_t)(vb * 2 + p) * kHalf + vi * 128;
-                load_part<M::kUP, kGradThreads>(base + M::kU + p * M::kUP, w + lay.u + from, vr * 128, tid);
-                load_part<M::kUP, kGradThreads>(base + M::kDU + p * M::kUP, w + lay.du + from, vr * 128, tid);
-            }
-            load_tile<T, kGradV>(base + M::kO, M::kUP, row_ptr<T>(a.dout, sp, seq, t0, head) + v0, a.dout.tok, rows,
-                                 a.s.v - v0, a.vec_do != 0, tid, kGradThreads);
-            cp_async_commit();
+        for (int s = 0; s < slices; ++s) {
+            const int it = hr * slices + s, vr = min(kGradV, vpad - s * kGradV);
+            const uint32_t st = base + M::kFirst + it % M::kStages * M::kStage;
             cp_async_wait<0>();
             __syncthreads();
+            if (M::kStages == 2 && it + 1 < rep * slices) load(it + 1);
 
+            const unsigned char *sp8 = smem + (st - base);
             for (int i = tid; i < kGradV * KP / 8; i += kGradThreads) {   // the same place in all four images
                 if (i % (kGradV * 8) >= vr * 8) continue;   // not loaded
-                const uint4 *s = reinterpret_cast<const uint4 *>(smem + M::kS) + i;
-                const uint4 *d = reinterpret_cast<const uint4 *>(smem + M::kDS) + i;
-                const uint4 sh = s[0], sl = s[M::kSP / 16], dh = d[0], dl = d[M::kSP / 16];
+                const uint4 *sv = reinterpret_cast<const uint4 *>(sp8 + M::kS) + i;
+                const uint4 *dv = reinterpret_cast<const uint4 *>(sp8 + M::kDS) + i;
+                const uint4 sh = sv[0], sl = sv[M::kSP / 16], dh = dv[0], dl = dv[M::kSP / 16];
                 const uint32_t *shp = &sh.x, *slp = &sl.x, *dhp = &dh.x, *dlp = &dl.x;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -123,52 +135,84 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 }
             }
             for (int kt = 0; kt < vr / 16; ++kt) {
-                uint32_t fo[NP][4], fu[2][4], fr[2][4];
+                {   // dO: dP and dO S^T
+                    uint32_t f[NP][4];
 #pragma unroll
-                for (int p = 0; p < NP; ++p) load_a(fo[p], base + M::kO + p * M::kUP, 16 * strip, 16 * kt, lane);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    load_a_t(fu[p], base + M::kU + p * M::kUP, 16 * kt, 16 * strip, lane);
-                    load_a_t(fr[p], base + M::kDU + p * M::kUP, 16 * kt, 16 * strip, lane);
-                }
-#pragma unroll
-                for (int np = 0; np < 2; ++np)
-                    if (32 * half + 16 * np <= 16 * strip)   // columns at or before the rows
+                    for (int p = 0; p < NP; ++p) load_a(f[p], st + M::kO + p * M::kOP, 16 * strip, 16 * kt, lane);
+                    if (quarter <= strip)   // columns at or before the rows
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
                             uint32_t b[4];
-                            load_b_t(b, base + M::kU + p * M::kUP, 16 * kt, 32 * half + 16 * np, lane);
+                            load_b_t(b, st + M::kU + p * M::kUP, 16 * kt, 16 * quarter, lane);
+#pragma unroll
+                            for (int h = 0; h < NP && h + p < 2; ++h) {
+                                mma_bf16(pa[0], f[h], b[0], b[1]);
+                                mma_bf16(pa[1], f[h], b[2], b[3]);
+                            }
+                        }
+#pragma unroll
+                    for (int np = 0; np < NQ / 2; ++np)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t b[4];
+                            load_b_t<kSlice>(b, st + M::kS + p * M::kSP, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
+#pragma unroll
+                            for (int h = 0; h < NP && h + p < 2; ++h) {
+                                mma_bf16(x1[2 * np], f[h], b[0], b[1]);
+                                mma_bf16(x1[2 * np + 1], f[h], b[2], b[3]);
+                            }
+                        }
+                }
+                {   // dU: dU U^T and dU S^T
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) load_a_t(f[p], st + M::kDU + p * M::kUP, 16 * kt, 16 * strip, lane);
+                    if (quarter <= strip)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t b[4];
+                            load_b_t(b, st + M::kU + p * M::kUP, 16 * kt, 16 * quarter, lane);
 #pragma unroll
                             for (int h = 0; h + p < 2; ++h) {
-                                if (h < NP) {
-                                    mma_bf16(pa[2 * np], fo[h < NP ? h : 0], b[0], b[1]);
-                                    mma_bf16(pa[2 * np + 1], fo[h < NP ? h : 0], b[2], b[3]);
-                                }
-                                mma_bf16(na[2 * np], fr[h], b[0], b[1]);
-                                mma_bf16(na[2 * np + 1], fr[h], b[2], b[3]);
+                                mma_bf16(na[0], f[h], b[0], b[1]);
+                                mma_bf16(na[1], f[h], b[2], b[3]);
                             }
                         }
 #pragma unroll
-                for (int np = 0; np < NH / 2; ++np)
+                    for (int np = 0; np < NQ / 2; ++np)
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t b[4], d[4];
-                        load_b_t<kSlice>(b, base + M::kS + p * M::kSP, 16 * kt, 8 * half * NH + 16 * np, lane);
-                        load_b_t<kSlice>(d, base + M::kDS + p * M::kSP, 16 * kt, 8 * half * NH + 16 * np, lane);
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t b[4];
+                            load_b_t<kSlice>(b, st + M::kS + p * M::kSP, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
 #pragma unroll
-                        for (int h = 0; h + p < 2; ++h) {
-                            if (h < NP) {
-                                mma_bf16(x1[2 * np], fo[h < NP ? h : 0], b[0], b[1]);
-                                mma_bf16(x1[2 * np + 1], fo[h < NP ? h : 0], b[2], b[3]);
+                            for (int h = 0; h + p < 2; ++h) {
+                                mma_bf16(x2[2 * np], f[h], b[0], b[1]);
+                                mma_bf16(x2[2 * np + 1], f[h], b[2], b[3]);
                             }
-                            mma_bf16(x2[2 * np], fr[h], b[0], b[1]);
-                            mma_bf16(x2[2 * np + 1], fr[h], b[2], b[3]);
-                            mma_bf16(x3[2 * np], fu[h], d[0], d[1]);
-                            mma_bf16(x3[2 * np + 1], fu[h], d[2], d[3]);
                         }
-                    }
+                }
+                {   // U: U dS'^T
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) load_a_t(f[p], st + M::kU + p * M::kUP, 16 * kt, 16 * strip, lane);
+#pragma unroll
+                    for (int np = 0; np < NQ / 2; ++np)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t b[4];
+                            load_b_t<kSlice>(b, st + M::kDS + p * M::kSP, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
+#pragma unroll
+                            for (int h = 0; h + p < 2; ++h) {
+                                mma_bf16(x3[2 * np], f[h], b[0], b[1]);
+                                mma_bf16(x3[2 * np + 1], f[h], b[2], b[3]);
+                            }
+                        }
+                }
             }
-            __syncthreads();
+            if (M::kStages == 1) {
+                __syncthreads();
+                if (it + 1 < rep * slices) load(it + 1);
+            }
         }
 
         // <S, dS'>, the parts of dQ and dK that go through the states, a_i and b_j
@@ -177,8 +221,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
         if (lane == 0) inner[warp] = prod;
         float dot[2] = {0.f, 0.f}, dob[2] = {0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < NH; ++n) {
-            const int col = 8 * (half * NH + n) + c2;
+        for (int n = 0; n < NQ; ++n) {
+            const int col = 8 * (quarter * NQ + n) + c2;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {   // rows i0, i0 + 8
                 const int i = i0 + 8 * e;
@@ -210,18 +254,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             dob[e] += __shfl_xor_sync(0xffffffffu, dob[e], 1);
             dob[e] += __shfl_xor_sync(0xffffffffu, dob[e], 2);
             if ((lane & 3) == 0) {
-                dots[half * kChunk + i0 + 8 * e] = dot[e];
-                dotb[half * kChunk + i0 + 8 * e] = dob[e];
+                dots[quarter * kChunk + i0 + 8 * e] = dot[e];
+                dotb[quarter * kChunk + i0 + 8 * e] = dob[e];
             }
         }
         // F1 = scale D dP, F2 = D dN as pairs, and Z
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-            const int cb = 32 * half + 16 * np;   // first column of the block
+        {
+            const int cb = 16 * quarter;   // first column of the block
             uint32_t f1h[4] = {0, 0, 0, 0}, f1l[4] = {0, 0, 0, 0}, f2h[4] = {0, 0, 0, 0}, f2l[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int n = 2 * np + (q >> 1), row = q & 1, i = i0 + 8 * row, j = cb + 8 * (q >> 1) + c2;
+                const int n = q >> 1, row = q & 1, i = i0 + 8 * row, j = cb + 8 * n + c2;
                 float z0 = 0.f, z1 = 0.f;
                 if (cb <= 16 * strip) {
                     const uint32_t at = img(0, i, j >> 3) + (j & 7) * 2;
@@ -274,12 +317,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                 for (int p = 0; p < 2; ++p) load_a_t(f1t[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
 #pragma unroll
-            for (int np = 0; np < NH / 2; ++np)
+            for (int np = 0; np < NQ / 2; ++np)
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     uint32_t bk[4], bq[4];
-                    load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * half * NH + 16 * np, lane);
-                    load_b_t(bq, base + M::kQ + p * M::kKQ, 16 * kt, 8 * half * NH + 16 * np, lane);
+                    load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
+                    load_b_t(bq, base + M::kQ + p * M::kKQ, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
 #pragma unroll
                     for (int h = 0; h + p < 2; ++h) {
                         if (down) {
@@ -298,11 +341,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                 for (int p = 0; p < 2; ++p) load_a_t(f1t[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
 #pragma unroll
-                for (int np = 0; np < NH / 2; ++np)
+                for (int np = 0; np < NQ / 2; ++np)
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
                         uint32_t bk[4];
-                        load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * half * NH + 16 * np, lane);
+                        load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
 #pragma unroll
                         for (int h = 0; h + p < 2; ++h) {
                             mma_bf16(dk[2 * np], f1t[h], bk[0], bk[1]);
@@ -313,35 +356,39 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
         }
 
         // sum over i >= t of Z_ij within quarters of 16 rows, then with the quarters below
-        {
-            const int j = tid & 63, quarter = tid >> 6;
+        if (tid < 256) {
+            const int j = tid & 63, q = tid >> 6;
             float s = 0.f;
-            for (int t = 16 * quarter + 15; t >= 16 * quarter; --t) {
-                s += Z[t * kZStride + j];
-                Z[t * kZStride + j] = s;
+#pragma unroll
+            for (int t = 15; t >= 0; --t) {
+                s += Z[(16 * q + t) * kZStride + j];
+                Z[(16 * q + t) * kZStride + j] = s;
             }
-            run[quarter * kChunk + j] = s;
+            run[q * kChunk + j] = s;
         }
         __syncthreads();
-        {   // row t: sum over j < t (four threads a row)
-            const int t = tid >> 2, part = tid & 3, quarter = t >> 4;
+        {   // row t: sum over j < t (eight threads a row)
+            const int t = tid >> 3, part = tid & 7;
             float s = 0.f;
-            for (int j = part; j < t; j += 4) {
+            for (int j = part; j < t; j += 8) {
                 s += Z[t * kZStride + j];
-                for (int q = quarter + 1; q < 4; ++q) s += run[q * kChunk + j];
+                for (int q = (t >> 4) + 1; q < 4; ++q) s += run[q * kChunk + j];
             }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
             __syncthreads();
             if (part == 0) run[t] = s;
         }
         __syncthreads();
         if (warp == 0) {   // tokens 2 lane, 2 lane + 1
             float av[2], b[2];
-            av[0] = dots[2 * lane] + dots[kChunk + 2 * lane];
-            av[1] = dots[2 * lane + 1] + dots[kChunk + 2 * lane + 1];
-            b[0] = dotb[2 * lane] + dotb[kChunk + 2 * lane];
-            b[1] = dotb[2 * lane + 1] + dotb[kChunk + 2 * lane + 1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                av[e] = (dots[t] + dots[kChunk + t]) + (dots[2 * kChunk + t] + dots[3 * kChunk + t]);
+                b[e] = (dotb[t] + dotb[kChunk + t]) + (dotb[2 * kChunk + t] + dotb[3 * kChunk + t]);
+            }
             float below = av[0] + av[1], above = b[0] + b[1];   // sums over i >= 2 lane, over j <= 2 lane + 1
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -380,10 +427,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     const bool pairs = sizeof(T) == 2 && (a.s.k & 1) == 0 &&
                        ((reinterpret_cast<uintptr_t>(a.dq) | reinterpret_cast<uintptr_t>(a.dk)) & 3) == 0;
 #pragma unroll
-    for (int n = 0; n < NH; ++n)
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int i = i0 + 8 * e, col = 8 * (half * NH + n) + c2;
+            const int i = i0 + 8 * e, col = 8 * (quarter * NQ + n) + c2;
             if (i >= rows) continue;
             if (pairs) {
                 if constexpr (sizeof(T) == 2) {
