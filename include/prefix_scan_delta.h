@@ -55,6 +55,9 @@ typedef struct ps_delta_tensor {
     int64_t head_stride;
 } ps_delta_tensor;
 
+/* The inputs of a call come as an array of five tensors in this order. */
+typedef enum ps_delta_input { PS_DELTA_Q = 0, PS_DELTA_K = 1, PS_DELTA_V = 2, PS_DELTA_G = 3, PS_DELTA_BETA = 4 } ps_delta_input;
+
 /*
  * num_seqs   sequences (0: nothing to do)
  * tokens     tokens of every sequence; with cu_seqlens, of all together
@@ -93,10 +96,8 @@ size_t ps_delta_workspace_size(const ps_delta_shape *shape, int train);
  *   train != 0: `ws` keeps what ps_delta_backward reads
  * An empty sequence hands its state on.
  */
-ps_status ps_delta_forward(const ps_delta_shape *shape, const ps_delta_tensor *q, const ps_delta_tensor *k,
-                           const ps_delta_tensor *v, const ps_delta_tensor *g, const ps_delta_tensor *beta,
-                           const float *h0, float *ht, void *o, int train, void *ws, size_t ws_bytes,
-                           ps_stream_t stream);
+ps_status ps_delta_forward(const ps_delta_shape *shape, const ps_delta_tensor inputs[5], const float *h0, float *ht,
+                           void *o, int train, void *ws, size_t ws_bytes, ps_stream_t stream);
 
 /*
  * Backward of one ps_delta_forward(train != 0) call with the same shape, q,
@@ -126,10 +127,8 @@ ps_status ps_delta_backward(const ps_delta_shape *shape, const ps_delta_tensor *
  *   o         contiguous [num_seqs, t, heads_v, dim_v]
  * No workspace.
  */
-ps_status ps_delta_step(const ps_delta_shape *shape, const ps_delta_tensor *q, const ps_delta_tensor *k,
-                        const ps_delta_tensor *v, const ps_delta_tensor *g, const ps_delta_tensor *beta,
-                        float *state, int64_t pages, const int32_t *slots, const int32_t *lengths, void *o,
-                        ps_stream_t stream);
+ps_status ps_delta_step(const ps_delta_shape *shape, const ps_delta_tensor inputs[5], float *state, int64_t pages,
+                        const int32_t *slots, const int32_t *lengths, void *o, ps_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@ library has not been built; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 
 from .build import LIBRARY
@@ -64,36 +65,25 @@ PS_NOALLOC_MAX_ELEMENTS = 1 << 29
 PS_REAL_F32, PS_REAL_BF16, PS_REAL_F16 = 0, 1, 2
 
 
-class DeltaTensor(ctypes.Structure):   # ps_delta_tensor
-    _fields_ = [("data", _vp), ("seq_stride", _i64), ("tok_stride", _i64), ("head_stride", _i64)]
-
-
-class DeltaShape(ctypes.Structure):    # ps_delta_shape
-    _fields_ = [("num_seqs", _i64), ("tokens", _i64), ("cu_seqlens", _vp), ("heads_k", ctypes.c_int32),
-                ("heads_v", ctypes.c_int32), ("dim_k", ctypes.c_int32), ("dim_v", ctypes.c_int32), ("type", _int),
-                ("beta_type", _int), ("scale", ctypes.c_float)]
-
-
-_dt, _ds = ctypes.POINTER(DeltaTensor), ctypes.POINTER(DeltaShape)
-SIGNATURES["ps_delta_workspace_size"] = (_sz, [_ds, _int])
-SIGNATURES["ps_delta_forward"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _vp, _vp, _int, _vp, _sz, _vp])
-SIGNATURES["ps_delta_backward"] = (_int, [_ds, _dt, _dt, _dt, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
-SIGNATURES["ps_delta_step"] = (_int, [_ds, _dt, _dt, _dt, _dt, _dt, _vp, _i64, _vp, _vp, _vp, _vp])
+# Structures go over as packed bytes (struct.pack), which costs a fraction of building them field by field.
+DELTA_TENSOR = struct.Struct("@Pqqq")           # ps_delta_tensor: data, seq_stride, tok_stride, head_stride
+DELTA_INPUTS = struct.Struct("@" + "Pqqq" * 5)  # q, k, v, g, beta
+DELTA_SHAPE = struct.Struct("@qqPiiiiiif4x")    # ps_delta_shape
+SIGNATURES["ps_delta_workspace_size"] = (_sz, [_vp, _int])
+SIGNATURES["ps_delta_forward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _sz, _vp])
+SIGNATURES["ps_delta_backward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_delta_step"] = (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp])
 
 PS_PAGES_MAX_POOLS = 128
 
 
-class PagePool(ctypes.Structure):      # ps_page_pool
-    _fields_ = [("data", _vp), ("page_bytes", _i64)]
-
-
-_pp, _i32 = ctypes.POINTER(PagePool), ctypes.c_int32
+_i32 = ctypes.c_int32
 SIGNATURES["ps_pages_workspace_size"] = (_sz, [_i64, _i64])
-SIGNATURES["ps_pages_copy"] = (_int, [_pp, _int, _i64, _vp, _vp, _i64, _vp])
-SIGNATURES["ps_pages_fork"] = (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _pp, _int, _i64, _vp, _vp, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_pages_copy"] = (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp])
+SIGNATURES["ps_pages_fork"] = (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _int, _i64, _vp, _vp, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_pages_grow"] = (_int, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_pages_free"] = (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp])
-SIGNATURES["ps_pages_compact"] = (_int, [_vp, _i64, _i64, _vp, _pp, _int, _i64, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_pages_compact"] = (_int, [_vp, _i64, _i64, _vp, _vp, _int, _i64, _vp, _vp, _sz, _vp])
 
 for _kind in ("inclusive", "exclusive"):
     for _t in ("i32", "i64", "f32"):
@@ -115,6 +105,8 @@ class PrefixScanError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load the CUDA library, raising if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not LIBRARY.exists():

@@ -6,13 +6,14 @@ import contextlib
 import torch
 
 _HERE = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def enter(device: torch.device, stream):
     """The CUDA stream handle to enqueue on, and a context for the call: inside it ``device`` is the current device and
     new tensors belong to the stream (the given one, or the device's current one)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return torch.cuda.current_stream().cuda_stream, _HERE
+        return (_raw_stream(device.index) if _raw_stream else torch.cuda.current_stream().cuda_stream), _HERE
     s = stream if stream is not None else torch.cuda.current_stream(device)
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))

@@ -93,12 +93,12 @@ extern "C" size_t ps_delta_workspace_size(const ps_delta_shape *d, int train) {
     return chunks_bytes(d, train) + kq_bytes(d);
 }
 
-extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_tensor *q, const ps_delta_tensor *k,
-                                      const ps_delta_tensor *v, const ps_delta_tensor *g, const ps_delta_tensor *beta,
-                                      const float *h0, float *ht, void *o, int train, void *ws, size_t ws_bytes,
-                                      ps_stream_t stream) {
-    if (!valid(d)) return PS_ERR_INVALID_ARG;
+extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_tensor in5[5], const float *h0, float *ht,
+                                      void *o, int train, void *ws, size_t ws_bytes, ps_stream_t stream) {
+    if (!valid(d) || in5 == nullptr) return PS_ERR_INVALID_ARG;
     if (d->num_seqs == 0) return PS_OK;
+    const ps_delta_tensor *q = in5 + PS_DELTA_Q, *k = in5 + PS_DELTA_K, *v = in5 + PS_DELTA_V, *g = in5 + PS_DELTA_G;
+    const ps_delta_tensor *beta = in5 + PS_DELTA_BETA;
     const size_t es = real_bytes(d->type), need = ps_delta_workspace_size(d, train);
     const bool packed = d->cu_seqlens != nullptr;
     const size_t state = (size_t)d->num_seqs * d->heads_v * d->dim_k * d->dim_v * 4;
@@ -208,12 +208,12 @@ extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_t
     return done(e);
 }
 
-extern "C" ps_status ps_delta_step(const ps_delta_shape *d, const ps_delta_tensor *q, const ps_delta_tensor *k,
-                                   const ps_delta_tensor *v, const ps_delta_tensor *g, const ps_delta_tensor *beta,
-                                   float *state, int64_t pages, const int32_t *slots, const int32_t *lengths, void *o,
-                                   ps_stream_t stream) {
-    if (!valid(d) || d->cu_seqlens != nullptr || pages < 0) return PS_ERR_INVALID_ARG;
+extern "C" ps_status ps_delta_step(const ps_delta_shape *d, const ps_delta_tensor in5[5], float *state, int64_t pages,
+                                   const int32_t *slots, const int32_t *lengths, void *o, ps_stream_t stream) {
+    if (!valid(d) || in5 == nullptr || d->cu_seqlens != nullptr || pages < 0) return PS_ERR_INVALID_ARG;
     if (d->num_seqs == 0 || d->tokens == 0) return PS_OK;
+    const ps_delta_tensor *q = in5 + PS_DELTA_Q, *k = in5 + PS_DELTA_K, *v = in5 + PS_DELTA_V, *g = in5 + PS_DELTA_G;
+    const ps_delta_tensor *beta = in5 + PS_DELTA_BETA;
     const size_t es = real_bytes(d->type);
     if (!tensor_ok(q, es) || !tensor_ok(k, es) || !tensor_ok(v, es) || !tensor_ok(g, 4) ||
         !tensor_ok(beta, real_bytes(d->beta_type)))

@@ -9,7 +9,6 @@ Tensors are passed as raw device pointers with their strides and the current
 """
 from __future__ import annotations
 
-import ctypes
 from dataclasses import dataclass
 
 import torch
@@ -47,23 +46,60 @@ def _check_inputs(fn, q, k, v, g, beta, cu_seqlens):
             raise ValueError(f"{fn}: cu_seqlens must be a contiguous 1-D int32 CUDA tensor of one offset more than sequences")
 
 
-def _tensor(t: torch.Tensor, packed: bool, inner: bool) -> _lib.DeltaTensor:
+@dataclass(frozen=True)
+class _Plan:
+    """What follows from the inputs' shapes, strides, types and device: kept from call to call (never their data)."""
+    dims: tuple       # tokens, key heads, value heads, K, V and the codes of both types
+    seqs: int         # sequences without cu_seqlens
+    states: tuple     # shape of the states, without the number of sequences
+    strides: tuple    # (seq, tok, head) of q, k, v, g, beta
+    scale: float
+
+
+_plans: dict = {}
+
+
+def _strides(t: torch.Tensor, packed: bool, inner: bool) -> tuple:
     """The strides of a [sequences,] tokens, heads[, size] tensor."""
     st = t.stride()
     head = -2 if inner else -1
-    return _lib.DeltaTensor(t.data_ptr() if t.numel() else None, 0 if packed else st[0], st[head - 1], st[head])
+    return (0 if packed else st[0], st[head - 1], st[head])
 
 
-def _shape(q, v, beta, cu_seqlens, scale) -> _lib.DeltaShape:
+def _plan(fn, q, k, v, g, beta, cu_seqlens) -> _Plan:
     packed = cu_seqlens is not None
-    return _lib.DeltaShape(cu_seqlens.numel() - 1 if packed else q.shape[0], q.shape[0] if packed else q.shape[1],
-                           cu_seqlens.data_ptr() if packed else None, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
-                           REAL_CODES[q.dtype], REAL_CODES[beta.dtype],
-                           q.shape[-1] ** -0.5 if scale is None else float(scale))
+    key = (packed, q.shape, v.shape, q.stride(), k.stride(), v.stride(), g.stride(), beta.stride(), k.shape, g.shape, beta.shape,
+           q.dtype, k.dtype, v.dtype, g.dtype, beta.dtype, q.device, k.device, v.device, g.device, beta.device)
+    plan = _plans.get(key)
+    if plan is None or (packed and (cu_seqlens.dtype != torch.int32 or cu_seqlens.device != q.device
+                                    or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous())):
+        _check_inputs(fn, q, k, v, g, beta, cu_seqlens)
+        hk, hv, ks, vs = q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1]
+        plan = _Plan((q.shape[0] if packed else q.shape[1], hk, hv, ks, vs, REAL_CODES[q.dtype], REAL_CODES[beta.dtype]),
+                     q.shape[0], (hv, ks, vs),
+                     tuple(_strides(t, packed, inner) for t, inner in ((q, True), (k, True), (v, True), (g, False), (beta, False))),
+                     ks ** -0.5)
+        if len(_plans) >= 4096:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _shape(plan: _Plan, cu_seqlens, scale) -> bytes:
+    """ps_delta_shape"""
+    tokens, hk, hv, ks, vs, code, beta_code = plan.dims
+    seqs, cu = (plan.seqs, 0) if cu_seqlens is None else (cu_seqlens.numel() - 1, cu_seqlens.data_ptr())
+    return _lib.DELTA_SHAPE.pack(seqs, tokens, cu, hk, hv, ks, vs, code, beta_code, plan.scale if scale is None else scale)
+
+
+def _inputs(plan: _Plan, q, k, v, g, beta) -> bytes:
+    """The array of five ps_delta_tensor"""
+    sq, sk, sv, sg, sb = plan.strides
+    return _lib.DELTA_INPUTS.pack(q.data_ptr(), *sq, k.data_ptr(), *sk, v.data_ptr(), *sv, g.data_ptr(), *sg, beta.data_ptr(), *sb)
 
 
 def _check_state(fn, name, t, shape, device):
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
 
 
@@ -79,8 +115,11 @@ def delta_rule_workspace_size(q: torch.Tensor, v: torch.Tensor, cu_seqlens: torc
                               train: bool = False) -> int:
     """Bytes of workspace :func:`delta_rule` needs for such inputs (``train``: the buffer that
     :func:`delta_rule_forward` leaves for the backward pass)."""
-    shape = _shape(q, v, q, cu_seqlens, 1.0)
-    return int(_lib.load().ps_delta_workspace_size(ctypes.byref(shape), int(train)))
+    packed = cu_seqlens is not None
+    shape = _lib.DELTA_SHAPE.pack(cu_seqlens.numel() - 1 if packed else q.shape[0], q.shape[0] if packed else q.shape[1],
+                                  cu_seqlens.data_ptr() if packed else 0, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
+                                  REAL_CODES[q.dtype], _lib.PS_REAL_F32, 1.0)
+    return int(_lib.load().ps_delta_workspace_size(shape, int(train)))
 
 
 @dataclass
@@ -91,40 +130,39 @@ class DeltaRuleSaved:
     v_shape: torch.Size
     beta_dtype: torch.dtype
     cu_seqlens: torch.Tensor | None
-    shape: _lib.DeltaShape
+    plan: object
+    shape: bytes
+    states: tuple
     has_initial_state: bool
     workspace: torch.Tensor
 
 
 def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state, workspace,
              stream, train):
-    _check_inputs(fn, q, k, v, g, beta, cu_seqlens)
-    shape = _shape(q, v, beta, cu_seqlens, scale)
-    states = (int(shape.num_seqs), v.shape[-2], q.shape[-1], v.shape[-1])
+    plan = _plan(fn, q, k, v, g, beta, cu_seqlens)
+    device = q.device
+    states = (plan.seqs if cu_seqlens is None else cu_seqlens.numel() - 1, *plan.states)
     if initial_state is not None:
-        _check_state(fn, "initial_state", initial_state, states, q.device)
+        _check_state(fn, "initial_state", initial_state, states, device)
     if final_state is not None:
-        _check_state(fn, "final_state", final_state, states, q.device)
-    if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != q.device or not out.is_contiguous()):
+        _check_state(fn, "final_state", final_state, states, device)
+    if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != device or not out.is_contiguous()):
         raise ValueError(f"{fn}: `out` must be contiguous and match v's shape, type and device")
-    packed = cu_seqlens is not None
+    shape, inputs = _shape(plan, cu_seqlens, scale), _inputs(plan, q, k, v, g, beta)
     lib = _lib.load()
-    s, ctx = enter(q.device, stream)
+    s, ctx = enter(device, stream)
     with ctx:
         if out is None:
-            out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty(v.shape, dtype=q.dtype, device=device)
         if final_state is None and output_final_state:
-            final_state = torch.empty(states, dtype=torch.float32, device=q.device)
-        need = int(lib.ps_delta_workspace_size(ctypes.byref(shape), int(train)))
-        workspace = _workspace(fn, workspace, need, q.device)
-        ts = [_tensor(t, packed, inner) for t, inner in ((q, True), (k, True), (v, True), (g, False), (beta, False))]
-        st = lib.ps_delta_forward(ctypes.byref(shape), *(ctypes.byref(t) for t in ts),
-                                  initial_state.data_ptr() if initial_state is not None else None,
-                                  final_state.data_ptr() if final_state is not None else None,
-                                  out.data_ptr() if out.numel() else None, int(train), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), s)
+            final_state = torch.empty(states, dtype=torch.float32, device=device)
+        need = lib.ps_delta_workspace_size(shape, train)
+        workspace = _workspace(fn, workspace, need, device)
+        st = lib.ps_delta_forward(shape, inputs, initial_state.data_ptr() if initial_state is not None else None,
+                                  final_state.data_ptr() if final_state is not None else None, out.data_ptr(), train,
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
     _lib.check("ps_delta_forward", st)
-    return out, final_state, shape, workspace
+    return out, final_state, plan, shape, states, workspace
 
 
 def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, *,
@@ -144,9 +182,8 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     ``cu_seqlens``, outputs of tokens that no sequence holds are not written.  For gradients see
     :func:`delta_rule_forward`.
     """
-    out, final_state, _, _ = _forward("delta_rule", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
-                                      out, final_state, workspace, stream, False)
-    return out, final_state
+    return _forward("delta_rule", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state,
+                    workspace, stream, 0)[:2]
 
 
 def delta_rule_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, *,
@@ -160,9 +197,11 @@ def delta_rule_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
     ``saved`` goes to :func:`delta_rule_backward`; it holds q and k (which must not change until then) and a workspace of
     ``delta_rule_workspace_size(q, v, cu_seqlens, train=True)`` bytes.
     """
-    out, final_state, shape, workspace = _forward("delta_rule_forward", q, k, v, g, beta, scale, cu_seqlens, initial_state,
-                                                  output_final_state, out, final_state, workspace, stream, True)
-    return out, final_state, DeltaRuleSaved(q, k, v.shape, beta.dtype, cu_seqlens, shape, initial_state is not None, workspace)
+    out, final_state, plan, shape, states, workspace = _forward(
+        "delta_rule_forward", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state, workspace,
+        stream, 1)
+    return out, final_state, DeltaRuleSaved(q, k, v.shape, beta.dtype, cu_seqlens, plan, shape, states, initial_state is not None,
+                                            workspace)
 
 
 def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_state: torch.Tensor | None = None, stream=None
@@ -180,10 +219,8 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
         raise ValueError(f"{fn}: d_o must match o's shape, type and device")
     if d_o.numel() and d_o.shape[-1] > 1 and d_o.stride(-1) != 1:
         d_o = d_o.contiguous()
-    hv, dv_size = saved.v_shape[-2:]
-    states = (int(saved.shape.num_seqs), hv, q.shape[-1], dv_size)
     if d_final_state is not None:
-        _check_state(fn, "d_final_state", d_final_state, states, q.device)
+        _check_state(fn, "d_final_state", d_final_state, saved.states, q.device)
     lib = _lib.load()
     s, ctx = enter(q.device, stream)
     with ctx:
@@ -193,10 +230,11 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
         dv = new(saved.v_shape, dtype=q.dtype, device=q.device)
         dg = new(heads, dtype=torch.float32, device=q.device)
         dbeta = new(heads, dtype=saved.beta_dtype, device=q.device)
-        dh0 = torch.empty(states, dtype=torch.float32, device=q.device) if saved.has_initial_state else None
-        ts = [_tensor(t, packed, True) for t in (q, k, d_o)]
+        dh0 = torch.empty(saved.states, dtype=torch.float32, device=q.device) if saved.has_initial_state else None
+        strides = (saved.plan.strides[0], saved.plan.strides[1], _strides(d_o, packed, True))
+        ts = [_lib.DELTA_TENSOR.pack(t.data_ptr(), *st) for t, st in zip((q, k, d_o), strides)]
         ptr = lambda t: t.data_ptr() if t is not None and t.numel() else None  # noqa: E731
-        st = lib.ps_delta_backward(ctypes.byref(saved.shape), *(ctypes.byref(t) for t in ts), ptr(d_final_state), ptr(dq),
+        st = lib.ps_delta_backward(saved.shape, *ts, ptr(d_final_state), ptr(dq),
                                    ptr(dk), ptr(dv), ptr(dg), ptr(dbeta), ptr(dh0), saved.workspace.data_ptr(),
                                    saved.workspace.numel() * saved.workspace.element_size(), s)
     _lib.check("ps_delta_backward", st)
@@ -214,27 +252,25 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     of the tokens count.  Outputs of tokens that do not count are 0.
     """
     fn = "delta_rule_step"
-    _check_inputs(fn, q, k, v, g, beta, None)
-    shape = _shape(q, v, beta, None, scale)
-    if state.dim() != 4:
+    plan = _plan(fn, q, k, v, g, beta, None)
+    device = q.device
+    if state.dim() != 4 or state.shape[1:] != plan.states:
         raise ValueError(f"{fn}: state must be [pages, value heads, K, V]")
-    _check_state(fn, "state", state, (state.shape[0], v.shape[-2], q.shape[-1], v.shape[-1]), q.device)
+    _check_state(fn, "state", state, state.shape, device)
     for name, t in (("slots", slots), ("lengths", lengths)):
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (q.shape[0],) or t.device != q.device
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != plan.seqs or t.device != device
                               or not t.is_contiguous()):
             raise ValueError(f"{fn}: {name} must be a contiguous int32 CUDA tensor with one entry per sequence")
-    if slots is None and state.shape[0] < q.shape[0]:
+    if slots is None and state.shape[0] < plan.seqs:
         raise ValueError(f"{fn}: fewer pages than sequences")
-    if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != q.device or not out.is_contiguous()):
+    if out is not None and (out.dtype != q.dtype or out.shape != v.shape or out.device != device or not out.is_contiguous()):
         raise ValueError(f"{fn}: `out` must be contiguous and match v's shape, type and device")
-    s, ctx = enter(q.device, stream)
+    s, ctx = enter(device, stream)
     with ctx:
         if out is None:
-            out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-        ts = [_tensor(t, False, inner) for t, inner in ((q, True), (k, True), (v, True), (g, False), (beta, False))]
-        st = _lib.load().ps_delta_step(ctypes.byref(shape), *(ctypes.byref(t) for t in ts), state.data_ptr(),
-                                       state.shape[0], slots.data_ptr() if slots is not None else None,
-                                       lengths.data_ptr() if lengths is not None else None,
-                                       out.data_ptr() if out.numel() else None, s)
+            out = torch.empty(v.shape, dtype=q.dtype, device=device)
+        st = _lib.load().ps_delta_step(_shape(plan, None, scale), _inputs(plan, q, k, v, g, beta), state.data_ptr(), state.shape[0],
+                                       slots.data_ptr() if slots is not None else None,
+                                       lengths.data_ptr() if lengths is not None else None, out.data_ptr(), s)
     _lib.check("ps_delta_step", st)
     return out

@@ -8,6 +8,8 @@ on ``stream`` (default: the current stream) and never synchronise.
 """
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import _lib
@@ -15,8 +17,9 @@ from ._streams import enter
 
 
 def _check_ints(fn, device, **tensors):
+    cuda = device.type == "cuda"
     for name, (t, dims) in tensors.items():
-        if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or not t.is_cuda or t.device != device:
+        if not cuda or t.dtype != torch.int32 or t.device != device or t.dim() != dims or not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be a contiguous {dims}-D int32 tensor on one CUDA device with the others")
 
 
@@ -25,16 +28,15 @@ def _pools(fn, pools, pages, device):
         pools = [pools]
     if len(pools) > _lib.PS_PAGES_MAX_POOLS:
         raise ValueError(f"{fn}: at most {_lib.PS_PAGES_MAX_POOLS} pools in one call")
-    out = (_lib.PagePool * len(pools))()
-    for i, p in enumerate(pools):
-        if not p.is_cuda or p.device != device or p.dim() < 1 or p.shape[0] != pages or not p.is_contiguous():
+    out = []
+    for p in pools:
+        if p.device != device or p.dim() < 1 or p.shape[0] != pages or not p.is_contiguous():
             raise ValueError(f"{fn}: pools must be contiguous CUDA tensors of {pages} pages on one device")
         size = p.numel() // pages * p.element_size() if pages else 1
         if size == 0:
             raise ValueError(f"{fn}: pages must not be empty")
-        out[i].data = p.data_ptr()
-        out[i].page_bytes = size
-    return out, len(pools)
+        out += (p.data_ptr(), size)
+    return struct.pack("@" + "Pq" * len(pools), *out), len(pools)   # ps_page_pool
 
 
 def pages_workspace_size(rows: int, pages: int) -> int:
