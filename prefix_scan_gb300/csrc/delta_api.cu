@@ -25,7 +25,8 @@ bool valid(const ps_delta_shape *d) {
     if (reinterpret_cast<uintptr_t>(d->cu_seqlens) % 4 != 0) return false;
     // grids are one-dimensional over chunks or over (sequence, head, block of columns)
     if (ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr) > INT_MAX / 2) return false;
-    return d->num_seqs * d->heads_v * ((d->dim_v + 31) / 32) <= INT_MAX;
+    const int64_t slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);   // no more segments than chunks and sequences
+    return (slots + d->num_seqs) <= INT_MAX / ((int64_t)d->heads_v * ((d->dim_v + 15) / 16 + 1));
 }
 long long total_tokens(const ps_delta_shape *d) { return d->cu_seqlens ? d->tokens : d->num_seqs * d->tokens; }
 
@@ -81,16 +82,52 @@ size_t chunks_bytes(const ps_delta_shape *d, int train) {
     const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
     return (size_t)slots * d->heads_v * ps::chunk_layout(d->dim_k, d->dim_v, train != 0).stride;
 }
-size_t kq_bytes(const ps_delta_shape *d) {
-    const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
-    return (size_t)slots * d->heads_k * ps::kq_stride(d->dim_k, d->type == PS_REAL_BF16 ? 1 : 2);
+// The workspace's parts after the chunks': keys and queries, and what segments need.
+struct Parts {
+    int seg;
+    long long seg_slots;
+    size_t kq, seg_m, seg_state, total;
+};
+Parts parts_of(const ps_delta_shape *d, int train) {
+    const bool packed = d->cu_seqlens != nullptr;
+    const long long slots = ps::delta_slots(d->num_seqs, d->tokens, packed);
+    Parts p{};
+    p.kq = chunks_bytes(d, train);
+    p.seg_m = p.kq + (size_t)slots * d->heads_k * ps::kq_stride(d->dim_k, d->type == PS_REAL_BF16 ? 1 : 2);
+    const long long chunks = packed ? d->tokens / ps::kChunk / (d->num_seqs ? d->num_seqs : 1) : (d->tokens + ps::kChunk - 1) / ps::kChunk;
+    p.seg = ps::segment_chunks(d->num_seqs * d->heads_v * ps::blocks_v(d->dim_v), chunks, train != 0);
+    p.seg_slots = ps::segment_slots(slots, d->num_seqs, p.seg);
+    p.seg_state = p.seg_m + (size_t)p.seg_slots * d->heads_v * ps::seg_m_bytes(d->dim_k);
+    p.total = p.seg_state + (p.seg ? (size_t)(p.seg_slots + 1) * d->heads_v * d->dim_k * d->dim_v * 4 : 0);
+    p.total = (p.total + 255) / 256 * 256;
+    return p;
+}
+void place(ps::DeltaArgs &a, const Parts &p, void *ws) {
+    a.ws = static_cast<unsigned char *>(ws);
+    a.kq = a.ws + p.kq;
+    a.seg = p.seg;
+    a.seg_slots = p.seg_slots;
+    a.seg_m = a.ws + p.seg_m;
+    a.seg_state = reinterpret_cast<float *>(a.ws + p.seg_state);
+}
+// The chain, or where sequences are cut the states of the segments, their join and the chain.
+template <typename Chain>
+cudaError_t run_chain(ps::DeltaArgs a, int type, bool backward, Chain chain, cudaStream_t s) {
+    if (a.seg) {
+        a.pass = ps::kPassStates;
+        cudaError_t e = chain(a, type, s);
+        if (e == cudaSuccess) e = ps::launch_delta_join(a, backward, s);
+        if (e != cudaSuccess) return e;
+        a.pass = ps::kPassAll;
+    }
+    return chain(a, type, s);
 }
 
 }  // namespace
 
 extern "C" size_t ps_delta_workspace_size(const ps_delta_shape *d, int train) {
     if (!valid(d)) return 0;
-    return chunks_bytes(d, train) + kq_bytes(d);
+    return parts_of(d, train).total;
 }
 
 extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_tensor in5[5], const float *h0, float *ht,
@@ -131,8 +168,7 @@ extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_te
         a.vec_qk = vectors(*q, d->dim_k, es, packed) && vectors(*k, d->dim_k, es, packed);
         a.vec_v = vectors(*v, d->dim_v, es, packed);
         a.o = o;
-        a.ws = static_cast<unsigned char *>(ws);
-        a.kq = a.ws + chunks_bytes(d, train);
+        place(a, parts_of(d, train), ws);
         a.slots = ps::delta_slots(d->num_seqs, d->tokens, packed);
         a.train = train != 0;
     } else {
@@ -147,7 +183,7 @@ extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_te
         if (e != cudaSuccess) return done(e);
     }
     if (d->tokens == 0 && ht == nullptr) return PS_OK;
-    return done(ps::launch_delta_chain(a, d->type, s));
+    return done(run_chain(a, d->type, false, ps::launch_delta_chain, s));
 }
 
 extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_tensor *q, const ps_delta_tensor *k,
@@ -191,8 +227,7 @@ extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_t
         a.dv = dv;
         a.dg = dg;
         a.dbeta = dbeta;
-        a.ws = static_cast<unsigned char *>(ws);
-        a.kq = a.ws + chunks_bytes(d, 1);
+        place(a, parts_of(d, 1), ws);
         a.slots = ps::delta_slots(d->num_seqs, d->tokens, packed);
         a.train = 1;
     } else {
@@ -203,7 +238,7 @@ extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_t
         a.s.cu = nullptr;
     }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = ps::launch_delta_chain_backward(a, d->type, s);
+    cudaError_t e = run_chain(a, d->type, true, ps::launch_delta_chain_backward, s);
     if (e == cudaSuccess && a.slots > 0) e = ps::launch_delta_gradients(a, d->type, s);
     return done(e);
 }

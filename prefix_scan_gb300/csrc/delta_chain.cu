@@ -22,6 +22,9 @@
 // one stores what training keeps, eight convert on the chain (row = lane, half of
 // the columns each), and four take the outputs, which the chain does not wait for:
 // U^T P^T of a chunk runs while the next one's X is on its way through registers.
+//
+// Long sequences over few heads come in segments (DeltaArgs::seg): the first of two
+// passes takes the states alone, and one more chain per segment finds its matrix M.
 #include "delta_tmem.cuh"
 
 namespace ps {
@@ -63,21 +66,34 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
     volatile int *gave_up = &bar.gave_up;
     const uint32_t base = smem_addr(smem);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be uniform
-    const int blocks = blocks_v(a.s.v), rep = a.s.hv / a.s.hk;
+    const bool states = a.pass == kPassStates;   // of segments, without outputs
+    const int blocks = blocks_v(a.s.v) + states, rep = a.s.hv / a.s.hk;
     const int vb = (int)(blockIdx.x % blocks);
     const int head = (int)(blockIdx.x / blocks % a.s.hv);
-    const long long seq = blockIdx.x / blocks / a.s.hv;
-    const Span sp = span_of(a.s, seq);
-    const int v0 = vb * kBlockV;
+    const bool matrix = states && vb == blocks - 1;   // this chain finds M
+    Chain chain;
+    if (!chain_of(a, blockIdx.x / blocks / a.s.hv, chain)) return;
+    if (states && (chain.last || (matrix && chain.first))) return;   // nobody needs it
+    const long long seq = chain.seq;
+    const Span sp = chain.span;
+    const int v0 = matrix ? 0 : vb * kBlockV;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
     const int chunks = (int)((sp.len + kChunk - 1) / kChunk);
-    const size_t state = (size_t)(seq * a.s.hv + head) * a.s.k * a.s.v;
+    const bool keep = a.train && !states;
+    // the state at the start and where it goes at the end
+    const size_t one_state = (size_t)a.s.k * a.s.v;
+    const float *from = chain.first ? (a.h0 ? a.h0 + (size_t)(seq * a.s.hv + head) * one_state : nullptr)
+                        : states   ? nullptr
+                                   : a.seg_state + (size_t)(chain.slot * a.s.hv + head) * one_state;
+    float *to_state = states ? (matrix ? nullptr : a.seg_state + (size_t)((chain.slot + 1) * a.s.hv + head) * one_state)
+                      : chain.last && a.ht ? a.ht + (size_t)(seq * a.s.hv + head) * one_state
+                                           : nullptr;
     auto chunk_ws = [&](int c) { return a.ws + (size_t)((sp.slot + c) * a.s.hv + head) * lay.stride; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], 1 + 4);
+            mbar_init(&bar.empty[i], states ? 1 : 1 + 4);
         }
         mbar_init(&bar.v_full, 32);
         mbar_init(&bar.v_empty, 8);
@@ -131,9 +147,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                 const int st = c % M::kStages;
                 const uint32_t at_stage = st * M::kStage;
                 const uint64_t kq = further(kq0, at_stage), kt = further(kt0, at_stage), tt = further(kq, M::kKQ);
-                if (M::kStages == 1 && c) outputs(c - 1);
+                if (M::kStages == 1 && c && !states) outputs(c - 1);
                 wait_phase(&bar.full[st], (c / M::kStages) & 1, gave_up);
-                if (c) wait_phase(&bar.q_read, (c - 1) & 1, gave_up);
+                if (c && !states) wait_phase(&bar.q_read, (c - 1) & 1, gave_up);
                 // S^T [K^T Q^T], by the columns of S that are ready together
 #pragma unroll
                 for (int r = 0; r < KH; ++r) {
@@ -152,7 +168,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                             }
                 }
                 mma_commit(one, &bar.x_done);
-                if (M::kStages == 2 && c) outputs(c - 1);
+                if (M::kStages == 2 && c && !states) outputs(c - 1);
                 wait_busy(&bar.r_ready, c & 1, gave_up);
                 tmem_fence_after();
                 // (beta R)^T T^T: the upper part of beta R with both of T's, the rest with T's upper one
@@ -175,14 +191,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                             mma_tmem(one, tm + kColS, tm + kColW + h * 32 + k * 8,
                                      further(kt, p * KH * kHalf + k * 16 * 128), shape(KP, false), true);
                 mma_commit(one, &bar.s_done);
+                if (states) mma_commit(one, &bar.empty[st]);
             }
-            if (chunks > 0 && !*gave_up) outputs(chunks - 1);
+            if (chunks > 0 && !*gave_up && !states) outputs(chunks - 1);
             mma_commit(one, &bar.drained);
             wait_drained(&bar.drained, 0);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && a.train) {   // what training keeps
+        if (lane == 0 && keep) {   // what training keeps
             const int rows = min(kBlockV, (a.s.v - v0 + 15) / 16 * 16);
             for (int c = 0; c < chunks; ++c) {
                 unsigned char *w = chunk_ws(c);
@@ -224,7 +241,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
     } else if (warp == 3) {
         const int cols = min(kBlockV, a.s.v - v0);
         int c = 0;
-        for (; c < chunks; ++c) {
+        for (; c < chunks && !matrix; ++c) {
             const int n = (int)min((long long)kChunk, sp.len - (long long)c * kChunk);
             if (c) wait_phase(&bar.v_empty, (c - 1) & 1, gave_up);
             if (*gave_up) break;
@@ -256,12 +273,19 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             const int k0 = half * (KP / 2) + 16 * b;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                x[0][i] = a.h0 != nullptr && k0 + i < a.s.k && v < a.s.v ? a.h0[state + (size_t)(k0 + i) * a.s.v + v] : 0.f;
+                x[0][i] = matrix ? (k0 + i == v ? 1.f : 0.f)
+                          : from && k0 + i < a.s.k && v < a.s.v ? from[(size_t)(k0 + i) * a.s.v + v]
+                                                                : 0.f;
             tmem_st16(at + kColS + k0, x[0]);
         }
         tmem_wait_st();
         // this half's values of a chunk; rows past the sequence's end and values past V hold anything and count as 0
-        auto values = [&](int c) {
+        auto fetch = [&](int c) {
+            if (matrix) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i >> 4][i & 15] = 0.f;
+                return;
+            }
             const T *vp = reinterpret_cast<const T *>(smem + M::kV) + 32 * half * kBlockV + row;
             const int n = v < a.s.v ? (int)min((long long)kChunk, sp.len - (long long)c * kChunk) - 32 * half : 0;
             wait_phase(&bar.v_full, c & 1, gave_up);
@@ -273,14 +297,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                     if (i >= n) y[i >> 4][i & 15] = 0.f;
             warp_arrive(&bar.v_empty, lane);
         };
-        if (chunks > 0) values(0);
+        if (chunks > 0) fetch(0);
         for (int c = 0; c < chunks; ++c) {
             const int st = c % M::kStages;
             const float *scal = reinterpret_cast<const float *>(smem + M::kScal + st * 3 * kChunk * 4) + 32 * half;
             wait_phase(&bar.full[st], (c / M::kStages) & 1, gave_up);
             const float eall = scal[kChunk - 1 - 32 * half];
             if (c > 0) {
-                if (a.train) wait_phase(&bar.u_free, (c - 1) & 1, gave_up);
+                if (keep) wait_phase(&bar.u_free, (c - 1) & 1, gave_up);
                 wait_phase(&bar.s_done, (c - 1) & 1, gave_up);
                 tmem_fence_after();
             }
@@ -295,9 +319,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                     tmem_st8(at + kColSLo + 8 * (k16 + b), lo);
                     scale16(x[b], eall);
                     tmem_st16(at + kColS + 16 * (k16 + b), x[b]);
-                    if (a.train) keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
+                    if (keep) keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
                 }
-                if (a.train) fence_async();
+                if (keep) fence_async();
                 tmem_wait_st();
                 tmem_fence_before();
                 warp_arrive(&bar.s_ready[r], lane);
@@ -317,7 +341,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                     const float2 y0 = mul2(make_float2(be.x, be.y), r0), y1 = mul2(make_float2(be.z, be.w), r1);
                     x[b][i] = y0.x; x[b][i + 1] = y0.y; x[b][i + 2] = y1.x; x[b][i + 3] = y1.y;
                 }
-            if (c > 0) wait_phase(&bar.o_done, (c - 1) & 1, gave_up);   // the last chunk's U was there
+            if (c > 0 && !states) wait_phase(&bar.o_done, (c - 1) & 1, gave_up);   // the last chunk's U was there
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 split16(x[b], hi, lo);
@@ -327,9 +351,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             tmem_wait_st();
             tmem_fence_before();
             warp_arrive(&bar.r_ready, lane);
-            if (c + 1 < chunks) values(c + 1);
+            if (c + 1 < chunks) fetch(c + 1);
 
-            if (c > 0) wait_phase(&bar.o_read, (c - 1) & 1, gave_up);   // the last outputs were where the next pair goes
+            if (c > 0 && !states) wait_phase(&bar.o_read, (c - 1) & 1, gave_up);   // the last outputs were where the next pair goes
             wait_phase(&bar.u_done, c & 1, gave_up);
             tmem_fence_after();
             {
@@ -353,30 +377,44 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             tmem_wait_st();
             tmem_fence_before();
             warp_arrive(&bar.w_ready, lane);
-            if (a.train) wait_phase(&bar.s_free, c & 1, gave_up);
+            if (states) continue;
+            if (keep) wait_phase(&bar.s_free, c & 1, gave_up);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 split16(x[b], hi, lo);
                 tmem_st8(at + kColR + 16 * half + 8 * b, hi);
                 tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
-                if (a.train) keep16(base + M::kSave, kHalf, row, 2 * half + b, hi, lo);
+                if (keep) keep16(base + M::kSave, kHalf, row, 2 * half + b, hi, lo);
             }
-            if (a.train) fence_async();
+            if (keep) fence_async();
             tmem_wait_st();
             tmem_fence_before();
             warp_arrive(&bar.u_ready, lane);
         }
-        if (a.ht != nullptr) {   // the state at the end
+        if (to_state || matrix) {   // the state at the end
             if (chunks > 0) wait_phase(&bar.s_done, (chunks - 1) & 1, gave_up);
             tmem_fence_after();
+            unsigned char *m = a.seg_m + (size_t)(chain.slot * a.s.hv + head) * seg_m_bytes(a.s.k);
 #pragma unroll 1
             for (int b = 0; b < KP / 32; ++b) {
                 const int k0 = half * (KP / 2) + 16 * b;
                 tmem_ld16(x[0], at + kColS + k0);
+                if (*gave_up)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k0 + i < a.s.k && v < a.s.v)
-                        a.ht[state + (size_t)(k0 + i) * a.s.v + v] = *gave_up ? __int_as_float(0x7fffffff) : x[0][i];
+                    for (int i = 0; i < 16; ++i) x[0][i] = __int_as_float(0x7fffffff);
+                if (matrix) {
+                    split16(x[0], hi, lo);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const uint32_t to = img(0, row, k0 / 8 + p);
+                        *reinterpret_cast<uint4 *>(m + to) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+                        *reinterpret_cast<uint4 *>(m + KH * kHalf + to) = make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (k0 + i < a.s.k && v < a.s.v) to_state[(size_t)(k0 + i) * a.s.v + v] = x[0][i];
+                }
             }
         }
     } else if (warp >= kFirstOut) {
@@ -384,7 +422,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
         const uint32_t at = (uint32_t)(warp & 3) << 21;
         const size_t ostride = (size_t)a.s.hv * a.s.v;
         const bool rows_out = (a.s.v * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 15) == 0;
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c < chunks && !states; ++c) {
             const int st = c % M::kStages;
             const float *scal = reinterpret_cast<const float *>(smem + M::kScal + st * 3 * kChunk * 4);
             const int n = (int)min((long long)kChunk, sp.len - (long long)c * kChunk);
@@ -447,7 +485,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
     }
     tmem_fence_before();
     __syncthreads();
-    if (*gave_up && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the outputs are not what they should be: say so
+    if (*gave_up && !states && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the outputs are not what they should be: say so
         for (long long t = 0; t < sp.len; ++t)
             static_cast<T *>(a.o)[((size_t)(sp.first + t) * a.s.hv + head) * a.s.v + v0 + threadIdx.x] =
                 from_f32<T>(__int_as_float(0x7fffffff));
@@ -460,10 +498,11 @@ namespace {
 template <typename T, int KP>
 cudaError_t chain(const DeltaArgs &a, cudaStream_t s) {
     using M = ChainSmem<T, KP>;
-    const int bytes = a.train ? M::kTrainBytes : M::kBytes;
+    const bool states = a.pass == kPassStates;
+    const int bytes = a.train && !states ? M::kTrainBytes : M::kBytes;
     cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kTrainBytes);
     if (e != cudaSuccess) return e;
-    const long long ctas = a.s.seqs * a.s.hv * blocks_v(a.s.v);
+    const long long ctas = (a.seg ? a.seg_slots : a.s.seqs) * a.s.hv * (blocks_v(a.s.v) + states);
     delta_chain_kernel<T, KP><<<(unsigned)ctas, kChainThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }

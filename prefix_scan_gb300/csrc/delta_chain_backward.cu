@@ -11,7 +11,8 @@
 // are the 128 rows of the accumulators, left operands go through registers back
 // into tensor memory, right operands are the images in shared memory.  P^T dO
 // runs while dS' is on its way through registers, scale (exp(G) Q)^T dO while Y
-// is; dO becomes a left operand while the state's product runs.
+// is; dO becomes a left operand while the state's product runs.  Segments and their
+// two passes are as there.
 #include "delta_tmem.cuh"
 
 namespace ps {
@@ -53,15 +54,26 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     volatile int *gave_up = &bar.gave_up;
     const uint32_t base = smem_addr(smem);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be uniform
+    const bool states = a.pass == kPassStates;   // of segments, without the gradients of values
     const int blocks = blocks_v(a.s.v), rep = a.s.hv / a.s.hk;
     const int vb = (int)(blockIdx.x % blocks);
     const int head = (int)(blockIdx.x / blocks % a.s.hv);
-    const long long seq = blockIdx.x / blocks / a.s.hv;
-    const Span sp = span_of(a.s, seq);
+    Chain chain;
+    if (!chain_of(a, blockIdx.x / blocks / a.s.hv, chain)) return;
+    if (states && chain.first) return;   // nobody needs it
+    const long long seq = chain.seq;
+    const Span sp = chain.span;
     const int v0 = vb * kBlockV;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
     const int chunks = (int)((sp.len + kChunk - 1) / kChunk);
-    const size_t state = (size_t)(seq * a.s.hv + head) * a.s.k * a.s.v;
+    // the gradient at the end and where it goes at the start
+    const size_t one_state = (size_t)a.s.k * a.s.v;
+    const float *from = chain.last ? (a.dht ? a.dht + (size_t)(seq * a.s.hv + head) * one_state : nullptr)
+                        : states  ? nullptr
+                                  : a.seg_state + (size_t)((chain.slot + 1) * a.s.hv + head) * one_state;
+    float *to_state = states ? a.seg_state + (size_t)(chain.slot * a.s.hv + head) * one_state
+                      : chain.first && a.dh0 ? a.dh0 + (size_t)(seq * a.s.hv + head) * one_state
+                                             : nullptr;
     // chunks are taken last to first: i counts them as they come
     auto chunk_ws = [&](int i) { return a.ws + (size_t)((sp.slot + chunks - 1 - i) * a.s.hv + head) * lay.stride; };
     auto first_token = [&](int i) { return (long long)(chunks - 1 - i) * kChunk; };
@@ -171,7 +183,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         mma_commit(one, &bar.drained);
         wait_drained(&bar.drained, 0);
     } else if (warp == 1) {
-        if (lane == 0) {   // dS' and dU for the gradients
+        if (lane == 0 && !states) {   // dS' and dU for the gradients
             const int rows = min(kBlockV, (a.s.v - v0 + 15) / 16 * 16);
             for (int i = 0; i < chunks; ++i) {
                 unsigned char *w = chunk_ws(i);
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
             const int k0 = half * (KP / 2) + 16 * b;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                x[0][i] = a.dht != nullptr && k0 + i < a.s.k && v < a.s.v ? a.dht[state + (size_t)(k0 + i) * a.s.v + v] : 0.f;
+                x[0][i] = from && k0 + i < a.s.k && v < a.s.v ? from[(size_t)(k0 + i) * a.s.v + v] : 0.f;
             tmem_st16(at + kColS + k0, x[0]);
         }
         tmem_wait_st();
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
             const float *scal = scalars(i);
             const float eall = scal[kChunk - 1 - 32 * half];
             if (i > 0) {
-                wait_phase(&bar.u_free, (i - 1) & 1, gave_up);
+                if (!states) wait_phase(&bar.u_free, (i - 1) & 1, gave_up);
                 wait_phase(&bar.s_done, (i - 1) & 1, gave_up);
                 tmem_fence_after();
             }
@@ -299,9 +311,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
                     tmem_st8(at + kColSLo + 8 * (k16 + b), lo);
                     scale16(x[b], eall);
                     tmem_st16(at + kColS + 16 * (k16 + b), x[b]);
-                    keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
+                    if (!states) keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
                 }
-                fence_async();
+                if (!states) fence_async();
                 tmem_wait_st();
                 tmem_fence_before();
                 warp_arrive(&bar.s_ready[r], lane);
@@ -359,6 +371,10 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
             tmem_fence_before();
             warp_arrive(&bar.w_ready, lane);
             // dU, and dV = beta dU by rows
+            if (states) {
+                if (i + 1 < chunks) outputs(i + 1);
+                continue;
+            }
             wait_phase(&bar.s_free, i & 1, gave_up);
             if (i > 0) wait_phase(&bar.out_free, (i - 1) & 1, gave_up);
             T *stage = reinterpret_cast<T *>(smem + M::kOut) + 32 * half * kBlockV + row;
@@ -374,7 +390,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
             warp_arrive(&bar.out_ready, lane);
             if (i + 1 < chunks) outputs(i + 1);
         }
-        if (a.dh0 != nullptr) {
+        if (to_state) {
             if (chunks > 0) wait_phase(&bar.s_done, (chunks - 1) & 1, gave_up);
             tmem_fence_after();
 #pragma unroll 1
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (k0 + i < a.s.k && v < a.s.v)
-                        a.dh0[state + (size_t)(k0 + i) * a.s.v + v] = *gave_up ? __int_as_float(0x7fffffff) : x[0][i];
+                        to_state[(size_t)(k0 + i) * a.s.v + v] = *gave_up ? __int_as_float(0x7fffffff) : x[0][i];
             }
         }
     } else {
@@ -392,7 +408,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         const size_t ostride = (size_t)a.s.hv * a.s.v;
         const int cols = min(kBlockV, a.s.v - v0);
         const bool rows_out = (a.s.v * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dv) & 15) == 0;
-        for (int i = 0; i < chunks; ++i) {
+        for (int i = 0; i < chunks && !states; ++i) {
             const int n = rows_of(i);
             T *out = static_cast<T *>(a.dv) + ((size_t)(sp.first + first_token(i)) * a.s.hv + head) * a.s.v + v0;
             const T *stage = reinterpret_cast<const T *>(smem + M::kOut);
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     }
     tmem_fence_before();
     __syncthreads();
-    if (*gave_up && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the gradients are not what they should be: say so
+    if (*gave_up && !states && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the gradients are not what they should be: say so
         for (long long t = 0; t < sp.len; ++t)
             static_cast<T *>(a.dv)[((size_t)(sp.first + t) * a.s.hv + head) * a.s.v + v0 + threadIdx.x] =
                 from_f32<T>(__int_as_float(0x7fffffff));
@@ -429,7 +445,7 @@ cudaError_t chain_back(const DeltaArgs &a, cudaStream_t s) {
     static_assert(bytes <= 227 * 1024, "too much shared memory");
     cudaError_t e = cudaFuncSetAttribute(delta_chain_backward_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const long long ctas = a.s.seqs * a.s.hv * blocks_v(a.s.v);
+    const long long ctas = (a.seg ? a.seg_slots : a.s.seqs) * a.s.hv * blocks_v(a.s.v);
     delta_chain_backward_kernel<T, KP><<<(unsigned)ctas, kBackThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }

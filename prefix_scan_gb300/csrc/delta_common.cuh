@@ -221,17 +221,6 @@ __device__ __forceinline__ void load_part(uint32_t dst, const void *src, int byt
     if (bytes == MOST) return load_image<MOST, THREADS>(dst, src, tid);
     for (int i = tid * 16; i < bytes; i += THREADS * 16) cp_async16(dst + i, static_cast<const char *>(src) + i, true);
 }
-// Stores BYTES of an image from shared memory by one warp.
-template <int BYTES>
-__device__ __forceinline__ void store_image(void *dst, const void *src, int lane) {
-#pragma unroll
-    for (int i = 0; i < BYTES / 512; ++i)
-        static_cast<uint4 *>(dst)[i * 32 + lane] = static_cast<const uint4 *>(src)[i * 32 + lane];
-}
-// Named barriers between a pair of warps: one announces, the other waits.
-__device__ __forceinline__ void announce(int id) { asm volatile("bar.arrive %0, 64;" :: "r"(id) : "memory"); }
-__device__ __forceinline__ void await(int id) { asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory"); }
-
 // ---- sequences and chunks ----------------------------------------------------------
 
 // Where a sequence's tokens lie.  Offsets that do not increase, or that leave
@@ -273,6 +262,35 @@ __device__ __forceinline__ long long seq_of_slot(const DeltaShape &s, long long 
     }
     const Span p = span_of(s, lo);
     return slot >= p.slot && slot - p.slot < (p.len + kChunk - 1) / kChunk ? lo : -1;
+}
+// A chain's work: the whole sequence, or one of the segments that it is cut into (span then is the
+// segment's alone).
+struct Chain {
+    long long seq, slot;   // slot: of the segment
+    bool first, last;      // first, last segment of its sequence
+    Span span;
+};
+__device__ __forceinline__ long long first_segment(const DeltaArgs &a, long long seq) { return span_of(a.s, seq).slot / a.seg + seq; }
+__device__ __forceinline__ bool chain_of(const DeltaArgs &a, long long index, Chain &c) {
+    if (a.seg == 0) {
+        c = Chain{index, 0, true, true, span_of(a.s, index)};
+        return true;
+    }
+    long long lo = 0, hi = a.s.seqs - 1;   // the last sequence whose first segment is <= index
+    while (lo < hi) {
+        const long long mid = (lo + hi + 1) / 2;
+        if (first_segment(a, mid) <= index) lo = mid; else hi = mid - 1;
+    }
+    const Span all = span_of(a.s, lo);
+    const long long part = index - first_segment(a, lo), tokens = (long long)a.seg * kChunk;
+    const long long parts = all.len > 0 ? (all.len + tokens - 1) / tokens : 1;
+    if (part < 0 || part >= parts) return false;
+    c = Chain{lo, index, part == 0, part == parts - 1, all};
+    c.span.first += part * tokens;
+    c.span.at += part * tokens;
+    c.span.slot += part * a.seg;
+    c.span.len = all.len - part * tokens < tokens ? all.len - part * tokens : tokens;
+    return true;
 }
 template <typename T>
 __device__ __forceinline__ const T *row_ptr(const DeltaTensor &t, const Span &sp, long long seq, long long tok, int head) {

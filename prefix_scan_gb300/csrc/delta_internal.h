@@ -72,6 +72,16 @@ constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
     return packed ? tokens / kChunk + seqs : seqs * ((tokens + kChunk - 1) / kChunk);
 }
 
+// Long sequences over few heads are cut into segments of `seg` chunks, so that more CTAs have a
+// chain to run.  The state at a segment's end is M S + B, S the state at its start, M a K x K matrix:
+// a first pass runs the segments' chains without outputs, B from S = 0 and M as the chain of K
+// values that start from the identity and add nothing; a join goes through the segments in order
+// (delta_join.cu); a second pass runs every segment from its own start.  The backward pass does the
+// same from the other end, with M's transpose.
+//   seg_state  [segment slots + 1, hv, K, V] f32: the state at each segment's start; backward, its
+//              gradient at each segment's end (one slot further on)
+//   seg_m      [segment slots, hv] pairs of images of M (row j, column k: M_kj), as S's
+enum DeltaPass { kPassAll = 0, kPassStates = 1 };
 struct DeltaArgs {
     DeltaShape s;
     DeltaTensor q, k, v, g, beta;
@@ -83,6 +93,11 @@ struct DeltaArgs {
     unsigned char *ws, *kq;
     long long slots;
     int train;                    // keep what the backward pass reads
+    int seg;                      // chunks of a segment, 0: sequences are not cut
+    int pass;
+    long long seg_slots;
+    float *seg_state;
+    unsigned char *seg_m;
     // backward
     DeltaTensor dout;
     int vec_do;
@@ -95,7 +110,27 @@ struct DeltaArgs {
 cudaError_t launch_delta_prepare(const DeltaArgs &a, int type, cudaStream_t s);
 cudaError_t launch_delta_chain(const DeltaArgs &a, int type, cudaStream_t s);
 cudaError_t launch_delta_chain_backward(const DeltaArgs &a, int type, cudaStream_t s);
+cudaError_t launch_delta_join(const DeltaArgs &a, bool backward, cudaStream_t s);
 cudaError_t launch_delta_gradients(const DeltaArgs &a, int type, cudaStream_t s);
+
+constexpr size_t seg_m_bytes(int k) { return 2 * s_plane(k); }
+// Chunks of a segment, for `chains` chains of `chunks` chunks on average; 0 where cutting does not pay.
+// A chain takes a CTA, of which 152 run at once.  n segments cost the waves of the first pass (n - 1
+// chains for B, n - 2 for M) and of the second, in chunks of time, and about a chunk's time for each
+// step of the join; the backward pass has no M to find.
+inline int segment_chunks(long long chains, long long chunks, bool train) {
+    if (chains <= 0 || chunks < 8) return 0;
+    auto waves = [](long long ctas) { return (ctas + 151) / 152; };
+    long long best = chunks * waves(chains) * (train ? 2 : 1), best_len = 0;
+    for (long long n = 3; n <= 64 && n * 4 <= chunks; ++n) {
+        const long long len = (chunks + n - 1) / n;
+        long long cost = len * (waves(chains * (2 * n - 3)) + waves(chains * n)) + n;
+        if (train) cost += len * (waves(chains * (n - 1)) + waves(chains * n)) + n;
+        if (cost < best) { best = cost; best_len = len; }
+    }
+    return (int)best_len;
+}
+constexpr long long segment_slots(long long slots, long long seqs, int seg) { return seg ? slots / seg + seqs : 0; }
 
 struct DeltaStepArgs {
     long long seqs, pages;

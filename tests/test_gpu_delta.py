@@ -89,6 +89,18 @@ def test_long_memory_and_long_sequence():
     near(last, want["state"], CHUNKED)
 
 
+@pytest.mark.parametrize("dtype,k,v", [(BF16, 128, 128), (F32, 64, 64), (F16, 80, 136), (BF16, 64, 40)])
+@pytest.mark.parametrize("lens", [[1900], [2000, 900, 0, 1500], [3000, 1, 1, 3000]])
+def test_sequences_cut_into_segments(dtype, k, v, lens):
+    # few heads and many chunks: the states at the segments' starts come from a first pass and a join
+    x = inputs(sum(lens), 1, 2, k, v, dtype, 7, decay=0.05)
+    h0 = states(len(lens), 2, k, v, 8)
+    o, last = api.delta_rule(*x, cu_seqlens=cu_of(lens), initial_state=h0, output_final_state=True)
+    want = ref.packed(*x, k ** -0.5, lens, h0)
+    near(o, want["o"], CHUNKED)
+    near(last, want["state"], CHUNKED)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_strides_and_alignment(dtype):
     T, hk, hv, k, v = 150, 2, 4, 64, 64

@@ -65,6 +65,14 @@ def test_lengths(tokens):
     check(inputs(tokens, 2, 4, 128, 128, BF16, tokens, beta_dtype=F32), [tokens], scale=0.5)
 
 
+@pytest.mark.parametrize("dtype,k,v", [(BF16, 128, 128), (F32, 64, 64), (F16, 80, 136)])
+@pytest.mark.parametrize("lens", [[1900], [2000, 900, 0, 1500]])
+def test_sequences_cut_into_segments(dtype, k, v, lens):
+    n = len(lens)
+    x = inputs(sum(lens), 1, 2, k, v, dtype, 7, decay=0.05)
+    check(x, lens, states(n, 2, k, v, 8), states(n, 2, k, v, 9))
+
+
 def test_batch_layout_and_strided_gradient():
     x = inputs(100, 1, 2, 64, 64, BF16, 21, seqs=3)
     do, _, _, saved, got = gradients(x)
