@@ -1,453 +1,506 @@
 // delta_gradients.cu -- the gradients of the gated delta rule's queries, keys,
 // gates and log decays, all chunks at once, from what the two chains left
 // (notation in delta_common.cuh and delta_chain_backward.cu).  Per chunk and
-// value head, with dP = dO U^T and dN = -dR U^T (j < i only):
+// value head, with dP = dO U^T and dN = -dR U^T (j < i only), dR = diag(beta) dU:
 //     dQ = scale diag(exp(G)) dO S^T + (scale D dP) K
 //     dK = (scale D dP)^T Q + (D dN) K + (D dN)^T K - diag(exp(G)) dR S^T + diag(exp(G_C - G)) U dS'^T
 //     dbeta_j = (dU_j . U_j) / beta_j          (U = beta (what was missing))
 //     dg_t = sum_{j < t <= i} Z_ij + sum_{i >= t} a_i + sum_{j < t} b_j + exp(G_C) <S, dS'>
 // where Z = P dP + N dN (element by element), a_i = exp(G_i) (scale q_i . S dO_i -
-// k_i . S dR_i) and b_j = exp(G_C - G_j) k_j . dS' U_j: every term that the decay of token t scales,
-// each counted once, so nothing cancels.
+// k_i . S dR_i) and b_j = exp(G_C - G_j) k_j . dS' U_j: every term that the decay of
+// token t scales, each counted once, so nothing cancels.
 //
-// One CTA per chunk and key head: gradients of a shared key head are sums over its
-// value heads in their order, in registers, without atomics.
-#include "delta_common.cuh"
+// One CTA takes a chunk and key head at a time, and goes on to another: gradients of a
+// shared key head are sums over its value heads in their order, without atomics.
+// The products run on tensor memory with both operands in shared memory, as the images
+// lie there, transposed so that keys' columns are the 128 rows:
+//     X1 = S dO^T, X2 = S dU^T, X3 = dS' U^T           (columns: tokens)
+// and, U's two parts one above the other as 128 rows, U dO^T and U dU^T.  One warp
+// issues them, one loads (64 values at a time, 32 where inputs are pairs; on into the
+// next item while the last one is being finished), sixteen take them apart: a lane per
+// column of the keys, or per token j, a quarter of the tokens i each.
+#include "delta_tmem.cuh"
 
 namespace ps {
 
 namespace {
 
-constexpr int kGradThreads = 512;   // sixteen warps: 16 rows and a quarter of the columns each
-constexpr int kGradV = 32;          // values taken at a time
-constexpr int kSlice = kGradV * 128;   // bytes of 64 columns of a block of the state
+constexpr int kGradWarps = 16, kGradThreads = 32 * (kGradWarps + 2);
 constexpr int kZStride = kChunk + 1;
+// Tensor-memory columns: X1, X2, X3, U dO^T, U dU^T (dU's two parts side by side), the products of
+// F that go to dQ and to dK (and before them [K; Q] [K; Q]^T)
+constexpr uint32_t kColX = 0, kColP = 192, kColN = 256, kColF = 384;
 
 template <int NP, int KP>
 struct GradSmem {
-    static constexpr int kKQ = (KP / 64) * kHalf, kSP = kGradV * KP * 2, kUP = kGradV * kChunk * 2, kOP = kChunk * 128;   // planes
-    static constexpr int kK = 0, kQ = kChunk * 128;
-    // a stage: S, dS', U, dU, dO of the values taken at a time
-    static constexpr int kS = 0, kDS = kS + 2 * kSP, kU = kDS + 2 * kSP, kDU = kU + 2 * kUP, kO = kDU + 2 * kUP, kStage = kO + NP * kOP;
-    static constexpr int kStages = NP == 1 ? 2 : 1, kFirst = NP * kKQ;
-    static constexpr int kF1 = kFirst + kStages * kStage, kF2 = kF1 + 2 * (int)kSquare, kZ = kF2 + 2 * (int)kSquare;
-    static constexpr int kScal = kZ + kChunk * kZStride * 4, kMore = kScal + 2 * 6 * kChunk * 4;   // scalars of two heads
-    static constexpr int kBytes = kMore + (4 * kChunk + 4 * kChunk + 4 * kChunk + kChunk + 16) * 4;
+    static constexpr int kV = NP == 1 ? 64 : 32, kSlice = kV * 128;   // values taken at a time, bytes of 64 columns of them
+    static constexpr int kKQ = (KP / 64) * kHalf, kSP = (KP / 64) * kSlice, kOP = kChunk * 128;   // planes
+    // of a slice: U, dU (pairs), dO; S, dS' (pairs)
+    static constexpr int kU = NP * kKQ, kDU = kU + 2 * kSlice, kO = kDU + 2 * kSlice, kS = kO + NP * kOP, kDS = kS + 2 * kSP;
+    static constexpr int kF1 = kDS + 2 * kSP, kF2 = kF1 + 2 * (int)kSquare;   // pairs; before them what lanes j and 64 + j exchange
+    static constexpr int kZ = kF2 + 2 * (int)kSquare, kKK = kZ + kChunk * kZStride * 4;
+    static constexpr int kScal = (kKK + 2 * kChunk * kChunk * 4 + 15) / 16 * 16, kMore = kScal + 2 * 6 * kChunk * 4;   // scalars of two heads
+    static constexpr int kBars = kMore + (4 * kChunk + 4 * kChunk + 4 * kChunk + kChunk + 16) * 4;
+    static constexpr int kBytes = kBars + 512;
     static_assert(kBytes <= 227 * 1024, "too much shared memory");
 };
+struct GradItem {          // a chunk and key head
+    long long token;         // its first token, among all of them
+    int head_k, rows;        // rows 0: there are no more items
+};
+struct GradBars {
+    uint64_t item_full[2], item_empty[2], u_full, u_empty, s_full, s_empty, kq_full, kq_empty, scal_full[2], scal_empty[2];
+    uint64_t x_done, acc_free, f_ready, f_done, drained;
+    GradItem item[2];
+    uint32_t tmem;
+    int gave_up;
+};
+static_assert(sizeof(GradBars) <= 512, "room for the barriers");
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" :: "n"(32 * kGradWarps) : "memory"); }   // the sixteen warps
+
+// Sums of 16 numbers each over the warp: lane l ends up with the l / 2-th.
+__device__ __forceinline__ float sum16(float (&x)[16], int lane) {
+#pragma unroll
+    for (int step = 8, m = 16; step >= 1; step >>= 1, m >>= 1) {
+        const bool high = lane & m;
+#pragma unroll
+        for (int i = 0; i < step; ++i) {
+            const float send = high ? x[i] : x[i + step], keep = high ? x[i + step] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+    }
+    return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
 
 }  // namespace
 
 template <typename T, int KP>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const DeltaArgs a) {
-    constexpr int NP = Planes<T>::NP, NQ = KP / 32, KH = KP / 64;   // NQ: column tiles of a quarter of a row
+    constexpr int NP = Planes<T>::NP, KH = KP / 64;
     using M = GradSmem<NP, KP>;
+    constexpr int kGradV = M::kV, kSlice = M::kSlice;
     extern __shared__ __align__(1024) unsigned char smem[];
+    GradBars &bar = *reinterpret_cast<GradBars *>(smem + M::kBars);
+    volatile int *gave_up = &bar.gave_up;
     const uint32_t base = smem_addr(smem);
-    float *Z = reinterpret_cast<float *>(smem + M::kZ);
-    float *dots = reinterpret_cast<float *>(smem + M::kMore);   // [4 quarters of the columns][64] of a_i
-    float *dotb = dots + 4 * kChunk;                            // the same of b_j
-    float *run = dotb + 4 * kChunk;                             // [4 quarters of the rows][64] column sums of Z
-    float *diag = run + 4 * kChunk;                             // [64] dU_j . U_j
-    float *inner = diag + kChunk;                               // <S, dS'> by warps
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int strip = warp & 3, quarter = warp >> 2;   // rows 16 strip.., this quarter of the columns
-    const int r8 = lane >> 2, c2 = 2 * (lane & 3), i0 = 16 * strip + r8;
-    const long long slot = blockIdx.x;
-    const int head_k = blockIdx.y, rep = a.s.hv / a.s.hk;
-
-    const long long seq = seq_of_slot(a.s, slot);
-    if (seq < 0) return;
-    const Span sp = span_of(a.s, seq);
-    const long long t0 = (slot - sp.slot) * kChunk;
-    const int rows = (int)min((long long)kChunk, sp.len - t0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be uniform
+    const int rep = a.s.hv / a.s.hk;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
     const int vpad = (a.s.v + 15) / 16 * 16;
 
-    load_image<NP * M::kKQ, kGradThreads>(base + M::kK, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), tid);
-
-    // all value heads' values, kGradV at a time, in one sequence of stages
-    const int slices = (vpad + kGradV - 1) / kGradV;
-    auto load = [&](int it) {
-        const int head = head_k * rep + it / slices, v0 = it % slices * kGradV, vr = min(kGradV, vpad - v0);
-        const int vb = v0 / kBlockV, vi = v0 % kBlockV;
-        const uint32_t st = base + M::kFirst + it % M::kStages * M::kStage;
-        const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-#pragma unroll
-            for (int h = 0; h < KH; ++h) {
-                const size_t from = ((size_t)(vb * 2 + p) * KH + h) * kHalf + vi * 128;
-                load_part<kSlice, kGradThreads>(st + M::kS + p * M::kSP + h * kSlice, w + lay.s + from, vr * 128, tid);
-                load_part<kSlice, kGradThreads>(st + M::kDS + p * M::kSP + h * kSlice, w + lay.ds + from, vr * 128, tid);
-            }
-            const size_t from = (size_t)(vb * 2 + p) * kHalf + vi * 128;
-            load_part<M::kUP, kGradThreads>(st + M::kU + p * M::kUP, w + lay.u + from, vr * 128, tid);
-            load_part<M::kUP, kGradThreads>(st + M::kDU + p * M::kUP, w + lay.du + from, vr * 128, tid);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.item_full[i], 1);
+            mbar_init(&bar.item_empty[i], kGradWarps + 1);
+            mbar_init(&bar.scal_full[i], 1);
+            mbar_init(&bar.scal_empty[i], kGradWarps);
         }
-        load_tile<T, kGradV>(st + M::kO, M::kOP, row_ptr<T>(a.dout, sp, seq, t0, head) + v0, a.dout.tok, rows, a.s.v - v0,
-                             a.vec_do != 0, tid, kGradThreads);
-        if (v0 == 0) load_image<6 * kChunk * 4, kGradThreads>(base + M::kScal + (it / slices & 1) * 6 * kChunk * 4, w + lay.scal, tid);
-        cp_async_commit();
-    };
-    load(0);
-
-    float dq[NQ][4], dk[NQ][4];   // rows i0 (+8), columns 8 (quarter NQ + n) + c2 (+1)
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dq[n][e] = dk[n][e] = 0.f;
-
-    for (int hr = 0; hr < rep; ++hr) {
-        const int head = head_k * rep + hr;
-        const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
-        const float *scal = reinterpret_cast<const float *>(smem + M::kScal + (hr & 1) * 6 * kChunk * 4);
-        float pa[2][4], na[2][4];                     // dP and dU U^T: columns 16 quarter + 8 n..
-        float x1[NQ][4], x2[NQ][4], x3[NQ][4];        // dO S^T, dU S^T, U dS'^T
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pa[n][e] = na[n][e] = 0.f;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x1[n][e] = x2[n][e] = x3[n][e] = 0.f;
-        float prod = 0.f;   // this thread's part of <S, dS'>
-
-        for (int s = 0; s < slices; ++s) {
-            const int it = hr * slices + s, vr = min(kGradV, vpad - s * kGradV);
-            const uint32_t st = base + M::kFirst + it % M::kStages * M::kStage;
-            cp_async_wait<0>();
-            __syncthreads();
-            if (M::kStages == 2 && it + 1 < rep * slices) load(it + 1);
-
-            const unsigned char *sp8 = smem + (st - base);
-            for (int i = tid; i < kGradV * KP / 8; i += kGradThreads) {   // the same place in all four images
-                if (i % (kGradV * 8) >= vr * 8) continue;   // not loaded
-                const uint4 *sv = reinterpret_cast<const uint4 *>(sp8 + M::kS) + i;
-                const uint4 *dv = reinterpret_cast<const uint4 *>(sp8 + M::kDS) + i;
-                const uint4 sh = sv[0], sl = sv[M::kSP / 16], dh = dv[0], dl = dv[M::kSP / 16];
-                const uint32_t *shp = &sh.x, *slp = &sl.x, *dhp = &dh.x, *dlp = &dl.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    prod += (bf16_low(shp[j]) + bf16_low(slp[j])) * (bf16_low(dhp[j]) + bf16_low(dlp[j]));
-                    prod += (bf16_high(shp[j]) + bf16_high(slp[j])) * (bf16_high(dhp[j]) + bf16_high(dlp[j]));
-                }
-            }
-            for (int kt = 0; kt < vr / 16; ++kt) {
-                {   // dO: dP and dO S^T
-                    uint32_t f[NP][4];
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) load_a(f[p], st + M::kO + p * M::kOP, 16 * strip, 16 * kt, lane);
-                    if (quarter <= strip)   // columns at or before the rows
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            uint32_t b[4];
-                            load_b_t(b, st + M::kU + p * M::kUP, 16 * kt, 16 * quarter, lane);
-#pragma unroll
-                            for (int h = 0; h < NP && h + p < 2; ++h) {
-                                mma_bf16(pa[0], f[h], b[0], b[1]);
-                                mma_bf16(pa[1], f[h], b[2], b[3]);
-                            }
-                        }
-#pragma unroll
-                    for (int np = 0; np < NQ / 2; ++np)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            uint32_t b[4];
-                            load_b_t<kSlice>(b, st + M::kS + p * M::kSP, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
-#pragma unroll
-                            for (int h = 0; h < NP && h + p < 2; ++h) {
-                                mma_bf16(x1[2 * np], f[h], b[0], b[1]);
-                                mma_bf16(x1[2 * np + 1], f[h], b[2], b[3]);
-                            }
-                        }
-                }
-                {   // dU: dU U^T and dU S^T
-                    uint32_t f[2][4];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) load_a_t(f[p], st + M::kDU + p * M::kUP, 16 * kt, 16 * strip, lane);
-                    if (quarter <= strip)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            uint32_t b[4];
-                            load_b_t(b, st + M::kU + p * M::kUP, 16 * kt, 16 * quarter, lane);
-#pragma unroll
-                            for (int h = 0; h + p < 2; ++h) {
-                                mma_bf16(na[0], f[h], b[0], b[1]);
-                                mma_bf16(na[1], f[h], b[2], b[3]);
-                            }
-                        }
-#pragma unroll
-                    for (int np = 0; np < NQ / 2; ++np)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            uint32_t b[4];
-                            load_b_t<kSlice>(b, st + M::kS + p * M::kSP, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
-#pragma unroll
-                            for (int h = 0; h + p < 2; ++h) {
-                                mma_bf16(x2[2 * np], f[h], b[0], b[1]);
-                                mma_bf16(x2[2 * np + 1], f[h], b[2], b[3]);
-                            }
-                        }
-                }
-                {   // U: U dS'^T
-                    uint32_t f[2][4];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) load_a_t(f[p], st + M::kU + p * M::kUP, 16 * kt, 16 * strip, lane);
-#pragma unroll
-                    for (int np = 0; np < NQ / 2; ++np)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            uint32_t b[4];
-                            load_b_t<kSlice>(b, st + M::kDS + p * M::kSP, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
-#pragma unroll
-                            for (int h = 0; h + p < 2; ++h) {
-                                mma_bf16(x3[2 * np], f[h], b[0], b[1]);
-                                mma_bf16(x3[2 * np + 1], f[h], b[2], b[3]);
-                            }
-                        }
-                }
-            }
-            if (M::kStages == 1) {
-                __syncthreads();
-                if (it + 1 < rep * slices) load(it + 1);
-            }
-        }
-
-        // <S, dS'>, the parts of dQ and dK that go through the states, a_i and b_j
-#pragma unroll
-        for (int m = 16; m; m >>= 1) prod += __shfl_xor_sync(0xffffffffu, prod, m);
-        if (lane == 0) inner[warp] = prod;
-        float dot[2] = {0.f, 0.f}, dob[2] = {0.f, 0.f};
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            const int col = 8 * (quarter * NQ + n) + c2;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {   // rows i0, i0 + 8
-                const int i = i0 + 8 * e;
-                const uint32_t at = img(0, i, col >> 3) + (col & 7) * 2;
-                uint32_t kw = *reinterpret_cast<const uint32_t *>(smem + M::kK + at);
-                uint32_t qw = *reinterpret_cast<const uint32_t *>(smem + M::kQ + at);
-                float k0 = bf16_low(kw), k1 = bf16_high(kw), q0 = bf16_low(qw), q1 = bf16_high(qw);
-                if constexpr (NP == 2) {
-                    kw = *reinterpret_cast<const uint32_t *>(smem + M::kK + M::kKQ + at);
-                    qw = *reinterpret_cast<const uint32_t *>(smem + M::kQ + M::kKQ + at);
-                    k0 += bf16_low(kw); k1 += bf16_high(kw); q0 += bf16_low(qw); q1 += bf16_high(qw);
-                }
-                const float eg = scal[i], el = scal[64 + i], sc = a.s.scale * eg, eb = eg * scal[128 + i];
-                const float y0 = sc * x1[n][2 * e], y1 = sc * x1[n][2 * e + 1];
-                const float z0 = eb * x2[n][2 * e], z1 = eb * x2[n][2 * e + 1];
-                dot[e] += q0 * y0 + q1 * y1 - (k0 * z0 + k1 * z1);
-                const float u0 = el * x3[n][2 * e], u1 = el * x3[n][2 * e + 1];
-                dob[e] += k0 * u0 + k1 * u1;
-                dq[n][2 * e] += y0;
-                dq[n][2 * e + 1] += y1;
-                dk[n][2 * e] += u0 - z0;
-                dk[n][2 * e + 1] += u1 - z1;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], 1);
-            dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], 2);
-            dob[e] += __shfl_xor_sync(0xffffffffu, dob[e], 1);
-            dob[e] += __shfl_xor_sync(0xffffffffu, dob[e], 2);
-            if ((lane & 3) == 0) {
-                dots[quarter * kChunk + i0 + 8 * e] = dot[e];
-                dotb[quarter * kChunk + i0 + 8 * e] = dob[e];
-            }
-        }
-        // F1 = scale D dP, F2 = D dN as pairs, and Z
-        {
-            const int cb = 16 * quarter;   // first column of the block
-            uint32_t f1h[4] = {0, 0, 0, 0}, f1l[4] = {0, 0, 0, 0}, f2h[4] = {0, 0, 0, 0}, f2l[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = q >> 1, row = q & 1, i = i0 + 8 * row, j = cb + 8 * n + c2;
-                float z0 = 0.f, z1 = 0.f;
-                if (cb <= 16 * strip) {
-                    const uint32_t at = img(0, i, j >> 3) + (j & 7) * 2;
-                    const uint32_t ph = *reinterpret_cast<const uint32_t *>(w + lay.p + at);
-                    const uint32_t pl = *reinterpret_cast<const uint32_t *>(w + lay.p + kSquare + at);
-                    const uint32_t nh = *reinterpret_cast<const uint32_t *>(w + lay.n + at);
-                    const uint32_t nl = *reinterpret_cast<const uint32_t *>(w + lay.n + kSquare + at);
-                    float f1[2], f2[2], z[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int c = j + e;
-                        const float dx = (scal[192 + i] - scal[192 + c]) + (scal[256 + i] - scal[256 + c]);
-                        const float D = i >= c && scal[320 + i] == scal[320 + c] ? expf(dx) : 0.f;
-                        const float dp = pa[n][2 * row + e], dn = -scal[128 + i] * na[n][2 * row + e];
-                        if (i == c) diag[i] = na[n][2 * row + e];
-                        const float pv = e ? bf16_high(ph) + bf16_high(pl) : bf16_low(ph) + bf16_low(pl);
-                        const float nv = e ? bf16_high(nh) + bf16_high(nl) : bf16_low(nh) + bf16_low(nl);
-                        f1[e] = i >= c ? a.s.scale * D * dp : 0.f;
-                        f2[e] = i > c ? D * dn : 0.f;
-                        z[e] = i > c ? pv * dp + nv * dn : 0.f;
-                    }
-                    split2(f1[0], f1[1], f1h[q], f1l[q]);
-                    split2(f2[0], f2[1], f2h[q], f2l[q]);
-                    z0 = z[0];
-                    z1 = z[1];
-                }
-                Z[i * kZStride + j] = z0;
-                Z[i * kZStride + j + 1] = z1;
-            }
-            const uint32_t at = img(0, 16 * strip + (lane & 15), (cb >> 3) + (lane >> 4));
-            stsm4(base + M::kF1 + at, f1h[0], f1h[1], f1h[2], f1h[3]);
-            stsm4(base + M::kF1 + (uint32_t)kSquare + at, f1l[0], f1l[1], f1l[2], f1l[3]);
-            stsm4(base + M::kF2 + at, f2h[0], f2h[1], f2h[2], f2h[3]);
-            stsm4(base + M::kF2 + (uint32_t)kSquare + at, f2l[0], f2l[1], f2l[2], f2l[3]);
-        }
-        __syncthreads();
-
-        // dQ += F1 K; dK += F1^T Q + F2 K + F2^T K
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t f1[2][4], f1t[2][4], f2[2][4];
-            const bool down = kt <= strip, up = kt >= strip;   // tokens kt at or before / at or after the rows
-            if (down)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    load_a(f1[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * strip, 16 * kt, lane);
-                    load_a(f2[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * strip, 16 * kt, lane);
-                }
-            if (up)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) load_a_t(f1t[p], base + M::kF1 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
-#pragma unroll
-            for (int np = 0; np < NQ / 2; ++np)
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    uint32_t bk[4], bq[4];
-                    load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
-                    load_b_t(bq, base + M::kQ + p * M::kKQ, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
-#pragma unroll
-                    for (int h = 0; h + p < 2; ++h) {
-                        if (down) {
-                            mma_bf16(dq[2 * np], f1[h], bk[0], bk[1]);
-                            mma_bf16(dq[2 * np + 1], f1[h], bk[2], bk[3]);
-                            mma_bf16(dk[2 * np], f2[h], bk[0], bk[1]);
-                            mma_bf16(dk[2 * np + 1], f2[h], bk[2], bk[3]);
-                        }
-                        if (up) {
-                            mma_bf16(dk[2 * np], f1t[h], bq[0], bq[1]);
-                            mma_bf16(dk[2 * np + 1], f1t[h], bq[2], bq[3]);
-                        }
-                    }
-                }
-            if (up) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) load_a_t(f1t[p], base + M::kF2 + p * (uint32_t)kSquare, 16 * kt, 16 * strip, lane);
-#pragma unroll
-                for (int np = 0; np < NQ / 2; ++np)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint32_t bk[4];
-                        load_b_t(bk, base + M::kK + p * M::kKQ, 16 * kt, 8 * quarter * NQ + 16 * np, lane);
-#pragma unroll
-                        for (int h = 0; h + p < 2; ++h) {
-                            mma_bf16(dk[2 * np], f1t[h], bk[0], bk[1]);
-                            mma_bf16(dk[2 * np + 1], f1t[h], bk[2], bk[3]);
-                        }
-                    }
-            }
-        }
-
-        // sum over i >= t of Z_ij within quarters of 16 rows, then with the quarters below
-        if (tid < 256) {
-            const int j = tid & 63, q = tid >> 6;
-            float s = 0.f;
-#pragma unroll
-            for (int t = 15; t >= 0; --t) {
-                s += Z[(16 * q + t) * kZStride + j];
-                Z[(16 * q + t) * kZStride + j] = s;
-            }
-            run[q * kChunk + j] = s;
-        }
-        __syncthreads();
-        {   // row t: sum over j < t (eight threads a row)
-            const int t = tid >> 3, part = tid & 7;
-            float s = 0.f;
-            for (int j = part; j < t; j += 8) {
-                s += Z[t * kZStride + j];
-                for (int q = (t >> 4) + 1; q < 4; ++q) s += run[q * kChunk + j];
-            }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            __syncthreads();
-            if (part == 0) run[t] = s;
-        }
-        __syncthreads();
-        if (warp == 0) {   // tokens 2 lane, 2 lane + 1
-            float av[2], b[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                av[e] = (dots[t] + dots[kChunk + t]) + (dots[2 * kChunk + t] + dots[3 * kChunk + t]);
-                b[e] = (dotb[t] + dotb[kChunk + t]) + (dotb[2 * kChunk + t] + dotb[3 * kChunk + t]);
-            }
-            float below = av[0] + av[1], above = b[0] + b[1];   // sums over i >= 2 lane, over j <= 2 lane + 1
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const float x = __shfl_down_sync(0xffffffffu, below, d), y = __shfl_up_sync(0xffffffffu, above, d);
-                if (lane + d < 32) below += x;
-                if (lane >= d) above += y;
-            }
-            const float upto = __shfl_up_sync(0xffffffffu, above, 1);   // over j < 2 lane
-            const float next = __shfl_down_sync(0xffffffffu, below, 1); // over i >= 2 lane + 2
-            float c = 0.f;
-#pragma unroll
-            for (int i = 0; i < kGradThreads / 32; ++i) c += inner[i];
-            c *= scal[kChunk - 1];
-            const size_t at = ((size_t)sp.first + t0) * a.s.hv + head;
-            const float before = lane ? upto : 0.f, after = lane < 31 ? next : 0.f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                if (t < rows) {
-                    // the decay of a token that forgets the state scales nothing
-                    const bool forgets = scal[320 + t] != (t ? scal[319 + t] : 0.f);
-                    const float s = run[t] + (e ? after + av[1] : below) + (e ? before + b[0] : before) + c;
-                    a.dg[at + (size_t)t * a.s.hv] = forgets ? 0.f : s;
-                    const float d = diag[t] / scal[128 + t];
-                    if (a.beta_f32) static_cast<float *>(a.dbeta)[at + (size_t)t * a.s.hv] = d;
-                    else static_cast<T *>(a.dbeta)[at + (size_t)t * a.s.hv] = from_f32<T>(d);
-                }
-            }
-        }
-        __syncthreads();
+        mbar_init(&bar.u_full, 1 + 32);
+        mbar_init(&bar.u_empty, 1);
+        mbar_init(&bar.s_full, 1);
+        mbar_init(&bar.s_empty, 1 + kGradWarps);
+        mbar_init(&bar.kq_full, 1);
+        mbar_init(&bar.kq_empty, kGradWarps);
+        mbar_init(&bar.x_done, 1);
+        mbar_init(&bar.acc_free, kGradWarps);
+        mbar_init(&bar.f_ready, kGradWarps);
+        mbar_init(&bar.f_done, 1);
+        mbar_init(&bar.drained, 1);
+        bar.gave_up = base & 1023 ? 1 : 0;   // images need their alignment
+        mbar_init_done();
     }
+    if (warp == 0) tmem_alloc(smem_addr(&bar.tmem));
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    constexpr uint32_t tm = 0;   // all columns are this CTA's
+    if (tid == 0 && bar.tmem != tm) bar.gave_up = 1;
 
-    T *oq = static_cast<T *>(a.dq) + ((size_t)(sp.first + t0) * a.s.hk + head_k) * a.s.k;
-    T *ok = static_cast<T *>(a.dk) + ((size_t)(sp.first + t0) * a.s.hk + head_k) * a.s.k;
-    const size_t ostride = (size_t)a.s.hk * a.s.k;
-    const bool pairs = sizeof(T) == 2 && (a.s.k & 1) == 0 &&
-                       ((reinterpret_cast<uintptr_t>(a.dq) | reinterpret_cast<uintptr_t>(a.dk)) & 3) == 0;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = i0 + 8 * e, col = 8 * (quarter * NQ + n) + c2;
-            if (i >= rows) continue;
-            if (pairs) {
-                if constexpr (sizeof(T) == 2) {
-                    if (col < a.s.k) {
-                        *reinterpret_cast<uint32_t *>(oq + i * ostride + col) = pack2<T>(dq[n][2 * e], dq[n][2 * e + 1]);
-                        *reinterpret_cast<uint32_t *>(ok + i * ostride + col) = pack2<T>(dk[n][2 * e], dk[n][2 * e + 1]);
+    if (warp == kGradWarps) {   // loads
+        uint32_t n = 0, items = 0, heads = 0;   // slices, items and value heads so far
+        const long long all = a.slots * a.s.hk;
+        auto announce_item = [&](const GradItem &item) {
+            if (items >= 2) wait_phase(&bar.item_empty[items & 1], (items / 2 - 1) & 1, gave_up);
+            if (lane == 0) {
+                bar.item[items & 1] = item;
+                mbar_arrive(&bar.item_full[items & 1]);
+            }
+            ++items;
+        };
+        for (long long i = blockIdx.x; i < all && !*gave_up; i += gridDim.x) {
+            const long long slot = i / a.s.hk, seq = seq_of_slot(a.s, slot);
+            if (seq < 0) continue;
+            const int head_k = (int)(i % a.s.hk);
+            const Span sp = span_of(a.s, seq);
+            const long long t0 = (slot - sp.slot) * kChunk;
+            const int rows = (int)min((long long)kChunk, sp.len - t0);
+            announce_item(GradItem{sp.first + t0, head_k, rows});
+            bool kq_due = true;
+            for (int hr = 0; hr < rep; ++hr, ++heads) {
+                const int head = head_k * rep + hr;
+                const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
+                if (heads >= 2) wait_phase(&bar.scal_empty[heads & 1], (heads / 2 - 1) & 1, gave_up);
+                if (lane == 0 && !*gave_up) {
+                    mbar_arrive_expect_tx(&bar.scal_full[heads & 1], 6 * kChunk * 4);
+                    bulk_load(smem + M::kScal + (heads & 1) * 6 * kChunk * 4, w + lay.scal, 6 * kChunk * 4, &bar.scal_full[heads & 1]);
+                }
+                const T *out = row_ptr<T>(a.dout, sp, seq, t0, head);
+                for (int v0 = 0; v0 < vpad && !*gave_up; v0 += kGradV, ++n) {
+                    const int bytes = min(kGradV, vpad - v0) * 128, vb = v0 / kBlockV, vi = v0 % kBlockV;
+                    if (n) wait_phase(&bar.u_empty, (n - 1) & 1, gave_up);
+                    if (*gave_up) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.u_full, 4 * bytes);
+                        for (int p = 0; p < 2; ++p) {
+                            const size_t from = (size_t)(vb * 2 + p) * kHalf + vi * 128;
+                            bulk_load(smem + M::kU + p * kSlice, w + lay.u + from, bytes, &bar.u_full);
+                            bulk_load(smem + M::kDU + p * kSlice, w + lay.du + from, bytes, &bar.u_full);
+                        }
+                    }
+                    load_tile<T, kGradV>(base + M::kO, M::kOP, out + v0, a.dout.tok, rows, a.s.v - v0, a.vec_do != 0, lane, 32);
+                    cp_async_commit();
+                    if (n) wait_phase(&bar.s_empty, (n - 1) & 1, gave_up);
+                    if (lane == 0 && !*gave_up) {
+                        mbar_arrive_expect_tx(&bar.s_full, 4 * KH * bytes);
+                        for (int p = 0; p < 2 * KH; ++p) {   // parts and halves
+                            const size_t from = (size_t)(vb * 2 * KH + p) * kHalf + vi * 128;
+                            bulk_load(smem + M::kS + p * kSlice, w + lay.s + from, bytes, &bar.s_full);
+                            bulk_load(smem + M::kDS + p * kSlice, w + lay.ds + from, bytes, &bar.s_full);
+                        }
+                    }
+                    cp_async_wait<0>();   // dO
+                    fence_async();
+                    mbar_arrive(&bar.u_full);
+                    if (kq_due) {   // after the slice that goes ahead while the last item's keys and queries are still in use
+                        kq_due = false;
+                        if (items >= 2) wait_phase(&bar.kq_empty, (items - 2) & 1, gave_up);
+                        if (lane == 0 && !*gave_up) {
+                            mbar_arrive_expect_tx(&bar.kq_full, NP * M::kKQ);
+                            bulk_load(smem, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), NP * M::kKQ, &bar.kq_full);
+                        }
                     }
                 }
-            } else {
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (col + x < a.s.k) {
-                        oq[i * ostride + col + x] = from_f32<T>(dq[n][2 * e + x]);
-                        ok[i * ostride + col + x] = from_f32<T>(dk[n][2 * e + x]);
-                    }
             }
         }
+        const uint32_t real = items;
+        announce_item(GradItem{0, 0, 0});
+        if (*gave_up && lane == 0 && n) {   // copies in flight; without it the others have waited for every one
+            wait_drained(&bar.u_full, (n - 1) & 1);
+            wait_drained(&bar.s_full, (n - 1) & 1);
+            if (real) wait_drained(&bar.kq_full, (real - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kGradWarps + 1) {   // products
+        const uint32_t one = elect_lane();
+        constexpr uint32_t kSplit = KH == 2 ? kSlice : 0, kKSplit = KH == 2 ? kHalf : 0;   // 64 columns of keys only: twice the same rows
+        const uint64_t u_left = operand(base + M::kU, false, kSlice), u_right = operand(base + M::kU, false, kSlice);
+        const uint64_t du = operand(base + M::kDU, false, kSlice), o = operand(base + M::kO, true, 0);
+        const uint64_t sl = operand(base + M::kS, false, kSplit), dsl = operand(base + M::kDS, false, kSplit);
+        const uint64_t kq_rows = operand(base, true, 0), k_left = operand(base, false, kKSplit);
+        const uint64_t f1_rows = operand(base + M::kF1, true, 0), f1_cols = operand(base + M::kF1, false, 0), f2 = operand(base + M::kF2, true, 0);
+        uint32_t n = 0, heads = 0;
+        for (uint32_t items = 0;; ++items) {
+            wait_phase(&bar.item_full[items & 1], (items / 2) & 1, gave_up);
+            const int rows = bar.item[items & 1].rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.item_empty[items & 1]);
+            if (rows == 0 || *gave_up) break;
+            for (int hr = 0; hr < rep; ++hr, ++heads) {
+                if (heads) wait_phase(&bar.acc_free, (heads - 1) & 1, gave_up);
+                for (int v0 = 0; v0 < vpad; v0 += kGradV, ++n) {
+                    const int steps = min(kGradV, vpad - v0) / 16;
+                    wait_phase(&bar.u_full, n & 1, gave_up);
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < steps; ++k) {
+                        const bool add = v0 + k > 0;
+#pragma unroll
+                        for (int p = 0; p < NP; ++p)
+                            mma_smem(one, tm + kColP, further(u_left, k * 2048), further(o, p * M::kOP + k * 32),
+                                     shape(kChunk, true) | kLeftByColumns, add || p);
+                        mma_smem(one, tm + kColN, further(u_left, k * 2048), further(du, k * 2048),
+                                 shape(2 * kChunk, false) | kLeftByColumns, add);
+                    }
+                    wait_phase(&bar.s_full, n & 1, gave_up);
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < steps; ++k) {
+                        const bool add = v0 + k > 0;
+                        const uint64_t s0 = further(sl, k * 2048), d0 = further(dsl, k * 2048);
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)   // S's parts with dO's upper one, its upper with dO's lower
+                            mma_smem(one, tm + kColX, further(s0, p * M::kSP), further(o, k * 32), shape(kChunk, true) | kLeftByColumns, add || p);
+                        if (NP == 2)
+                            mma_smem(one, tm + kColX, s0, further(o, M::kOP + k * 32), shape(kChunk, true) | kLeftByColumns, true);
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) {   // hi hi, lo hi, hi lo
+                            const uint32_t l = t == 1 ? M::kSP : 0, r = t == 2 ? kSlice : 0;
+                            mma_smem(one, tm + kColX + 64, further(s0, l), further(du, r + k * 2048), shape(kChunk, false) | kLeftByColumns, add || t);
+                            mma_smem(one, tm + kColX + 128, further(d0, l), further(u_right, r + k * 2048), shape(kChunk, false) | kLeftByColumns, add || t);
+                        }
+                    }
+                    mma_commit(one, &bar.u_empty);
+                    mma_commit(one, &bar.s_empty);
+                }
+                if (hr == 0) {   // [K; Q] [K; Q]^T
+                    wait_phase(&bar.kq_full, items & 1, gave_up);
+                    tmem_fence_after();
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+#pragma unroll
+                        for (int q = 0; q + p < NP; ++q)
+#pragma unroll 1
+                            for (int k = 0; k < KP / 16; ++k) {
+                                const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+                                mma_smem(one, tm + kColF, further(kq_rows, p * M::kKQ + at), further(kq_rows, q * M::kKQ + at),
+                                         shape(2 * kChunk, true), p + q + k > 0);
+                            }
+                }
+                mma_commit(one, &bar.x_done);
+                wait_phase(&bar.f_ready, heads & 1, gave_up);
+                tmem_fence_after();
+                // F1 K to dQ, F1^T Q + (F2 + F2^T) K to dK, all transposed
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+#pragma unroll
+                    for (int h = 0; h + p < 2; ++h)
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            const bool add = hr + p + h + k > 0;
+                            const uint64_t kl = further(k_left, p * M::kKQ + k * 2048), ql = further(kl, kChunk * 128);
+                            mma_smem(one, tm + kColF, kl, further(f1_rows, h * (uint32_t)kSquare + k * 32), shape(kChunk, true) | kLeftByColumns, add);
+                            mma_smem(one, tm + kColF + 64, ql, further(f1_cols, h * (uint32_t)kSquare + k * 2048), shape(kChunk, false) | kLeftByColumns, add);
+                            mma_smem(one, tm + kColF + 64, kl, further(f2, h * (uint32_t)kSquare + k * 32), shape(kChunk, true) | kLeftByColumns, true);
+                        }
+                mma_commit(one, &bar.f_done);
+            }
+        }
+        mma_commit(one, &bar.drained);
+        wait_drained(&bar.drained, 0);
+    } else {
+        const int quadrant = warp & 3, part = warp >> 2, tok = 16 * part;   // this thread's tokens i: tok ..
+        const uint32_t at = (uint32_t)quadrant << 21;                       // lane 32 quadrant
+        const int col = 32 * quadrant + lane;                               // this thread's column of the keys
+        const int j = col & 63, role = quadrant >> 1;                       // and its token j, with U's upper or lower part
+        float *exch = reinterpret_cast<float *>(smem + M::kF1), *Z = reinterpret_cast<float *>(smem + M::kZ);
+        float *kk = reinterpret_cast<float *>(smem + M::kKK), *qk = kk + kChunk * kChunk;   // [i][j]
+        float *dots = reinterpret_cast<float *>(smem + M::kMore);   // [4 quadrants][64] of a_i
+        float *dotb = dots + 4 * kChunk;                            // the same of b_j
+        float *run = dotb + 4 * kChunk;                             // [4 quarters of the rows][64] column sums of Z
+        float *diag = run + 4 * kChunk;                             // [64] dU_j . U_j
+        float *inner = diag + kChunk;                               // <S, dS'> by warps
+        uint32_t n = 0, heads = 0;
+        for (uint32_t items = 0;; ++items) {
+            wait_phase(&bar.item_full[items & 1], (items / 2) & 1, gave_up);
+            const GradItem item = bar.item[items & 1];
+            meet();   // one decision for all
+            const bool stop = item.rows == 0 || *gave_up;
+            if (tid == 0) inner[0] = stop ? 1.f : 0.f;
+            meet();
+            const bool all_stop = inner[0] != 0.f;
+            meet();
+            warp_arrive(&bar.item_empty[items & 1], lane);
+            if (all_stop) break;
+            float dq[16], dk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dq[i] = dk[i] = 0.f;
+
+            for (int hr = 0; hr < rep; ++hr, ++heads) {
+                const int head = item.head_k * rep + hr;
+                const float *scal = reinterpret_cast<const float *>(smem + M::kScal + (heads & 1) * 6 * kChunk * 4);
+                float prod = 0.f;   // this thread's part of <S, dS'>
+                for (int v0 = 0; v0 < vpad; v0 += kGradV, ++n) {
+                    const int vr = min(kGradV, vpad - v0);
+                    wait_phase(&bar.s_full, n & 1, gave_up);
+#pragma unroll 1
+                    for (int i = tid; i < kGradV * KP / 8; i += 32 * kGradWarps) {   // the same place in all four images
+                        if (i % (kGradV * 8) >= vr * 8) continue;                    // not loaded
+                        const uint4 *sv = reinterpret_cast<const uint4 *>(smem + M::kS) + i;
+                        const uint4 *dv = reinterpret_cast<const uint4 *>(smem + M::kDS) + i;
+                        const uint4 sh = sv[0], sl = sv[M::kSP / 16], dh = dv[0], dl = dv[M::kSP / 16];
+                        const uint32_t *shp = &sh.x, *slp = &sl.x, *dhp = &dh.x, *dlp = &dl.x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            prod += (bf16_low(shp[e]) + bf16_low(slp[e])) * (bf16_low(dhp[e]) + bf16_low(dlp[e]));
+                            prod += (bf16_high(shp[e]) + bf16_high(slp[e])) * (bf16_high(dhp[e]) + bf16_high(dlp[e]));
+                        }
+                    }
+                    warp_arrive(&bar.s_empty, lane);
+                }
+#pragma unroll
+                for (int m = 16; m; m >>= 1) prod += __shfl_xor_sync(0xffffffffu, prod, m);
+                if (lane == 0) inner[warp] = prod;
+                wait_phase(&bar.scal_full[heads & 1], (heads / 2) & 1, gave_up);
+                if (hr == 0) wait_phase(&bar.kq_full, items & 1, gave_up);
+                if (heads) wait_phase(&bar.f_done, (heads - 1) & 1, gave_up);   // F has been used
+                wait_phase(&bar.x_done, heads & 1, gave_up);
+                tmem_fence_after();
+
+                // U dO^T and U dU^T: lanes j and 64 + j hold what U's two parts give; each of the two
+                // threads takes eight of the sixteen tokens i and sends the other eight
+                float dp[8], dn[8];
+                {
+                    float p[16], u[16], w[16];
+                    tmem_ld16(p, at + kColP + tok);
+                    tmem_ld16(u, at + kColN + tok, w, at + kColN + kChunk + tok);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) u[i] += w[i];
+                    float *to = exch + (1 - role) * (kChunk * kChunk);   // [16 of P and N, 4 parts][64 j]
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        to[(part * 16 + i) * kChunk + j] = role ? p[i] : p[8 + i];
+                        to[(part * 16 + 8 + i) * kChunk + j] = role ? u[i] : u[8 + i];
+                        dp[i] = role ? p[8 + i] : p[i];
+                        dn[i] = role ? u[8 + i] : u[i];
+                    }
+                    if (hr == 0 && role == 0) {   // k_j . k_i and k_j . q_i
+                        tmem_ld16(u, at + kColF + tok, w, at + kColF + kChunk + tok);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            kk[(tok + i) * kChunk + j] = u[i];
+                            qk[(tok + i) * kChunk + j] = w[i];
+                        }
+                    }
+                }
+                meet();
+                float *from = exch + role * (kChunk * kChunk);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dp[i] += from[(part * 16 + i) * kChunk + j];
+                    dn[i] += from[(part * 16 + 8 + i) * kChunk + j];
+                }
+                meet();   // the images of F take the place of what was exchanged
+
+                // F1 = scale D dP, F2 = D dN (with its transpose) as pairs, and Z
+                {
+                    const float ghj = scal[192 + j], glj = scal[256 + j], rj = scal[320 + j];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = tok + 8 * role + e;
+                        const float D = i >= j && scal[320 + i] == rj ? expf((scal[192 + i] - ghj) + (scal[256 + i] - glj)) : 0.f;
+                        if (i == j) diag[j] = dn[e];
+                        const float f1 = i >= j ? a.s.scale * D * dp[e] : 0.f, f2 = i > j ? -scal[128 + i] * D * dn[e] : 0.f;
+                        Z[i * kZStride + j] = i > j ? f1 * qk[i * kChunk + j] + f2 * kk[i * kChunk + j] : 0.f;
+                        const __nv_bfloat16 h1 = __float2bfloat16_rn(f1), h2 = __float2bfloat16_rn(f2);
+                        const __nv_bfloat16 l1 = __float2bfloat16_rn(f1 - __bfloat162float(h1)), l2 = __float2bfloat16_rn(f2 - __bfloat162float(h2));
+                        const uint32_t ij = img(0, i, j >> 3) + (j & 7) * 2, ji = img(0, j, i >> 3) + (i & 7) * 2;
+                        *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF1 + ij) = h1;
+                        *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF1 + kSquare + ij) = l1;
+                        if (i >= j) {
+                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + ij) = h2;
+                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + kSquare + ij) = l2;
+                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + ji) = h2;
+                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + kSquare + ji) = l2;
+                        }
+                    }
+                }
+                fence_async();
+                tmem_fence_before();
+                warp_arrive(&bar.f_ready, lane);
+
+                // through the states: a lane is a column of the keys
+                {
+                    float x[16], y[16], z[16];
+                    tmem_ld16(x, at + kColX + tok, y, at + kColX + 64 + tok);
+                    tmem_ld16(z, at + kColX + 128 + tok);
+                    tmem_fence_before();
+                    warp_arrive(&bar.acc_free, lane);
+                    const uint32_t piece = (uint32_t)(col >> 3), in = (uint32_t)(col & 7) * 2;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float eg = scal[tok + i], el = scal[64 + tok + i], be = scal[128 + tok + i];
+                        float kv = 0.f, qv = 0.f;
+                        if (col < KP) {
+                            const uint32_t k0 = img(0, tok + i, piece) + in, q0 = k0 + kChunk * 128;
+                            kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + k0));
+                            qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + q0));
+                            if constexpr (NP == 2) {
+                                kv += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + M::kKQ + k0));
+                                qv += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + M::kKQ + q0));
+                            }
+                        }
+                        const float x1 = a.s.scale * eg * x[i], x2 = eg * be * y[i], x3 = el * z[i];
+                        dq[i] += x1;
+                        dk[i] += x3 - x2;
+                        x[i] = qv * x1 - kv * x2;   // to a_i
+                        y[i] = kv * x3;             // to b_j
+                    }
+                    const float sa = sum16(x, lane), sb = sum16(y, lane);
+                    if ((lane & 1) == 0) {
+                        dots[quadrant * kChunk + tok + (lane >> 1)] = sa;
+                        dotb[quadrant * kChunk + tok + (lane >> 1)] = sb;
+                    }
+                }
+                meet();   // Z, the dots
+
+                // sum over i >= t of Z_ij within quarters of 16 rows, then with the quarters below
+                if (tid < 256) {
+                    const int jj = tid & 63, q = tid >> 6;
+                    float s = 0.f;
+#pragma unroll
+                    for (int t = 15; t >= 0; --t) {
+                        s += Z[(16 * q + t) * kZStride + jj];
+                        Z[(16 * q + t) * kZStride + jj] = s;
+                    }
+                    run[q * kChunk + jj] = s;
+                }
+                meet();
+                {   // row t: sum over j < t (eight threads a row), and all else for token t
+                    const int t = tid >> 3, sub = tid & 7;
+                    float s = 0.f;
+                    for (int jj = sub; jj < t; jj += 8) {
+                        s += Z[t * kZStride + jj];
+                        for (int q = (t >> 4) + 1; q < 4; ++q) s += run[q * kChunk + jj];
+                    }
+                    // a_i of i >= t, b_j of j < t, <S, dS'>
+                    for (int i = sub; i < kChunk; i += 8) {
+                        const float *d = i >= t ? dots : dotb;
+                        s += (d[i] + d[kChunk + i]) + (d[2 * kChunk + i] + d[3 * kChunk + i]);
+                    }
+                    s += scal[kChunk - 1] * (inner[sub] + inner[8 + sub]);
+#pragma unroll
+                    for (int m = 1; m < 8; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                    if (sub == 0 && t < item.rows) {
+                        // the decay of a token that forgets the state scales nothing
+                        const bool forgets = scal[320 + t] != (t ? scal[319 + t] : 0.f);
+                        const size_t out = (size_t)(item.token + t) * a.s.hv + head;
+                        a.dg[out] = forgets ? 0.f : s;
+                        const float d = diag[t] / scal[128 + t];
+                        if (a.beta_f32) static_cast<float *>(a.dbeta)[out] = d;
+                        else static_cast<T *>(a.dbeta)[out] = from_f32<T>(d);
+                    }
+                }
+                meet();
+                warp_arrive(&bar.scal_empty[heads & 1], lane);
+            }
+            wait_phase(&bar.f_done, (heads - 1) & 1, gave_up);
+            tmem_fence_after();
+            {
+                float x[16], y[16];
+                tmem_ld16(x, at + kColF + tok, y, at + kColF + 64 + tok);
+                tmem_fence_before();
+                warp_arrive(&bar.kq_empty, lane);
+                const size_t ostride = (size_t)a.s.hk * a.s.k, first = ((size_t)(item.token + tok) * a.s.hk + item.head_k) * a.s.k + col;
+                T *oq = static_cast<T *>(a.dq) + first, *ok = static_cast<T *>(a.dk) + first;
+                const float bad = *gave_up ? __int_as_float(0x7fffffff) : 0.f;   // not what they should be: say so
+                if (col < a.s.k)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (tok + i < item.rows) {
+                            oq[i * ostride] = from_f32<T>(dq[i] + x[i] + bad);
+                            ok[i * ostride] = from_f32<T>(dk[i] + y[i] + bad);
+                        }
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (*gave_up) {   // items that were not reached
+        const long long tokens = a.s.cu ? a.s.tokens : a.s.seqs * a.s.tokens;
+        for (long long i = tid; i < tokens * a.s.hv; i += kGradThreads) a.dg[i] = __int_as_float(0x7fffffff);
+    }
+    if (warp == 0) tmem_free(bar.tmem);
 }
 
 namespace {
@@ -457,7 +510,8 @@ cudaError_t gradients(const DeltaArgs &a, cudaStream_t s) {
     constexpr int bytes = GradSmem<Planes<T>::NP, KP>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(delta_gradients_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    delta_gradients_kernel<T, KP><<<dim3((unsigned)a.slots, (unsigned)a.s.hk), kGradThreads, bytes, s>>>(a);
+    const long long items = a.slots * a.s.hk;
+    delta_gradients_kernel<T, KP><<<(unsigned)(items < 152 ? items : 152), kGradThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -31,8 +31,6 @@ struct DeltaShape {
 //          tokens up to here have forgotten the state
 //   T      2 x 64 x 64       row i, column j
 //   P      2 x 64 x 64
-//   N      2 x 64 x 64       (blocks of 16 above the diagonal are not written; kept for the
-//                            backward pass only)
 // and for the backward pass, for each block of 128 values (rows past the values, to a multiple
 // of 16, are 0; further ones are not written)
 //   S      2 x 128 x K       row v, column k: the state at the chunk's start
@@ -42,7 +40,7 @@ struct DeltaShape {
 // and queries (rows 64-127) as one image of 128 rows of K, one plane for bf16 and two for other
 // types: rows past the sequence's end and columns past K are 0.
 struct ChunkLayout {
-    size_t scal, t, p, n, s, u, ds, du, stride;
+    size_t scal, t, p, s, u, ds, du, stride;
 };
 constexpr size_t kSquare = (size_t)kChunk * kChunk * 2;   // bytes of one 64 x 64 plane
 constexpr int kBlockV = 128;                              // values of a block
@@ -58,7 +56,6 @@ constexpr ChunkLayout chunk_layout(int k, int v, bool train) {
     l.t = at; at += 2 * kSquare;
     l.p = at; at += 2 * kSquare;
     if (train) {
-        l.n = at; at += 2 * kSquare;
         l.s = at; at += sb;
         l.u = at; at += ub;
         l.ds = at; at += sb;

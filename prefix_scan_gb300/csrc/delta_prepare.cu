@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
         __syncthreads();
 
         unsigned char *out = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
-        const int imgs = (a.train ? 6 : 4) * (int)kSquare / 16;   // T, P, N follow one another on both sides
+        constexpr int imgs = 4 * (int)kSquare / 16;   // T and P follow one another on both sides
 #pragma unroll 4
         for (int i = tid; i < imgs; i += kPrepThreads)
             reinterpret_cast<uint4 *>(out + lay.t)[i] = reinterpret_cast<const uint4 *>(smem + M::kT)[i];

@@ -124,7 +124,7 @@ __device__ __forceinline__ void keep16(uint32_t image, uint32_t lower, int row, 
 }
 
 // ---- products --------------------------------------------------------------------
-// Descriptor of a 16-bit right operand in a 128-byte-swizzled image (rows of 64 numbers,
+// Descriptor of a 16-bit operand in a 128-byte-swizzled image (rows of 64 numbers,
 // eight rows to 1024 bytes; delta_common.cuh's img() is that swizzle).  by_rows: the rows
 // are the product's columns n and their numbers run along its inner dimension; otherwise
 // rows run along the inner dimension, numbers along n, and 64 numbers further on along n lie
@@ -153,6 +153,15 @@ __device__ __forceinline__ void mma_tmem(uint32_t one, uint32_t d, uint32_t a, u
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         :: "r"(d), "r"(a), "l"(b), "r"(shape_word), "r"((uint32_t)add), "r"(one) : "memory");
+}
+// The same with the left operand in shared memory: an image whose rows are the product's rows, or
+// (shape_word | kLeftByColumns) run along its inner dimension.
+constexpr uint32_t kLeftByColumns = 1u << 15;
+__device__ __forceinline__ void mma_smem(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t shape_word, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(shape_word), "r"((uint32_t)add), "r"(one) : "memory");
 }
 // The barrier completes its phase when all products issued so far have.
 __device__ __forceinline__ void mma_commit(uint32_t one, uint64_t *bar) {
