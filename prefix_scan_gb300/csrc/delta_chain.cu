@@ -14,7 +14,8 @@
 //
 // A product of 128 rows, 16 inner and up to 128 columns takes 64 clocks however
 // few the columns (measured), so keys and queries are one operand of 128 columns,
-// and so are the two parts of T: U comes as two accumulators, added on their way out.
+// and so are the two parts of T: U comes as two accumulators, added on their way out
+// (to beta R: the image holds T - 1, so that the greater part of U passes no pair).
 //
 // Bounded by the chain S -> X -> U -> S' of each chunk: three products and, between
 // them, the way of 128 x 128 and twice 128 x 64 numbers through registers.  So the
@@ -133,11 +134,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                 wait_phase(&bar.u_ready, c & 1, gave_up);
                 tmem_fence_after();
 #pragma unroll
-                for (int t = 0; t < 3; ++t)   // hi hi, lo hi, hi lo
+                for (int t = 0; t < (NP == 1 ? 3 : 4); ++t)   // hi hi, lo hi, hi lo, and lo lo where outputs may be f32
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_tmem(one, tm + kColO + 16 * k, tm + kColR + (t == 1 ? 32 : 0) + k * 8,
-                                 further(pp, (t == 2 ? (uint32_t)kSquare : 0) + k * (16 * 128 + 32)), shape(kChunk - 16 * k, true),
+                        mma_tmem(one, tm + kColO + 16 * k, tm + kColR + (t & 1 ? 32 : 0) + k * 8,
+                                 further(pp, (t & 2 ? (uint32_t)kSquare : 0) + k * (16 * 128 + 32)), shape(kChunk - 16 * k, true),
                                  t + k > 0);
                 mma_commit(one, &bar.o_done);
                 mma_commit(one, &bar.empty[st]);
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
 #pragma unroll
-                        for (int h = 0; h + p < 2; ++h)
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int k = (i >> 1) * (KP / 32) + 2 * r + (i & 1);   // columns 16 k..
@@ -171,13 +172,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                 if (M::kStages == 2 && c && !states) outputs(c - 1);
                 wait_busy(&bar.r_ready, c & 1, gave_up);
                 tmem_fence_after();
-                // (beta R)^T T^T: the upper part of beta R with both of T's, the rest with T's upper one
+                // (beta R)^T (T - 1)^T: both parts of beta R with both of T - 1's
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_tmem(one, tm + kColU, tm + kColR + k * 8, further(tt, k * 32), shape(2 * kChunk, true), k > 0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_tmem(one, tm + kColU, tm + kColR + 32 + k * 8, further(tt, k * 32), shape(kChunk, true), true);
+                for (int k = 0; k < 8; ++k)
+                    mma_tmem(one, tm + kColU, tm + kColR + k * 8, further(tt, (k & 3) * 32), shape(2 * kChunk, true), k > 0);
                 mma_commit(one, &bar.u_done);
                 wait_busy(&bar.w_ready, c & 1, gave_up);
                 tmem_fence_after();
@@ -185,7 +183,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
-                    for (int h = 0; h + p < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_tmem(one, tm + kColS, tm + kColW + h * 32 + k * 8,
@@ -356,23 +354,21 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             if (c > 0 && !states) wait_phase(&bar.o_read, (c - 1) & 1, gave_up);   // the last outputs were where the next pair goes
             wait_phase(&bar.u_done, c & 1, gave_up);
             tmem_fence_after();
-            {
-                float z[2][16];
-                tmem_ld16(x[0], at + kColU + 32 * half, z[0], at + kColU + kChunk + 32 * half);
-                tmem_ld16(x[1], at + kColU + 32 * half + 16, z[1], at + kColU + kChunk + 32 * half + 16);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < 2; ++b) {   // U = beta R + (T - 1) beta R: only the second part goes through pairs
+                float z[16], w[16];
+                tmem_ld16(z, at + kColU + 32 * half + 16 * b, w, at + kColU + kChunk + 32 * half + 16 * b);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 u = fma2(make_float2(1.f, 1.f), make_float2(x[b][i], x[b][i + 1]), make_float2(z[b][i], z[b][i + 1]));
-                        z[b][i] = x[b][i] = u.x;
-                        z[b][i + 1] = x[b][i + 1] = u.y;
-                    }
-                    scale16(z[b], scal + 64 + 16 * b);
-                    split16(z[b], hi, lo);
-                    tmem_st8(at + kColW + 16 * half + 8 * b, hi);
-                    tmem_st8(at + kColW + 32 + 16 * half + 8 * b, lo);
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 t = fma2(make_float2(1.f, 1.f), make_float2(z[i], z[i + 1]), make_float2(w[i], w[i + 1]));
+                    const float2 u = fma2(make_float2(1.f, 1.f), make_float2(x[b][i], x[b][i + 1]), t);
+                    z[i] = x[b][i] = u.x;
+                    z[i + 1] = x[b][i + 1] = u.y;
                 }
+                scale16(z, scal + 64 + 16 * b);
+                split16(z, hi, lo);
+                tmem_st8(at + kColW + 16 * half + 8 * b, hi);
+                tmem_st8(at + kColW + 32 + 16 * half + 8 * b, lo);
             }
             tmem_wait_st();
             tmem_fence_before();

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int p = 0; p + t < (NP == 1 ? 1 + t : 2); ++p)   // dO's parts with P's upper, dO's upper with P's lower
+                for (int p = 0; p < NP; ++p)   // P's parts, dO's parts
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_tmem(one, tm + kColP, tm + kColO + p * 32 + k * 8,
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
-                    for (int h = 0; h + p < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int k = (j >> 1) * (KP / 32) + 2 * r + (j & 1);   // columns 16 k..
@@ -151,20 +151,17 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
 #pragma unroll
             for (int p = 0; p < NP; ++p)
 #pragma unroll
-                for (int h = 0; h + p < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_tmem(one, tm + kColS, tm + kColQ + h * 32 + k * 8,
                                  further(kt, p * KH * kHalf + kChunk * 128 + k * 16 * 128), shape(KP, false), true);
             wait_busy(&bar.r_ready, i & 1, gave_up);
             tmem_fence_after();
-            // dU^T = Y^T T
+            // Y^T (T - 1)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_tmem(one, tm + kColU, tm + kColR + k * 8, further(tt, k * 16 * 128), shape(2 * kChunk, false), k > 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_tmem(one, tm + kColU, tm + kColR + 32 + k * 8, further(tt, k * 16 * 128), shape(kChunk, false), true);
+            for (int k = 0; k < 8; ++k)
+                mma_tmem(one, tm + kColU, tm + kColR + k * 8, further(tt, (k & 3) * 16 * 128), shape(2 * kChunk, false), k > 0);
             mma_commit(one, &bar.u_done);
             wait_busy(&bar.w_ready, i & 1, gave_up);
             tmem_fence_after();
@@ -172,7 +169,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
 #pragma unroll
             for (int p = 0; p < NP; ++p)
 #pragma unroll
-                for (int h = 0; h + p < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_tmem(one, tm + kColS, tm + kColR + h * 32 + k * 8,
@@ -345,27 +342,26 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
 
             wait_phase(&bar.u_done, i & 1, gave_up);
             tmem_fence_after();
-            {
-                float z[2][16];
-                tmem_ld16(x[0], at + kColU + 32 * half, z[0], at + kColU + kChunk + 32 * half);
-                tmem_ld16(x[1], at + kColU + 32 * half + 16, z[1], at + kColU + kChunk + 32 * half + 16);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < 2; ++b) {   // dU = Y + (T - 1)^T Y, and -exp(G) beta dU
+                float z[16], w[16];
+                tmem_ld16(z, at + kColU + 32 * half + 16 * b, w, at + kColU + kChunk + 32 * half + 16 * b);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {   // dU, and -exp(G) beta dU
-                        const float4 eg = *reinterpret_cast<const float4 *>(scal + 16 * b + j);
-                        const float4 be = *reinterpret_cast<const float4 *>(scal + 128 + 16 * b + j);
-                        const float2 u0 = fma2(make_float2(1.f, 1.f), make_float2(x[b][j], x[b][j + 1]), make_float2(z[b][j], z[b][j + 1]));
-                        const float2 u1 = fma2(make_float2(1.f, 1.f), make_float2(x[b][j + 2], x[b][j + 3]), make_float2(z[b][j + 2], z[b][j + 3]));
-                        const float2 g0 = mul2(mul2(make_float2(-eg.x, -eg.y), make_float2(be.x, be.y)), u0);
-                        const float2 g1 = mul2(mul2(make_float2(-eg.z, -eg.w), make_float2(be.z, be.w)), u1);
-                        x[b][j] = u0.x; x[b][j + 1] = u0.y; x[b][j + 2] = u1.x; x[b][j + 3] = u1.y;
-                        z[b][j] = g0.x; z[b][j + 1] = g0.y; z[b][j + 2] = g1.x; z[b][j + 3] = g1.y;
-                    }
-                    split16(z[b], hi, lo);
-                    tmem_st8(at + kColR + 16 * half + 8 * b, hi);
-                    tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 eg = *reinterpret_cast<const float4 *>(scal + 16 * b + j);
+                    const float4 be = *reinterpret_cast<const float4 *>(scal + 128 + 16 * b + j);
+                    const float2 t0 = fma2(make_float2(1.f, 1.f), make_float2(z[j], z[j + 1]), make_float2(w[j], w[j + 1]));
+                    const float2 t1 = fma2(make_float2(1.f, 1.f), make_float2(z[j + 2], z[j + 3]), make_float2(w[j + 2], w[j + 3]));
+                    const float2 u0 = fma2(make_float2(1.f, 1.f), make_float2(x[b][j], x[b][j + 1]), t0);
+                    const float2 u1 = fma2(make_float2(1.f, 1.f), make_float2(x[b][j + 2], x[b][j + 3]), t1);
+                    const float2 g0 = mul2(mul2(make_float2(-eg.x, -eg.y), make_float2(be.x, be.y)), u0);
+                    const float2 g1 = mul2(mul2(make_float2(-eg.z, -eg.w), make_float2(be.z, be.w)), u1);
+                    x[b][j] = u0.x; x[b][j + 1] = u0.y; x[b][j + 2] = u1.x; x[b][j + 3] = u1.y;
+                    z[j] = g0.x; z[j + 1] = g0.y; z[j + 2] = g1.x; z[j + 3] = g1.y;
                 }
+                split16(z, hi, lo);
+                tmem_st8(at + kColR + 16 * half + 8 * b, hi);
+                tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
             }
             tmem_wait_st();
             tmem_fence_before();

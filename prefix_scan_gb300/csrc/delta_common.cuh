@@ -16,11 +16,11 @@
 // o = scale q^T S with the tokens of a chunk taken together.
 //
 // Precision.  States, T, P, N and every sum are 32-bit.  As operands of the
-// matrix units they are pairs hi + lo of bf16 (16 significant bits; the
-// product lo*lo, at most 2^-16 of the whole, is left out), so that states and
-// the gradients of g come out to about 2^-17 and not to bf16's 2^-9.  bf16
-// inputs are exact with one number (NP = 1); f16 and f32 inputs are pairs
-// too (NP = 2).
+// matrix units they are pairs hi + lo of bf16 (16 significant bits, off by 2^-18.4
+// of the number in the root mean square), so that states and the gradients of g
+// come out to about 2^-18 and not to bf16's 2^-9.  bf16 inputs are exact with one
+// number (NP = 1); f16 and f32 inputs are pairs too (NP = 2).  Where outputs are
+// rounded to 16 bits anyway, U^T P^T leaves out the product of the two lower parts.
 #pragma once
 
 #include <cuda_bf16.h>

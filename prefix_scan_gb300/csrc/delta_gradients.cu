@@ -228,13 +228,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                         const bool add = v0 + k > 0;
                         const uint64_t s0 = further(sl, k * 2048), d0 = further(dsl, k * 2048);
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)   // S's parts with dO's upper one, its upper with dO's lower
-                            mma_smem(one, tm + kColX, further(s0, p * M::kSP), further(o, k * 32), shape(kChunk, true) | kLeftByColumns, add || p);
-                        if (NP == 2)
-                            mma_smem(one, tm + kColX, s0, further(o, M::kOP + k * 32), shape(kChunk, true) | kLeftByColumns, true);
+                        for (int p = 0; p < 2 * NP; ++p)   // S's parts, dO's parts
+                            mma_smem(one, tm + kColX, further(s0, (p & 1) * M::kSP), further(o, (p >> 1) * M::kOP + k * 32),
+                                     shape(kChunk, true) | kLeftByColumns, add || p);
 #pragma unroll
-                        for (int t = 0; t < 3; ++t) {   // hi hi, lo hi, hi lo
-                            const uint32_t l = t == 1 ? M::kSP : 0, r = t == 2 ? kSlice : 0;
+                        for (int t = 0; t < 2 + NP; ++t) {   // hi hi, lo hi, hi lo, and lo lo where gradients may be f32
+                            const uint32_t l = t & 1 ? M::kSP : 0, r = t & 2 ? kSlice : 0;
                             mma_smem(one, tm + kColX + 64, further(s0, l), further(du, r + k * 2048), shape(kChunk, false) | kLeftByColumns, add || t);
                             mma_smem(one, tm + kColX + 128, further(d0, l), further(u_right, r + k * 2048), shape(kChunk, false) | kLeftByColumns, add || t);
                         }
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
 #pragma unroll
-                        for (int q = 0; q + p < NP; ++q)
+                        for (int q = 0; q < NP; ++q)
 #pragma unroll 1
                             for (int k = 0; k < KP / 16; ++k) {
                                 const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
-                    for (int h = 0; h + p < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
                             const bool add = hr + p + h + k > 0;

@@ -29,7 +29,7 @@ struct DeltaShape {
 // images are swizzled as in delta_common.cuh and kept as pairs hi, lo of bf16.
 //   scal   6 x 64 f32: exp(G), exp(G_C - G), beta, G as a sum of two floats, and how many
 //          tokens up to here have forgotten the state
-//   T      2 x 64 x 64       row i, column j
+//   T - 1  2 x 64 x 64       row i, column j (T's diagonal is 1)
 //   P      2 x 64 x 64
 // and for the backward pass, for each block of 128 values (rows past the values, to a multiple
 // of 16, are 0; further ones are not written)

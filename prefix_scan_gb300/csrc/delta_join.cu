@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const DeltaArg
                     if constexpr (BACK) load_b(b, m + p * KH * kHalf, 8 * warp * NQ + 16 * np, 16 * kt, lane);
                     else load_b_t(b, m + p * KH * kHalf, 16 * kt, 8 * warp * NQ + 16 * np, lane);
 #pragma unroll
-                    for (int h = 0; h + p < 2; ++h) {
+                    for (int h = 0; h < 2; ++h) {
                         mma_bf16(acc[2 * np], f[h], b[0], b[1]);
                         mma_bf16(acc[2 * np + 1], f[h], b[2], b[3]);
                     }

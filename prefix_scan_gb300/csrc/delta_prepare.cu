@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
                     uint32_t b[4];
                     load_b(b, base + M::kK + p * M::kPlane, 16 * np, 16 * kt, lane);
 #pragma unroll
-                    for (int f = 0; f + p < NP; ++f) {   // lo lo is left out
+                    for (int f = 0; f < NP; ++f) {
                         mma_bf16(kk[2 * np], ak[f], b[0], b[1]);
                         mma_bf16(kk[2 * np + 1], ak[f], b[2], b[3]);
                         mma_bf16(qk[2 * np], aq[f], b[0], b[1]);
@@ -238,6 +238,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
                     mma_bf16(y[1], x[l][1], bh[2], bh[3]);
                     mma_bf16(y[0], x[l][0], bl[0], bl[1]);
                     mma_bf16(y[1], x[l][0], bl[2], bl[3]);
+                    mma_bf16(y[0], x[l][1], bl[0], bl[1]);
+                    mma_bf16(y[1], x[l][1], bl[2], bl[3]);
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -254,6 +256,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
                 mma_bf16(z[1], f[1], bh[2], bh[3]);
                 mma_bf16(z[0], f[0], bl[0], bl[1]);
                 mma_bf16(z[1], f[0], bl[2], bl[3]);
+                mma_bf16(z[0], f[1], bl[0], bl[1]);
+                mma_bf16(z[1], f[1], bl[2], bl[3]);
                 split_tiles(z[0], z[1], x[d]);
                 const uint32_t at = img(base + M::kT, 16 * i + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1));
                 stsm4_t(at, x[d][0][0], x[d][0][1], x[d][0][2], x[d][0][3]);
@@ -262,6 +266,12 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
         }
         __syncthreads();
 
+        if (tid < kChunk) {   // the image is T - 1
+            const uint32_t at = img(0, tid, tid >> 3) + (tid & 7) * 2;
+            *reinterpret_cast<uint16_t *>(smem + M::kT + at) = 0;
+            *reinterpret_cast<uint16_t *>(smem + M::kT + kSquare + at) = 0;
+        }
+        __syncthreads();
         unsigned char *out = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
         constexpr int imgs = 4 * (int)kSquare / 16;   // T and P follow one another on both sides
 #pragma unroll 4
