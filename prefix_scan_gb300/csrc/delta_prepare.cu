@@ -16,6 +16,10 @@ namespace ps {
 namespace {
 
 constexpr int kPrepThreads = 128;   // four warps: 16 rows of a 64 x 64 product each
+// Scalars of a value head: the six arrays of ChunkLayout; exp(G_i - G_m) with m the last token before i's
+// block of 16 (1 in the first block); exp(G_m - G_j) for the m of each of blocks 1, 2, 3.  Both are at most
+// 1, and their product is D below the diagonal blocks, at one exponential a row and column.
+constexpr int kRow = 6 * kChunk, kCol = 7 * kChunk, kScalars = 10 * kChunk;
 constexpr int kDiag = 264;          // floats from one diagonal block to the next: 16 x 16, and 8 against bank conflicts
 
 template <int NP, int KP>
@@ -24,7 +28,7 @@ struct PrepSmem {
     static constexpr int kK = 0, kQ = kChunk * 128;
     static constexpr int kT = 0, kP = 2 * (int)kSquare, kN = 4 * (int)kSquare;   // in the place of K and Q
     static constexpr int kScal = NP * kPlane > 6 * (int)kSquare ? NP * kPlane : 6 * (int)kSquare;
-    static constexpr int kL = kScal + 6 * kChunk * 4;                            // f32 diagonal blocks of diag(beta) N
+    static constexpr int kL = kScal + 4 * kScalars * 4;                          // f32 diagonal blocks of diag(beta) N
     static constexpr int kBytes = kL + 4 * kDiag * 4;
 };
 
@@ -36,13 +40,12 @@ constexpr float kLeastBeta = 0x1p-60f;
 }  // namespace
 
 template <typename T, int KP>
-__global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const DeltaArgs a) {
     constexpr int NP = Planes<T>::NP;
     using M = PrepSmem<NP, KP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
     float *L = reinterpret_cast<float *>(smem + M::kL);
-    float *scal = reinterpret_cast<float *>(smem + M::kScal);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long slot = blockIdx.x;
     const int head_k = blockIdx.y, rep = a.s.hv / a.s.hk;
@@ -58,6 +61,66 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
     load_tile<T, KP>(base + M::kQ, M::kPlane, row_ptr<T>(a.q, sp, seq, t0, head_k), a.q.tok, rows, a.s.k, a.vec_qk != 0,
                      tid, kPrepThreads);
     cp_async_commit();
+    // the scalars of four value heads from the hr-th on, one per warp: tokens 2 lane, 2 lane + 1
+    auto scalars = [&](int hr) {
+        if (hr + warp < rep) {
+            float *sc = reinterpret_cast<float *>(smem + M::kScal) + warp * kScalars;
+            const int head = head_k * rep + hr + warp;
+            const float *gp = row_ptr<float>(a.g, sp, seq, t0, head);
+            float g[2], b[2] = {0.f, 0.f};
+            bool f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                g[e] = i < rows ? gp[i * a.g.tok] : 0.f;
+                if (i < rows)
+                    b[e] = a.beta_f32 ? row_ptr<float>(a.beta, sp, seq, t0, head)[i * a.beta.tok]
+                                      : to_f32<T>(row_ptr<T>(a.beta, sp, seq, t0, head)[i * a.beta.tok]);
+                if (fabsf(b[e]) < kLeastBeta) b[e] = kLeastBeta;
+                f[e] = g[e] <= kForget;
+                if (f[e]) g[e] = 0.f;
+            }
+            // running sums of g in 64 bits, kept as two floats: differences of far sums stay exact to
+            // f32.  Tokens that forget the state start a new count r; sums go on without them.
+            double sum = (double)g[0] + (double)g[1];
+            int cnt = (int)f[0] + (int)f[1];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const double s2 = __shfl_up_sync(0xffffffffu, sum, d);
+                const int c2 = __shfl_up_sync(0xffffffffu, cnt, d);
+                if (lane >= d) { sum += s2; cnt += c2; }
+            }
+            const double last = __shfl_sync(0xffffffffu, sum, 31);
+            const int rlast = __shfl_sync(0xffffffffu, cnt, 31);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                const double G = e ? sum : sum - (double)g[1];
+                const int r = e ? cnt : cnt - (int)f[1];
+                const float hi = (float)G;
+                sc[i] = r == 0 ? expf((float)G) : 0.f;
+                sc[64 + i] = i < rows && r == rlast ? expf((float)(last - G)) : 0.f;
+                sc[128 + i] = b[e];
+                sc[192 + i] = hi;
+                sc[256 + i] = (float)(G - (double)hi);
+                sc[320 + i] = (float)r;
+            }
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {   // m = 16 blk - 1, in lane 8 blk - 1
+                const double Gm = __shfl_sync(0xffffffffu, sum, blk ? 8 * blk - 1 : 0);
+                const int rm = __shfl_sync(0xffffffffu, cnt, blk ? 8 * blk - 1 : 0);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 2 * lane + e;
+                    const double G = e ? sum : sum - (double)g[1];
+                    const int r = e ? cnt : cnt - (int)f[1];
+                    if (i >> 4 == blk) sc[kRow + i] = blk == 0 ? 1.f : r == rm ? expf((float)(G - Gm)) : 0.f;
+                    if (blk && i < 16 * blk) sc[kCol + (blk - 1) * kChunk + i] = r == rm ? expf((float)(Gm - G)) : 0.f;
+                }
+            }
+        }
+    };
+    scalars(0);   // while keys and queries are on their way
     cp_async_wait<0>();
     __syncthreads();
 
@@ -104,84 +167,59 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prepare_kernel(const Delta
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
     for (int hr = 0; hr < rep; ++hr) {
         const int head = head_k * rep + hr;
-        if (warp == 0) {
-            // running sums of g in 64 bits, kept as two floats: differences of far sums stay exact to
-            // f32.  Tokens that forget the state start a new count r; sums go on without them.
-            const float *gp = row_ptr<float>(a.g, sp, seq, t0, head);
-            float g0 = 2 * lane < rows ? gp[(2 * lane) * a.g.tok] : 0.f;
-            float g1 = 2 * lane + 1 < rows ? gp[(2 * lane + 1) * a.g.tok] : 0.f;
-            const bool f0 = g0 <= kForget, f1 = g1 <= kForget;
-            if (f0) g0 = 0.f;
-            if (f1) g1 = 0.f;
-            double sum = (double)g0 + (double)g1;
-            int cnt = (int)f0 + (int)f1;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double s2 = __shfl_up_sync(0xffffffffu, sum, d);
-                const int c2 = __shfl_up_sync(0xffffffffu, cnt, d);
-                if (lane >= d) { sum += s2; cnt += c2; }
-            }
-            const double last = __shfl_sync(0xffffffffu, sum, 31);
-            const int rlast = __shfl_sync(0xffffffffu, cnt, 31);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * lane + e;
-                const double G = e ? sum : sum - (double)g1;
-                const int r = e ? cnt : cnt - (int)f1;
-                const float hi = (float)G;
-                scal[i] = r == 0 ? expf((float)G) : 0.f;
-                scal[64 + i] = i < rows && r == rlast ? expf((float)(last - G)) : 0.f;
-                scal[192 + i] = hi;
-                scal[256 + i] = (float)(G - (double)hi);
-                scal[320 + i] = (float)r;
-            }
-        } else if (warp < 3) {
-            const int i = tid - 32;
-            float b = 0.f;
-            if (i < rows)
-                b = a.beta_f32 ? row_ptr<float>(a.beta, sp, seq, t0, head)[i * a.beta.tok]
-                               : to_f32<T>(row_ptr<T>(a.beta, sp, seq, t0, head)[i * a.beta.tok]);
-            if (fabsf(b) < kLeastBeta) b = kLeastBeta;
-            scal[128 + i] = b;
+        float *scal = reinterpret_cast<float *>(smem + M::kScal) + (hr & 3) * kScalars;
+        if (hr > 0 && (hr & 3) == 0) {
+            scalars(hr);
+            __syncthreads();
         }
-        __syncthreads();
 
         {   // P and N as pairs, the diagonal blocks of diag(beta) N in f32
-            const int r8 = lane >> 2, i0 = 16 * warp + r8;
-            const float gh0 = scal[192 + i0], gl0 = scal[256 + i0], r0 = scal[320 + i0], b0 = scal[128 + i0];
-            const float gh1 = scal[200 + i0], gl1 = scal[264 + i0], r1 = scal[328 + i0], b1 = scal[136 + i0];
+            const int r8 = lane >> 2, i0 = 16 * warp + r8, c2 = 2 * (lane & 3);
+            const float row0 = scal[kRow + i0], row1 = scal[kRow + i0 + 8];
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
+                const uint32_t at = img(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
                 if (np > warp) {   // above the diagonal: T and P are 0, N is not read
-                    const uint32_t at = img(base + M::kT, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) stsm4(at + m * (uint32_t)kSquare, 0, 0, 0, 0);
+                    for (int m = 0; m < 4; ++m) stsm4(base + M::kT + at + m * (uint32_t)kSquare, 0, 0, 0, 0);
                     continue;
                 }
-                uint32_t ph[4], pl[4], nh[4], nl[4];
+                float nv[2][4], pv[2][4];   // tiles of the block
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {   // register q of the block's fragment: tile q >> 1, rows +8 for odd q
-                    const int n = 2 * np + (q >> 1), row = q & 1, i = i0 + 8 * row, j = 8 * n + 2 * (lane & 3);
-                    float pv[2], nv[2];
+                for (int t = 0; t < 2; ++t) {
+                    const int n = 2 * np + t, j = 8 * n + c2;
+                    if (np < warp) {
+                        const float2 col = *reinterpret_cast<const float2 *>(scal + kCol + (warp - 1) * kChunk + j);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int c = j + e;
-                        const float dx = ((row ? gh1 : gh0) - scal[192 + c]) + ((row ? gl1 : gl0) - scal[256 + c]);
-                        const float D = i >= c && (row ? r1 : r0) == scal[320 + c] ? expf(dx) : 0.f;
-                        nv[e] = i > c ? D * kk[n][2 * row + e] : 0.f;
-                        pv[e] = i >= c ? a.s.scale * D * qk[n][2 * row + e] : 0.f;
+                        for (int e = 0; e < 4; ++e) {
+                            const float D = (e < 2 ? row0 : row1) * (e & 1 ? col.y : col.x);
+                            nv[t][e] = D * kk[n][e];
+                            pv[t][e] = a.s.scale * D * qk[n][e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = i0 + 8 * (e >> 1), c = j + (e & 1);
+                            const float dx = (scal[192 + i] - scal[192 + c]) + (scal[256 + i] - scal[256 + c]);
+                            const float D = i >= c && scal[320 + i] == scal[320 + c] ? expf(dx) : 0.f;
+                            nv[t][e] = i > c ? D * kk[n][e] : 0.f;
+                            pv[t][e] = i >= c ? a.s.scale * D * qk[n][e] : 0.f;
+                        }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float be = scal[128 + i0 + 8 * r];
+                            *reinterpret_cast<float2 *>(L + warp * kDiag + (r8 + 8 * r) * 16 + 8 * t + c2) =
+                                make_float2(be * nv[t][2 * r], be * nv[t][2 * r + 1]);
+                        }
                     }
-                    if (np == warp)
-                        *reinterpret_cast<float2 *>(L + warp * kDiag + (r8 + 8 * row) * 16 + (j & 15)) =
-                            make_float2((row ? b1 : b0) * nv[0], (row ? b1 : b0) * nv[1]);
-                    split2(pv[0], pv[1], ph[q], pl[q]);
-                    split2(nv[0], nv[1], nh[q], nl[q]);
                 }
-                const uint32_t at = img(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
-                stsm4(base + M::kP + at, ph[0], ph[1], ph[2], ph[3]);
-                stsm4(base + M::kP + (uint32_t)kSquare + at, pl[0], pl[1], pl[2], pl[3]);
-                stsm4(base + M::kN + at, nh[0], nh[1], nh[2], nh[3]);
-                stsm4(base + M::kN + (uint32_t)kSquare + at, nl[0], nl[1], nl[2], nl[3]);
+                uint32_t f[2][4];
+                split_tiles(pv[0], pv[1], f);
+                stsm4(base + M::kP + at, f[0][0], f[0][1], f[0][2], f[0][3]);
+                stsm4(base + M::kP + (uint32_t)kSquare + at, f[1][0], f[1][1], f[1][2], f[1][3]);
+                split_tiles(nv[0], nv[1], f);
+                stsm4(base + M::kN + at, f[0][0], f[0][1], f[0][2], f[0][3]);
+                stsm4(base + M::kN + (uint32_t)kSquare + at, f[1][0], f[1][1], f[1][2], f[1][3]);
             }
         }
         __syncthreads();
