@@ -12,14 +12,20 @@
  *
  * Types: q, k, v and o are of one type (f32, bf16 or f16); beta of that type
  * or f32; g, states and gradients of states and of g are f32.  States and all
- * sums are held in 32 bits; matrix products take operands of 16 significant
- * bits or more (pairs of bf16), so results carry errors of about 2^-17
- * relative to the terms that make them up, before their own rounding.
+ * sums are held in 32 bits; over whole sequences matrix products take operands
+ * of 16 significant bits or more (pairs of bf16), so results carry errors of
+ * about 2^-18 relative to the terms that make them up, before their own
+ * rounding.  Single steps are f32 throughout.
  *
  * Extreme inputs: a log decay at or below -87 (-infinity too), where exp(g)
  * leaves the normal range of f32, forgets the state entirely and has gradient
- * 0.  NaN and infinities reach the outputs of their own sequence and value
- * heads and no others.
+ * 0.  Log decays above 0 make states grow; sums of them over 64 tokens have to
+ * stay below 80.  A gate of 0 counts as 2^-60.  NaN and infinities reach the
+ * outputs of their own sequence, and of the heads that share the input, and
+ * no others (within a chunk of 64 tokens also those before them).
+ *
+ * A kernel of the sequence calls whose bounded waits ran out, which a correct
+ * launch never does, finishes with NaN in its outputs instead of hanging.
  *
  * Conventions: device pointers owned by the caller; work is enqueued on
  * `stream` and the call returns without waiting for it; no device memory is
@@ -100,9 +106,9 @@ ps_status ps_delta_forward(const ps_delta_shape *shape, const ps_delta_tensor in
                            void *o, int train, void *ws, size_t ws_bytes, ps_stream_t stream);
 
 /*
- * Backward of one ps_delta_forward(train != 0) call with the same shape, q,
- * k and beta; `ws` is that call's workspace, which one backward call may use
- * any number of times but which must not change otherwise.
+ * Backward of one ps_delta_forward(train != 0) call with the same shape, q
+ * and k; `ws` is that call's workspace, which any number of backward calls may
+ * use one after the other but which must not change otherwise.
  *   d_o   gradient of o;  d_ht  gradient of ht or NULL (0)
  *   dq, dk [.., heads_k, dim_k], dv [.., heads_v, dim_v], dbeta, dg
  *         [.., heads_v]: contiguous; dq and dk are summed over the value

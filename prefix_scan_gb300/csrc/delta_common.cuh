@@ -215,12 +215,6 @@ __device__ __forceinline__ void load_image(uint32_t dst, const void *src, int ti
     constexpr int DONE = BYTES / (16 * THREADS) * 16 * THREADS;
     if (DONE < BYTES && DONE + tid * 16 < BYTES) cp_async16(dst + DONE, s + DONE, true);
 }
-// The same for the first `bytes` of an image of at most MOST.
-template <int MOST, int THREADS>
-__device__ __forceinline__ void load_part(uint32_t dst, const void *src, int bytes, int tid) {
-    if (bytes == MOST) return load_image<MOST, THREADS>(dst, src, tid);
-    for (int i = tid * 16; i < bytes; i += THREADS * 16) cp_async16(dst + i, static_cast<const char *>(src) + i, true);
-}
 // ---- sequences and chunks ----------------------------------------------------------
 
 // Where a sequence's tokens lie.  Offsets that do not increase, or that leave
