@@ -45,12 +45,15 @@ struct ChainSmem {
     static constexpr int kStages = NP == 1 ? 2 : 1;
     static constexpr int kScal = 256, kTiles = 2048, kStage = kKQ + kTP;   // barriers and scalars come first
     static constexpr int kVRow = kBlockV * (int)sizeof(T), kVTile = kChunk * kVRow, kV = kTiles + kStages * kStage;
-    static constexpr int kOut = kV + kVTile, kSave = kOut + kVTile;   // outputs; what training keeps: S, later U
-    static constexpr int kBytes = kSave, kTrainBytes = kSave + 2 * (KP / 64 > 1 ? 2 : 1) * kHalf;
+    // outputs; S on its way out in training; U, which at K = 128 takes the place of T and of the queries
+    // (both used by then) in its stage
+    static constexpr int kOut = kV + kVTile, kSave = kOut + kVTile, kSaveU = kSave + 2 * (KP / 64) * kHalf;
+    static constexpr bool kInStage = KP == 128;
+    static constexpr int kBytes = kSave, kTrainBytes = kSaveU + (kInStage ? 0 : 2 * kHalf);
     static_assert(kTrainBytes <= 227 * 1024, "too much shared memory");
 };
 struct ChainBars {
-    uint64_t full[2], empty[2], v_full, v_empty, s_ready[2], x_done, q_read, r_ready, u_done, w_ready, u_ready, s_done, o_done, o_read, s_free, u_free, drained;
+    uint64_t full[2], empty[2], v_full, v_empty, s_ready[2], x_done, q_read, r_ready, u_done, w_ready, u_ready, s_done, o_done, o_read, s_kept, s_free, u_free, drained;
     uint32_t tmem;
     int gave_up;
 };
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], states ? 1 : 1 + 4);
+            mbar_init(&bar.empty[i], states ? 1 : 1 + 4 + (keep && M::kInStage));
         }
         mbar_init(&bar.v_full, 32);
         mbar_init(&bar.v_empty, 8);
@@ -109,6 +112,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
         mbar_init(&bar.s_done, 1);
         mbar_init(&bar.o_done, 1);
         mbar_init(&bar.o_read, 4);
+        mbar_init(&bar.s_kept, 8);
         mbar_init(&bar.s_free, 1);
         mbar_init(&bar.u_free, 1);
         mbar_init(&bar.drained, 1);
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             const int rows = min(kBlockV, (a.s.v - v0 + 15) / 16 * 16);
             for (int c = 0; c < chunks; ++c) {
                 unsigned char *w = chunk_ws(c);
-                for (int r = 0; r < KH; ++r) wait_phase(&bar.s_ready[r], c & 1, gave_up);
+                wait_phase(&bar.s_kept, c & 1, gave_up);
 #pragma unroll
                 for (int p = 0; p < 2 * KH; ++p)
                     bulk_store(w + lay.s + (size_t)(vb * 2 * KH + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
@@ -209,12 +213,18 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                 bulk_wait_read();
                 mbar_arrive(&bar.s_free);
                 wait_phase(&bar.u_ready, c & 1, gave_up);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    bulk_store(w + lay.u + (size_t)(vb * 2 + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
+                unsigned char *u = w + lay.u + (size_t)vb * 2 * kHalf;
+                if (M::kInStage) {
+                    const uint32_t tiles = base + M::kTiles + c % M::kStages * M::kStage;
+                    bulk_store(u, tiles + M::kKQ, rows * 128);
+                    bulk_store(u + kHalf, tiles + kChunk * 128, min(rows, kChunk) * 128);
+                    if (rows > kChunk) bulk_store(u + kHalf + kChunk * 128, tiles + kHalf + kChunk * 128, (rows - kChunk) * 128);
+                } else {
+                    for (int p = 0; p < 2; ++p) bulk_store(u + p * kHalf, base + M::kSaveU + p * kHalf, rows * 128);
+                }
                 bulk_commit();
                 bulk_wait_read();
-                mbar_arrive(&bar.u_free);
+                mbar_arrive(M::kInStage ? &bar.empty[c % M::kStages] : &bar.u_free);
             }
             bulk_wait();
         }
@@ -302,7 +312,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             wait_phase(&bar.full[st], (c / M::kStages) & 1, gave_up);
             const float eall = scal[kChunk - 1 - 32 * half];
             if (c > 0) {
-                if (keep) wait_phase(&bar.u_free, (c - 1) & 1, gave_up);
+                if (keep) wait_phase(&bar.s_free, (c - 1) & 1, gave_up);
                 wait_phase(&bar.s_done, (c - 1) & 1, gave_up);
                 tmem_fence_after();
             }
@@ -319,10 +329,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                     tmem_st16(at + kColS + 16 * (k16 + b), x[b]);
                     if (keep) keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
                 }
-                if (keep) fence_async();
                 tmem_wait_st();
                 tmem_fence_before();
                 warp_arrive(&bar.s_ready[r], lane);
+            }
+            if (keep) {
+                fence_async();
+                warp_arrive(&bar.s_kept, lane);
             }
 
             wait_phase(&bar.x_done, c & 1, gave_up);
@@ -374,13 +387,17 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             tmem_fence_before();
             warp_arrive(&bar.w_ready, lane);
             if (states) continue;
-            if (keep) wait_phase(&bar.s_free, c & 1, gave_up);
+            if (keep && !M::kInStage && c > 0) wait_phase(&bar.u_free, (c - 1) & 1, gave_up);
+            // U's upper part where T was, the lower one where the queries were: row 64 in the second half
+            const uint32_t tiles = base + M::kTiles + st * M::kStage;
+            const uint32_t u_hi = M::kInStage ? tiles + M::kKQ : base + M::kSaveU;
+            const uint32_t u_lo = M::kInStage ? tiles + (row < kChunk ? kChunk * 128 : kHalf) : base + M::kSaveU + kHalf;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 split16(x[b], hi, lo);
                 tmem_st8(at + kColR + 16 * half + 8 * b, hi);
                 tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
-                if (keep) keep16(base + M::kSave, kHalf, row, 2 * half + b, hi, lo);
+                if (keep) keep16(u_hi, u_lo - u_hi, row, 2 * half + b, hi, lo);
             }
             if (keep) fence_async();
             tmem_wait_st();

@@ -32,12 +32,16 @@ struct BackSmem {
     static constexpr int kStages = NP == 1 ? 2 : 1;
     static constexpr int kScal = 256, kTiles = 2048, kStage = kKQ + kTP;   // barriers and two chunks' scalars come first
     static constexpr int kRow = kBlockV * (int)sizeof(T), kTile = kChunk * kRow;
-    static constexpr int kDO = kTiles + kStages * kStage, kOut = kDO + kTile, kSave = kOut + kTile;   // kSave: dS', later dU
-    static constexpr int kBytes = kSave + 2 * (KP / 64 > 1 ? 2 : 1) * kHalf;
+    static constexpr int kDO = kTiles + kStages * kStage, kOut = kDO + kTile, kSave = kOut + kTile;
+    // dS' on its way out, and dU, which at K = 128 takes the place of T and of the queries (both used by
+    // then) in its stage
+    static constexpr int kSaveU = kSave + 2 * (KP / 64) * kHalf;
+    static constexpr bool kInStage = KP == 128;
+    static constexpr int kBytes = kSaveU + (kInStage ? 0 : 2 * kHalf);
 };
 struct BackBars {
     uint64_t full[2], empty[2], o_full, o_empty, o_ready, s_ready[2], y_done, r_ready, u_done, w_ready, s_done, out_ready, out_free;
-    uint64_t s_free, u_free, drained;
+    uint64_t s_kept, s_free, u_free, drained;
     uint32_t tmem;
     int gave_up;
 };
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], 1);
+            mbar_init(&bar.empty[i], 1 + (!states && M::kInStage));
             mbar_init(&bar.s_ready[i], 8);
         }
         mbar_init(&bar.o_full, 32);
@@ -95,6 +99,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         mbar_init(&bar.s_done, 1);
         mbar_init(&bar.out_ready, 8);
         mbar_init(&bar.out_free, 4);
+        mbar_init(&bar.s_kept, 8);
         mbar_init(&bar.s_free, 1);
         mbar_init(&bar.u_free, 1);
         mbar_init(&bar.drained, 1);
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
             const int rows = min(kBlockV, (a.s.v - v0 + 15) / 16 * 16);
             for (int i = 0; i < chunks; ++i) {
                 unsigned char *w = chunk_ws(i);
-                for (int r = 0; r < KH; ++r) wait_phase(&bar.s_ready[r], i & 1, gave_up);
+                wait_phase(&bar.s_kept, i & 1, gave_up);
 #pragma unroll
                 for (int p = 0; p < 2 * KH; ++p)
                     bulk_store(w + lay.ds + (size_t)(vb * 2 * KH + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
@@ -192,12 +197,18 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
                 bulk_wait_read();
                 mbar_arrive(&bar.s_free);
                 wait_phase(&bar.out_ready, i & 1, gave_up);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    bulk_store(w + lay.du + (size_t)(vb * 2 + p) * kHalf, base + M::kSave + p * kHalf, rows * 128);
+                unsigned char *u = w + lay.du + (size_t)vb * 2 * kHalf;
+                if (M::kInStage) {
+                    const uint32_t tiles = base + M::kTiles + i % M::kStages * M::kStage;
+                    bulk_store(u, tiles + M::kKQ, rows * 128);
+                    bulk_store(u + kHalf, tiles + kChunk * 128, min(rows, kChunk) * 128);
+                    if (rows > kChunk) bulk_store(u + kHalf + kChunk * 128, tiles + kHalf + kChunk * 128, (rows - kChunk) * 128);
+                } else {
+                    for (int p = 0; p < 2; ++p) bulk_store(u + p * kHalf, base + M::kSaveU + p * kHalf, rows * 128);
+                }
                 bulk_commit();
                 bulk_wait_read();
-                mbar_arrive(&bar.u_free);
+                mbar_arrive(M::kInStage ? &bar.empty[i % M::kStages] : &bar.u_free);
             }
             bulk_wait();
         }
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
             const float *scal = scalars(i);
             const float eall = scal[kChunk - 1 - 32 * half];
             if (i > 0) {
-                if (!states) wait_phase(&bar.u_free, (i - 1) & 1, gave_up);
+                if (!states) wait_phase(&bar.s_free, (i - 1) & 1, gave_up);
                 wait_phase(&bar.s_done, (i - 1) & 1, gave_up);
                 tmem_fence_after();
             }
@@ -310,10 +321,13 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
                     tmem_st16(at + kColS + 16 * (k16 + b), x[b]);
                     if (!states) keep16(base + M::kSave, KH * kHalf, row, k16 + b, hi, lo);
                 }
-                if (!states) fence_async();
                 tmem_wait_st();
                 tmem_fence_before();
                 warp_arrive(&bar.s_ready[r], lane);
+            }
+            if (!states) {
+                fence_async();
+                warp_arrive(&bar.s_kept, lane);
             }
 
             wait_phase(&bar.y_done, i & 1, gave_up);
@@ -371,13 +385,17 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
                 if (i + 1 < chunks) outputs(i + 1);
                 continue;
             }
-            wait_phase(&bar.s_free, i & 1, gave_up);
+            if (!M::kInStage && i > 0) wait_phase(&bar.u_free, (i - 1) & 1, gave_up);
+            // dU's upper part where T was, the lower one where the queries were: row 64 in the second half
+            const uint32_t tiles = base + M::kTiles + i % M::kStages * M::kStage;
+            const uint32_t u_hi = M::kInStage ? tiles + M::kKQ : base + M::kSaveU;
+            const uint32_t u_lo = M::kInStage ? tiles + (row < kChunk ? kChunk * 128 : kHalf) : base + M::kSaveU + kHalf;
             if (i > 0) wait_phase(&bar.out_free, (i - 1) & 1, gave_up);
             T *stage = reinterpret_cast<T *>(smem + M::kOut) + 32 * half * kBlockV + row;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 split16(x[b], hi, lo);
-                keep16(base + M::kSave, kHalf, row, 2 * half + b, hi, lo);
+                keep16(u_hi, u_lo - u_hi, row, 2 * half + b, hi, lo);
                 scale16(x[b], scal + 128 + 16 * b);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) stage[(16 * b + j) * kBlockV] = from_f32<T>(x[b][j]);
