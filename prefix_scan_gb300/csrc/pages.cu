@@ -3,9 +3,9 @@
 //
 // Each call that hands out or moves pages is a plan and a move.  The plan is
 // one CTA of 1024 threads that scans the reference counts in tiles of 16384
-// pages (sixteen per thread, in order: ranks of free or used pages by warp and
-// block scans) and writes lists into the workspace; a plan that hands out pages
-// ends at the first tile that holds enough of them.  The move is a grid of CTAs
+// pages (ranks of free or used pages from ballots and a sum over the warps) and
+// writes lists into the workspace; a plan that hands out pages ends at the first
+// tile that holds enough of them.  The move is a grid of CTAs
 // that copy pieces of pages and rewrite the tables.  Moves are bound by memory:
 // a moved page is read once and written once.
 #include <climits>
@@ -70,41 +70,57 @@ __device__ __forceinline__ int block_exclusive(int x, int *warps, int &total) {
     return s - x + __shfl_sync(0xffffffffu, t - w, warp);
 }
 
-// This thread's counts of a tile, -1 past the end (used: not free, but not to be counted either).
-__device__ __forceinline__ void load_counts(int (&c)[kPlanItems], const int32_t *refcount, long long at, long long pages,
-                                            bool vec, int pad) {
-#pragma unroll
-    for (int i = 0; i < kPlanItems; i += 4) {
-        if (vec && at + i + 4 <= pages) {
-            const int4 v = *reinterpret_cast<const int4 *>(refcount + at + i);
-            c[i] = v.x; c[i + 1] = v.y; c[i + 2] = v.z; c[i + 3] = v.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[i + j] = at + i + j < pages ? refcount[at + i + j] : pad;
-        }
-    }
+// A tile's pages by warps: warp w holds pages 512 w ... 512 w + 511 of it, lane l of its item i page 32 i + l, so loads
+// and the lists' stores are whole lines, and a page's rank comes from the ballots of its warp.
+__device__ __forceinline__ long long tile_page(long long base, int item) {
+    return base + (threadIdx.x >> 5) * (32 * kPlanItems) + item * 32 + (threadIdx.x & 31);
 }
+// Bit l of mask[i]: whether page 32 i + l of the warp's holds `is_used`; pages past the end hold neither.
+__device__ __forceinline__ void load_masks(uint32_t (&mask)[kPlanItems], const int32_t *refcount, long long base,
+                                           long long pages, bool is_used) {
+    int32_t c[kPlanItems];
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+        const long long p = tile_page(base, i);
+        c[i] = p < pages ? refcount[p] : is_used ? 0 : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) mask[i] = __ballot_sync(0xffffffffu, (c[i] > 0) == is_used);
+}
+// How many pages of the masks come before the warp's; `total` receives how many the tile has.
+__device__ __forceinline__ int before_warp(const uint32_t (&mask)[kPlanItems], int *warps, int &total) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) n += __popc(mask[i]);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();   // the last call's sums have been read
+    if (lane == 0) warps[warp] = n;
+    __syncthreads();
+    const int w = warps[lane];
+    total = __reduce_add_sync(0xffffffffu, w);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+}
+__device__ __forceinline__ uint32_t lanes_before() { return (1u << (threadIdx.x & 31)) - 1; }
 
 // Hands out the `want` lowest free pages: list[i] is the i-th, its count becomes 1.  Returns how many there were.
 __device__ int take_free(int32_t *refcount, long long pages, long long want, int32_t *list, int *warps) {
-    const bool vec = (reinterpret_cast<uintptr_t>(refcount) & 15) == 0;
+    const int lane = threadIdx.x & 31;
     long long have = 0;
     for (long long base = 0; base < pages && have < want; base += kPlanTile) {
-        const long long at = base + (long long)threadIdx.x * kPlanItems;
-        int c[kPlanItems], n = 0, total;
-        load_counts(c, refcount, at, pages, vec, 1);
+        uint32_t free_pages[kPlanItems];
+        int total;
+        load_masks(free_pages, refcount, base, pages, false);
+        long long r = have + before_warp(free_pages, warps, total);
 #pragma unroll
-        for (int i = 0; i < kPlanItems; ++i) n += c[i] <= 0;
-        long long r = have + block_exclusive(n, warps, total);
-#pragma unroll
-        for (int i = 0; i < kPlanItems; ++i)
-            if (c[i] <= 0) {
-                if (r < want) {
-                    list[r] = (int32_t)(at + i);
-                    refcount[at + i] = 1;
-                }
-                ++r;
+        for (int i = 0; i < kPlanItems; ++i) {
+            const long long at = r + __popc(free_pages[i] & lanes_before());
+            if ((free_pages[i] >> lane & 1) && at < want) {
+                const long long p = tile_page(base, i);
+                list[at] = (int32_t)p;
+                refcount[p] = 1;
             }
+            r += __popc(free_pages[i]);
+        }
         have += total;
     }
     return (int)(have < want ? have : want);
@@ -297,55 +313,44 @@ struct CompactArgs {
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const CompactArgs a) {
     __shared__ int warps[32];
     __shared__ int below;   // pages in use below m
-    const bool vec = (reinterpret_cast<uintptr_t>(a.refcount) & 15) == 0;
-    int c[kPlanItems];
+    const int lane = threadIdx.x & 31;
+    uint32_t used[kPlanItems];
     long long m = 0;
     for (long long base = 0; base < a.pages; base += kPlanTile) {
-        const long long at = base + (long long)threadIdx.x * kPlanItems;
-        int n = 0, total;
-        load_counts(c, a.refcount, at, a.pages, vec, 0);
-#pragma unroll
-        for (int i = 0; i < kPlanItems; ++i) n += c[i] > 0;
-        block_exclusive(n, warps, total);
+        int total;
+        load_masks(used, a.refcount, base, a.pages, true);
+        before_warp(used, warps, total);
         m += total;
     }
     if (threadIdx.x == 0) below = (int)m;   // m == pages: nothing moves
     long long rank = 0;                     // pages in use before the tile
     for (long long base = 0; base < a.pages; base += kPlanTile) {
-        const long long at = base + (long long)threadIdx.x * kPlanItems;
-        int n = 0, total;
-        if (a.pages > kPlanTile) load_counts(c, a.refcount, at, a.pages, vec, 0);
-#pragma unroll
-        for (int i = 0; i < kPlanItems; ++i) n += c[i] > 0;
-        const long long r0 = rank + block_exclusive(n, warps, total);
+        int total;
+        if (a.pages > kPlanTile) load_masks(used, a.refcount, base, a.pages, true);
+        const long long r0 = rank + before_warp(used, warps, total);
         long long r = r0;
 #pragma unroll
         for (int i = 0; i < kPlanItems; ++i) {
-            if (at + i == m && m < a.pages) below = (int)r;
-            r += c[i] > 0;
+            if (tile_page(base, i) == m && m < a.pages) below = (int)(r + __popc(used[i] & lanes_before()));
+            r += __popc(used[i]);
         }
         __syncthreads();
         r = r0;
 #pragma unroll
         for (int i = 0; i < kPlanItems; ++i) {
-            const long long p = at + i;
+            const long long p = tile_page(base, i), at = r + __popc(used[i] & lanes_before());
             if (p < a.pages) {
-                const bool in = c[i] > 0;
-                if (in && p >= m) a.w.from[r - below] = (int32_t)p;
-                if (!in && p < m) a.w.list[p - r] = (int32_t)p;
-                a.w.to[p] = !in ? -1 : p < m ? (int32_t)p : -2 - (int32_t)(r - below);
-                r += in;
+                const bool in = used[i] >> lane & 1;
+                if (in && p >= m) a.w.from[at - below] = (int32_t)p;
+                if (!in && p < m) a.w.list[p - at] = (int32_t)p;
+                a.w.to[p] = !in ? -1 : p < m ? (int32_t)p : -2 - (int32_t)(at - below);
             }
+            r += __popc(used[i]);
         }
         rank += total;
     }
     __syncthreads();
     const int moves = (int)(m - below);
-    for (int i = threadIdx.x; i < moves; i += kPlanThreads) {   // no page is on both lists
-        const int32_t f = a.w.from[i], t = a.w.list[i];
-        a.refcount[t] = a.refcount[f];
-        a.refcount[f] = 0;
-    }
     if (threadIdx.x == 0) {
         a.w.head[0] = moves;
         if (a.used) *a.used = (int32_t)m;
@@ -356,6 +361,11 @@ __global__ void __launch_bounds__(kMoveThreads) pages_compact_kernel(const Compa
     for (long long t = blockIdx.x; t < tasks; t += gridDim.x) {
         const long long i = t / pools.pieces;
         move_piece(pools, (int)(t % pools.pieces), a.w.from[i], a.w.list[i]);
+    }
+    for (long long i = (long long)blockIdx.x * kMoveThreads + threadIdx.x; i < a.w.head[0]; i += (long long)gridDim.x * kMoveThreads) {
+        const int32_t f = a.w.from[i], to = a.w.list[i];   // no page is on both lists
+        a.refcount[to] = a.refcount[f];
+        a.refcount[f] = 0;
     }
     const long long n = a.rows * a.width;
     for (long long i = (long long)blockIdx.x * kMoveThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kMoveThreads) {
@@ -531,7 +541,7 @@ extern "C" ps_status ps_pages_compact(int32_t *table, int64_t rows, int64_t widt
     pages_compact_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && pages > 0) {
-        const long long tasks = (long long)p.pieces * pages / 2 + (rows * width + kMoveThreads - 1) / kMoveThreads;
+        const long long tasks = (long long)p.pieces * pages / 2 + (rows * width + pages / 2) / kMoveThreads + 1;
         pages_compact_kernel<<<move_grid(tasks), kMoveThreads, 0, s>>>(a, p);
         e = cudaGetLastError();
     }
