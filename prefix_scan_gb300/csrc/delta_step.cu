@@ -8,7 +8,7 @@
 // summed in one pass over the decayed state, because
 //     q^T (S + k u^T) = q^T S + (q.k) u,
 // so a token costs one exchange between the warps.
-#include "delta_common.cuh"
+#include "delta_tmem.cuh"
 
 namespace ps {
 
@@ -32,7 +32,7 @@ __device__ __forceinline__ void fma4(float4 &d, float a, const float4 &b) {
 
 // VT columns of the state per CTA: VT / 4 lanes hold a row's columns, four each.
 template <typename T, int KP, int VT>
-__global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaStepArgs a, const int vec4) {
+__global__ void __launch_bounds__(kStepThreads, 3) delta_step_kernel(const DeltaStepArgs a, const int vec4) {
     constexpr int LPR = VT / 4, GROUPS = kStepThreads / LPR, ROWS = KP / GROUPS;
     __shared__ float sk[kStepTokens][KP], sq[kStepTokens][KP];
     __shared__ float sa[kStepTokens], sb[kStepTokens], sqk[kStepTokens];
@@ -156,6 +156,243 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaSte
     }
 }
 
+// ---- many large states: a ring of whole states in shared memory --------------------
+// One CTA per SM takes its share of the heads in turn.  A head's state is one run of
+// bytes, so one thread moves it with one bulk copy each way: it stores the state that
+// is done and loads the one that is next in its place, two others being on their way
+// or at work meanwhile, so that reads and writes never pause for the sums.  Four warps
+// bring the tokens' small inputs (a token each) ahead of them, eight warps compute.
+
+namespace {
+
+constexpr int kRingStages = 3, kRingTokens = 4, kRingKV = 128;
+constexpr int kRingWarps = 8, kRingCompute = 32 * kRingWarps, kRingThreads = kRingCompute + 32 * (1 + kRingTokens);
+constexpr int kRingRows = kRingKV / kRingWarps, kRingCtas = 152;
+
+struct RingTokens {
+    float k[kRingTokens][kRingKV], q[kRingTokens][kRingKV], v[kRingTokens][kRingKV];
+    float decay[kRingTokens], beta[kRingTokens], qk[kRingTokens];
+    int count;
+    int pad[3];
+};
+struct RingSmem {
+    float state[kRingStages][kRingKV * kRingKV];
+    RingTokens in[kRingStages];
+    float4 sum_k[2][kRingWarps][32], sum_q[2][kRingWarps][32];
+    uint64_t state_full[kRingStages], in_full[kRingStages], done[kRingStages];
+    int gave_up;
+};
+static_assert(sizeof(RingSmem) <= 227 * 1024, "too much shared memory");
+
+// Whether any of the computing threads says so; all of them wait for one another.
+__device__ __forceinline__ bool any_computing(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)x), "n"(kRingCompute) : "memory");
+    return r != 0;
+}
+// How many tokens of the sequence count; 0 where its page does not exist.
+__device__ __forceinline__ int step_tokens(const DeltaStepArgs &a, long long seq, long long &page) {
+    page = a.slots ? a.slots[seq] : seq;
+    const int count = a.lengths ? a.lengths[seq] : a.t;
+    return page < 0 || page >= a.pages || count < 0 ? 0 : count > a.t ? a.t : count;
+}
+
+}  // namespace
+
+template <typename T>
+__global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const DeltaStepArgs a) {
+    extern __shared__ __align__(128) unsigned char ring_bytes[];
+    RingSmem &m = *reinterpret_cast<RingSmem *>(ring_bytes);
+    volatile int *gave_up = &m.gave_up;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long heads = a.seqs * a.hv;
+    const int items = (int)((heads - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    auto item = [&](int i, long long &seq, int &head) {
+        const long long x = blockIdx.x + (long long)i * gridDim.x;
+        seq = x / a.hv;
+        head = (int)(x % a.hv);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < kRingStages; ++i) {
+            mbar_init(&m.state_full[i], 1);
+            mbar_init(&m.in_full[i], kRingTokens);
+            mbar_init(&m.done[i], kRingWarps);
+        }
+        m.gave_up = 0;
+        mbar_init_done();
+    }
+    __syncthreads();
+
+    if (warp == kRingWarps) {   // states
+        if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(a.k * a.v) * 4;
+            const size_t words = (size_t)a.k * a.v;
+            float *at[kRingStages];   // where the stages' states belong; null where there is none
+#pragma unroll
+            for (int st = 0; st < kRingStages; ++st) at[st] = nullptr;
+            int begun = 0;   // loads
+            int i = 0;
+            for (; i < items + kRingStages; i += kRingStages)
+#pragma unroll
+                for (int st = 0; st < kRingStages; ++st) {
+                    const int now = i + st, before = now - kRingStages;
+                    long long seq, page;
+                    int head;
+                    float *to = nullptr;
+                    if (now < items) {
+                        item(now, seq, head);
+                        if (step_tokens(a, seq, page) > 0) to = a.state + (size_t)(page * a.hv + head) * words;
+                    }
+                    if (before >= 0 && before < items) {
+                        wait_phase(&m.done[st], (before / kRingStages) & 1, gave_up);
+                        if (!*gave_up && at[st] != nullptr) {
+                            bulk_store(at[st], smem_u32(m.state[st]), bytes);
+                            bulk_commit();
+                            bulk_wait_read();
+                        }
+                    }
+                    at[st] = to;
+                    if (now >= items || *gave_up) continue;
+                    begun = now + 1;
+                    if (to != nullptr) {
+                        mbar_arrive_expect_tx(&m.state_full[st], bytes);
+                        bulk_load(m.state[st], to, bytes, &m.state_full[st]);
+                    } else {
+                        mbar_arrive(&m.state_full[st]);
+                    }
+                }
+            bulk_wait();
+            if (*gave_up)   // loads in flight
+                for (int x = begun < kRingStages ? 0 : begun - kRingStages; x < begun; ++x)
+                    wait_drained(&m.state_full[x % kRingStages], (x / kRingStages) & 1);
+        }
+    } else if (warp > kRingWarps) {   // a token's inputs
+        const int t = warp - kRingWarps - 1;
+        const Span none{};
+        for (int i = 0; i < items; ++i) {
+            const int st = i % kRingStages;
+            long long seq, page;
+            int head;
+            item(i, seq, head);
+            const int head_k = head / (a.hv / a.hk), count = step_tokens(a, seq, page);
+            float k[4], q[4], v[4], g = 0.f, beta = 0.f, d = 0.f;
+            if (t < count) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int x = lane + 32 * j;
+                    k[j] = x < a.k ? to_f32<T>(row_ptr<T>(a.kk, none, seq, t, head_k)[x]) : 0.f;
+                    q[j] = x < a.k ? to_f32<T>(row_ptr<T>(a.q, none, seq, t, head_k)[x]) : 0.f;
+                    v[j] = x < a.v ? to_f32<T>(row_ptr<T>(a.vv, none, seq, t, head)[x]) : 0.f;
+                }
+                g = row_ptr<float>(a.g, none, seq, t, head)[0];
+                beta = a.beta_f32 ? row_ptr<float>(a.beta, none, seq, t, head)[0] : to_f32<T>(row_ptr<T>(a.beta, none, seq, t, head)[0]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d += k[j] * q[j];
+#pragma unroll
+                for (int x = 16; x; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+            }
+            if (i >= kRingStages) wait_phase(&m.done[st], (i / kRingStages - 1) & 1, gave_up);
+            if (__any_sync(0xffffffffu, *gave_up)) break;
+            RingTokens &in = m.in[st];
+            if (t < count) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    in.k[t][lane + 32 * j] = k[j];
+                    in.q[t][lane + 32 * j] = q[j];
+                    in.v[t][lane + 32 * j] = v[j];
+                }
+                if (lane == 0) {
+                    in.decay[t] = g <= -87.f ? 0.f : expf(g);
+                    in.beta[t] = beta;
+                    in.qk[t] = d;
+                }
+            }
+            if (t == 0 && lane == 0) in.count = count;
+            warp_arrive(&m.in_full[st], lane);
+        }
+    } else {
+        const int c0 = 4 * lane;
+        const bool in_row = c0 < a.v;   // the columns come in fours
+        const size_t ostride = (size_t)a.hv * a.v;
+        int n = 0;   // tokens so far
+        bool failed = false;
+        for (int i = 0; i < items; ++i) {
+            const int st = i % kRingStages;
+            long long seq;
+            int head;
+            item(i, seq, head);
+            wait_phase(&m.in_full[st], (i / kRingStages) & 1, gave_up);
+            wait_phase(&m.state_full[st], (i / kRingStages) & 1, gave_up);
+            failed = any_computing(*gave_up != 0);   // all eight warps leave together
+            if (failed) break;
+            const RingTokens &in = m.in[st];
+            T *out = static_cast<T *>(a.o) + ((size_t)seq * a.t * a.hv + head) * a.v;
+            const int count = in.count;
+            for (int x = tid; x < (a.t - count) * kRingKV; x += kRingCompute)   // outputs of tokens that do not count
+                if (x % kRingKV < a.v) out[(count + x / kRingKV) * ostride + x % kRingKV] = from_f32<T>(0.f);
+            if (count > 0) {
+                float4 S[kRingRows];
+                float *state = m.state[st] + c0;
+#pragma unroll
+                for (int r = 0; r < kRingRows; ++r) {
+                    const int k = warp + r * kRingWarps;
+                    S[r] = in_row && k < a.k ? *reinterpret_cast<const float4 *>(state + k * a.v) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                for (int t = 0; t < count; ++t, ++n) {
+                    const float decay = in.decay[t], beta = in.beta[t];
+                    float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
+#pragma unroll
+                    for (int r = 0; r < kRingRows; ++r) {
+                        // a forgotten state is 0 even where it held an infinity or a NaN
+                        if (decay == 0.f) S[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        S[r].x *= decay; S[r].y *= decay; S[r].z *= decay; S[r].w *= decay;
+                        fma4(pk, in.k[t][warp + r * kRingWarps], S[r]);
+                        fma4(pq, in.q[t][warp + r * kRingWarps], S[r]);
+                    }
+                    m.sum_k[n & 1][warp][lane] = pk;
+                    m.sum_q[n & 1][warp][lane] = pq;
+                    any_computing(false);
+                    pk = m.sum_k[n & 1][0][lane];
+#pragma unroll
+                    for (int w = 1; w < kRingWarps; ++w) fma4(pk, 1.f, m.sum_k[n & 1][w][lane]);
+                    const float4 v = *reinterpret_cast<const float4 *>(in.v[t] + c0);
+                    const float4 u = make_float4(beta * (v.x - pk.x), beta * (v.y - pk.y), beta * (v.z - pk.z), beta * (v.w - pk.w));
+#pragma unroll
+                    for (int r = 0; r < kRingRows; ++r) fma4(S[r], in.k[t][warp + r * kRingWarps], u);
+                    if (warp == t % kRingWarps && in_row) {
+                        pq = m.sum_q[n & 1][0][lane];
+#pragma unroll
+                        for (int w = 1; w < kRingWarps; ++w) fma4(pq, 1.f, m.sum_q[n & 1][w][lane]);
+                        fma4(pq, in.qk[t], u);
+                        T *op = out + t * ostride + c0;
+                        op[0] = from_f32<T>(a.scale * pq.x);
+                        op[1] = from_f32<T>(a.scale * pq.y);
+                        op[2] = from_f32<T>(a.scale * pq.z);
+                        op[3] = from_f32<T>(a.scale * pq.w);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < kRingRows; ++r) {
+                    const int k = warp + r * kRingWarps;
+                    if (in_row && k < a.k) *reinterpret_cast<float4 *>(state + k * a.v) = S[r];
+                }
+                fence_async();
+            }
+            warp_arrive(&m.done[st], lane);
+        }
+        if (failed)   // the outputs are not what they should be: say so
+            for (int i = 0; i < items; ++i) {
+                long long seq;
+                int head;
+                item(i, seq, head);
+                T *out = static_cast<T *>(a.o) + ((size_t)seq * a.t * a.hv + head) * a.v;
+                for (int x = tid; x < a.t * kRingKV; x += kRingCompute)
+                    if (x % kRingKV < a.v) out[x / kRingKV * ostride + x % kRingKV] = from_f32<T>(__int_as_float(0x7fc00000));
+            }
+    }
+}
+
 namespace {
 
 template <typename T, int KP, int VT>
@@ -165,18 +402,27 @@ cudaError_t step(const DeltaStepArgs &a, cudaStream_t s) {
     delta_step_kernel<T, KP, VT><<<(unsigned)ctas, kStepThreads, 0, s>>>(a, vec4);
     return cudaGetLastError();
 }
+template <typename T>
+cudaError_t step_ring(const DeltaStepArgs &a, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(delta_step_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RingSmem));
+    if (e != cudaSuccess) return e;
+    delta_step_ring_kernel<T><<<kRingCtas, kRingThreads, sizeof(RingSmem), s>>>(a);
+    return cudaGetLastError();
+}
 template <typename T, int KP>
 cudaError_t step_for(const DeltaStepArgs &a, cudaStream_t s) {
-    // Whole rows of up to 128 columns where there are CTAs enough for the machine, narrower blocks
-    // where there are not: more of the state's bytes are then in flight at once.
     const long long heads = a.seqs * a.hv;
+    // Blocks of 64 columns where there are CTAs enough for the machine, narrower ones where there are
+    // not: more of the state's bytes are then in flight at once.
     if (a.v <= 32 || heads * ((a.v + 63) / 64) < 2 * 152) return step<T, KP, 32>(a, s);
-    if (a.v <= 64 || heads * ((a.v + 127) / 128) < 2 * 152) return step<T, KP, 64>(a, s);
-    return step<T, KP, 128>(a, s);
+    return step<T, KP, 64>(a, s);
 }
 template <typename T>
 cudaError_t step_type(const DeltaStepArgs &a, cudaStream_t s) {
-    return a.k <= 64 ? step_for<T, 64>(a, s) : step_for<T, 128>(a, s);
+    if (a.k <= 64) return step_for<T, 64>(a, s);
+    const bool whole = a.v % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;   // as bulk copies want them
+    if (a.v > 64 && whole && a.t <= kRingTokens && a.seqs * a.hv >= 4 * kRingCtas) return step_ring<T>(a, s);
+    return step_for<T, 128>(a, s);
 }
 
 }  // namespace

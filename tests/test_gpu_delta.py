@@ -232,6 +232,34 @@ def test_step_lengths_and_absent_sequences():
     assert torch.equal(pool[[1, 2, 3]], was[[1, 2, 3]])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("n,t,hk,hv,k,v", [(160, 1, 2, 4, 128, 128), (77, 3, 2, 8, 100, 68), (210, 4, 1, 3, 65, 124)])
+def test_step_many_states(dtype, n, t, hk, hv, k, v):
+    # enough heads for states to pass through shared memory; some sequences absent, some with fewer tokens
+    x = inputs(t, hk, hv, k, v, dtype, 95, seqs=n)
+    x[3][5:9] = -float("inf")
+    pool = states(n + 3, hv, k, v, 96)
+    slots = torch.randperm(n + 3, device=DEV)[:n].to(torch.int32)
+    pool[slots[6].long()] = float("nan")
+    slots[11], slots[12] = -1, n + 3
+    lengths = torch.randint(0, t + 2, (n,), device=DEV).to(torch.int32)
+    lengths[5:9] = t
+    was = pool.clone()
+    o = api.delta_rule_step(*x, pool, slots=slots, lengths=lengths)
+    untouched = torch.ones(n + 3, dtype=torch.bool, device=DEV)
+    for i in range(n):
+        count = min(int(lengths[i]), t) if 0 <= slots[i] < n + 3 else 0
+        assert (o[i, count:] == 0).all()
+        if count:
+            page = int(slots[i])
+            untouched[page] = False
+            before = torch.zeros_like(was[page]) if 5 <= i < 9 else was[page]
+            want = ref.sequence(*(y[i, :count] for y in x), k ** -0.5, before)
+            near(o[i, :count], want["o"], STEP)
+            near(pool[page], want["state"], STEP)
+    assert torch.equal(pool[untouched], was[untouched])
+
+
 def test_steps_continue_a_prompt():
     # a prompt by chunks, its state handed to single steps, against the whole sequence
     x = inputs(80, 2, 4, 128, 128, F32, 111, seqs=2)
