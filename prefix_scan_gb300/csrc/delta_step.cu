@@ -2,12 +2,17 @@
 // in a pool of pages (notation in delta_common.cuh).
 //
 // Bound by memory: a token reads and writes its K x V f32 state once (128 KiB
-// at 128 x 128) and does 7 K V operations on it.  A CTA holds one head's state,
-// or a block of its columns, in registers: all loads are in flight at once, and
-// all tokens of the call run before the state goes back.  k^T S and q^T S are
-// summed in one pass over the decayed state, because
+// at 128 x 128) and does 7 K V operations on it, in f32; all tokens of the call
+// run before the state goes back.  k^T S and q^T S are summed in one pass over
+// the decayed state, because
 //     q^T (S + k u^T) = q^T S + (q.k) u,
 // so a token costs one exchange between the warps.
+//
+// With few heads, latency counts: a CTA holds a block of a head's columns in
+// registers, all of its loads in flight at once (32 states of 128 x 128: 15 us with
+// the call, which the host bounds).  With many, bandwidth does: whole states pass through
+// a ring of bulk copies (8192 states of 128 x 128: 171 us, 6.33 TB/s; loads,
+// sums and stores of a CTA in turn, at two or three CTAs an SM, reached 5.0-5.2).
 #include "delta_tmem.cuh"
 
 namespace ps {
@@ -157,32 +162,36 @@ __global__ void __launch_bounds__(kStepThreads, 3) delta_step_kernel(const Delta
 }
 
 // ---- many large states: a ring of whole states in shared memory --------------------
-// One CTA per SM takes its share of the heads in turn.  A head's state is one run of
+// A CTA takes its share of the heads in turn.  A head's state is one run of
 // bytes, so one thread moves it with one bulk copy each way: it stores the state that
 // is done and loads the one that is next in its place, two others being on their way
 // or at work meanwhile, so that reads and writes never pause for the sums.  Four warps
 // bring the tokens' small inputs (a token each) ahead of them, eight warps compute.
+// Smaller states take less of the SM, which then runs two or three such CTAs.
 
 namespace {
 
-constexpr int kRingStages = 3, kRingTokens = 4, kRingKV = 128;
+constexpr int kRingStages = 3, kRingTokens = 4;
 constexpr int kRingWarps = 8, kRingCompute = 32 * kRingWarps, kRingThreads = kRingCompute + 32 * (1 + kRingTokens);
-constexpr int kRingRows = kRingKV / kRingWarps, kRingCtas = 152;
+// CTAs of an SM: as many as their shared memory and registers admit
+constexpr int ring_ctas(int kp, int vp) { return kp * vp > 8192 ? 1 : kp * vp > 4096 ? 2 : 3; }
 
+template <int KP, int VP>
 struct RingTokens {
-    float k[kRingTokens][kRingKV], q[kRingTokens][kRingKV], v[kRingTokens][kRingKV];
+    float k[kRingTokens][KP], q[kRingTokens][KP], v[kRingTokens][VP];
     float decay[kRingTokens], beta[kRingTokens], qk[kRingTokens];
     int count;
     int pad[3];
 };
+template <int KP, int VP>
 struct RingSmem {
-    float state[kRingStages][kRingKV * kRingKV];
-    RingTokens in[kRingStages];
-    float4 sum_k[2][kRingWarps][32], sum_q[2][kRingWarps][32];
+    float state[kRingStages][KP * VP];
+    RingTokens<KP, VP> in[kRingStages];
+    float4 sum_k[2][kRingWarps][VP / 4], sum_q[2][kRingWarps][VP / 4];
     uint64_t state_full[kRingStages], in_full[kRingStages], done[kRingStages];
     int gave_up;
 };
-static_assert(sizeof(RingSmem) <= 227 * 1024, "too much shared memory");
+static_assert(sizeof(RingSmem<128, 128>) <= 227 * 1024, "too much shared memory");
 
 // Whether any of the computing threads says so; all of them wait for one another.
 __device__ __forceinline__ bool any_computing(bool x) {
@@ -200,10 +209,12 @@ __device__ __forceinline__ int step_tokens(const DeltaStepArgs &a, long long seq
 
 }  // namespace
 
-template <typename T>
-__global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const DeltaStepArgs a) {
+// VP / 4 lanes hold a row's columns, four each.
+template <typename T, int KP, int VP>
+__global__ void __launch_bounds__(kRingThreads, ring_ctas(KP, VP)) delta_step_ring_kernel(const DeltaStepArgs a) {
+    constexpr int LPR = VP / 4, GROUPS = kRingCompute / LPR, ROWS = KP / GROUPS;
     extern __shared__ __align__(128) unsigned char ring_bytes[];
-    RingSmem &m = *reinterpret_cast<RingSmem *>(ring_bytes);
+    RingSmem<KP, VP> &m = *reinterpret_cast<RingSmem<KP, VP> *>(ring_bytes);
     volatile int *gave_up = &m.gave_up;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long heads = a.seqs * a.hv;
@@ -276,32 +287,37 @@ __global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const 
             int head;
             item(i, seq, head);
             const int head_k = head / (a.hv / a.hk), count = step_tokens(a, seq, page);
-            float k[4], q[4], v[4], g = 0.f, beta = 0.f, d = 0.f;
+            float k[KP / 32], q[KP / 32], v[VP / 32], g = 0.f, beta = 0.f, d = 0.f;
             if (t < count) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < KP / 32; ++j) {
                     const int x = lane + 32 * j;
                     k[j] = x < a.k ? to_f32<T>(row_ptr<T>(a.kk, none, seq, t, head_k)[x]) : 0.f;
                     q[j] = x < a.k ? to_f32<T>(row_ptr<T>(a.q, none, seq, t, head_k)[x]) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < VP / 32; ++j) {
+                    const int x = lane + 32 * j;
                     v[j] = x < a.v ? to_f32<T>(row_ptr<T>(a.vv, none, seq, t, head)[x]) : 0.f;
                 }
                 g = row_ptr<float>(a.g, none, seq, t, head)[0];
                 beta = a.beta_f32 ? row_ptr<float>(a.beta, none, seq, t, head)[0] : to_f32<T>(row_ptr<T>(a.beta, none, seq, t, head)[0]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d += k[j] * q[j];
+                for (int j = 0; j < KP / 32; ++j) d += k[j] * q[j];
 #pragma unroll
                 for (int x = 16; x; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
             }
             if (i >= kRingStages) wait_phase(&m.done[st], (i / kRingStages - 1) & 1, gave_up);
             if (__any_sync(0xffffffffu, *gave_up)) break;
-            RingTokens &in = m.in[st];
+            RingTokens<KP, VP> &in = m.in[st];
             if (t < count) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < KP / 32; ++j) {
                     in.k[t][lane + 32 * j] = k[j];
                     in.q[t][lane + 32 * j] = q[j];
-                    in.v[t][lane + 32 * j] = v[j];
                 }
+#pragma unroll
+                for (int j = 0; j < VP / 32; ++j) in.v[t][lane + 32 * j] = v[j];
                 if (lane == 0) {
                     in.decay[t] = g <= -87.f ? 0.f : expf(g);
                     in.beta[t] = beta;
@@ -312,7 +328,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const 
             warp_arrive(&m.in_full[st], lane);
         }
     } else {
-        const int c0 = 4 * lane;
+        const int col = tid % LPR, group = tid / LPR, c0 = 4 * col;
         const bool in_row = c0 < a.v;   // the columns come in fours
         const size_t ostride = (size_t)a.hv * a.v;
         int n = 0;   // tokens so far
@@ -326,44 +342,45 @@ __global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const 
             wait_phase(&m.state_full[st], (i / kRingStages) & 1, gave_up);
             failed = any_computing(*gave_up != 0);   // all eight warps leave together
             if (failed) break;
-            const RingTokens &in = m.in[st];
+            const RingTokens<KP, VP> &in = m.in[st];
             T *out = static_cast<T *>(a.o) + ((size_t)seq * a.t * a.hv + head) * a.v;
             const int count = in.count;
-            for (int x = tid; x < (a.t - count) * kRingKV; x += kRingCompute)   // outputs of tokens that do not count
-                if (x % kRingKV < a.v) out[(count + x / kRingKV) * ostride + x % kRingKV] = from_f32<T>(0.f);
+            for (int x = tid; x < (a.t - count) * VP; x += kRingCompute)   // outputs of tokens that do not count
+                if (x % VP < a.v) out[(count + x / VP) * ostride + x % VP] = from_f32<T>(0.f);
             if (count > 0) {
-                float4 S[kRingRows];
+                float4 S[ROWS];
                 float *state = m.state[st] + c0;
 #pragma unroll
-                for (int r = 0; r < kRingRows; ++r) {
-                    const int k = warp + r * kRingWarps;
+                for (int r = 0; r < ROWS; ++r) {
+                    const int k = group + r * GROUPS;
                     S[r] = in_row && k < a.k ? *reinterpret_cast<const float4 *>(state + k * a.v) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
                 for (int t = 0; t < count; ++t, ++n) {
                     const float decay = in.decay[t], beta = in.beta[t];
                     float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
 #pragma unroll
-                    for (int r = 0; r < kRingRows; ++r) {
+                    for (int r = 0; r < ROWS; ++r) {
                         // a forgotten state is 0 even where it held an infinity or a NaN
                         if (decay == 0.f) S[r] = make_float4(0.f, 0.f, 0.f, 0.f);
                         S[r].x *= decay; S[r].y *= decay; S[r].z *= decay; S[r].w *= decay;
-                        fma4(pk, in.k[t][warp + r * kRingWarps], S[r]);
-                        fma4(pq, in.q[t][warp + r * kRingWarps], S[r]);
+                        fma4(pk, in.k[t][group + r * GROUPS], S[r]);
+                        fma4(pq, in.q[t][group + r * GROUPS], S[r]);
                     }
-                    m.sum_k[n & 1][warp][lane] = pk;
-                    m.sum_q[n & 1][warp][lane] = pq;
-                    any_computing(false);
-                    pk = m.sum_k[n & 1][0][lane];
 #pragma unroll
-                    for (int w = 1; w < kRingWarps; ++w) fma4(pk, 1.f, m.sum_k[n & 1][w][lane]);
+                    for (int x = LPR; x < 32; x <<= 1) { pk = shfl_add(pk, x); pq = shfl_add(pq, x); }
+                    if (lane < LPR) { m.sum_k[n & 1][warp][lane] = pk; m.sum_q[n & 1][warp][lane] = pq; }
+                    any_computing(false);
+                    pk = m.sum_k[n & 1][0][col];
+#pragma unroll
+                    for (int w = 1; w < kRingWarps; ++w) fma4(pk, 1.f, m.sum_k[n & 1][w][col]);
                     const float4 v = *reinterpret_cast<const float4 *>(in.v[t] + c0);
                     const float4 u = make_float4(beta * (v.x - pk.x), beta * (v.y - pk.y), beta * (v.z - pk.z), beta * (v.w - pk.w));
 #pragma unroll
-                    for (int r = 0; r < kRingRows; ++r) fma4(S[r], in.k[t][warp + r * kRingWarps], u);
-                    if (warp == t % kRingWarps && in_row) {
-                        pq = m.sum_q[n & 1][0][lane];
+                    for (int r = 0; r < ROWS; ++r) fma4(S[r], in.k[t][group + r * GROUPS], u);
+                    if (warp == t && lane < LPR && in_row) {
+                        pq = m.sum_q[n & 1][0][col];
 #pragma unroll
-                        for (int w = 1; w < kRingWarps; ++w) fma4(pq, 1.f, m.sum_q[n & 1][w][lane]);
+                        for (int w = 1; w < kRingWarps; ++w) fma4(pq, 1.f, m.sum_q[n & 1][w][col]);
                         fma4(pq, in.qk[t], u);
                         T *op = out + t * ostride + c0;
                         op[0] = from_f32<T>(a.scale * pq.x);
@@ -373,8 +390,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const 
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < kRingRows; ++r) {
-                    const int k = warp + r * kRingWarps;
+                for (int r = 0; r < ROWS; ++r) {
+                    const int k = group + r * GROUPS;
                     if (in_row && k < a.k) *reinterpret_cast<float4 *>(state + k * a.v) = S[r];
                 }
                 fence_async();
@@ -387,8 +404,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) delta_step_ring_kernel(const 
                 int head;
                 item(i, seq, head);
                 T *out = static_cast<T *>(a.o) + ((size_t)seq * a.t * a.hv + head) * a.v;
-                for (int x = tid; x < a.t * kRingKV; x += kRingCompute)
-                    if (x % kRingKV < a.v) out[x / kRingKV * ostride + x % kRingKV] = from_f32<T>(__int_as_float(0x7fc00000));
+                for (int x = tid; x < a.t * VP; x += kRingCompute)
+                    if (x % VP < a.v) out[x / VP * ostride + x % VP] = from_f32<T>(__int_as_float(0x7fc00000));
             }
     }
 }
@@ -402,16 +419,25 @@ cudaError_t step(const DeltaStepArgs &a, cudaStream_t s) {
     delta_step_kernel<T, KP, VT><<<(unsigned)ctas, kStepThreads, 0, s>>>(a, vec4);
     return cudaGetLastError();
 }
-template <typename T>
+template <typename T, int KP, int VP>
 cudaError_t step_ring(const DeltaStepArgs &a, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(delta_step_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RingSmem));
+    constexpr int bytes = sizeof(RingSmem<KP, VP>);
+    cudaError_t e = cudaFuncSetAttribute(delta_step_ring_kernel<T, KP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    delta_step_ring_kernel<T><<<kRingCtas, kRingThreads, sizeof(RingSmem), s>>>(a);
+    delta_step_ring_kernel<T, KP, VP><<<152 * ring_ctas(KP, VP), kRingThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int KP>
 cudaError_t step_for(const DeltaStepArgs &a, cudaStream_t s) {
     const long long heads = a.seqs * a.hv;
+    const bool whole = a.v % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;   // as bulk copies want them
+    // The ring against the states in registers, us of a token each (caches flushed before, bf16):
+    //   128 x 128: 608 heads 23 / 25, 1024 33 / 37, 8192 173 / 238, four tokens 301 / 384
+    //   64 x 64: 640 heads 13 / 14, 2048 21 / 29, 8192 50 / 89    64 x 128: 640 19 / 20, 8192 119 / 164
+    //   128 x 64: 640 heads 19 / 17, 1280 27 / 25, 2048 35 / 38, 8192 103 / 126
+    // Fewer heads leave the ring's CTAs with two or three states each.
+    if (whole && a.v > 32 && a.t <= kRingTokens && heads >= (KP == 128 && a.v <= 64 ? 12 : 4) * 152)
+        return a.v <= 64 ? step_ring<T, KP, 64>(a, s) : step_ring<T, KP, 128>(a, s);
     // Blocks of 64 columns where there are CTAs enough for the machine, narrower ones where there are
     // not: more of the state's bytes are then in flight at once.
     if (a.v <= 32 || heads * ((a.v + 63) / 64) < 2 * 152) return step<T, KP, 32>(a, s);
@@ -419,10 +445,7 @@ cudaError_t step_for(const DeltaStepArgs &a, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t step_type(const DeltaStepArgs &a, cudaStream_t s) {
-    if (a.k <= 64) return step_for<T, 64>(a, s);
-    const bool whole = a.v % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;   // as bulk copies want them
-    if (a.v > 64 && whole && a.t <= kRingTokens && a.seqs * a.hv >= 4 * kRingCtas) return step_ring<T>(a, s);
-    return step_for<T, 128>(a, s);
+    return a.k <= 64 ? step_for<T, 64>(a, s) : step_for<T, 128>(a, s);
 }
 
 }  // namespace
