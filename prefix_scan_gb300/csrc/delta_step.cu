@@ -436,7 +436,7 @@ cudaError_t step_for(const DeltaStepArgs &a, cudaStream_t s) {
     //   64 x 64: 640 heads 13 / 14, 2048 21 / 29, 8192 50 / 89    64 x 128: 640 19 / 20, 8192 119 / 164
     //   128 x 64: 640 heads 19 / 17, 1280 27 / 25, 2048 35 / 38, 8192 103 / 126
     // Fewer heads leave the ring's CTAs with two or three states each.
-    if (whole && a.v > 32 && a.t <= kRingTokens && heads >= (KP == 128 && a.v <= 64 ? 12 : 4) * 152)
+    if (whole && a.v > 32 && a.v <= 128 && a.t <= kRingTokens && heads >= (KP == 128 && a.v <= 64 ? 12 : 4) * 152)
         return a.v <= 64 ? step_ring<T, KP, 64>(a, s) : step_ring<T, KP, 128>(a, s);
     // Blocks of 64 columns where there are CTAs enough for the machine, narrower ones where there are
     // not: more of the state's bytes are then in flight at once.

@@ -234,7 +234,8 @@ def test_step_lengths_and_absent_sequences():
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("n,t,hk,hv,k,v", [(160, 1, 2, 4, 128, 128), (77, 3, 2, 8, 100, 68), (210, 4, 1, 3, 65, 124),
-                                           (400, 2, 2, 4, 64, 64), (160, 4, 1, 4, 33, 36), (90, 1, 8, 8, 128, 60), (90, 2, 4, 8, 48, 128)])
+                                           (400, 2, 2, 4, 64, 64), (160, 4, 1, 4, 33, 36), (90, 1, 8, 8, 128, 60), (90, 2, 4, 8, 48, 128),
+                                           (110, 1, 3, 6, 72, 200)])
 def test_step_many_states(dtype, n, t, hk, hv, k, v):
     # enough heads for states to pass through shared memory; some sequences absent, some with fewer tokens
     x = inputs(t, hk, hv, k, v, dtype, 95, seqs=n)
