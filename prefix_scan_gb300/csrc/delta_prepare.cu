@@ -26,8 +26,9 @@ template <int NP, int KP>
 struct PrepSmem {
     static constexpr int kPlane = 2 * kChunk * KP * 2;                           // keys, then queries
     static constexpr int kK = 0, kQ = kChunk * 128;
-    static constexpr int kT = 0, kP = 2 * (int)kSquare, kN = 4 * (int)kSquare;   // in the place of K and Q
-    static constexpr int kScal = NP * kPlane > 6 * (int)kSquare ? NP * kPlane : 6 * (int)kSquare;
+    // in the place of K and Q: P, later T; N below its diagonal blocks, and T's diagonal blocks in theirs
+    static constexpr int kT = 0, kN = 2 * (int)kSquare;
+    static constexpr int kScal = NP * kPlane > 4 * (int)kSquare ? NP * kPlane : 4 * (int)kSquare;
     static constexpr int kL = kScal + 4 * kScalars * 4;                          // f32 diagonal blocks of diag(beta) N
     static constexpr int kBytes = kL + 4 * kDiag * 4;
 };
@@ -40,7 +41,7 @@ constexpr float kLeastBeta = 0x1p-60f;
 }  // namespace
 
 template <typename T, int KP>
-__global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, Planes<T>::NP == 1 ? 4 : KP == 64 ? 3 : 2) delta_prepare_kernel(const DeltaArgs a) {
     constexpr int NP = Planes<T>::NP;
     using M = PrepSmem<NP, KP>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -124,34 +125,40 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const De
     cp_async_wait<0>();
     __syncthreads();
 
-    // rows 16 warp .. of k k^T and q k^T, columns j <= i only
-    float kk[8][4], qk[8][4];
+    // k k^T and q k^T: a warp's diagonal block, and one or two of the six below them
+    int bi[3], bj[3];
+    bi[0] = bj[0] = warp;
+    bi[1] = warp < 2 ? 3 : warp == 2 ? 2 : 1;
+    bj[1] = warp == 1 ? 2 : warp == 2 ? 1 : 0;
+    bi[2] = 3 - warp;
+    bj[2] = 1 - warp;
+    const int blocks = warp < 2 ? 3 : 2;
+    float kk[3][2][4], qk[3][2][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < 3; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) kk[n][0][e] = kk[n][1][e] = qk[n][0][e] = qk[n][1][e] = 0.f;
 #pragma unroll
     for (int kt = 0; kt < KP / 16; ++kt) {
-        uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            load_a(ak[p], base + M::kK + p * M::kPlane, 16 * warp, 16 * kt, lane);
-            load_a(aq[p], base + M::kQ + p * M::kPlane, 16 * warp, 16 * kt, lane);
-        }
+        for (int n = 0; n < 3; ++n) {
+            if (n >= blocks) continue;
+            uint32_t ak[NP][4], aq[NP][4];
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-            if (np <= warp) {
+            for (int p = 0; p < NP; ++p) {
+                load_a(ak[p], base + M::kK + p * M::kPlane, 16 * bi[n], 16 * kt, lane);
+                load_a(aq[p], base + M::kQ + p * M::kPlane, 16 * bi[n], 16 * kt, lane);
+            }
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    uint32_t b[4];
-                    load_b(b, base + M::kK + p * M::kPlane, 16 * np, 16 * kt, lane);
+            for (int p = 0; p < NP; ++p) {
+                uint32_t b[4];
+                load_b(b, base + M::kK + p * M::kPlane, 16 * bj[n], 16 * kt, lane);
 #pragma unroll
-                    for (int f = 0; f < NP; ++f) {
-                        mma_bf16(kk[2 * np], ak[f], b[0], b[1]);
-                        mma_bf16(kk[2 * np + 1], ak[f], b[2], b[3]);
-                        mma_bf16(qk[2 * np], aq[f], b[0], b[1]);
-                        mma_bf16(qk[2 * np + 1], aq[f], b[2], b[3]);
-                    }
+                for (int f = 0; f < NP; ++f) {
+                    mma_bf16(kk[n][0], ak[f], b[0], b[1]);
+                    mma_bf16(kk[n][1], ak[f], b[2], b[3]);
+                    mma_bf16(qk[n][0], aq[f], b[0], b[1]);
+                    mma_bf16(qk[n][1], aq[f], b[2], b[3]);
                 }
             }
         }
@@ -164,63 +171,68 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const De
     }
     __syncthreads();
 
+#pragma unroll
+    for (int np = 1; np < 4; ++np)   // above the diagonal blocks P and T are 0, for all heads
+        if (np > warp) {
+            const uint32_t at = img(base + M::kT, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
+            stsm4(at, 0, 0, 0, 0);
+            stsm4(at + (uint32_t)kSquare, 0, 0, 0, 0);
+        }
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
     for (int hr = 0; hr < rep; ++hr) {
         const int head = head_k * rep + hr;
         float *scal = reinterpret_cast<float *>(smem + M::kScal) + (hr & 3) * kScalars;
+        unsigned char *out = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
         if (hr > 0 && (hr & 3) == 0) {
             scalars(hr);
             __syncthreads();
         }
 
-        {   // P and N as pairs, the diagonal blocks of diag(beta) N in f32
-            const int r8 = lane >> 2, i0 = 16 * warp + r8, c2 = 2 * (lane & 3);
-            const float row0 = scal[kRow + i0], row1 = scal[kRow + i0 + 8];
+        // P and N as pairs, the diagonal blocks of diag(beta) N in f32
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                const uint32_t at = img(0, 16 * warp + (lane & 15), 2 * np + (lane >> 4));
-                if (np > warp) {   // above the diagonal: T and P are 0, N is not read
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) stsm4(base + M::kT + at + m * (uint32_t)kSquare, 0, 0, 0, 0);
-                    continue;
-                }
-                float nv[2][4], pv[2][4];   // tiles of the block
+        for (int n = 0; n < 3; ++n) {
+            if (n >= blocks) continue;
+            const int r8 = lane >> 2, i0 = 16 * bi[n] + r8, c2 = 2 * (lane & 3);
+            const uint32_t at = img(base + M::kT, 16 * bi[n] + (lane & 15), 2 * bj[n] + (lane >> 4));
+            float nv[2][4], pv[2][4];   // tiles of the block
+            uint32_t f[2][4];
+            if (n > 0) {
+                const float row0 = scal[kRow + i0], row1 = scal[kRow + i0 + 8];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const int n = 2 * np + t, j = 8 * n + c2;
-                    if (np < warp) {
-                        const float2 col = *reinterpret_cast<const float2 *>(scal + kCol + (warp - 1) * kChunk + j);
+                    const float2 col = *reinterpret_cast<const float2 *>(scal + kCol + (bi[n] - 1) * kChunk + 16 * bj[n] + 8 * t + c2);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float D = (e < 2 ? row0 : row1) * (e & 1 ? col.y : col.x);
-                            nv[t][e] = D * kk[n][e];
-                            pv[t][e] = a.s.scale * D * qk[n][e];
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = i0 + 8 * (e >> 1), c = j + (e & 1);
-                            const float dx = (scal[192 + i] - scal[192 + c]) + (scal[256 + i] - scal[256 + c]);
-                            const float D = i >= c && scal[320 + i] == scal[320 + c] ? expf(dx) : 0.f;
-                            nv[t][e] = i > c ? D * kk[n][e] : 0.f;
-                            pv[t][e] = i >= c ? a.s.scale * D * qk[n][e] : 0.f;
-                        }
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float be = scal[128 + i0 + 8 * r];
-                            *reinterpret_cast<float2 *>(L + warp * kDiag + (r8 + 8 * r) * 16 + 8 * t + c2) =
-                                make_float2(be * nv[t][2 * r], be * nv[t][2 * r + 1]);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float D = (e < 2 ? row0 : row1) * (e & 1 ? col.y : col.x);
+                        nv[t][e] = D * kk[n][t][e];
+                        pv[t][e] = a.s.scale * D * qk[n][t][e];
                     }
                 }
-                uint32_t f[2][4];
-                split_tiles(pv[0], pv[1], f);
-                stsm4(base + M::kP + at, f[0][0], f[0][1], f[0][2], f[0][3]);
-                stsm4(base + M::kP + (uint32_t)kSquare + at, f[1][0], f[1][1], f[1][2], f[1][3]);
                 split_tiles(nv[0], nv[1], f);
-                stsm4(base + M::kN + at, f[0][0], f[0][1], f[0][2], f[0][3]);
-                stsm4(base + M::kN + (uint32_t)kSquare + at, f[1][0], f[1][1], f[1][2], f[1][3]);
+                stsm4(at + M::kN, f[0][0], f[0][1], f[0][2], f[0][3]);
+                stsm4(at + M::kN + (uint32_t)kSquare, f[1][0], f[1][1], f[1][2], f[1][3]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = i0 + 8 * (e >> 1), c = 16 * warp + 8 * t + c2 + (e & 1);
+                        const float dx = (scal[192 + i] - scal[192 + c]) + (scal[256 + i] - scal[256 + c]);
+                        const float D = i >= c && scal[320 + i] == scal[320 + c] ? expf(dx) : 0.f;
+                        nv[t][e] = i > c ? D * kk[n][t][e] : 0.f;
+                        pv[t][e] = i >= c ? a.s.scale * D * qk[n][t][e] : 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float be = scal[128 + i0 + 8 * e];
+                        *reinterpret_cast<float2 *>(L + warp * kDiag + (r8 + 8 * e) * 16 + 8 * t + c2) =
+                            make_float2(be * nv[t][2 * e], be * nv[t][2 * e + 1]);
+                    }
+                }
             }
+            split_tiles(pv[0], pv[1], f);
+            stsm4(at, f[0][0], f[0][1], f[0][2], f[0][3]);
+            stsm4(at + (uint32_t)kSquare, f[1][0], f[1][1], f[1][2], f[1][3]);
         }
         __syncthreads();
 
@@ -247,17 +259,29 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const De
                 const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
                 const __nv_bfloat16 l = __float2bfloat16_rn(x[i] - __bfloat162float(h));
                 const int at = (int)img(0, (tid & ~15) + i, tid >> 3) + (tid & 7) * 2;
-                *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + at) = h;
-                *reinterpret_cast<__nv_bfloat16 *>(smem + M::kT + kSquare + at) = l;
+                *reinterpret_cast<__nv_bfloat16 *>(smem + M::kN + at) = h;
+                *reinterpret_cast<__nv_bfloat16 *>(smem + M::kN + kSquare + at) = l;
             }
+        } else {   // the other warps take P out meanwhile
+#pragma unroll 4
+            for (int i = tid - kChunk; i < 2 * (int)kSquare / 16; i += kPrepThreads - kChunk)
+                reinterpret_cast<uint4 *>(out + lay.p)[i] = reinterpret_cast<const uint4 *>(smem + M::kT)[i];
         }
         __syncthreads();
 
-        {   // block column `warp` below its diagonal block
+        if (warp == 3) {   // which has no blocks below its diagonal one: T's diagonal blocks
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t at = img(p * (uint32_t)kSquare, 16 * i + (lane & 15), 2 * i + (lane >> 4));
+                    *reinterpret_cast<uint4 *>(smem + M::kT + at) = *reinterpret_cast<const uint4 *>(smem + M::kN + at);
+                }
+        } else {   // block column `warp` below its diagonal block
             uint32_t x[4][2][4];   // T_lj^T as left operands
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-                load_a_t(x[0][p], base + M::kT + p * (uint32_t)kSquare, 16 * warp, 16 * warp, lane);
+                load_a_t(x[0][p], base + M::kN + p * (uint32_t)kSquare, 16 * warp, 16 * warp, lane);
 #pragma unroll
             for (int d = 1; d < 4; ++d) {
                 const int i = warp + d;
@@ -286,8 +310,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const De
                 }
                 uint32_t f[2][4], bh[4], bl[4];
                 split_tiles(y[0], y[1], f);
-                load_b(bh, base + M::kT, 16 * i, 16 * i, lane);
-                load_b(bl, base + M::kT + (uint32_t)kSquare, 16 * i, 16 * i, lane);
+                load_b(bh, base + M::kN, 16 * i, 16 * i, lane);
+                load_b(bl, base + M::kN + (uint32_t)kSquare, 16 * i, 16 * i, lane);
                 mma_bf16(z[0], f[0], bh[0], bh[1]);
                 mma_bf16(z[1], f[0], bh[2], bh[3]);
                 mma_bf16(z[0], f[1], bh[0], bh[1]);
@@ -304,17 +328,16 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prepare_kernel(const De
         }
         __syncthreads();
 
-        if (tid < kChunk) {   // the image is T - 1
-            const uint32_t at = img(0, tid, tid >> 3) + (tid & 7) * 2;
-            *reinterpret_cast<uint16_t *>(smem + M::kT + at) = 0;
-            *reinterpret_cast<uint16_t *>(smem + M::kT + kSquare + at) = 0;
-        }
-        __syncthreads();
-        unsigned char *out = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
-        constexpr int imgs = 4 * (int)kSquare / 16;   // T and P follow one another on both sides
 #pragma unroll 4
-        for (int i = tid; i < imgs; i += kPrepThreads)
-            reinterpret_cast<uint4 *>(out + lay.t)[i] = reinterpret_cast<const uint4 *>(smem + M::kT)[i];
+        for (int i = tid; i < 2 * (int)kSquare / 16; i += kPrepThreads) {
+            uint4 x = reinterpret_cast<const uint4 *>(smem + M::kT)[i];
+            const int row = i >> 3 & 63;
+            if (((i ^ row) & 7) == row >> 3) {   // the image is T - 1
+                const uint32_t keep = row & 1 ? 0xffffu : 0xffff0000u;
+                (row & 4 ? row & 2 ? x.w : x.z : row & 2 ? x.y : x.x) &= keep;
+            }
+            reinterpret_cast<uint4 *>(out + lay.t)[i] = x;
+        }
         for (int i = tid; i < 6 * kChunk; i += kPrepThreads) reinterpret_cast<float *>(out + lay.scal)[i] = scal[i];
         __syncthreads();
     }
