@@ -25,8 +25,8 @@ namespace ps {
 
 namespace {
 
-constexpr int kGradWarps = 16, kGradThreads = 32 * (kGradWarps + 2);
-constexpr int kZStride = kChunk + 1;
+constexpr int kGradWarps = 16, kGradThreads = 32 * (kGradWarps + 3);
+constexpr int kZStride = kChunk + 8;   // eight columns of four rows in different banks
 // Tensor-memory columns: X1, X2, X3, U dO^T, U dU^T (dU's two parts side by side), the products of
 // F that go to dQ and to dK (and before them [K; Q] [K; Q]^T)
 constexpr uint32_t kColX = 0, kColP = 192, kColN = 256, kColF = 384;
@@ -56,6 +56,13 @@ struct GradBars {
     int gave_up;
 };
 static_assert(sizeof(GradBars) <= 512, "room for the barriers");
+// Whether any of the sixteen warps' threads says so; they wait for one another.
+__device__ __forceinline__ bool meet_any(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)x), "n"(32 * kGradWarps) : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" :: "n"(32 * kGradWarps) : "memory"); }   // the sixteen warps
 
 // Sums of 16 numbers each over the warp: lane l ends up with the l / 2-th.
@@ -70,6 +77,25 @@ __device__ __forceinline__ float sum16(float (&x)[16], int lane) {
         }
     }
     return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
+
+// Lane l holds column l of 16 tokens and stores four columns (from `to` on) of tokens l % 4, l % 4 + 4, ... below `rows`.
+template <typename T>
+__device__ __forceinline__ void store_quads(const float (&x)[16], T *to, size_t stride, int lane, int rows, bool take) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+    uint32_t w[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const float got = __shfl_xor_sync(0xffffffffu, b0 ? x[2 * p] : x[2 * p + 1], 1);
+        w[p] = b0 ? pack2<T>(got, x[2 * p + 1]) : pack2<T>(x[2 * p], got);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? w[2 * m] : w[2 * m + 1], 2);
+        const int token = 4 * m + (lane & 3);
+        if (take && token < rows)
+            *reinterpret_cast<uint2 *>(to + token * stride) = b1 ? make_uint2(got, w[2 * m + 1]) : make_uint2(w[2 * m], got);
+    }
 }
 
 }  // namespace
@@ -87,6 +113,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     const int rep = a.s.hv / a.s.hk;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
     const int vpad = (a.s.v + 15) / 16 * 16;
+    const bool quads = a.s.k % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.dq) | reinterpret_cast<uintptr_t>(a.dk)) & 7) == 0;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -116,7 +143,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     constexpr uint32_t tm = 0;   // all columns are this CTA's
     if (tid == 0 && bar.tmem != tm) bar.gave_up = 1;
 
-    if (warp == kGradWarps) {   // loads
+    if (warp == kGradWarps) {   // loads: items, scalars, U, dU, dO
         uint32_t n = 0, items = 0, heads = 0;   // slices, items and value heads so far
         const long long all = a.slots * a.s.hk;
         auto announce_item = [&](const GradItem &item) {
@@ -135,7 +162,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             const long long t0 = (slot - sp.slot) * kChunk;
             const int rows = (int)min((long long)kChunk, sp.len - t0);
             announce_item(GradItem{sp.first + t0, head_k, rows});
-            bool kq_due = true;
             for (int hr = 0; hr < rep; ++hr, ++heads) {
                 const int head = head_k * rep + hr;
                 const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head) * lay.stride;
@@ -159,35 +185,51 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                     }
                     load_tile<T, kGradV>(base + M::kO, M::kOP, out + v0, a.dout.tok, rows, a.s.v - v0, a.vec_do != 0, lane, 32);
                     cp_async_commit();
-                    if (n) wait_phase(&bar.s_empty, (n - 1) & 1, gave_up);
-                    if (lane == 0 && !*gave_up) {
+                    cp_async_wait<0>();   // dO
+                    fence_async();
+                    mbar_arrive(&bar.u_full);
+                }
+            }
+        }
+        announce_item(GradItem{0, 0, 0});
+        if (*gave_up && lane == 0 && n) wait_drained(&bar.u_full, (n - 1) & 1);   // copies in flight; without it the others have waited for every one
+        __syncwarp();
+    } else if (warp == kGradWarps + 2) {   // loads: S, dS', keys and queries
+        if (lane == 0) {
+            uint32_t n = 0, items = 0;
+            const long long all = a.slots * a.s.hk;
+            for (long long i = blockIdx.x; i < all && !*gave_up; i += gridDim.x) {
+                const long long slot = i / a.s.hk;
+                if (seq_of_slot(a.s, slot) < 0) continue;
+                const int head_k = (int)(i % a.s.hk);
+                // after the slices that go ahead while the last item's keys and queries are still in use
+                int kq_after = vpad > kGradV ? 2 : 1;
+                for (int hr = 0; hr < rep; ++hr) {
+                    const unsigned char *w = a.ws + (size_t)(slot * a.s.hv + head_k * rep + hr) * lay.stride;
+                    for (int v0 = 0; v0 < vpad && !*gave_up; v0 += kGradV, ++n) {
+                        const int bytes = min(kGradV, vpad - v0) * 128, vb = v0 / kBlockV, vi = v0 % kBlockV;
+                        if (n) wait_phase(&bar.s_empty, (n - 1) & 1, gave_up);
+                        if (*gave_up) break;
                         mbar_arrive_expect_tx(&bar.s_full, 4 * KH * bytes);
                         for (int p = 0; p < 2 * KH; ++p) {   // parts and halves
                             const size_t from = (size_t)(vb * 2 * KH + p) * kHalf + vi * 128;
                             bulk_load(smem + M::kS + p * kSlice, w + lay.s + from, bytes, &bar.s_full);
                             bulk_load(smem + M::kDS + p * kSlice, w + lay.ds + from, bytes, &bar.s_full);
                         }
-                    }
-                    cp_async_wait<0>();   // dO
-                    fence_async();
-                    mbar_arrive(&bar.u_full);
-                    if (kq_due) {   // after the slice that goes ahead while the last item's keys and queries are still in use
-                        kq_due = false;
-                        if (items >= 2) wait_phase(&bar.kq_empty, (items - 2) & 1, gave_up);
-                        if (lane == 0 && !*gave_up) {
+                        if (--kq_after == 0) {
+                            if (items) wait_phase(&bar.kq_empty, (items - 1) & 1, gave_up);
+                            if (*gave_up) { ++n; break; }
                             mbar_arrive_expect_tx(&bar.kq_full, NP * M::kKQ);
                             bulk_load(smem, a.kq + (size_t)(slot * a.s.hk + head_k) * kq_stride(a.s.k, NP), NP * M::kKQ, &bar.kq_full);
+                            ++items;
                         }
                     }
                 }
             }
-        }
-        const uint32_t real = items;
-        announce_item(GradItem{0, 0, 0});
-        if (*gave_up && lane == 0 && n) {   // copies in flight; without it the others have waited for every one
-            wait_drained(&bar.u_full, (n - 1) & 1);
-            wait_drained(&bar.s_full, (n - 1) & 1);
-            if (real) wait_drained(&bar.kq_full, (real - 1) & 1);
+            if (*gave_up && n) {   // copies in flight
+                wait_drained(&bar.s_full, (n - 1) & 1);
+                if (items) wait_drained(&bar.kq_full, (items - 1) & 1);
+            }
         }
         __syncwarp();
     } else if (warp == kGradWarps + 1) {   // products
@@ -197,7 +239,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
         const uint64_t du = operand(base + M::kDU, false, kSlice), o = operand(base + M::kO, true, 0);
         const uint64_t sl = operand(base + M::kS, false, kSplit), dsl = operand(base + M::kDS, false, kSplit);
         const uint64_t kq_rows = operand(base, true, 0), k_left = operand(base, false, kKSplit);
-        const uint64_t f1_rows = operand(base + M::kF1, true, 0), f1_cols = operand(base + M::kF1, false, 0), f2 = operand(base + M::kF2, true, 0);
+        const uint64_t f_rows = operand(base + M::kF1, true, 0), f_cols = operand(base + M::kF1, false, M::kF2 - M::kF1);
         uint32_t n = 0, heads = 0;
         for (uint32_t items = 0;; ++items) {
             wait_phase(&bar.item_full[items & 1], (items / 2) & 1, gave_up);
@@ -258,7 +300,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 mma_commit(one, &bar.x_done);
                 wait_phase(&bar.f_ready, heads & 1, gave_up);
                 tmem_fence_after();
-                // F1 K to dQ, F1^T Q + (F2 + F2^T) K to dK, all transposed
+                // F1 K to dQ and F2 K to dK, F1^T Q + F2^T K to dK, all transposed
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
@@ -267,9 +309,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                         for (int k = 0; k < 4; ++k) {
                             const bool add = hr + p + h + k > 0;
                             const uint64_t kl = further(k_left, p * M::kKQ + k * 2048), ql = further(kl, kChunk * 128);
-                            mma_smem(one, tm + kColF, kl, further(f1_rows, h * (uint32_t)kSquare + k * 32), shape(kChunk, true) | kLeftByColumns, add);
-                            mma_smem(one, tm + kColF + 64, ql, further(f1_cols, h * (uint32_t)kSquare + k * 2048), shape(kChunk, false) | kLeftByColumns, add);
-                            mma_smem(one, tm + kColF + 64, kl, further(f2, h * (uint32_t)kSquare + k * 32), shape(kChunk, true) | kLeftByColumns, true);
+                            const uint64_t fr = further(f_rows, h * (uint32_t)kSquare + k * 32);
+                            mma_smem(one, tm + kColF, kl, further(f_cols, h * (uint32_t)kSquare + k * 2048), shape(2 * kChunk, false) | kLeftByColumns, add);
+                            mma_smem(one, tm + kColF + 64, ql, fr, shape(kChunk, true) | kLeftByColumns, true);
+                            mma_smem(one, tm + kColF + 64, kl, further(fr, M::kF2 - M::kF1), shape(kChunk, true) | kLeftByColumns, true);
                         }
                 mma_commit(one, &bar.f_done);
             }
@@ -288,18 +331,38 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
         float *run = dotb + 4 * kChunk;                             // [4 quarters of the rows][64] column sums of Z
         float *diag = run + 4 * kChunk;                             // [64] dU_j . U_j
         float *inner = diag + kChunk;                               // <S, dS'> by warps
-        uint32_t n = 0, heads = 0;
-        for (uint32_t items = 0;; ++items) {
+        uint32_t n = 0, heads = 0, items = 0;
+        GradItem item;
+        float prod = 0.f;   // this thread's part of <S, dS'>
+        auto products = [&](int v0) {   // of a slice
+            const int vr = min(kGradV, vpad - v0);
+            wait_phase(&bar.s_full, n & 1, gave_up);
+#pragma unroll 1
+            for (int i = tid; i < kGradV * KP / 8; i += 32 * kGradWarps) {   // the same place in all four images
+                if (i % (kGradV * 8) >= vr * 8) continue;                    // not loaded
+                const uint4 *sv = reinterpret_cast<const uint4 *>(smem + M::kS) + i;
+                const uint4 *dv = reinterpret_cast<const uint4 *>(smem + M::kDS) + i;
+                const uint4 sh = sv[0], sl = sv[M::kSP / 16], dh = dv[0], dl = dv[M::kSP / 16];
+                const uint32_t *shp = &sh.x, *slp = &sl.x, *dhp = &dh.x, *dlp = &dl.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    prod += (bf16_low(shp[e]) + bf16_low(slp[e])) * (bf16_low(dhp[e]) + bf16_low(dlp[e]));
+                    prod += (bf16_high(shp[e]) + bf16_high(slp[e])) * (bf16_high(dhp[e]) + bf16_high(dlp[e]));
+                }
+            }
+            warp_arrive(&bar.s_empty, lane);
+            ++n;
+        };
+        auto next_item = [&]() -> bool {   // one decision for all; then the first slice, so that the second is loaded early
             wait_phase(&bar.item_full[items & 1], (items / 2) & 1, gave_up);
-            const GradItem item = bar.item[items & 1];
-            meet();   // one decision for all
-            const bool stop = item.rows == 0 || *gave_up;
-            if (tid == 0) inner[0] = stop ? 1.f : 0.f;
-            meet();
-            const bool all_stop = inner[0] != 0.f;
-            meet();
+            item = bar.item[items & 1];
+            const bool stop = meet_any(item.rows == 0 || *gave_up);
             warp_arrive(&bar.item_empty[items & 1], lane);
-            if (all_stop) break;
+            ++items;
+            if (!stop) products(0);
+            return !stop;
+        };
+        for (bool more = next_item(); more;) {
             float dq[16], dk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) dq[i] = dk[i] = 0.f;
@@ -307,30 +370,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             for (int hr = 0; hr < rep; ++hr, ++heads) {
                 const int head = item.head_k * rep + hr;
                 const float *scal = reinterpret_cast<const float *>(smem + M::kScal + (heads & 1) * 6 * kChunk * 4);
-                float prod = 0.f;   // this thread's part of <S, dS'>
-                for (int v0 = 0; v0 < vpad; v0 += kGradV, ++n) {
-                    const int vr = min(kGradV, vpad - v0);
-                    wait_phase(&bar.s_full, n & 1, gave_up);
-#pragma unroll 1
-                    for (int i = tid; i < kGradV * KP / 8; i += 32 * kGradWarps) {   // the same place in all four images
-                        if (i % (kGradV * 8) >= vr * 8) continue;                    // not loaded
-                        const uint4 *sv = reinterpret_cast<const uint4 *>(smem + M::kS) + i;
-                        const uint4 *dv = reinterpret_cast<const uint4 *>(smem + M::kDS) + i;
-                        const uint4 sh = sv[0], sl = sv[M::kSP / 16], dh = dv[0], dl = dv[M::kSP / 16];
-                        const uint32_t *shp = &sh.x, *slp = &sl.x, *dhp = &dh.x, *dlp = &dl.x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            prod += (bf16_low(shp[e]) + bf16_low(slp[e])) * (bf16_low(dhp[e]) + bf16_low(dlp[e]));
-                            prod += (bf16_high(shp[e]) + bf16_high(slp[e])) * (bf16_high(dhp[e]) + bf16_high(dlp[e]));
-                        }
-                    }
-                    warp_arrive(&bar.s_empty, lane);
-                }
+                for (int v0 = kGradV; v0 < vpad; v0 += kGradV) products(v0);
 #pragma unroll
                 for (int m = 16; m; m >>= 1) prod += __shfl_xor_sync(0xffffffffu, prod, m);
                 if (lane == 0) inner[warp] = prod;
+                prod = 0.f;
                 wait_phase(&bar.scal_full[heads & 1], (heads / 2) & 1, gave_up);
-                if (hr == 0) wait_phase(&bar.kq_full, items & 1, gave_up);
+                if (hr == 0) wait_phase(&bar.kq_full, (items - 1) & 1, gave_up);
                 if (heads) wait_phase(&bar.f_done, (heads - 1) & 1, gave_up);   // F has been used
                 wait_phase(&bar.x_done, heads & 1, gave_up);
                 tmem_fence_after();
@@ -370,28 +416,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 }
                 meet();   // the images of F take the place of what was exchanged
 
-                // F1 = scale D dP, F2 = D dN (with its transpose) as pairs, and Z
+                // F1 = scale D dP and F2 = D dN, transposed, as pairs, and Z
                 {
                     const float ghj = scal[192 + j], glj = scal[256 + j], rj = scal[320 + j];
+                    const int i0 = tok + 8 * role;
+                    float f1[8], f2[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = tok + 8 * role + e;
-                        const float D = i >= j && scal[320 + i] == rj ? expf((scal[192 + i] - ghj) + (scal[256 + i] - glj)) : 0.f;
-                        if (i == j) diag[j] = dn[e];
-                        const float f1 = i >= j ? a.s.scale * D * dp[e] : 0.f, f2 = i > j ? -scal[128 + i] * D * dn[e] : 0.f;
-                        Z[i * kZStride + j] = i > j ? f1 * qk[i * kChunk + j] + f2 * kk[i * kChunk + j] : 0.f;
-                        const __nv_bfloat16 h1 = __float2bfloat16_rn(f1), h2 = __float2bfloat16_rn(f2);
-                        const __nv_bfloat16 l1 = __float2bfloat16_rn(f1 - __bfloat162float(h1)), l2 = __float2bfloat16_rn(f2 - __bfloat162float(h2));
-                        const uint32_t ij = img(0, i, j >> 3) + (j & 7) * 2, ji = img(0, j, i >> 3) + (i & 7) * 2;
-                        *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF1 + ij) = h1;
-                        *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF1 + kSquare + ij) = l1;
-                        if (i >= j) {
-                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + ij) = h2;
-                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + kSquare + ij) = l2;
-                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + ji) = h2;
-                            *reinterpret_cast<__nv_bfloat16 *>(smem + M::kF2 + kSquare + ji) = l2;
-                        }
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 be = *reinterpret_cast<const float4 *>(scal + 128 + i0 + e), gh = *reinterpret_cast<const float4 *>(scal + 192 + i0 + e);
+                        const float4 gl = *reinterpret_cast<const float4 *>(scal + 256 + i0 + e), rr = *reinterpret_cast<const float4 *>(scal + 320 + i0 + e);
+                        auto one = [&](int m, float beta, float high, float low, float count) {
+                            const int i = i0 + m;
+                            const float D = i >= j && count == rj ? expf((high - ghj) + (low - glj)) : 0.f;
+                            if (i == j) diag[j] = dn[m];
+                            f1[m] = i >= j ? a.s.scale * D * dp[m] : 0.f;
+                            f2[m] = i > j ? -beta * D * dn[m] : 0.f;
+                            Z[i * kZStride + j] = i > j ? f1[m] * qk[i * kChunk + j] + f2[m] * kk[i * kChunk + j] : 0.f;
+                        };
+                        one(e, be.x, gh.x, gl.x, rr.x);
+                        one(e + 1, be.y, gh.y, gl.y, rr.y);
+                        one(e + 2, be.z, gh.z, gl.z, rr.z);
+                        one(e + 3, be.w, gh.w, gl.w, rr.w);
                     }
+                    const uint32_t ji = img(base + M::kF1, j, i0 >> 3);   // eight tokens i of row j
+                    uint4 h, l;
+                    split2(f1[0], f1[1], h.x, l.x); split2(f1[2], f1[3], h.y, l.y); split2(f1[4], f1[5], h.z, l.z); split2(f1[6], f1[7], h.w, l.w);
+                    st_shared16(ji, h);
+                    st_shared16(ji + (uint32_t)kSquare, l);
+                    split2(f2[0], f2[1], h.x, l.x); split2(f2[2], f2[3], h.y, l.y); split2(f2[4], f2[5], h.z, l.z); split2(f2[6], f2[7], h.w, l.w);
+                    st_shared16(ji + (M::kF2 - M::kF1), h);
+                    st_shared16(ji + (M::kF2 - M::kF1) + (uint32_t)kSquare, l);
                 }
                 fence_async();
                 tmem_fence_before();
@@ -406,23 +460,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                     warp_arrive(&bar.acc_free, lane);
                     const uint32_t piece = (uint32_t)(col >> 3), in = (uint32_t)(col & 7) * 2;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float eg = scal[tok + i], el = scal[64 + tok + i], be = scal[128 + tok + i];
-                        float kv = 0.f, qv = 0.f;
-                        if (col < KP) {
-                            const uint32_t k0 = img(0, tok + i, piece) + in, q0 = k0 + kChunk * 128;
-                            kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + k0));
-                            qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + q0));
-                            if constexpr (NP == 2) {
-                                kv += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + M::kKQ + k0));
-                                qv += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + M::kKQ + q0));
+                    for (int i4 = 0; i4 < 16; i4 += 4) {
+                        const float4 eg4 = *reinterpret_cast<const float4 *>(scal + tok + i4), el4 = *reinterpret_cast<const float4 *>(scal + 64 + tok + i4);
+                        const float4 be4 = *reinterpret_cast<const float4 *>(scal + 128 + tok + i4);
+                        auto one = [&](int i, float eg, float el, float be) {
+                            float kv = 0.f, qv = 0.f;
+                            if (col < KP) {
+                                const uint32_t k0 = img(0, tok + i, piece) + in, q0 = k0 + kChunk * 128;
+                                kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + k0));
+                                qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + q0));
+                                if constexpr (NP == 2) {
+                                    kv += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + M::kKQ + k0));
+                                    qv += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(smem + M::kKQ + q0));
+                                }
                             }
-                        }
-                        const float x1 = a.s.scale * eg * x[i], x2 = eg * be * y[i], x3 = el * z[i];
-                        dq[i] += x1;
-                        dk[i] += x3 - x2;
-                        x[i] = qv * x1 - kv * x2;   // to a_i
-                        y[i] = kv * x3;             // to b_j
+                            const float x1 = a.s.scale * eg * x[i], x2 = eg * be * y[i], x3 = el * z[i];
+                            dq[i] += x1;
+                            dk[i] += x3 - x2;
+                            x[i] = qv * x1 - kv * x2;   // to a_i
+                            y[i] = kv * x3;             // to b_j
+                        };
+                        one(i4, eg4.x, el4.x, be4.x);
+                        one(i4 + 1, eg4.y, el4.y, be4.y);
+                        one(i4 + 2, eg4.z, el4.z, be4.z);
+                        one(i4 + 3, eg4.w, el4.w, be4.w);
                     }
                     const float sa = sum16(x, lane), sb = sum16(y, lane);
                     if ((lane & 1) == 0) {
@@ -442,19 +503,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                         Z[(16 * q + t) * kZStride + jj] = s;
                     }
                     run[q * kChunk + jj] = s;
+                } else if (tid < 256 + 2 * kChunk) {   // the quadrants' dots
+                    float *d = (tid & kChunk ? dotb : dots) + (tid & 63);
+                    d[0] = (d[0] + d[kChunk]) + (d[2 * kChunk] + d[3 * kChunk]);
                 }
                 meet();
                 {   // row t: sum over j < t (eight threads a row), and all else for token t
                     const int t = tid >> 3, sub = tid & 7;
                     float s = 0.f;
-                    for (int jj = sub; jj < t; jj += 8) {
-                        s += Z[t * kZStride + jj];
-                        for (int q = (t >> 4) + 1; q < 4; ++q) s += run[q * kChunk + jj];
-                    }
-                    // a_i of i >= t, b_j of j < t, <S, dS'>
-                    for (int i = sub; i < kChunk; i += 8) {
-                        const float *d = i >= t ? dots : dotb;
-                        s += (d[i] + d[kChunk + i]) + (d[2 * kChunk + i] + d[3 * kChunk + i]);
+#pragma unroll
+                    for (int m = 0; m < kChunk; m += 8) {
+                        const int jj = sub + m;
+                        float z = Z[t * kZStride + jj];
+#pragma unroll
+                        for (int q = 1; q < 4; ++q) z += q > t >> 4 ? run[q * kChunk + jj] : 0.f;
+                        // a_i of i >= t, b_j of j < t, <S, dS'>
+                        s += jj < t ? z + dotb[jj] : dots[jj];
                     }
                     s += scal[kChunk - 1] * (inner[sub] + inner[8 + sub]);
 #pragma unroll
@@ -471,7 +535,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 }
                 meet();
                 warp_arrive(&bar.scal_empty[heads & 1], lane);
+                if (hr + 1 < rep) products(0);   // of the next head
             }
+            const GradItem was = item;
+            more = next_item();
             wait_phase(&bar.f_done, (heads - 1) & 1, gave_up);
             tmem_fence_after();
             {
@@ -479,16 +546,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 tmem_ld16(x, at + kColF + tok, y, at + kColF + 64 + tok);
                 tmem_fence_before();
                 warp_arrive(&bar.kq_empty, lane);
-                const size_t ostride = (size_t)a.s.hk * a.s.k, first = ((size_t)(item.token + tok) * a.s.hk + item.head_k) * a.s.k + col;
+                const size_t ostride = (size_t)a.s.hk * a.s.k, first = ((size_t)(was.token + tok) * a.s.hk + was.head_k) * a.s.k + col;
                 T *oq = static_cast<T *>(a.dq) + first, *ok = static_cast<T *>(a.dk) + first;
                 const float bad = *gave_up ? __int_as_float(0x7fffffff) : 0.f;   // not what they should be: say so
-                if (col < a.s.k)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    dq[i] += x[i] + bad;
+                    dk[i] += y[i] + bad;
+                }
+                if constexpr (sizeof(T) == 2)
+                    if (quads) {   // four lanes exchange, so that each has four columns of every fourth token
+                        store_quads<T>(dq, oq - (lane & 3), ostride, lane, was.rows - tok, col < a.s.k);
+                        store_quads<T>(dk, ok - (lane & 3), ostride, lane, was.rows - tok, col < a.s.k);
+                    }
+                if ((sizeof(T) > 2 || !quads) && col < a.s.k) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (tok + i < item.rows) {
-                            oq[i * ostride] = from_f32<T>(dq[i] + x[i] + bad);
-                            ok[i * ostride] = from_f32<T>(dk[i] + y[i] + bad);
+                        if (tok + i < was.rows) {
+                            oq[i * ostride] = from_f32<T>(dq[i]);
+                            ok[i * ostride] = from_f32<T>(dk[i]);
                         }
+                }
             }
         }
     }
