@@ -24,7 +24,7 @@
  * outputs of their own sequence, and of the heads that share the input, and
  * no others (within a chunk of 64 tokens also those before them).
  *
- * A kernel of the sequence calls whose bounded waits ran out, which a correct
+ * A kernel whose bounded waits ran out, which a correct
  * launch never does, finishes with NaN in its outputs instead of hanging.
  *
  * Conventions: device pointers owned by the caller; work is enqueued on

@@ -12,7 +12,8 @@
 // into tensor memory, right operands are the images in shared memory.  P^T dO
 // runs while dS' is on its way through registers, scale (exp(G) Q)^T dO while Y
 // is; dO becomes a left operand while the state's product runs.  Segments and their
-// two passes are as there.
+// two passes are as there, and so is what bounds it: 4 x 4096 tokens, 16 heads of
+// 128 x 128, take 240 us; 16384 tokens of 8 heads two passes of 56.
 #include "delta_tmem.cuh"
 
 namespace ps {

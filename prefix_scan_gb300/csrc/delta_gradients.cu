@@ -16,9 +16,15 @@
 // lie there, transposed so that keys' columns are the 128 rows:
 //     X1 = S dO^T, X2 = S dU^T, X3 = dS' U^T           (columns: tokens)
 // and, U's two parts one above the other as 128 rows, U dO^T and U dU^T.  One warp
-// issues them, one loads (64 values at a time, 32 where inputs are pairs; on into the
+// issues them, two load (64 values at a time, 32 where inputs are pairs; on into the
 // next item while the last one is being finished), sixteen take them apart: a lane per
 // column of the keys, or per token j, a quarter of the tokens i each.
+//
+// Bounded by shared memory: products read both operands there, and so do the sixteen
+// warps, whose steps follow one another.  So F is stored by whole 16-byte pieces (eight
+// tokens i of a row j; number by number it took a sixth of the kernel), and gradients
+// leave four columns at a time.  4 x 4096 tokens, 16 heads of 128 x 128: 280 us for
+// 1.1 GB read and written, 4.0 TB/s.
 #include "delta_tmem.cuh"
 
 namespace ps {

@@ -7,7 +7,9 @@
 // writes lists into the workspace; a plan that hands out pages ends at the first
 // tile that holds enough of them.  The move is a grid of CTAs
 // that copy pieces of pages and rewrite the tables.  Moves are bound by memory:
-// a moved page is read once and written once.
+// a moved page is read once and written once.  Compacting 16384 pages of two pools
+// of 32 KiB, of which 3585 move: 100 us, the move 75 of it at 6.3 TB/s.  Smaller calls
+// are bound by their launches and the host: 37 pages copied in 10 us.
 #include <climits>
 #include <cstdint>
 
