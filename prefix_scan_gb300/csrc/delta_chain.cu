@@ -47,7 +47,7 @@ template <typename T, int KP>
 struct ChainSmem {
     static constexpr int NP = Planes<T>::NP;
     static constexpr int kKQ = NP * (KP / 64) * kHalf, kTP = 4 * (int)kSquare;
-    static constexpr int kStages = NP == 1 ? 2 : 1;
+    static constexpr int kStages = NP == 1 || (KP == 64 && sizeof(T) == 2) ? 2 : 1;   // as many as there is room for
     static constexpr int kScal = 256, kTiles = 2048, kStage = kKQ + kTP;   // barriers and scalars come first
     static constexpr int kVRow = kBlockV * (int)sizeof(T), kVTile = kChunk * kVRow, kV = kTiles + kStages * kStage;
     // outputs; S on its way out in training; U, which at K = 128 takes the place of T and of the queries

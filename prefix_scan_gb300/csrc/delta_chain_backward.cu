@@ -30,7 +30,7 @@ template <typename T, int KP>
 struct BackSmem {
     static constexpr int NP = Planes<T>::NP;
     static constexpr int kKQ = NP * (KP / 64) * kHalf, kTP = 4 * (int)kSquare;
-    static constexpr int kStages = NP == 1 ? 2 : 1;
+    static constexpr int kStages = NP == 1 || (KP == 64 && sizeof(T) == 2) ? 2 : 1;   // as many as there is room for
     static constexpr int kScal = 256, kTiles = 2048, kStage = kKQ + kTP;   // barriers and two chunks' scalars come first
     static constexpr int kRow = kBlockV * (int)sizeof(T), kTile = kChunk * kRow;
     static constexpr int kDO = kTiles + kStages * kStage, kOut = kDO + kTile, kSave = kOut + kTile;
