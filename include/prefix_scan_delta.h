@@ -114,6 +114,7 @@ ps_status ps_delta_forward(const ps_delta_shape *shape, const ps_delta_tensor in
  *         [.., heads_v]: contiguous; dq and dk are summed over the value
  *         heads that share a key head, in a fixed order
  *   dh0   gradient of h0, or NULL
+ * Gradients of tokens that no sequence holds are 0.
  * Results are bitwise reproducible from call to call (no atomics).
  */
 ps_status ps_delta_backward(const ps_delta_shape *shape, const ps_delta_tensor *q, const ps_delta_tensor *k,

@@ -25,6 +25,8 @@
 // tokens i of a row j; number by number it took a sixth of the kernel), and gradients
 // leave four columns at a time.  4 x 4096 tokens, 16 heads of 128 x 128: 280 us for
 // 1.1 GB read and written, 4.0 TB/s.
+#include <type_traits>
+
 #include "delta_tmem.cuh"
 
 namespace ps {
@@ -579,6 +581,34 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
+    if (a.s.cu) {   // tokens of no sequence: before the first one and after the last, or between them where offsets fall
+        int falls = 0;
+        for (long long i = tid; i < a.s.seqs; i += kGradThreads) falls |= a.s.cu[i + 1] < a.s.cu[i];
+        falls = __syncthreads_or(falls);
+        const Span last = span_of(a.s, a.s.seqs - 1);
+        const long long before = span_of(a.s, 0).first, from = last.first + last.len;
+        const long long n = falls ? a.s.tokens : before + a.s.tokens - from;
+        for (long long i = blockIdx.x; i < n; i += gridDim.x) {
+            const long long t = falls || i < before ? i : i - before + from;
+            if (falls) {
+                int held = 0;
+                for (long long q = tid; q < a.s.seqs; q += kGradThreads) {
+                    const Span sp = span_of(a.s, q);
+                    held |= t >= sp.first && t < sp.first + sp.len;
+                }
+                if (__syncthreads_or(held)) continue;
+            }
+            auto clear = [&](auto *p, int width) {
+                for (int x = tid; x < width; x += kGradThreads) p[t * width + x] = from_f32<std::remove_reference_t<decltype(*p)>>(0.f);
+            };
+            clear(static_cast<T *>(a.dq), a.s.hk * a.s.k);
+            clear(static_cast<T *>(a.dk), a.s.hk * a.s.k);
+            clear(static_cast<T *>(a.dv), a.s.hv * a.s.v);
+            clear(a.dg, a.s.hv);
+            if (a.beta_f32) clear(static_cast<float *>(a.dbeta), a.s.hv);
+            else clear(static_cast<T *>(a.dbeta), a.s.hv);
+        }
+    }
     if (*gave_up) {   // items that were not reached
         const long long tokens = a.s.cu ? a.s.tokens : a.s.seqs * a.s.tokens;
         for (long long i = tid; i < tokens * a.s.hv; i += kGradThreads) a.dg[i] = __int_as_float(0x7fffffff);

@@ -224,7 +224,7 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
     lib = _lib.load()
     s, ctx = enter(q.device, stream)
     with ctx:
-        new = torch.zeros if packed else torch.empty
+        new = torch.zeros if packed and saved.cu_seqlens.numel() == 1 else torch.empty   # with no sequence nothing is enqueued
         heads = saved.v_shape[:-1]
         dq, dk = (new(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))
         dv = new(saved.v_shape, dtype=q.dtype, device=q.device)

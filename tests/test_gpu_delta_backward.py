@@ -131,6 +131,22 @@ def test_tokens_of_no_sequence_have_no_gradient():
         assert (t[:10] == 0).all() and (t[90:] == 0).all() and torch.isfinite(t).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cu", [[0, 5], [7, 7], [130, 130, 200, 250], [3, 300], [300, 300], [90, 20, 40]])
+def test_tokens_of_no_sequence_in_used_memory(dtype, cu):
+    # new tensors come from memory that held NaN; offsets that fall count as empty sequences
+    x = inputs(300, 2, 4, 24, 40, dtype, 51)
+    o, _, saved = api.delta_rule_forward(*x, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV))
+    held = [torch.full_like(t, float("nan")) for t in (*x, *x)]
+    del held
+    grads = api.delta_rule_backward(saved, torch.ones_like(o))[:5]
+    outside = torch.ones(300, dtype=torch.bool, device=DEV)
+    for a, b in zip(cu, cu[1:]):
+        outside[a:max(a, b)] = False
+    for grad in grads:
+        assert (grad[outside] == 0).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_bad_gradients_stay_in_their_sequence(bad):
     lens = [70, 33, 90]
