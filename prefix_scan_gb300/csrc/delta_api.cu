@@ -82,11 +82,12 @@ size_t chunks_bytes(const ps_delta_shape *d, int train) {
     const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
     return (size_t)slots * d->heads_v * ps::chunk_layout(d->dim_k, d->dim_v, train != 0).stride;
 }
-// The workspace's parts after the chunks': keys and queries, and what segments need.
+// The workspace's parts after the chunks': keys and queries, what segments need, the sequences' order.
 struct Parts {
     int seg;
     long long seg_slots;
-    size_t kq, seg_m, seg_state, total;
+    size_t kq, seg_m, seg_state, order, total;
+    bool ordered;
 };
 Parts parts_of(const ps_delta_shape *d, int train) {
     const bool packed = d->cu_seqlens != nullptr;
@@ -98,7 +99,10 @@ Parts parts_of(const ps_delta_shape *d, int train) {
     p.seg = ps::segment_chunks(d->num_seqs * d->heads_v * ps::blocks_v(d->dim_v), chunks, train != 0);
     p.seg_slots = ps::segment_slots(slots, d->num_seqs, p.seg);
     p.seg_state = p.seg_m + (size_t)p.seg_slots * d->heads_v * ps::seg_m_bytes(d->dim_k);
-    p.total = p.seg_state + (p.seg ? (size_t)(p.seg_slots + 1) * d->heads_v * d->dim_k * d->dim_v * 4 : 0);
+    p.order = p.seg_state + (p.seg ? (size_t)(p.seg_slots + 1) * d->heads_v * d->dim_k * d->dim_v * 4 : 0);
+    p.ordered = packed && !p.seg && d->num_seqs > 1 && d->num_seqs <= ps::kOrdered &&
+                d->num_seqs * d->heads_v * ps::blocks_v(d->dim_v) > 152;   // as many run at once
+    p.total = p.order + (p.ordered ? (size_t)d->num_seqs * 4 : 0);
     p.total = (p.total + 255) / 256 * 256;
     return p;
 }
@@ -109,6 +113,7 @@ void place(ps::DeltaArgs &a, const Parts &p, void *ws) {
     a.seg_slots = p.seg_slots;
     a.seg_m = a.ws + p.seg_m;
     a.seg_state = reinterpret_cast<float *>(a.ws + p.seg_state);
+    a.order = p.ordered ? reinterpret_cast<int32_t *>(a.ws + p.order) : nullptr;
 }
 // The chain, or where sequences are cut the states of the segments, their join and the chain.
 template <typename Chain>

@@ -29,7 +29,7 @@
 //
 // Measured at 128 x 128 and bf16: a chunk takes 5600 clocks of its chain, products
 // being issued in about half of them (tensor pipe 32 % busy).  12345 tokens in 48
-// sequences, 32 heads: 286 us; 4 x 4096 tokens, 16 heads, with what training keeps:
+// sequences, 32 heads: 254 us; 4 x 4096 tokens, 16 heads, with what training keeps:
 // 243 us; 32768 tokens, 8 heads: two passes of 128 us (uncut, 1.3 ms).
 #include "delta_tmem.cuh"
 

@@ -267,6 +267,7 @@ struct Chain {
 __device__ __forceinline__ long long first_segment(const DeltaArgs &a, long long seq) { return span_of(a.s, seq).slot / a.seg + seq; }
 __device__ __forceinline__ bool chain_of(const DeltaArgs &a, long long index, Chain &c) {
     if (a.seg == 0) {
+        if (a.order) index = a.order[index];
         c = Chain{index, 0, true, true, span_of(a.s, index)};
         return true;
     }

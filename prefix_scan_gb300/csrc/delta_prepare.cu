@@ -57,6 +57,17 @@ __global__ void __launch_bounds__(kPrepThreads, Planes<T>::NP == 1 ? 4 : KP == 6
     const long long slot = blockIdx.x;
     const int head_k = blockIdx.y, rep = a.s.hv / a.s.hk;
 
+    if (a.order && slot == 0 && head_k == 0) {
+        int *len = reinterpret_cast<int *>(smem);
+        for (int i = tid; i < a.s.seqs; i += kPrepThreads) len[i] = (int)span_of(a.s, i).len;
+        __syncthreads();
+        for (int i = tid; i < a.s.seqs; i += kPrepThreads) {
+            int rank = 0;
+            for (int j = 0; j < a.s.seqs; ++j) rank += len[j] > len[i] || (len[j] == len[i] && j < i);
+            a.order[rank] = i;
+        }
+        __syncthreads();
+    }
     const long long seq = seq_of_slot(a.s, slot);
     if (seq < 0) return;
     const Span sp = span_of(a.s, seq);

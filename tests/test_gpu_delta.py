@@ -262,6 +262,18 @@ def test_step_many_states(dtype, n, t, hk, hv, k, v):
     assert torch.equal(pool[untouched], was[untouched])
 
 
+def test_many_sequences_of_different_lengths():
+    # more chains than run at once, in another order than they come; and more sequences than are ordered
+    for n, hv in ((100, 4), (300, 2)):
+        lens = [(37 * i) % 131 for i in range(n)]
+        x = inputs(sum(lens), 1, hv, 32, 40, F32, 131)
+        h0 = states(n, hv, 32, 40, 132)
+        o, last = api.delta_rule(*x, cu_seqlens=cu_of(lens), initial_state=h0, output_final_state=True)
+        want = ref.packed(*x, 32 ** -0.5, lens, h0)
+        near(o, want["o"], CHUNKED)
+        near(last, want["state"], CHUNKED)
+
+
 def test_steps_continue_a_prompt():
     # a prompt by chunks, its state handed to single steps, against the whole sequence
     x = inputs(80, 2, 4, 128, 128, F32, 111, seqs=2)
