@@ -29,7 +29,7 @@
 //
 // Measured at 128 x 128 and bf16: a chunk takes 5600 clocks of its chain, products
 // being issued in about half of them (tensor pipe 32 % busy).  12345 tokens in 48
-// sequences, 32 heads: 254 us; 4 x 4096 tokens, 16 heads, with what training keeps:
+// sequences, 32 heads: 230 us; 4 x 4096 tokens, 16 heads, with what training keeps:
 // 243 us; 32768 tokens, 8 heads: two passes of 128 us (uncut, 1.3 ms).
 #include "delta_tmem.cuh"
 
@@ -281,15 +281,19 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
         const uint32_t at = (uint32_t)(warp & 3) << 21;                                             // lane 32 (warp % 4)
         float x[2][16], y[2][16];
         uint32_t hi[8], lo[8];
-#pragma unroll 1
-        for (int b = 0; b < KP / 32; ++b) {   // 16 columns of the state at a time
-            const int k0 = half * (KP / 2) + 16 * b;
+        {   // the state at the start: all of its loads in flight at once
+            float s[KP / 32][16];
+            const float *row_from = from + (size_t)half * (KP / 2) * a.s.v + v;
+            const int n = from && !matrix && v < a.s.v ? a.s.k - half * (KP / 2) : 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x[0][i] = matrix ? (k0 + i == v ? 1.f : 0.f)
-                          : from && k0 + i < a.s.k && v < a.s.v ? from[(size_t)(k0 + i) * a.s.v + v]
-                                                                : 0.f;
-            tmem_st16(at + kColS + k0, x[0]);
+            for (int b = 0; b < KP / 32; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[b][i] = matrix && half * (KP / 2) + 16 * b + i == v ? 1.f : 0.f;
+                    if (16 * b + i < n) s[b][i] = row_from[(size_t)(16 * b + i) * a.s.v];
+                }
+#pragma unroll
+            for (int b = 0; b < KP / 32; ++b) tmem_st16(at + kColS + half * (KP / 2) + 16 * b, s[b]);
         }
         tmem_wait_st();
         // this half's values of a chunk; rows past the sequence's end and values past V hold anything and count as 0

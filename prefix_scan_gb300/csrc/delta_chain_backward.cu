@@ -260,13 +260,19 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         const uint32_t at = (uint32_t)(warp & 3) << 21;                                             // lane 32 (warp % 4)
         float x[2][16];
         uint32_t hi[8], lo[8];
-#pragma unroll 1
-        for (int b = 0; b < KP / 32; ++b) {   // 16 columns of the state at a time
-            const int k0 = half * (KP / 2) + 16 * b;
+        {   // the gradient at the end: all of its loads in flight at once
+            float s[KP / 32][16];
+            const float *row_from = from + (size_t)half * (KP / 2) * a.s.v + v;
+            const int n = from && v < a.s.v ? a.s.k - half * (KP / 2) : 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x[0][i] = from && k0 + i < a.s.k && v < a.s.v ? from[(size_t)(k0 + i) * a.s.v + v] : 0.f;
-            tmem_st16(at + kColS + k0, x[0]);
+            for (int b = 0; b < KP / 32; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[b][i] = 0.f;
+                    if (16 * b + i < n) s[b][i] = row_from[(size_t)(16 * b + i) * a.s.v];
+                }
+#pragma unroll
+            for (int b = 0; b < KP / 32; ++b) tmem_st16(at + kColS + half * (KP / 2) + 16 * b, s[b]);
         }
         tmem_wait_st();
         auto scalars = [&](int i) { return reinterpret_cast<const float *>(smem + M::kScal + (i & 1) * 3 * kChunk * 4) + 32 * half; };

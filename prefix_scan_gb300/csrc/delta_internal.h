@@ -82,7 +82,7 @@ constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
 // Packed sequences of very different lengths: the chains of the longest are launched first, so that the
 // last ones to run are short.  Their order is counted by one CTA of the prepare kernel, in time that grows
 // with the square of the sequences' number; with more than kOrdered, chains are many and even out.  48
-// sequences of 0 to 35 chunks, 32 heads: 254 us against 286 in the order in which they come.
+// sequences of 0 to 35 chunks, 32 heads: 31 us less than in the order in which they come (of 286).
 constexpr long long kOrdered = 256;
 enum DeltaPass { kPassAll = 0, kPassStates = 1 };
 struct DeltaArgs {
