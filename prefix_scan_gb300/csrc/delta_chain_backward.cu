@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], 1 + (!states && M::kInStage));
+            mbar_init(&bar.empty[i], 1 + (!states && (M::kInStage || M::kStages == 2)));
             mbar_init(&bar.s_ready[i], 8);
         }
         mbar_init(&bar.o_full, 32);
@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
                 bulk_wait_read();
                 mbar_arrive(&bar.s_free);
                 wait_phase(&bar.out_ready, i & 1, gave_up);
+                // dV has taken its gates: with two stages the next but one chunk's scalars come in their place
+                if (M::kStages == 2 && !M::kInStage) mbar_arrive(&bar.empty[i % M::kStages]);
                 unsigned char *u = w + lay.du + (size_t)vb * 2 * kHalf;
                 if (M::kInStage) {
                     const uint32_t tiles = base + M::kTiles + i % M::kStages * M::kStage;

@@ -115,6 +115,22 @@ def test_gates_of_zero_and_one():
     check(x, [100], states(1, 2, 64, 32, 42), states(1, 2, 64, 32, 43))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("k,v", [(37, 19), (64, 64), (128, 19)])
+def test_value_gradients_do_not_depend_on_how_fast_they_are_stored(dtype, k, v):
+    # many chunks behind rows that are stored number by number, again and again
+    lens = [700, 640, 65, 0, 330]
+    x = inputs(sum(lens), 2, 4, k, v, dtype, 14)
+    do, _, _, saved, got = gradients(x, lens)
+    want = ref.packed(*x, k ** -0.5, lens, None, do)
+    for name, t in zip(NAMES, got):
+        if t is not None:
+            near(t, want[name], GRAD, name)
+    for _ in range(30):
+        for a, b in zip(api.delta_rule_backward(saved, do), got):
+            assert a is None or torch.equal(a, b)
+
+
 def test_reproducible_and_repeatable():
     x = inputs(500, 2, 6, 128, 128, BF16, 51)
     do, _, _, saved, got = gradients(x, [200, 300])
