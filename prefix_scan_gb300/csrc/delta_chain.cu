@@ -136,19 +136,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
         {
             // operands: keys and queries by rows, keys by columns, T and P after it
             const uint64_t kq0 = operand(base + M::kTiles, true, 0), kt0 = operand(base + M::kTiles, false, kHalf);
-            // U^T P^T: tokens 16 k.. of U reach tokens 16 k.. and later
+            // U^T P^T, all of it: leaving out that tokens 16 k.. of U reach no earlier ones would save no time,
+            // and accumulators of different shapes have no order among them
             auto outputs = [&](int c) {
                 const int st = c % M::kStages;
                 const uint64_t pp = further(kq0, st * M::kStage + M::kKQ + 2 * (uint32_t)kSquare);
                 wait_phase(&bar.u_ready, c & 1, gave_up);
+                wait_phase(&bar.s_done, c & 1, gave_up);   // which has read the pair that was in this place
                 tmem_fence_after();
 #pragma unroll
                 for (int t = 0; t < (NP == 1 ? 3 : 4); ++t)   // hi hi, lo hi, hi lo, and lo lo where outputs may be f32
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_tmem(one, tm + kColO + 16 * k, tm + kColR + (t & 1 ? 32 : 0) + k * 8,
-                                 further(pp, (t & 2 ? (uint32_t)kSquare : 0) + k * (16 * 128 + 32)), shape(kChunk - 16 * k, true),
-                                 t + k > 0);
+                        mma_tmem(one, tm + kColO, tm + kColR + (t & 1 ? 32 : 0) + k * 8,
+                                 further(pp, (t & 2 ? (uint32_t)kSquare : 0) + k * 32), shape(kChunk, true), t + k > 0);
                 mma_commit(one, &bar.o_done);
                 mma_commit(one, &bar.empty[st]);
             };

@@ -41,7 +41,7 @@ struct BackSmem {
     static constexpr int kBytes = kSaveU + (kInStage ? 0 : 2 * kHalf);
 };
 struct BackBars {
-    uint64_t full[2], empty[2], o_full, o_empty, o_ready, s_ready[2], y_done, r_ready, u_done, w_ready, s_done, out_ready, out_free;
+    uint64_t full[2], empty[2], o_full, o_empty, o_ready, p_done, s_ready[2], y_done, r_ready, u_done, w_ready, s_done, out_ready, out_free;
     uint64_t s_kept, s_free, u_free, drained;
     uint32_t tmem;
     int gave_up;
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         mbar_init(&bar.o_full, 32);
         mbar_init(&bar.o_empty, 8);
         mbar_init(&bar.o_ready, 8);
+        mbar_init(&bar.p_done, 1);
         mbar_init(&bar.y_done, 1);
         mbar_init(&bar.r_ready, 8);
         mbar_init(&bar.u_done, 1);
@@ -136,10 +137,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
                     for (int k = 0; k < 4; ++k)
                         mma_tmem(one, tm + kColP, tm + kColO + p * 32 + k * 8,
                                  further(tt, (2 + t) * (uint32_t)kSquare + k * 16 * 128), shape(kChunk, false), t + p + k > 0);
+            mma_commit(one, &bar.p_done);
             // dS'^T K^T, by the columns of dS' that are ready together
 #pragma unroll
             for (int r = 0; r < KH; ++r) {
                 wait_busy(&bar.s_ready[r], i & 1, gave_up);
+                if (r == 0) wait_busy(&bar.p_done, i & 1, gave_up);   // dO has been read: K dS' takes its place
                 tmem_fence_after();
 #pragma unroll
                 for (int p = 0; p < NP; ++p)

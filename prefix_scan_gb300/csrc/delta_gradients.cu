@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 mma_commit(one, &bar.x_done);
                 wait_phase(&bar.f_ready, heads & 1, gave_up);
                 tmem_fence_after();
-                // F1 K to dQ and F2 K to dK, F1^T Q + F2^T K to dK, all transposed
+                // F1 K to dQ; F2 K, F1^T Q and F2^T K to dK, all transposed.  (F1 and F2 side by side would make one
+                // product of the first two, but of another shape than those that add to half of its columns.)
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
@@ -317,8 +318,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                         for (int k = 0; k < 4; ++k) {
                             const bool add = hr + p + h + k > 0;
                             const uint64_t kl = further(k_left, p * M::kKQ + k * 2048), ql = further(kl, kChunk * 128);
-                            const uint64_t fr = further(f_rows, h * (uint32_t)kSquare + k * 32);
-                            mma_smem(one, tm + kColF, kl, further(f_cols, h * (uint32_t)kSquare + k * 2048), shape(2 * kChunk, false) | kLeftByColumns, add);
+                            const uint64_t fr = further(f_rows, h * (uint32_t)kSquare + k * 32), fc = further(f_cols, h * (uint32_t)kSquare + k * 2048);
+                            mma_smem(one, tm + kColF, kl, fc, shape(kChunk, false) | kLeftByColumns, add);
+                            mma_smem(one, tm + kColF + 64, kl, further(fc, M::kF2 - M::kF1), shape(kChunk, false) | kLeftByColumns, add);
                             mma_smem(one, tm + kColF + 64, ql, fr, shape(kChunk, true) | kLeftByColumns, true);
                             mma_smem(one, tm + kColF + 64, kl, further(fr, M::kF2 - M::kF1), shape(kChunk, true) | kLeftByColumns, true);
                         }

@@ -147,6 +147,9 @@ __device__ __forceinline__ uint32_t elect_lane() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
+// Products run in the order of issue only where one adds to the accumulator of the one before it, at the
+// same columns and of the same shape.  All else that shares columns of tensor memory (another shape, an
+// accumulator where an operand was) waits for a commit in between.
 // d (128 x n) = (add ? d : 0) + a (128 x 16) b (16 x n)
 __device__ __forceinline__ void mma_tmem(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t shape_word, bool add) {
     asm volatile(

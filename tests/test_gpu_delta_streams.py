@@ -1,0 +1,51 @@
+"""The gated delta rule beside other work on the GPU: results do not depend on when its kernels' parts come to run.
+
+Every comparison is bit for bit: the kernels have one order of sums, so any difference is a missing wait."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from prefix_scan_gb300 import api  # noqa: E402
+from test_gpu_delta import BF16, DEV, F16, F32, cu_of, inputs, states  # noqa: E402
+
+
+class Busy:
+    """Small kernels of memory traffic and matrix products on another stream while the block runs."""
+
+    def __enter__(self):
+        self.stream = torch.cuda.Stream()
+        a, b = torch.randn(1024, 1024, device=DEV), torch.randn(1 << 22, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(self.stream):
+            for _ in range(150):
+                a @ a
+                b * 2
+        return self.stream
+
+    def __exit__(self, *_):
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("k,v,lens", [(128, 128, [700, 65, 0, 330]), (64, 64, [700, 65, 0, 330]), (128, 200, [1900]), (40, 24, [1900])])
+def test_results_repeat_beside_other_work(dtype, k, v, lens):
+    x = inputs(sum(lens), 2, 4, k, v, dtype, 3)
+    h0, dht = states(len(lens), 4, k, v, 4), states(len(lens), 4, k, v, 5)
+    do = torch.randn(x[2].shape, device=DEV).to(dtype)
+
+    def run():
+        o, last, saved = api.delta_rule_forward(*x, cu_seqlens=cu_of(lens), initial_state=h0, output_final_state=True)
+        return (o, last, *api.delta_rule_backward(saved, do, d_final_state=dht))
+
+    want = run()
+    torch.cuda.synchronize()
+    with Busy():
+        for _ in range(10):
+            for a, b in zip(run(), want):
+                assert torch.equal(a, b)
