@@ -12,7 +12,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from prefix_scan_gb300 import api  # noqa: E402
-from test_gpu_delta import BF16, DEV, F16, F32, cu_of, inputs, states  # noqa: E402
+from test_gpu_delta import BF16, CHUNKED, DEV, F16, F32, cu_of, inputs, off, states  # noqa: E402
 
 
 class Busy:
@@ -49,3 +49,31 @@ def test_results_repeat_beside_other_work(dtype, k, v, lens):
         for _ in range(10):
             for a, b in zip(run(), want):
                 assert torch.equal(a, b)
+
+
+# 2 to 8 chains of 14 to 72 chunks are cut into segments, and so are 22 of 160 (more segments than run at once)
+CUT = [(BF16, 2, 128, 128, [1900]), (F32, 2, 64, 200, [1900]), (F16, 2, 80, 136, [2000, 900, 0, 1500]), (BF16, 8, 64, 40, [4608]),
+       (BF16, 22, 128, 128, [10240])]
+
+
+@pytest.mark.parametrize("dtype,hv,k,v,lens", CUT)
+def test_state_in_place_of_cut_sequences(dtype, hv, k, v, lens):
+    # the last segment writes the state at the end where the first one has read the state at the start
+    x = inputs(sum(lens), 1, hv, k, v, dtype, 17, decay=0.05)
+    h0, cu = states(len(lens), hv, k, v, 18), cu_of(lens)
+    o, last = api.delta_rule(*x, cu_seqlens=cu, initial_state=h0, output_final_state=True)
+    with Busy():
+        for _ in range(8):
+            h = h0.clone()
+            again = api.delta_rule(*x, cu_seqlens=cu, initial_state=h, final_state=h)[0]
+            assert torch.equal(again, o) and torch.equal(h, last)
+
+
+def test_long_prompt_in_pieces():
+    # pieces long enough to be cut, the state carried in place, against the whole prompt
+    x = inputs(4096, 1, 2, 128, 128, BF16, 19, seqs=1, decay=0.02)
+    _, want = api.delta_rule(*x, output_final_state=True)
+    h = torch.zeros_like(want)
+    for i in range(0, 4096, 2048):
+        api.delta_rule(*(t[:, i:i + 2048] for t in x), initial_state=h, final_state=h)
+    assert off(h, want.double()) <= 2 * CHUNKED
