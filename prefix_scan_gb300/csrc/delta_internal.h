@@ -75,8 +75,9 @@ constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
 // values that start from the identity and add nothing; a join goes through the segments in order
 // (delta_join.cu); a second pass runs every segment from its own start.  The backward pass does the
 // same from the other end, with M's transpose.
-//   seg_state  [segment slots + 1, hv, K, V] f32: the state at each segment's start; backward, its
-//              gradient at each segment's end (one slot further on)
+//   seg_state  [segment slots + 1, hv, K, V] f32: the state at each segment's start (of a sequence's first
+//              segment too, as h0 may be ht); backward, its gradient at each segment's end (one slot further
+//              on; of the last segment too)
 //   seg_m      [segment slots, hv] pairs of images of M (row j, column k: M_kj), as S's
 
 // Packed sequences of very different lengths: the chains of the longest are launched first, so that the

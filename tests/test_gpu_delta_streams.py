@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from prefix_scan_gb300 import api  # noqa: E402
+from prefix_scan_gb300 import _lib, api  # noqa: E402
 from test_gpu_delta import BF16, CHUNKED, DEV, F16, F32, cu_of, inputs, off, states  # noqa: E402
 
 
@@ -77,3 +77,23 @@ def test_long_prompt_in_pieces():
     for i in range(0, 4096, 2048):
         api.delta_rule(*(t[:, i:i + 2048] for t in x), initial_state=h, final_state=h)
     assert off(h, want.double()) <= 2 * CHUNKED
+
+
+@pytest.mark.parametrize("dtype,hv,k,v,lens", CUT)
+def test_state_gradient_in_place_of_cut_sequences(dtype, hv, k, v, lens):
+    # the C ABI lets the gradient of the state at the start take the place of the one at the end
+    x = inputs(sum(lens), 1, hv, k, v, dtype, 27, decay=0.05)
+    h0, dht = states(len(lens), hv, k, v, 28), states(len(lens), hv, k, v, 29)
+    do = torch.randn(x[2].shape, device=DEV).to(dtype)
+    _, _, saved = api.delta_rule_forward(*x, cu_seqlens=cu_of(lens), initial_state=h0)
+    want = api.delta_rule_backward(saved, do, d_final_state=dht)
+    got = [torch.empty_like(t) for t in want[:5]]
+    ts = [_lib.DELTA_TENSOR.pack(t.data_ptr(), 0, t.stride(0), t.stride(1)) for t in (*x[:2], do)]
+    with Busy():
+        for _ in range(8):
+            d = dht.clone()
+            st = _lib.load().ps_delta_backward(saved.shape, *ts, d.data_ptr(), *(t.data_ptr() for t in got), d.data_ptr(),
+                                               saved.workspace.data_ptr(), saved.workspace.numel(), torch.cuda.current_stream().cuda_stream)
+            assert st == _lib.PS_OK
+            for a, b in zip((*got, d), want):
+                assert torch.equal(a, b)
