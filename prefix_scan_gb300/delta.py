@@ -217,13 +217,13 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
     q, k, packed = saved.q, saved.k, saved.cu_seqlens is not None
     if d_o.shape != saved.v_shape or d_o.dtype != q.dtype or d_o.device != q.device:
         raise ValueError(f"{fn}: d_o must match o's shape, type and device")
-    if d_o.numel() and d_o.shape[-1] > 1 and d_o.stride(-1) != 1:
-        d_o = d_o.contiguous()
     if d_final_state is not None:
         _check_state(fn, "d_final_state", d_final_state, saved.states, q.device)
     lib = _lib.load()
     s, ctx = enter(q.device, stream)
     with ctx:
+        if d_o.numel() and d_o.shape[-1] > 1 and d_o.stride(-1) != 1:
+            d_o = d_o.contiguous()   # on the call's stream
         new = torch.zeros if packed and saved.cu_seqlens.numel() == 1 else torch.empty   # with no sequence nothing is enqueued
         heads = saved.v_shape[:-1]
         dq, dk = (new(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))

@@ -97,3 +97,26 @@ def test_state_gradient_in_place_of_cut_sequences(dtype, hv, k, v, lens):
             assert st == _lib.PS_OK
             for a, b in zip((*got, d), want):
                 assert torch.equal(a, b)
+
+
+def test_backward_on_another_stream():
+    # a gradient that has to be made contiguous first: the copy, too, belongs to the given stream.  Its old memory holds NaN,
+    # and the current stream is held up, so that a copy made there would come late.
+    x = inputs(600, 1, 2, 64, 64, BF16, 37, seqs=2)
+    o, _, saved = api.delta_rule_forward(*x)
+    grads = [torch.ones((), device=DEV, dtype=BF16).expand(o.shape),
+             torch.randn(2, 600, 64, 2, device=DEV).to(BF16).transpose(2, 3)]
+    s, big = torch.cuda.Stream(), torch.randn(4096, 4096, device=DEV)
+    for do in grads:
+        want = api.delta_rule_backward(saved, do.contiguous())
+        torch.cuda.synchronize()
+        held = [torch.full(o.shape, float("nan"), device=DEV, dtype=BF16) for _ in range(4)]
+        del held
+        for _ in range(20):
+            big @ big
+        got = api.delta_rule_backward(saved, do, stream=s)
+        for _ in range(4):   # what the current stream is given next
+            torch.full(o.shape, float("nan"), device=DEV, dtype=BF16)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert a is b is None or torch.equal(a, b)
