@@ -135,6 +135,7 @@ class DeltaRuleSaved:
     states: tuple
     has_initial_state: bool
     workspace: torch.Tensor
+    stream: int   # handle of the stream that the forward call ran on
 
 
 def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state, workspace,
@@ -162,7 +163,7 @@ def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_fina
                                   final_state.data_ptr() if final_state is not None else None, out.data_ptr(), train,
                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
     _lib.check("ps_delta_forward", st)
-    return out, final_state, plan, shape, states, workspace
+    return out, final_state, plan, shape, states, workspace, s
 
 
 def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, *,
@@ -197,11 +198,11 @@ def delta_rule_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
     ``saved`` goes to :func:`delta_rule_backward`; it holds q and k (which must not change until then) and a workspace of
     ``delta_rule_workspace_size(q, v, cu_seqlens, train=True)`` bytes.
     """
-    out, final_state, plan, shape, states, workspace = _forward(
+    out, final_state, plan, shape, states, workspace, s = _forward(
         "delta_rule_forward", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state, workspace,
         stream, 1)
     return out, final_state, DeltaRuleSaved(q, k, v.shape, beta.dtype, cu_seqlens, plan, shape, states, initial_state is not None,
-                                            workspace)
+                                            workspace, s)
 
 
 def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_state: torch.Tensor | None = None, stream=None
@@ -237,6 +238,11 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
         st = lib.ps_delta_backward(saved.shape, *ts, ptr(d_final_state), ptr(dq),
                                    ptr(dk), ptr(dv), ptr(dg), ptr(dbeta), ptr(dh0), saved.workspace.data_ptr(),
                                    saved.workspace.numel() * saved.workspace.element_size(), s)
+        if s != saved.stream:   # `saved` may be dropped while this stream still reads what it holds
+            used = torch.cuda.current_stream(q.device)
+            for t in (saved.workspace, q, k, saved.cu_seqlens, d_o, d_final_state):
+                if t is not None:
+                    t.record_stream(used)
     _lib.check("ps_delta_backward", st)
     return dq, dk, dv, dg, dbeta, dh0
 

@@ -120,3 +120,35 @@ def test_backward_on_another_stream():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert a is b is None or torch.equal(a, b)
+
+
+def test_saved_memory_outlives_a_backward_call_on_another_stream():
+    # `saved`, its workspace and the inputs are dropped right after the call; the forward call's stream gets their memory next
+    def inputs_and_saved():
+        x = inputs(900, 2, 4, 64, 64, BF16, 47, seqs=2)
+        return x, api.delta_rule_forward(*x)[2]
+
+    do = torch.randn(2, 900, 4, 64, device=DEV).to(BF16)
+    x, saved = inputs_and_saved()
+    want = api.delta_rule_backward(saved, do)
+    del x, saved
+    big, s = torch.randn(4096, 4096, device=DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (True, False):
+        x, saved = inputs_and_saved()
+        sizes = [t.numel() * t.element_size() for t in (saved.workspace, *x[:2])]
+        gradient = do.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                big @ big
+            if not given:
+                got = api.delta_rule_backward(saved, gradient)
+        if given:
+            got = api.delta_rule_backward(saved, gradient, stream=s)
+        del x, saved, gradient
+        new = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in (*sizes, do.numel() * 2)]
+        torch.cuda.synchronize()
+        del new
+        for a, b in zip(got, want):
+            assert a is b is None or torch.equal(a, b)
