@@ -24,8 +24,11 @@
  * outputs of their own sequence, and of the heads that share the input, and
  * no others (within a chunk of 64 tokens also those before them).
  *
- * A kernel whose bounded waits ran out, which a correct
- * launch never does, finishes with NaN in its outputs instead of hanging.
+ * A kernel whose bounded waits ran out, which a correct launch never does,
+ * finishes instead of hanging, with NaN in the outputs that it is to blame for:
+ * a chain's o and state at the end, a step's o (the states in its pages are
+ * undefined then).  In training all gradients are NaN from then on, until the
+ * next forward call on that workspace.
  *
  * Conventions: device pointers owned by the caller; work is enqueued on
  * `stream` and the call returns without waiting for it; no device memory is

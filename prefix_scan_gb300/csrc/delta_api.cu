@@ -82,11 +82,12 @@ size_t chunks_bytes(const ps_delta_shape *d, int train) {
     const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
     return (size_t)slots * d->heads_v * ps::chunk_layout(d->dim_k, d->dim_v, train != 0).stride;
 }
-// The workspace's parts after the chunks': keys and queries, what segments need, the sequences' order.
+// The workspace's parts after the chunks': keys and queries, what segments need, the sequences' order, and in
+// training the word of a chain that gave up, 256 bytes before the end.
 struct Parts {
     int seg;
     long long seg_slots;
-    size_t kq, seg_m, seg_state, order, total;
+    size_t kq, seg_m, seg_state, order, failed, total;
     bool ordered;
 };
 Parts parts_of(const ps_delta_shape *d, int train) {
@@ -102,8 +103,9 @@ Parts parts_of(const ps_delta_shape *d, int train) {
     p.order = p.seg_state + (p.seg ? (size_t)(p.seg_slots + 1) * d->heads_v * d->dim_k * d->dim_v * 4 : 0);
     p.ordered = packed && !p.seg && d->num_seqs > 1 && d->num_seqs <= ps::kOrdered &&
                 d->num_seqs * d->heads_v * ps::blocks_v(d->dim_v) > 152;   // as many run at once
-    p.total = p.order + (p.ordered ? (size_t)d->num_seqs * 4 : 0);
-    p.total = (p.total + 255) / 256 * 256;
+    p.failed = p.order + (p.ordered ? (size_t)d->num_seqs * 4 : 0);
+    p.failed = (p.failed + 255) / 256 * 256;
+    p.total = p.failed + (train && slots > 0 ? 256 : 0);
     return p;
 }
 void place(ps::DeltaArgs &a, const Parts &p, void *ws) {
@@ -114,6 +116,7 @@ void place(ps::DeltaArgs &a, const Parts &p, void *ws) {
     a.seg_m = a.ws + p.seg_m;
     a.seg_state = reinterpret_cast<float *>(a.ws + p.seg_state);
     a.order = p.ordered ? reinterpret_cast<int32_t *>(a.ws + p.order) : nullptr;
+    a.failed = p.total > p.failed ? reinterpret_cast<int *>(a.ws + p.failed) : nullptr;
 }
 // The chain, or where sequences are cut the states of the segments, their join and the chain.
 template <typename Chain>

@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
     }
     tmem_fence_before();
     __syncthreads();
+    if (*gave_up && a.failed && threadIdx.x == 0) *a.failed = 1;
     if (*gave_up && !states && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the outputs are not what they should be: say so
         for (long long t = 0; t < sp.len; ++t)
             static_cast<T *>(a.o)[((size_t)(sp.first + t) * a.s.hv + head) * a.s.v + v0 + threadIdx.x] =

@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     auto rows_of = [&](int i) { return (int)min((long long)kChunk, sp.len - first_token(i)); };
 
     if (threadIdx.x == 0) {
+        const int failed = a.failed ? *a.failed : 0;   // what the forward chains kept is not to be used
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.empty[i], 1 + (!states && (M::kInStage || M::kStages == 2)));
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         mbar_init(&bar.s_free, 1);
         mbar_init(&bar.u_free, 1);
         mbar_init(&bar.drained, 1);
-        bar.gave_up = base & 1023 ? 1 : 0;   // images need their alignment
+        bar.gave_up = failed || base & 1023 ? 1 : 0;   // images need their alignment
         mbar_init_done();
     }
     if (warp == 0) tmem_alloc(smem_addr(&bar.tmem));
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     }
     tmem_fence_before();
     __syncthreads();
+    if (*gave_up && a.failed && threadIdx.x == 0) *a.failed = 1;
     if (*gave_up && !states && v0 + (int)threadIdx.x < a.s.v && threadIdx.x < kBlockV)   // the gradients are not what they should be: say so
         for (long long t = 0; t < sp.len; ++t)
             static_cast<T *>(a.dv)[((size_t)(sp.first + t) * a.s.hv + head) * a.s.v + v0 + threadIdx.x] =

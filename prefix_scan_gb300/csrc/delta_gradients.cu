@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
     const bool quads = a.s.k % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.dq) | reinterpret_cast<uintptr_t>(a.dk)) & 7) == 0;
 
     if (tid == 0) {
+        const int failed = *a.failed;   // what the chains kept is not to be used
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.item_full[i], 1);
             mbar_init(&bar.item_empty[i], kGradWarps + 1);
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
         mbar_init(&bar.f_ready, kGradWarps);
         mbar_init(&bar.f_done, 1);
         mbar_init(&bar.drained, 1);
-        bar.gave_up = base & 1023 ? 1 : 0;   // images need their alignment
+        bar.gave_up = failed || base & 1023 ? 1 : 0;   // images need their alignment
         mbar_init_done();
     }
     if (warp == 0) tmem_alloc(smem_addr(&bar.tmem));
@@ -558,11 +559,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                 warp_arrive(&bar.kq_empty, lane);
                 const size_t ostride = (size_t)a.s.hk * a.s.k, first = ((size_t)(was.token + tok) * a.s.hk + was.head_k) * a.s.k + col;
                 T *oq = static_cast<T *>(a.dq) + first, *ok = static_cast<T *>(a.dk) + first;
-                const float bad = *gave_up ? __int_as_float(0x7fffffff) : 0.f;   // not what they should be: say so
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    dq[i] += x[i] + bad;
-                    dk[i] += y[i] + bad;
+                    dq[i] += x[i];
+                    dk[i] += y[i];
                 }
                 if constexpr (sizeof(T) == 2)
                     if (quads) {   // four lanes exchange, so that each has four columns of every fourth token
@@ -611,9 +611,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
             else clear(static_cast<T *>(a.dbeta), a.s.hv);
         }
     }
-    if (*gave_up) {   // items that were not reached
-        const long long tokens = a.s.cu ? a.s.tokens : a.s.seqs * a.s.tokens;
-        for (long long i = tid; i < tokens * a.s.hv; i += kGradThreads) a.dg[i] = __int_as_float(0x7fffffff);
+    if (*gave_up) {   // this CTA's items are not what they should be: say so
+        const float bad = __int_as_float(0x7fffffff);
+        for (long long i = blockIdx.x; i < a.slots * a.s.hk; i += gridDim.x) {
+            const long long slot = i / a.s.hk, seq = seq_of_slot(a.s, slot);
+            if (seq < 0) continue;
+            const Span sp = span_of(a.s, seq);
+            const long long t0 = (slot - sp.slot) * kChunk;
+            const int rows = (int)min((long long)kChunk, sp.len - t0), head_k = (int)(i % a.s.hk);
+            for (int x = tid; x < rows * a.s.k; x += kGradThreads) {
+                const size_t at = ((size_t)(sp.first + t0 + x / a.s.k) * a.s.hk + head_k) * a.s.k + x % a.s.k;
+                static_cast<T *>(a.dq)[at] = static_cast<T *>(a.dk)[at] = from_f32<T>(bad);
+            }
+            for (int x = tid; x < rows * rep; x += kGradThreads) {
+                const size_t at = (size_t)(sp.first + t0 + x / rep) * a.s.hv + head_k * rep + x % rep;
+                a.dg[at] = bad;
+                if (a.beta_f32) static_cast<float *>(a.dbeta)[at] = bad;
+                else static_cast<T *>(a.dbeta)[at] = from_f32<T>(bad);
+            }
+        }
     }
     if (warp == 0) tmem_free(bar.tmem);
 }

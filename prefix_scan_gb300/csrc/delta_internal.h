@@ -102,6 +102,8 @@ struct DeltaArgs {
     long long seg_slots;
     float *seg_state;
     int32_t *order;               // [seqs] by falling length, or null: as they come
+    int *failed;                  // training: cleared by the prepare kernel, set by a chain whose waits ran out
+                                  // (what it kept then is not to be used: all gradients become NaN); else null
     unsigned char *seg_m;
     // backward
     DeltaTensor dout;

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kPrepThreads, Planes<T>::NP == 1 ? 4 : KP == 6
     const long long slot = blockIdx.x;
     const int head_k = blockIdx.y, rep = a.s.hv / a.s.hk;
 
+    if (a.failed && slot == 0 && head_k == 0 && tid == 0) *a.failed = 0;
     if (a.order && slot == 0 && head_k == 0) {
         int *len = reinterpret_cast<int *>(smem);
         for (int i = tid; i < a.s.seqs; i += kPrepThreads) len[i] = (int)span_of(a.s, i).len;

@@ -187,6 +187,7 @@ __device__ __forceinline__ void mbar_arrive_after_copies(uint64_t *bar) {
 // barrier; wait_busy() polls instead, which wakes sooner, for the few warps that hold up all others.
 constexpr uint32_t kWaitNs = 10000;
 static __device__ __noinline__ void wait_long(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+    if (*gave_up) return;
     const unsigned long long t0 = global_ns();
     for (uint32_t i = 0; i < kMbarSpinCap; ++i) {
         if (mbar_try_wait_for(bar, parity, kWaitNs)) return;
