@@ -98,6 +98,13 @@ def _inputs(plan: _Plan, q, k, v, g, beta) -> bytes:
     return _lib.DELTA_INPUTS.pack(q.data_ptr(), *sq, k.data_ptr(), *sk, v.data_ptr(), *sv, g.data_ptr(), *sg, beta.data_ptr(), *sb)
 
 
+def _check_no_graph(fn, tensors):
+    """Outputs have no autograd graph: where torch would record one, gradients would be lost without a word."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{fn}: an input requires gradients, which do not pass through this call; use delta_rule_forward and "
+                         "delta_rule_backward, or call it under torch.no_grad()")
+
+
 def _check_state(fn, name, t, shape, device):
     if t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
@@ -180,9 +187,10 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     [sequences, value heads, K, V] float32 (0 if not given); the states at the end are written to
     ``final_state`` (which may be ``initial_state``), or returned in a new tensor with ``output_final_state``.
     ``scale`` is K ** -0.5 if not given.  Asynchronous on ``stream`` (default: the current stream).  With
-    ``cu_seqlens``, outputs of tokens that no sequence holds are not written.  For gradients see
-    :func:`delta_rule_forward`.
+    ``cu_seqlens``, outputs of tokens that no sequence holds are not written.  No gradients pass through
+    (inputs that require them are refused where torch records them): see :func:`delta_rule_forward`.
     """
+    _check_no_graph("delta_rule", (q, k, v, g, beta, initial_state))
     return _forward("delta_rule", q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state, out, final_state,
                     workspace, stream, 0)[:2]
 
@@ -195,7 +203,8 @@ def delta_rule_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
                        ) -> tuple[torch.Tensor, torch.Tensor | None, DeltaRuleSaved]:
     """:func:`delta_rule` for training: ``(o, final_state, saved)``.
 
-    ``saved`` goes to :func:`delta_rule_backward`; it holds q and k (which must not change until then) and a workspace of
+    The outputs have no autograd graph: ``saved`` goes to :func:`delta_rule_backward`, whose results a
+    ``torch.autograd.Function`` can hand on.  It holds q and k (which must not change until then) and a workspace of
     ``delta_rule_workspace_size(q, v, cu_seqlens, train=True)`` bytes.
     """
     out, final_state, plan, shape, states, workspace, s = _forward(
@@ -255,9 +264,11 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     ``q`` .. ``beta`` as for :func:`delta_rule` without ``cu_seqlens``.  ``state``: a pool of pages, [pages, value
     heads, K, V] float32.  ``slots`` (int32, one per sequence, all different): the page of each sequence's state, -1
     for one that takes no part; page i for sequence i if not given.  ``lengths`` (int32, one per sequence): how many
-    of the tokens count.  Outputs of tokens that do not count are 0.
+    of the tokens count.  Outputs of tokens that do not count are 0.  Inputs that require gradients are refused where
+    torch records them: there is no backward pass of single steps.
     """
     fn = "delta_rule_step"
+    _check_no_graph(fn, (q, k, v, g, beta, state))
     plan = _plan(fn, q, k, v, g, beta, None)
     device = q.device
     if state.dim() != 4 or state.shape[1:] != plan.states:
