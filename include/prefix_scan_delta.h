@@ -72,7 +72,11 @@ typedef enum ps_delta_input { PS_DELTA_Q = 0, PS_DELTA_K = 1, PS_DELTA_V = 2, PS
  * tokens     tokens of every sequence; with cu_seqlens, of all together
  * cu_seqlens NULL, or a device array of num_seqs + 1 offsets: sequence i has
  *            tokens [cu[i], cu[i+1]).  Offsets are read on the device and
- *            clamped into [0, tokens] and to increasing order.
+ *            clamped into [0, tokens]; an end before its start is an empty
+ *            sequence.  They must not fall: sequences that share tokens then
+ *            write the same outputs and the same workspace, so results are
+ *            unspecified, and may differ from call to call, for all
+ *            sequences; no access leaves the tensors.
  * heads_k, heads_v, dim_k, dim_v  heads_v is a multiple of heads_k; dim_k at
  *            most 128, dim_v at most 1024
  */
@@ -118,7 +122,8 @@ ps_status ps_delta_forward(const ps_delta_shape *shape, const ps_delta_tensor in
  *         heads that share a key head, in a fixed order
  *   dh0   gradient of h0, or NULL
  * Gradients of tokens that no sequence holds are 0.
- * Results are bitwise reproducible from call to call (no atomics).
+ * Results are bitwise reproducible from call to call (no atomics) where offsets
+ * do not fall.
  */
 ps_status ps_delta_backward(const ps_delta_shape *shape, const ps_delta_tensor *q, const ps_delta_tensor *k,
                             const ps_delta_tensor *d_o, const float *d_ht, void *dq, void *dk, void *dv,

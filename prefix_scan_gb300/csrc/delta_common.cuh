@@ -217,9 +217,10 @@ __device__ __forceinline__ void load_image(uint32_t dst, const void *src, int ti
 }
 // ---- sequences and chunks ----------------------------------------------------------
 
-// Where a sequence's tokens lie.  Offsets that do not increase, or that leave
-// [0, tokens], are clamped, so that wrong ones give wrong results and no access
-// out of range.
+// Where a sequence's tokens lie.  Offsets that leave [0, tokens] are clamped, each
+// sequence by itself, so that wrong ones give wrong results and no access out of
+// range.  Where they fall, sequences may share tokens and slots: a running maximum
+// would keep them apart, at the price of another launch for every call.
 struct Span {
     long long first;   // token of the whole input (outputs are stored by it)
     long long at;      // token offset to add to a tensor's base (0 where seq_stride is used)

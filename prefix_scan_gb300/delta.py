@@ -182,8 +182,8 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
 
     ``q``, ``k``: [sequences, tokens, key heads, K]; ``v``: [sequences, tokens, value heads, V]; ``g`` (log decays,
     float32) and ``beta`` (gates, float32 or q's type): [sequences, tokens, value heads].  With ``cu_seqlens``
-    (int32, on the device, one offset more than sequences) the first two dimensions are one that packs all
-    sequences' tokens.  Any strides go, as long as the last dimension is contiguous.  ``initial_state``:
+    (int32, on the device, one offset more than sequences, never falling) the first two dimensions are one that packs
+    all sequences' tokens.  Any strides go, as long as the last dimension is contiguous.  ``initial_state``:
     [sequences, value heads, K, V] float32 (0 if not given); the states at the end are written to
     ``final_state`` (which may be ``initial_state``), or returned in a new tensor with ``output_final_state``.
     ``scale`` is K ** -0.5 if not given.  Asynchronous on ``stream`` (default: the current stream).  With
