@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kStepThreads, 3) delta_step_kernel(const Delta
     T *out = static_cast<T *>(a.o) + ((size_t)seq * a.t * a.hv + head) * a.v;
     const size_t ostride = (size_t)a.hv * a.v;
     if (count < a.t)   // outputs of tokens that do not count
-        for (int i = tid; i < (a.t - count) * VT; i += kStepThreads)
+        for (long long i = tid; i < (long long)(a.t - count) * VT; i += kStepThreads)
             if (vb * VT + i % VT < a.v) out[(count + i / VT) * ostride + vb * VT + i % VT] = from_f32<T>(0.f);
     if (count == 0) return;
 
@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kStepThreads, 3) delta_step_kernel(const Delta
     }
 
     const Span none{};
-    for (int t0 = 0; t0 < count; t0 += kStepTokens) {
-        const int nt = min(kStepTokens, count - t0);
+    for (unsigned t0 = 0; t0 < (unsigned)count; t0 += kStepTokens) {
+        const int nt = min(kStepTokens, count - (int)t0);
         if (t0) __syncthreads();
         for (int i = tid; i < nt * KP; i += kStepThreads) {
             const int t = i / KP, k = i % KP;
