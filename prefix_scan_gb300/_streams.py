@@ -15,6 +15,8 @@ def enter(device: torch.device, stream):
     if stream is None and device.index == torch.cuda.current_device():
         return (_raw_stream(device.index) if _raw_stream else torch.cuda.current_stream().cuda_stream), _HERE
     s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"the stream belongs to {s.device} and the tensors to {device}")
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     ctx.enter_context(torch.cuda.stream(s))
