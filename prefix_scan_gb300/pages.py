@@ -60,7 +60,8 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> N
     _check_ints(fn, src.device, src=(src, 1), dst=(dst, 1))
     if src.numel() != dst.numel():
         raise ValueError(f"{fn}: src and dst differ in length")
-    pages = (pools if isinstance(pools, torch.Tensor) else pools[0]).shape[0]
+    pools = [pools] if isinstance(pools, torch.Tensor) else pools
+    pages = pools[0].shape[0] if len(pools) else 0
     arr, n = _pools(fn, pools, pages, src.device)
     s, ctx = enter(src.device, stream)
     with ctx:
