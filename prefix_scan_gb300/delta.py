@@ -122,6 +122,8 @@ def delta_rule_workspace_size(q: torch.Tensor, v: torch.Tensor, cu_seqlens: torc
                               train: bool = False) -> int:
     """Bytes of workspace :func:`delta_rule` needs for such inputs (``train``: the buffer that
     :func:`delta_rule_forward` leaves for the backward pass)."""
+    if q.dtype not in REAL_CODES:
+        raise TypeError(f"delta_rule_workspace_size supports float32, bfloat16 and float16, not {q.dtype}")
     packed = cu_seqlens is not None
     shape = _lib.DELTA_SHAPE.pack(cu_seqlens.numel() - 1 if packed else q.shape[0], q.shape[0] if packed else q.shape[1],
                                   cu_seqlens.data_ptr() if packed else 0, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1],
