@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kPrepThreads, Planes<T>::NP == 1 ? 4 : KP == 6
                 const double G = e ? sum : sum - (double)g[1];
                 const int r = e ? cnt : cnt - (int)f[1];
                 const float hi = (float)G;
-                sc[i] = r == 0 ? expf((float)G) : 0.f;
+                sc[i] = r == 0 ? exp_rounded((float)G) : 0.f;   // the 63rd multiplies the state
                 sc[64 + i] = i < rows && r == rlast ? expf((float)(last - G)) : 0.f;
                 sc[128 + i] = b[e];
                 sc[192 + i] = hi;

@@ -29,10 +29,8 @@ __device__ __forceinline__ float4 shfl_add(float4 x, int d) {
     x.w += __shfl_xor_sync(0xffffffffu, x.w, d);
     return x;
 }
-// exp(g), 0 where it leaves f32's normal range.  Errors of decays near 1 multiply up over the many tokens that such a state
-// remembers, so there 1 + expm1(g), rounded once, takes the place of expf, whose errors of an ulp have one sign: 300 tokens
-// of g = -0.00005 .. -0.05 leave outputs off by 1.3e-6 with it.
-__device__ __forceinline__ float decay_of(float g) { return g > -0.5f ? 1.f + expm1f(g) : g <= -87.f ? 0.f : expf(g); }
+// exp(g), 0 where it leaves f32's normal range.
+__device__ __forceinline__ float decay_of(float g) { return g <= -87.f ? 0.f : exp_rounded(g); }
 __device__ __forceinline__ void fma4(float4 &d, float a, const float4 &b) {
     d.x += a * b.x; d.y += a * b.y; d.z += a * b.z; d.w += a * b.w;
 }
