@@ -13,9 +13,13 @@
  * Types: q, k, v and o are of one type (f32, bf16 or f16); beta of that type
  * or f32; g, states and gradients of states and of g are f32.  States and all
  * sums are held in 32 bits; over whole sequences matrix products take operands
- * of 16 significant bits or more (pairs of bf16), so results carry errors of
- * about 2^-18 relative to the terms that make them up, before their own
- * rounding.  Single steps are f32 throughout.
+ * of 16 significant bits (pairs of bf16), f32 q, k and d_o among them, so results
+ * carry errors of about 2^-18 relative to the terms that make them up, before
+ * their own rounding: chosen for the matrix units' speed, see
+ * csrc/delta_common.cuh.  Single steps are f32 throughout.  ps_delta_step takes
+ * any number of tokens, so a caller who needs f32's 24 bits of a prompt runs it
+ * there, token after token (1111 tokens in three sequences, 3 heads of 80 x 56:
+ * off by 1.3e-7 in 492 us, against 5.0e-6 in 88); training has the pairs alone.
  *
  * Extreme inputs: a log decay at or below -87 (-infinity too), where exp(g)
  * leaves the normal range of f32, forgets the state entirely and has gradient

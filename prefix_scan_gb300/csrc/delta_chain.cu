@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                 wait_phase(&bar.s_done, c & 1, gave_up);   // which has read the pair that was in this place
                 tmem_fence_after();
 #pragma unroll
-                for (int t = 0; t < (NP == 1 ? 3 : 4); ++t)   // hi hi, lo hi, hi lo, and lo lo where outputs may be f32
+                for (int t = 0; t < (NP == 1 ? 3 : 4); ++t)   // hi hi, lo hi, hi lo, and lo lo for f16 and f32 (delta_common.cuh says why)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_tmem(one, tm + kColO, tm + kColR + (t & 1 ? 32 : 0) + k * 8,
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                 tmem_ld16(x[0], at + kColS + 16 * k16, x[1], at + kColS + 16 * k16 + 16);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    split16(x[b], hi, lo);
+                    split16(x[b], hi, lo);   // what X reads; the state itself goes on in f32
                     tmem_st8(at + kColSHi + 8 * (k16 + b), hi);
                     tmem_st8(at + kColSLo + 8 * (k16 + b), lo);
                     scale16(x[b], eall);
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
             if (c > 0 && !states) wait_phase(&bar.o_done, (c - 1) & 1, gave_up);   // the last chunk's U was there
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                split16(x[b], hi, lo);
+                split16(x[b], hi, lo);   // for (T - 1) beta R alone: U adds beta R in f32
                 tmem_st8(at + kColR + 16 * half + 8 * b, hi);
                 tmem_st8(at + kColR + 32 + 16 * half + 8 * b, lo);
             }
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
                     z[i + 1] = x[b][i + 1] = u.y;
                 }
                 scale16(z, scal + 64 + 16 * b);
-                split16(z, hi, lo);
+                split16(z, hi, lo);   // where a state's error comes from: 2^-18.4 of each term that a token adds
                 tmem_st8(at + kColW + 16 * half + 8 * b, hi);
                 tmem_st8(at + kColW + 32 + 16 * half + 8 * b, lo);
             }
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[0][i] = __int_as_float(0x7fffffff);
                 if (matrix) {
-                    split16(x[0], hi, lo);
+                    split16(x[0], hi, lo);   // as the join's products read it
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const uint32_t to = img(0, row, k0 / 8 + p);

@@ -19,8 +19,25 @@
 // matrix units they are pairs hi + lo of bf16 (16 significant bits, off by 2^-18.4
 // of the number in the root mean square), so that states and the gradients of g
 // come out to about 2^-18 and not to bf16's 2^-9.  bf16 inputs are exact with one
-// number (NP = 1); f16 and f32 inputs are pairs too (NP = 2).  Where outputs are
-// rounded to 16 bits anyway, U^T P^T leaves out the product of the two lower parts.
+// number (NP = 1), f16 inputs with a pair (NP = 2); f32 inputs become pairs, and lose
+// eight bits, where they meet a matrix unit: q, k and dO (v meets none).
+// Why two parts: a third one would keep 24 bits, at half as many products again (three
+// for two beside an exact input, six for four of two pairs) and half as many bytes of
+// every image; and the chains would not fit, as the state of 128 columns, its operand in
+// three parts (192), X and S^T Q^T (128) and the two other operands (96 each) take more
+// than tensor memory's 512.  16-bit outputs are the rounding of what they would be anyway;
+// f32 ones (states, gradients of states and of g, everything of f32 inputs) are off by
+// 1.3e-6 to 5e-6 where f32 sums are by 1e-7 to 4e-7.  The single-step kernel is f32
+// throughout, for whole prompts too.  Where a number goes into pairs:
+//     q, k, dO of f32                 load_tile() here; dO of the chains in delta_chain_backward.cu
+//     P, N, T's blocks, T - 1         delta_prepare.cu
+//     S, beta R, exp(G_C - G) U, U    delta_chain.cu; a segment's M too
+//     dS', Y, exp(G) dR, dU, scaled dO    delta_chain_backward.cu
+//     a segment's state               delta_join.cu
+//     S, U, dS', dU as they were left, F1, F2    delta_gradients.cu
+// For bf16 inputs U^T P^T and X2, X3 of the gradients leave out the product of the two
+// lower parts, 2^-19.6 of its terms: nothing in results that are rounded at 2^-9, and in
+// the gradients of g, which are f32 always, a twentieth on top of the pairs' own errors.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -196,7 +213,7 @@ __device__ __forceinline__ void load_tile(uint32_t hi, uint32_t plane, const T *
                 for (int j = 0; j < 8; ++j)
                     x[j] = r < rows && p * 8 + j < cols ? to_f32<T>(src[r * stride + p * 8 + j]) : 0.f;
             }
-            uint32_t h[4], l[4];
+            uint32_t h[4], l[4];   // exact for f16; f32 keeps 16 bits (see above)
 #pragma unroll
             for (int j = 0; j < 4; ++j) split2(x[2 * j], x[2 * j + 1], h[j], l[j]);
             st_shared16(dst, make_uint4(h[0], h[1], h[2], h[3]));

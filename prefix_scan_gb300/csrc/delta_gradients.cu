@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                             mma_smem(one, tm + kColX, further(s0, (p & 1) * M::kSP), further(o, (p >> 1) * M::kOP + k * 32),
                                      shape(kChunk, true) | kLeftByColumns, add || p);
 #pragma unroll
-                        for (int t = 0; t < 2 + NP; ++t) {   // hi hi, lo hi, hi lo, and lo lo where gradients may be f32
+                        for (int t = 0; t < 2 + NP; ++t) {   // hi hi, lo hi, hi lo, and lo lo for f16 and f32 (delta_common.cuh says why)
                             const uint32_t l = t & 1 ? M::kSP : 0, r = t & 2 ? kSlice : 0;
                             mma_smem(one, tm + kColX + 64, further(s0, l), further(du, r + k * 2048), shape(kChunk, false) | kLeftByColumns, add || t);
                             mma_smem(one, tm + kColX + 128, further(d0, l), further(u_right, r + k * 2048), shape(kChunk, false) | kLeftByColumns, add || t);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_gradients_kernel(const 
                         one(e + 3, be.w, gh.w, gl.w, rr.w);
                     }
                     const uint32_t ji = img(base + M::kF1, j, i0 >> 3);   // eight tokens i of row j
-                    uint4 h, l;
+                    uint4 h, l;   // 16 bits, as of all that these products read
                     split2(f1[0], f1[1], h.x, l.x); split2(f1[2], f1[3], h.y, l.y); split2(f1[4], f1[5], h.z, l.z); split2(f1[6], f1[7], h.w, l.w);
                     st_shared16(ji, h);
                     st_shared16(ji + (uint32_t)kSquare, l);

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const DeltaArg
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float2 x = *reinterpret_cast<const float2 *>(S + (r8 + 8 * (q & 1)) * kRow + 16 * kt + 8 * (q >> 1) + c2);
-                split2(x.x, x.y, f[0][q], f[1][q]);
+                split2(x.x, x.y, f[0][q], f[1][q]);   // for the product alone: what is added to and kept is f32
             }
 #pragma unroll
             for (int np = 0; np < NQ / 2; ++np)

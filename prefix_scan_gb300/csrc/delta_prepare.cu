@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kPrepThreads, Planes<T>::NP == 1 ? 4 : KP == 6
                         pv[t][e] = a.s.scale * D * qk[n][t][e];
                     }
                 }
-                split_tiles(nv[0], nv[1], f);
+                split_tiles(nv[0], nv[1], f);   // 16 bits: T's blocks and P are read as pairs by the chains anyway
                 stsm4(at + M::kN, f[0][0], f[0][1], f[0][2], f[0][3]);
                 stsm4(at + M::kN + (uint32_t)kSquare, f[1][0], f[1][1], f[1][2], f[1][3]);
             } else {
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kPrepThreads, Planes<T>::NP == 1 ? 4 : KP == 6
                 x[i] = (s[0] + s[1]) + (s[2] + s[3]);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 16; ++i) {   // solved in f32, 16 bits of it for the products below and for the chains
                 const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
                 const __nv_bfloat16 l = __float2bfloat16_rn(x[i] - __bfloat162float(h));
                 const int at = (int)img(0, (tid & ~15) + i, tid >> 3) + (tid & 7) * 2;

@@ -188,7 +188,9 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     all sequences' tokens.  Any strides go, as long as the last dimension is contiguous.  ``initial_state``:
     [sequences, value heads, K, V] float32 (0 if not given); the states at the end are written to
     ``final_state`` (which may be ``initial_state``), or returned in a new tensor with ``output_final_state``.
-    ``scale`` is K ** -0.5 if not given.  Asynchronous on ``stream`` (default: the current stream).  With
+    ``scale`` is K ** -0.5 if not given.  Matrix products take operands of 16 significant bits, float32 q and k too, so
+    float32 results are off by some 1e-6 to 5e-6; :func:`delta_rule_step`, which is float32 throughout, takes whole
+    prompts as well, token after token.  Asynchronous on ``stream`` (default: the current stream).  With
     ``cu_seqlens``, outputs of tokens that no sequence holds are not written.  No gradients pass through
     (inputs that require them are refused where torch records them): see :func:`delta_rule_forward`.
     """
