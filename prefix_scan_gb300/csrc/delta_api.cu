@@ -78,6 +78,7 @@ bool outputs_meet(const Range (&out)[NO], const Range (&in)[NI]) {
     return false;
 }
 
+size_t state_bytes(const ps_delta_shape *d) { return (size_t)d->heads_v * d->dim_k * d->dim_v * 4; }   // of a sequence
 size_t chunks_bytes(const ps_delta_shape *d, int train) {
     const long long slots = ps::delta_slots(d->num_seqs, d->tokens, d->cu_seqlens != nullptr);
     return (size_t)slots * d->heads_v * ps::chunk_layout(d->dim_k, d->dim_v, train != 0).stride;
@@ -87,7 +88,7 @@ size_t chunks_bytes(const ps_delta_shape *d, int train) {
 struct Parts {
     int seg;
     long long seg_slots;
-    size_t kq, seg_m, seg_state, order, failed, total;
+    size_t kq, seg_m, seg_state, seg_h, order, failed, total;
     bool ordered;
 };
 Parts parts_of(const ps_delta_shape *d, int train) {
@@ -100,7 +101,8 @@ Parts parts_of(const ps_delta_shape *d, int train) {
     p.seg = ps::segment_chunks(d->num_seqs * d->heads_v * ps::blocks_v(d->dim_v), chunks, train != 0);
     p.seg_slots = ps::segment_slots(slots, d->num_seqs, p.seg);
     p.seg_state = p.seg_m + (size_t)p.seg_slots * d->heads_v * ps::seg_m_bytes(d->dim_k);
-    p.order = p.seg_state + (p.seg ? (size_t)(p.seg_slots + 1) * d->heads_v * d->dim_k * d->dim_v * 4 : 0);
+    p.seg_h = p.seg_state + (p.seg ? (size_t)(p.seg_slots + 1) * state_bytes(d) : 0);
+    p.order = p.seg_h + (p.seg ? (size_t)d->num_seqs * state_bytes(d) : 0);
     p.ordered = packed && !p.seg && d->num_seqs > 1 && d->num_seqs <= ps::kOrdered &&
                 d->num_seqs * d->heads_v * ps::blocks_v(d->dim_v) > 152;   // as many run at once
     p.failed = p.order + (p.ordered ? (size_t)d->num_seqs * 4 : 0);
@@ -115,15 +117,24 @@ void place(ps::DeltaArgs &a, const Parts &p, void *ws) {
     a.seg_slots = p.seg_slots;
     a.seg_m = a.ws + p.seg_m;
     a.seg_state = reinterpret_cast<float *>(a.ws + p.seg_state);
+    a.seg_h = reinterpret_cast<float *>(a.ws + p.seg_h);
     a.order = p.ordered ? reinterpret_cast<int32_t *>(a.ws + p.order) : nullptr;
     a.failed = p.total > p.failed ? reinterpret_cast<int *>(a.ws + p.failed) : nullptr;
 }
-// The chain, or where sequences are cut the states of the segments, their join and the chain.
+// The chain, or where sequences are cut the states of the segments, their join and the chain.  There one CTA reads the
+// state at a sequence's start and another of the same launch writes the one at its end: where both have one place, the
+// first is read from a copy.
 template <typename Chain>
 cudaError_t run_chain(ps::DeltaArgs a, int type, bool backward, Chain chain, cudaStream_t s) {
     if (a.seg) {
+        cudaError_t e = cudaSuccess;
+        const float *&start = backward ? a.dht : a.h0;
+        if (start != nullptr && start == (backward ? a.dh0 : a.ht)) {
+            e = cudaMemcpyAsync(a.seg_h, start, (size_t)(a.s.seqs * a.s.hv) * a.s.k * a.s.v * 4, cudaMemcpyDeviceToDevice, s);
+            start = a.seg_h;
+        }
         a.pass = ps::kPassStates;
-        cudaError_t e = chain(a, type, s);
+        if (e == cudaSuccess) e = chain(a, type, s);
         if (e == cudaSuccess) e = ps::launch_delta_join(a, backward, s);
         if (e != cudaSuccess) return e;
         a.pass = ps::kPassAll;
@@ -146,7 +157,7 @@ extern "C" ps_status ps_delta_forward(const ps_delta_shape *d, const ps_delta_te
     const ps_delta_tensor *beta = in5 + PS_DELTA_BETA;
     const size_t es = real_bytes(d->type), need = ps_delta_workspace_size(d, train);
     const bool packed = d->cu_seqlens != nullptr;
-    const size_t state = (size_t)d->num_seqs * d->heads_v * d->dim_k * d->dim_v * 4;
+    const size_t state = (size_t)d->num_seqs * state_bytes(d);
     const size_t obytes = (size_t)total_tokens(d) * d->heads_v * d->dim_v * es;
     if (reinterpret_cast<uintptr_t>(h0) % 4 != 0 || reinterpret_cast<uintptr_t>(ht) % 4 != 0) return PS_ERR_INVALID_ARG;
     ps::DeltaArgs a{};
@@ -202,7 +213,7 @@ extern "C" ps_status ps_delta_backward(const ps_delta_shape *d, const ps_delta_t
     if (d->num_seqs == 0) return PS_OK;
     const size_t es = real_bytes(d->type), bs = real_bytes(d->beta_type), need = ps_delta_workspace_size(d, 1);
     const bool packed = d->cu_seqlens != nullptr;
-    const size_t state = (size_t)d->num_seqs * d->heads_v * d->dim_k * d->dim_v * 4;
+    const size_t state = (size_t)d->num_seqs * state_bytes(d);
     const size_t tokens = (size_t)total_tokens(d);
     if (reinterpret_cast<uintptr_t>(d_ht) % 4 != 0 || reinterpret_cast<uintptr_t>(dh0) % 4 != 0) return PS_ERR_INVALID_ARG;
     ps::DeltaArgs a{};

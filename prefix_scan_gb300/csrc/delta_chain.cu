@@ -89,11 +89,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, a.train != 0);
     const int chunks = (int)((sp.len + kChunk - 1) / kChunk);
     const bool keep = a.train && !states;
-    // the state at the start and where it goes at the end.  Where a sequence is cut, the first pass reads h0 and leaves it
-    // in the first segment's slot for the second, in which the last segment may write ht, in the same place, first.
+    // the state at the start and where it goes at the end
     const size_t one_state = (size_t)a.s.k * a.s.v;
-    const bool left_h0 = a.seg && !states && !chain.last && a.h0;
-    const float *from = chain.first && !left_h0 ? (a.h0 ? a.h0 + (size_t)(seq * a.s.hv + head) * one_state : nullptr)
+    const float *from = chain.first ? (a.h0 ? a.h0 + (size_t)(seq * a.s.hv + head) * one_state : nullptr)
                         : states   ? nullptr
                                    : a.seg_state + (size_t)(chain.slot * a.s.hv + head) * one_state;
     float *to_state = states ? (matrix ? nullptr : a.seg_state + (size_t)((chain.slot + 1) * a.s.hv + head) * one_state)
@@ -447,18 +445,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(const Del
         const uint32_t at = (uint32_t)(warp & 3) << 21;
         const size_t ostride = (size_t)a.s.hv * a.s.v;
         const bool rows_out = (a.s.v * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 15) == 0;
-        if (states && chain.first && from && v0 + row < a.s.v) {   // these warps have no outputs in this pass
-            float *left = a.seg_state + (size_t)(chain.slot * a.s.hv + head) * one_state + v0 + row;
-            for (int k = 0; k < a.s.k; k += 16) {
-                float s[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k + i < a.s.k) s[i] = from[(size_t)(k + i) * a.s.v + v0 + row];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k + i < a.s.k) left[(size_t)(k + i) * a.s.v] = s[i];
-            }
-        }
         for (int c = 0; c < chunks && !states; ++c) {
             const int st = c % M::kStages;
             const float *scal = reinterpret_cast<const float *>(smem + M::kScal + st * 3 * kChunk * 4);

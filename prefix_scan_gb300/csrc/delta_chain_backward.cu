@@ -71,11 +71,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
     const int v0 = vb * kBlockV;
     const ChunkLayout lay = chunk_layout(a.s.k, a.s.v, true);
     const int chunks = (int)((sp.len + kChunk - 1) / kChunk);
-    // the gradient at the end and where it goes at the start.  Where a sequence is cut, the first pass reads d_ht and leaves
-    // it in the slot after the last segment's for the second, in which the first segment may write dh0, in the same place, first.
+    // the gradient at the end and where it goes at the start
     const size_t one_state = (size_t)a.s.k * a.s.v;
-    const bool left_dht = a.seg && !states && !chain.first && a.dht;
-    const float *from = chain.last && !left_dht ? (a.dht ? a.dht + (size_t)(seq * a.s.hv + head) * one_state : nullptr)
+    const float *from = chain.last ? (a.dht ? a.dht + (size_t)(seq * a.s.hv + head) * one_state : nullptr)
                         : states  ? nullptr
                                   : a.seg_state + (size_t)((chain.slot + 1) * a.s.hv + head) * one_state;
     float *to_state = states ? a.seg_state + (size_t)(chain.slot * a.s.hv + head) * one_state
@@ -437,18 +435,6 @@ __global__ void __launch_bounds__(kBackThreads, 1) delta_chain_backward_kernel(c
         const size_t ostride = (size_t)a.s.hv * a.s.v;
         const int cols = min(kBlockV, a.s.v - v0);
         const bool rows_out = (a.s.v * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dv) & 15) == 0;
-        if (states && chain.last && from && tid < cols) {   // these warps have no outputs in this pass
-            float *left = a.seg_state + (size_t)((chain.slot + 1) * a.s.hv + head) * one_state + v0 + tid;
-            for (int k = 0; k < a.s.k; k += 16) {
-                float s[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k + i < a.s.k) s[i] = from[(size_t)(k + i) * a.s.v + v0 + tid];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k + i < a.s.k) left[(size_t)(k + i) * a.s.v] = s[i];
-            }
-        }
         for (int i = 0; i < chunks && !states; ++i) {
             const int n = rows_of(i);
             T *out = static_cast<T *>(a.dv) + ((size_t)(sp.first + first_token(i)) * a.s.hv + head) * a.s.v + v0;

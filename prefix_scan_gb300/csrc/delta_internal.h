@@ -75,9 +75,10 @@ constexpr long long delta_slots(long long seqs, long long tokens, bool packed) {
 // values that start from the identity and add nothing; a join goes through the segments in order
 // (delta_join.cu); a second pass runs every segment from its own start.  The backward pass does the
 // same from the other end, with M's transpose.
-//   seg_state  [segment slots + 1, hv, K, V] f32: the state at each segment's start (of a sequence's first
-//              segment too, as h0 may be ht); backward, its gradient at each segment's end (one slot further
-//              on; of the last segment too)
+//   seg_state  [segment slots + 1, hv, K, V] f32: the state at each segment's start; backward, its
+//              gradient at each segment's end (one slot further on)
+//   seg_h      [seqs, hv, K, V] f32: a copy of h0 that ht takes the place of (of d_ht and dh0): the segment
+//              that reads the one and the segment that writes the other run at the same time
 //   seg_m      [segment slots, hv] pairs of images of M (row j, column k: M_kj), as S's
 
 // Packed sequences of very different lengths: the chains of the longest are launched first, so that the
@@ -100,7 +101,7 @@ struct DeltaArgs {
     int seg;                      // chunks of a segment, 0: sequences are not cut
     int pass;
     long long seg_slots;
-    float *seg_state;
+    float *seg_state, *seg_h;
     int32_t *order;               // [seqs] by falling length, or null: as they come
     int *failed;                  // training: cleared by the prepare kernel, set by a chain whose waits ran out
                                   // (what it kept then is not to be used: all gradients become NaN); else null
