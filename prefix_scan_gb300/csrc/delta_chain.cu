@@ -28,9 +28,9 @@
 // passes takes the states alone, and one more chain per segment finds its matrix M.
 //
 // Measured at 128 x 128 and bf16: a chunk takes 5600 clocks of its chain, products
-// being issued in about half of them (tensor pipe 32 % busy).  12345 tokens in 48
-// sequences, 32 heads: 230 us; 4 x 4096 tokens, 16 heads, with what training keeps:
-// 243 us; 32768 tokens, 8 heads: two passes of 128 us (uncut, 1.3 ms).
+// being issued in about half of them (tensor pipe 33 % busy).  12345 tokens in 48
+// sequences, 32 heads: 231 us; 4 x 4096 tokens, 16 heads, with what training keeps:
+// 246 us; 32768 tokens, 8 heads: two passes of 128 us (uncut, 1.3 ms).
 #include "delta_tmem.cuh"
 
 namespace ps {

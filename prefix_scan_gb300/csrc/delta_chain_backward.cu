@@ -13,7 +13,7 @@
 // runs while dS' is on its way through registers, scale (exp(G) Q)^T dO while Y
 // is; dO becomes a left operand while the state's product runs.  Segments and their
 // two passes are as there, and so is what bounds it: 4 x 4096 tokens, 16 heads of
-// 128 x 128, take 240 us; 16384 tokens of 8 heads two passes of 56.
+// 128 x 128, take 246 us; 16384 tokens of 8 heads two passes of 59.
 #include "delta_tmem.cuh"
 
 namespace ps {
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kBackThreads = 16 * 32, kFirstConvert = 4, kFirstOut = 12;   // warps
 // Tensor-memory columns: dS; its pair, later dU's two accumulators; dO, later K dS'; P^T dO; the
-// pair of Y, later of -exp(G) dR; the pair of scale exp(G) dO.
+// pair of Y, later of -exp(G) dR; the pair of scale exp(G) dO.  (All 512: K dS' waits until P^T dO has read dO.)
 constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColU = 128, kColY = 256, kColO = 256, kColP = 320;
 constexpr uint32_t kColR = 384, kColQ = 448;
 

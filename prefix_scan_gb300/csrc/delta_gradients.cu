@@ -23,8 +23,8 @@
 // Bounded by shared memory: products read both operands there, and so do the sixteen
 // warps, whose steps follow one another.  So F is stored by whole 16-byte pieces (eight
 // tokens i of a row j; number by number it took a sixth of the kernel), and gradients
-// leave four columns at a time.  4 x 4096 tokens, 16 heads of 128 x 128: 280 us for
-// 1.1 GB read and written, 4.0 TB/s.
+// leave four columns at a time.  4 x 4096 tokens, 16 heads of 128 x 128: 282 us for
+// 1.1 GB read and written, 3.9 TB/s.
 #include <type_traits>
 
 #include "delta_tmem.cuh"
