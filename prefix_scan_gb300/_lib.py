@@ -74,6 +74,13 @@ SIGNATURES["ps_delta_forward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _sz
 SIGNATURES["ps_delta_backward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_delta_step"] = (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp])
 
+LINREC_TENSOR = struct.Struct("@Pqq")           # ps_linrec_tensor: data, seq_stride, tok_stride
+LINREC_SHAPE = struct.Struct("@qqPqiii4x")      # ps_linrec_shape
+SIGNATURES["ps_linrec_workspace_size"] = (_sz, [_vp, _int])
+SIGNATURES["ps_linrec_forward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _sz, _vp])
+SIGNATURES["ps_linrec_backward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_linrec_step"] = (_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp])
+
 PS_PAGES_MAX_POOLS = 128
 
 

@@ -17,6 +17,9 @@ from .delta import (DeltaRuleSaved, delta_rule, delta_rule_backward,  # noqa: F4
                     delta_rule_forward, delta_rule_step, delta_rule_workspace_size)
 from .pages import (pages_compact, pages_copy, pages_fork, pages_free, pages_grow,  # noqa: F401
                     pages_workspace_size)
+from .recurrence import (LinearRecurrenceSaved, linear_recurrence,  # noqa: F401
+                         linear_recurrence_backward, linear_recurrence_forward, linear_recurrence_step,
+                         linear_recurrence_workspace_size)
 
 DTYPE_CODES = {torch.int32: PS_INT32, torch.int64: PS_INT64, torch.float32: PS_FLOAT32}
 _SUFFIX = {PS_INT32: "i32", PS_INT64: "i64", PS_FLOAT32: "f32"}
