@@ -17,7 +17,7 @@ size_t real_bytes(int t) { return t == PS_REAL_F32 ? 4 : 2; }
 bool known(int t) { return t == PS_REAL_F32 || t == PS_REAL_BF16 || t == PS_REAL_F16; }
 long long total_tokens(const ps_linrec_shape *d) { return d->cu_seqlens ? d->tokens : d->num_seqs * d->tokens; }
 long long tiles_of(const ps_linrec_shape *d) { return (total_tokens(d) + ps::kLinrecTile - 1) / ps::kLinrecTile; }
-long long blocks_of(const ps_linrec_shape *d, bool vec) { return (d->channels + (vec ? 63 : 31)) / (vec ? 64 : 32); }
+long long blocks_of(const ps_linrec_shape *d) { return (d->channels + 63) / 64; }
 
 bool valid(const ps_linrec_shape *d) {
     if (d == nullptr || !known(d->type)) return false;
@@ -25,9 +25,9 @@ bool valid(const ps_linrec_shape *d) {
     if (d->num_seqs < 0 || d->tokens < 0 || d->num_seqs > INT_MAX || d->tokens > INT_MAX) return false;
     if (d->channels < 1 || d->channels > INT_MAX) return false;
     if (reinterpret_cast<uintptr_t>(d->cu_seqlens) % 4 != 0) return false;
-    if (total_tokens(d) > INT_MAX - ps::kLinrecTile) return false;
-    // one CTA a tile, and one a sequence and part of the channels
-    if (blocks_of(d, false) * (tiles_of(d) > 1 ? tiles_of(d) : 1) > INT_MAX) return false;
+    if (total_tokens(d) > INT_MAX - 128) return false;
+    // a ticket a tile, and in steps a CTA a sequence and part of the channels
+    if (blocks_of(d) * (tiles_of(d) > 1 ? tiles_of(d) : 1) > INT_MAX) return false;
     return (d->channels + 127) / 128 * (d->num_seqs > 1 ? d->num_seqs : 1) <= INT_MAX;
 }
 
@@ -39,8 +39,13 @@ bool rows_on(const ps_linrec_tensor *t, size_t es, int n, bool packed) {
     return reinterpret_cast<uintptr_t>(t->data) % (n * es) == 0 && ((packed ? 0 : t->seq_stride) | t->tok_stride) % n == 0;
 }
 bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-ps::LinrecTensor tensor(const ps_linrec_tensor *t, bool packed) {
-    return {t->data, packed ? 0 : (long long)t->seq_stride, (long long)t->tok_stride};
+ps::LinrecTensor tensor(const ps_linrec_shape *d, const ps_linrec_tensor *t, size_t es) {
+    const bool packed = d->cu_seqlens != nullptr;
+    const bool flat = packed || d->num_seqs == 1 || t->seq_stride == t->tok_stride * d->tokens;
+    int piece = (int)es;
+    for (int bytes : {4, 16})
+        if (rows_on(t, es, bytes / (int)es, packed) && d->channels % (bytes / (int)es) == 0) piece = bytes;
+    return {t->data, packed ? 0 : (long long)t->seq_stride, (long long)t->tok_stride, flat, piece};
 }
 
 struct Range {
@@ -73,37 +78,36 @@ bool outputs_meet(const Range (&out)[NO], const Range (&in)[NI]) {
     return false;
 }
 
-// Ticket and flags, maps, states, a copy of the states at the start for calls in place, and in training the states before
-// the tiles.
+// Ticket, maps, states, a copy of the states at the start for calls in place, and in training the states before
+// the backward pass's tiles.
 struct Parts {
-    size_t cleared, map, state, copy, start, total;
+    size_t map, state, copy, start, total;
 };
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 Parts parts_of(const ps_linrec_shape *d, int train) {
     Parts p{};
-    const size_t tiles = (size_t)tiles_of(d), wide = (size_t)blocks_of(d, false) * 32 + 32;   // channels in whole blocks of either size
+    const size_t tiles = (size_t)tiles_of(d), places = tiles * (size_t)blocks_of(d);
     const bool chained = tiles > 1;
-    p.cleared = chained ? 256 + tiles * (size_t)blocks_of(d, false) * 4 : 0;
-    p.map = up(p.cleared);
-    p.state = p.map + (chained ? up(tiles * wide * 8) : 0);
-    p.copy = p.state + (chained ? up(tiles * wide * 4) : 0);
+    p.map = chained ? 256 : 0;
+    p.state = p.map + (chained ? places * 64 * 8 : 0);
+    p.copy = p.state + (chained ? places * 64 * 4 : 0);
     p.start = p.copy + up((size_t)d->num_seqs * (size_t)d->channels * 4);
-    p.total = p.start + (train ? up(tiles * (size_t)d->channels * 4) : 0);
+    const size_t tokens = ps::linrec_start_tokens(real_bytes(d->type));
+    p.total = p.start + (train ? up(((size_t)total_tokens(d) + tokens - 1) / tokens * (size_t)d->channels * 4) : 0);
     return p;
 }
-// The chain's parts of the workspace, with tickets and flags cleared.
-cudaError_t place(ps::LinrecArgs &a, const ps_linrec_shape *d, bool vec, int train, void *ws, cudaStream_t s) {
+// The chain's parts of the workspace, prepared.
+cudaError_t place(ps::LinrecArgs &a, const ps_linrec_shape *d, int train, void *ws, cudaStream_t s) {
     const Parts p = parts_of(d, train);
     unsigned char *w = static_cast<unsigned char *>(ws);
-    a.tiles = (int)tiles_of(d);
-    a.blocks = (int)blocks_of(d, vec);
+    a.blocks = (int)blocks_of(d);
+    a.start_tokens = ps::linrec_start_tokens(real_bytes(d->type));
     a.ticket = reinterpret_cast<unsigned *>(w);
-    a.flag = reinterpret_cast<unsigned *>(w + 256);
-    a.map = reinterpret_cast<float2 *>(w + p.map);
-    a.state = reinterpret_cast<float *>(w + p.state);
+    a.map = reinterpret_cast<float4 *>(w + p.map);
+    a.state = reinterpret_cast<float2 *>(w + p.state);
     a.start = train ? reinterpret_cast<float *>(w + p.start) : nullptr;
-    if (a.tiles < 2) return cudaSuccess;
-    return cudaMemsetAsync(ws, 0, 256 + (size_t)a.tiles * a.blocks * 4, s);
+    if (tiles_of(d) < 2) return cudaSuccess;
+    return cudaMemsetAsync(ws, 0xff, p.copy, s);
 }
 // Tiles read the states at the start while others write those at the end: where both have one place, the first are read
 // from a copy.
@@ -122,6 +126,29 @@ cudaError_t hand_on(const float *from, float *to, size_t bytes, cudaStream_t s) 
 
 }  // namespace
 
+bool ps::linrec_tensor_map(CUtensorMap &map, const LinrecTensor &x, const LinrecArgs &a, size_t bytes, bool f16, int tokens) {
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    const long long row = x.tok * (long long)bytes;
+    if (encode == nullptr || !x.flat || row % 16 != 0 || row <= 0 || row >= 1ll << 40 || !on(x.p, 16)) return false;
+    const cuuint64_t sizes[2] = {(cuuint64_t)a.channels, (cuuint64_t)a.total}, strides[1] = {(cuuint64_t)row};
+    const cuuint32_t box[2] = {64, (cuuint32_t)tokens}, steps[2] = {1, 1};
+    const CUtensorMapDataType type = bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : f16      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode(&map, type, 2, const_cast<void *>(x.p), sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" size_t ps_linrec_workspace_size(const ps_linrec_shape *d, int train) {
     if (!valid(d) || d->num_seqs == 0) return 0;
     return parts_of(d, train).total;
@@ -133,7 +160,6 @@ extern "C" ps_status ps_linrec_forward(const ps_linrec_shape *d, const ps_linrec
     if (!valid(d)) return PS_ERR_INVALID_ARG;
     if (d->num_seqs == 0) return PS_OK;
     const size_t es = real_bytes(d->type), gs = real_bytes(d->gate_type), need = ps_linrec_workspace_size(d, train);
-    const bool packed = d->cu_seqlens != nullptr;
     const size_t states = (size_t)d->num_seqs * d->channels * 4;
     const long long total = total_tokens(d);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -151,21 +177,21 @@ extern "C" ps_status ps_linrec_forward(const ps_linrec_shape *d, const ps_linrec
                         range(d->cu_seqlens, ((size_t)d->num_seqs + 1) * 4)};
     const Range out[] = {range(h, (size_t)total * d->channels * es), range(ht, states), range(ws, need)};
     if (outputs_meet(out, in)) return PS_ERR_OVERLAP;
-    const bool vec = d->channels % 2 == 0 && on(h, 2 * es) && rows_on(x, es, 2, packed) && rows_on(g, gs, 2, packed);
     ps::LinrecArgs a{};
     a.seqs = d->num_seqs;
     a.tokens = d->tokens;
     a.total = total;
     a.cu = d->cu_seqlens;
     a.channels = d->channels;
-    a.x = tensor(x, packed);
-    a.g = tensor(g, packed);
+    a.x = tensor(d, x, es);
+    a.g = tensor(d, g, gs);
+    a.pairs = d->channels % 2 == 0 && on(h, 2 * es);
     a.h0 = h0;
     a.ht = ht;
     a.h = h;
-    cudaError_t e = place(a, d, vec, train, ws, s);
+    cudaError_t e = place(a, d, train, ws, s);
     if (e == cudaSuccess) e = apart(a.h0, ht, d, train, ws, s);
-    if (e == cudaSuccess) e = ps::launch_linrec_forward(a, d->type, d->gate_type, d->tied != 0, vec, s);
+    if (e == cudaSuccess) e = ps::launch_linrec_forward(a, d->type, d->gate_type, d->tied != 0, s);
     return done(e);
 }
 
@@ -175,7 +201,6 @@ extern "C" ps_status ps_linrec_backward(const ps_linrec_shape *d, const ps_linre
     if (!valid(d)) return PS_ERR_INVALID_ARG;
     if (d->num_seqs == 0) return PS_OK;
     const size_t es = real_bytes(d->type), gs = real_bytes(d->gate_type), need = ps_linrec_workspace_size(d, 1);
-    const bool packed = d->cu_seqlens != nullptr;
     const size_t states = (size_t)d->num_seqs * d->channels * 4;
     const long long total = total_tokens(d);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -193,25 +218,24 @@ extern "C" ps_status ps_linrec_backward(const ps_linrec_shape *d, const ps_linre
     const Range out[] = {range(dx, (size_t)total * d->channels * es), range(dg, (size_t)total * d->channels * gs),
                          range(dh0, states), range(ws, need)};
     if (outputs_meet(out, in)) return PS_ERR_OVERLAP;
-    const bool vec = d->channels % 2 == 0 && on(dx, 2 * es) && on(dg, 2 * gs) && rows_on(x, es, 2, packed) &&
-                     rows_on(g, gs, 2, packed) && rows_on(d_h, es, 2, packed);
     ps::LinrecArgs a{};
     a.seqs = d->num_seqs;
     a.tokens = d->tokens;
     a.total = total;
     a.cu = d->cu_seqlens;
     a.channels = d->channels;
-    a.x = tensor(x, packed);
-    a.g = tensor(g, packed);
-    a.dout = tensor(d_h, packed);
+    a.x = tensor(d, x, es);
+    a.g = tensor(d, g, gs);
+    a.dout = tensor(d, d_h, es);
+    a.pairs = d->channels % 2 == 0 && on(dx, 2 * es) && on(dg, 2 * gs);
     a.h0 = h0;
     a.dht = d_ht;
     a.dh0 = dh0;
     a.dx = dx;
     a.dg = dg;
-    cudaError_t e = place(a, d, vec, 1, ws, s);
+    cudaError_t e = place(a, d, 1, ws, s);
     if (e == cudaSuccess) e = apart(a.dht, dh0, d, 1, ws, s);
-    if (e == cudaSuccess) e = ps::launch_linrec_backward(a, d->type, d->gate_type, d->tied != 0, vec, s);
+    if (e == cudaSuccess) e = ps::launch_linrec_backward(a, d->type, d->gate_type, d->tied != 0, s);
     return done(e);
 }
 
@@ -234,8 +258,8 @@ extern "C" ps_status ps_linrec_step(const ps_linrec_shape *d, const ps_linrec_te
     a.pages = pages;
     a.channels = d->channels;
     a.t = (int)d->tokens;
-    a.x = tensor(x, false);
-    a.g = tensor(g, false);
+    a.x = tensor(d, x, es);
+    a.g = tensor(d, g, gs);
     a.state = state;
     a.slots = slots;
     a.lengths = lengths;

@@ -1,124 +1,153 @@
 // linrec_forward.cu -- the gated linear recurrence over whole sequences
 // (notation and tiles in linrec_common.cuh).
 //
-// Bound by memory: x and g are read once, h is written once.  Every run is scanned twice in registers, first from 0 for
-// what it adds, then from the state before it.
+// Bound by memory: x and g are read once, h is written once.  A run is scanned once, from 0, and each token's state and the
+// factor P of what was there before the run stay in registers; when the state H before the run is known, h + P H goes
+// out.  P is a plain product of at most 16 factors: its 2^-20 is of one output alone, as states go from run to run by the
+// runs' maps, whose factors come from sums of log decays.
+#include <type_traits>
+
 #include "linrec_common.cuh"
 
 namespace ps {
 
 namespace {
 
-// One token: h becomes a h + w x.
-template <int V, bool TIED> __device__ __forceinline__ void token(float (&h)[V], const float (&f)[V], const float (&x)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = apply(f[v], h[v], TIED ? forgotten(f[v]) * x[v] : x[v]);
-}
+template <typename TX, typename TG, int R> struct ForwardSpace {
+    alignas(128) TG g[kLrWarps * R * kLrWide];
+    alignas(128) TX x[kLrWarps * R * kLrWide];
+    Shared<R> shared;
+};
 
-template <typename TX, typename TG, int V, bool TIED>
-__global__ void __launch_bounds__(kLrThreads, 2) linrec_forward_kernel(const LinrecArgs a) {
-    __shared__ Marks marks;
-    __shared__ Sums<V> sums;
-    __shared__ float before[32 * V];
-    __shared__ unsigned ticket;
+template <typename TX, typename TG, bool TIED, int R>
+__global__ void __launch_bounds__(kLrThreads, 2) linrec_forward_kernel(const LinrecArgs a, const __grid_constant__ LinrecMaps maps) {
+    typedef ForwardSpace<TX, TG, R> Space;
+    constexpr int TOKENS = kLrWarps * R;
+    extern __shared__ __align__(128) unsigned char raw[];
+    Space &space = *reinterpret_cast<Space *>(raw);
+    Shared<R> &sm = space.shared;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) ticket = a.tiles > 1 ? atomicAdd(a.ticket, 1u) : blockIdx.x;
+    const unsigned all = (unsigned)a.tiles * (unsigned)a.blocks;
+    const bool tensor_copies = a.tensor_copies;
+    if (tid == 0) {
+        mbar_init(&sm.landed, 1);
+        mbar_init(&sm.summed, kLrWarps);
+        mbar_init(&sm.read, kLrWarps);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     __syncthreads();
-    const int k = (int)(ticket / (unsigned)a.blocks), block = (int)(ticket % (unsigned)a.blocks);
-    const uint32_t n0 = (uint32_t)k * kLinrecTile, first = n0 + warp * kLinrecRun, total = (uint32_t)a.total;
-    const long long c0 = (long long)block * (32 * V), ch = c0 + lane * V;
-    const bool in = ch < a.channels;
 
-    Lanes<TX, V> x[kLinrecRun];
-    Lanes<TG, V> g[kLinrecRun];
-    load_run<TG, V>(g, a.g, first, total, (uint32_t)a.tokens, ch, a.channels);
-    load_run<TX, V>(x, a.x, first, total, (uint32_t)a.tokens, ch, a.channels);
-    mark_tile(marks, a, n0, k == a.tiles - 1, a.h0, a.ht, c0, 32 * V);
-    const uint32_t starts = run_bits(marks.start, warp), ends = run_bits(marks.end, warp);
-    auto start = [&](float (&h)[V], int i) {
-        const float *p = a.h0 + marks.start_seq[warp * kLinrecRun + i] * a.channels + ch;
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = a.h0 && in ? p[v] : 0.f;
+    if (warp == kLrWarps) {
+        ninth_warp<R, false>(a, sm, a.h0, a.ht, tensor_copies, [&](unsigned k, unsigned block) {
+            mbar_arrive_expect_tx(&sm.landed, sizeof(space.g) + sizeof(space.x));
+            tile_copy(space.g, maps.g, k * TOKENS, (int)(block * kLrWide), &sm.landed);
+            tile_copy(space.x, maps.x, k * TOKENS, (int)(block * kLrWide), &sm.landed);
+        });
+        return;
+    }
+
+    auto load = [&](unsigned ticket) {
+        const uint32_t n = ticket / (unsigned)a.blocks * TOKENS;
+        const long long c = (long long)(ticket % (unsigned)a.blocks) * kLrWide;
+        load_tile<TG, TOKENS>(space.g, a.g, a, n, c);
+        load_tile<TX, TOKENS>(space.x, a.x, a, n, c);
     };
+    meet(2);
+    unsigned ticket = sm.ticket[0];
+    if (!tensor_copies && ticket < all) load(ticket);
+    for (int turn = 0; ticket < all; turn ^= 1) {
+        const Marks<TOKENS> &m = sm.marks[turn];
+        bool whole_tile = true;
+        if (tensor_copies) whole_tile = mbar_wait(&sm.landed, turn);
+        else copies_landed();
+        meet(1);
+        const Run<R> r(a, m, ticket, (int)(ticket / (unsigned)a.blocks), warp);
+        const TX *xs = space.x + warp * R * kLrWide;
+        const TG *gs = space.g + warp * R * kLrWide;
+        float2 hs[R], ps[R], h = both(0.f), p = both(1.f), s = both(whole_tile ? 0.f : __uint_as_float(0x7fffffffu));
+        auto token = [&](int i) {
+            const float2 g = pair_at(gs, i), x = pair_at(xs, i), f = factor(g);
+            s = add2(s, g);
+            const float2 one = make_float2(near_one(f.x) ? 1.f : 0.f, near_one(f.y) ? 1.f : 0.f);
+            const float2 b = TIED ? mul2(make_float2((near_one(f.x) ? 0.f : 1.f) - f.x, (near_one(f.y) ? 0.f : 1.f) - f.y), x) : x;
+            h = fma2(one, h, fma2(f, h, b));
+            p = fma2(one, p, mul2(f, p));
+            hs[i] = h;
+            ps[i] = p;
+        };
+        if (r.starts == 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) token(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (r.starts >> i & 1) {
+                    h = r.start(a, m, i);
+                    p = both(0.f);
+                }
+                token(i);
+            }
+        }
+        sm.sums.s[warp][lane] = s;
+        sm.sums.f[warp][lane] = factor_of_sum(s);
+        sm.sums.b[warp][lane] = h;
+        __syncwarp();
+        if (!tensor_copies) meet(2);   // before the ninth warp may come to its next ticket
+        if (lane == 0) mbar_arrive(&sm.summed);
+        if (!tensor_copies && sm.ticket[turn ^ 1] < all) load(sm.ticket[turn ^ 1]);
 
-    float f[kLinrecRun][V], h[V], s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = s[v] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kLinrecRun; ++i) {
-        float xi[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float gi = to_f32<TG>(g[i].v[v]);
-            f[i][v] = factor(gi);
-            s[v] += gi;
-            xi[v] = to_f32<TX>(x[i].v[v]);
+        meet(3);
+        float2 H = sm.before[lane];
+        for (int w = 0; w < warp; ++w) {
+            const float2 b = sm.sums.b[w][lane];
+            H = m.starts && run_bits<R>(m.start, w) != 0 ? b : apply(sm.sums.f[w][lane], H, b);
         }
-        if (starts >> i & 1) start(h, i);
-        token<V, TIED>(h, f[i], xi);
-    }
+        if (a.start != nullptr && warp * R % a.start_tokens == 0 && r.first < (uint32_t)a.total)
+            put_f32(a.start + r.first / a.start_tokens * a.channels + r.ch, H, r.in0, r.in1);
+        TX *out = static_cast<TX *>(a.h) + (long long)r.first * a.channels + r.ch;
+        if (r.plain) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sums.s[warp][lane * V + v] = s[v];
-        sums.b[warp][lane * V + v] = h[v];
-    }
-    __syncthreads();
-    if (warp == 0) {
-        float carry[V];
-        tile_carry<V>(carry, a, k, block, sums, [&](int w) { return run_bits(marks.start, w) != 0; }, any_bits(marks.start),
-                      (marks.start[0] & 1) == 0, false);
+            for (int i = 0; i < R; ++i) {
+                if (r.in0) *reinterpret_cast<typename Pair<TX>::type *>(out) = Pair<TX>::put(fma2(ps[i], H, hs[i]));
+                out += a.channels;
+            }
+        } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) before[lane * V + v] = carry[v];
-        if (a.start != nullptr && in) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) a.start[k * a.channels + ch + v] = carry[v];
+            for (int i = 0; i < R; ++i) {
+                if (r.starts >> i & 1) H = both(0.f);   // whatever came before, NaN too, is forgotten
+                const float2 y = fma2(ps[i], H, hs[i]);
+                if (r.first + i - m.lo < m.held) put_pair<TX>(out, y, r.whole, r.in0, r.in1);
+                if ((r.ends >> i & 1) && a.ht != nullptr)
+                    put_f32(a.ht + m.end_seq[warp * R + i] * a.channels + r.ch, y, r.in0, r.in1);
+                out += a.channels;
+            }
         }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = before[lane * V + v];
-    for (int w = 0; w < warp; ++w) {
-        const bool reset = run_bits(marks.start, w) != 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float b = sums.b[w][lane * V + v];
-            h[v] = reset ? b : apply(factor_of_sum(sums.s[w][lane * V + v]), h[v], b);
-        }
-    }
-    TX *out = static_cast<TX *>(a.h) + (long long)first * a.channels + ch;
-    const uint32_t held = marks.hi > marks.lo ? marks.hi - marks.lo : 0;
-#pragma unroll
-    for (int i = 0; i < kLinrecRun; ++i) {
-        float xi[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) xi[v] = to_f32<TX>(x[i].v[v]);
-        if (starts >> i & 1) start(h, i);
-        token<V, TIED>(h, f[i], xi);
-        if (in && first + i - marks.lo < held) store_lanes<TX, V>(out + i * a.channels, h);
-        if ((ends >> i & 1) && a.ht != nullptr && in) {
-            float *p = a.ht + marks.end_seq[warp * kLinrecRun + i] * a.channels + ch;
-#pragma unroll
-            for (int v = 0; v < V; ++v) p[v] = h[v];
-        }
+        ticket = sm.ticket[turn ^ 1];
+        named_barrier(4, kLrCompute);   // all have read the sums
     }
 }
 
-template <typename TX, typename TG> cudaError_t launch(const LinrecArgs &a, bool tied, bool vec, cudaStream_t s) {
-    const unsigned grid = (unsigned)(a.tiles * (long long)a.blocks);
-    if (vec) {
-        if (tied) linrec_forward_kernel<TX, TG, 2, true><<<grid, kLrThreads, 0, s>>>(a);
-        else linrec_forward_kernel<TX, TG, 2, false><<<grid, kLrThreads, 0, s>>>(a);
-    } else {
-        if (tied) linrec_forward_kernel<TX, TG, 1, true><<<grid, kLrThreads, 0, s>>>(a);
-        else linrec_forward_kernel<TX, TG, 1, false><<<grid, kLrThreads, 0, s>>>(a);
-    }
+template <typename TX, typename TG, bool TIED> cudaError_t launch(LinrecArgs a, cudaStream_t s) {
+    constexpr int R = 16;
+    typedef ForwardSpace<TX, TG, R> Space;
+    a.tiles = (int)((a.total + kLrWarps * R - 1) / (kLrWarps * R));
+    LinrecMaps maps{};
+    a.tensor_copies = linrec_tensor_map(maps.g, a.g, a, sizeof(TG), std::is_same<TG, __half>::value, kLrWarps * R) &&
+                      linrec_tensor_map(maps.x, a.x, a, sizeof(TX), std::is_same<TX, __half>::value, kLrWarps * R);
+    const auto kernel = linrec_forward_kernel<TX, TG, TIED, R>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Space));
+    if (e != cudaSuccess) return e;
+    kernel<<<linrec_grid(a), kLrThreads, sizeof(Space), s>>>(a, maps);
     return cudaGetLastError();
+}
+template <typename TX, typename TG> cudaError_t launch(const LinrecArgs &a, bool tied, cudaStream_t s) {
+    return tied ? launch<TX, TG, true>(a, s) : launch<TX, TG, false>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_linrec_forward(const LinrecArgs &a, int type, int gate_type, bool tied, bool vec, cudaStream_t s) {
-#define CALL(TX, TG) launch<TX, TG>(a, tied, vec, s)
+cudaError_t launch_linrec_forward(const LinrecArgs &a, int type, int gate_type, bool tied, cudaStream_t s) {
+#define CALL(TX, TG) launch<TX, TG>(a, tied, s)
     PS_LINREC_DISPATCH(CALL);
 #undef CALL
 }

@@ -33,10 +33,15 @@ __global__ void __launch_bounds__(kStepThreads) linrec_step_kernel(const LinrecS
             const Wide<TG, V> gi = *reinterpret_cast<const Wide<TG, V> *>(g + i * a.g.tok);
             Wide<TX, V> o;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float f = factor(to_f32<TG>(gi.v[v])), y = to_f32<TX>(xi.v[v]);
-                h.v[v] = apply(f, h.v[v], TIED ? forgotten(f) * y : y);
-                o.v[v] = from_f32<TX>(h.v[v]);
+            for (int v = 0; v < V; v += 2) {
+                constexpr int N = V > 1;   // a channel alone takes the place of both
+                const float2 f = factor(make_float2(to_f32<TG>(gi.v[v]), to_f32<TG>(gi.v[v + N])));
+                const float2 y = make_float2(to_f32<TX>(xi.v[v]), to_f32<TX>(xi.v[v + N]));
+                const float2 next = apply(f, make_float2(h.v[v], h.v[v + N]), TIED ? mul2(forgotten(f), y) : y);
+                h.v[v] = next.x;
+                h.v[v + N] = next.y;
+                o.v[v] = from_f32<TX>(next.x);
+                o.v[v + N] = from_f32<TX>(next.y);
             }
             *reinterpret_cast<Wide<TX, V> *>(out + i * a.channels) = o;
         }
