@@ -71,6 +71,24 @@ ps_status ps_pages_fork(const int32_t *table, const int32_t *lengths, int64_t ro
                         int32_t *new_lengths, int32_t *missing, void *ws, size_t ws_bytes, ps_stream_t stream);
 
 /*
+ * Reorders: row i, which has the page slots[i] to itself (-1 for none), becomes
+ * a branch of row parents[i] in place: no page is handed out or let go.  Of the
+ * rows with one parent the lowest takes over the parent's page; the others, in
+ * order, take the pages that no row continues, also in order, and the parent's
+ * page is copied there in every pool.  Pages that are left go, in order, to rows
+ * without a parent (an index outside [0, rows), or a row without a page), whose
+ * content is what it was; when there are none, these rows have -1.
+ *   slots      device int32 [rows], pages all different
+ *   parents    device int32 [rows]
+ *   new_slots  device int32 [rows]
+ *   missing    device int32 [1]: how many branches found no page (their places
+ *              are -1), which takes rows without pages; may be NULL
+ */
+ps_status ps_pages_reorder(const int32_t *slots, const int32_t *parents, int64_t rows, const ps_page_pool *pools,
+                           int npools, int64_t pages, int32_t *new_slots, int32_t *missing, void *ws, size_t ws_bytes,
+                           ps_stream_t stream);
+
+/*
  * Grows: gives row r the pages it needs to hold new_lengths[r] tokens instead
  * of lengths[r], at the places of its row that these add and that hold none.
  *   missing  device int32 [1]: places that found no free page, or that lie past

@@ -15,7 +15,8 @@ def __getattr__(name):
                 "device_status", "tile_elements", "delta_rule", "delta_rule_forward", "delta_rule_backward",
                 "delta_rule_step", "delta_rule_workspace_size", "pages_copy", "pages_fork", "pages_grow", "pages_free",
                 "pages_compact", "pages_workspace_size", "linear_recurrence", "linear_recurrence_forward",
-                "linear_recurrence_backward", "linear_recurrence_step", "linear_recurrence_workspace_size"):
+                "linear_recurrence_backward", "linear_recurrence_step", "linear_recurrence_workspace_size", "beam_select",
+                "beam_workspace_size", "pages_reorder"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

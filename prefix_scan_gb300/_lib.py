@@ -81,6 +81,11 @@ SIGNATURES["ps_linrec_forward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _v
 SIGNATURES["ps_linrec_backward"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_linrec_step"] = (_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp])
 
+BEAM_SHAPE = struct.Struct("@qiiqqqii")         # ps_beam_shape
+PS_BEAM_MAX_BEAMS, PS_BEAM_MAX_WIDTH = 256, 64
+SIGNATURES["ps_beam_workspace_size"] = (_sz, [_vp])
+SIGNATURES["ps_beam_select"] = (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+
 PS_PAGES_MAX_POOLS = 128
 
 
@@ -88,6 +93,7 @@ _i32 = ctypes.c_int32
 SIGNATURES["ps_pages_workspace_size"] = (_sz, [_i64, _i64])
 SIGNATURES["ps_pages_copy"] = (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp])
 SIGNATURES["ps_pages_fork"] = (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _int, _i64, _vp, _vp, _vp, _vp, _sz, _vp])
+SIGNATURES["ps_pages_reorder"] = (_int, [_vp, _vp, _i64, _vp, _int, _i64, _vp, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_pages_grow"] = (_int, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
 SIGNATURES["ps_pages_free"] = (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp])
 SIGNATURES["ps_pages_compact"] = (_int, [_vp, _i64, _i64, _vp, _vp, _int, _i64, _vp, _vp, _sz, _vp])

@@ -15,8 +15,9 @@ from ._lib import (PS_ALGO_CHAINED, PS_ALGO_DECOUPLED_LOOKBACK, PS_ALGO_REDUCE_T
                    PS_FLOAT32, PS_INT32, PS_INT64)
 from .delta import (DeltaRuleSaved, delta_rule, delta_rule_backward,  # noqa: F401
                     delta_rule_forward, delta_rule_step, delta_rule_workspace_size)
+from .beam import BeamChoice, beam_select, beam_workspace_size  # noqa: F401
 from .pages import (pages_compact, pages_copy, pages_fork, pages_free, pages_grow,  # noqa: F401
-                    pages_workspace_size)
+                    pages_reorder, pages_workspace_size)
 from .recurrence import (LinearRecurrenceSaved, linear_recurrence,  # noqa: F401
                          linear_recurrence_backward, linear_recurrence_forward, linear_recurrence_step,
                          linear_recurrence_workspace_size)

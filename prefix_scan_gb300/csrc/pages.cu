@@ -1,4 +1,4 @@
-// pages.cu -- pages of a cache: copy, fork, grow, free, compact
+// pages.cu -- pages of a cache: copy, fork, reorder, grow, free, compact
 // (include/prefix_scan_pages.h).
 //
 // Each call that hands out or moves pages is a plan and a move.  The plan is
@@ -232,6 +232,78 @@ __global__ void __launch_bounds__(kMoveThreads) pages_fork_kernel(const ForkArgs
             a.new_table[i * a.width + j] = page;
         }
         if (threadIdx.x == 0) a.new_lengths[i] = (int32_t)len;
+    }
+}
+
+// ---- reorder --------------------------------------------------------------------------
+
+struct ReorderArgs {
+    const int32_t *slots, *parents;
+    long long rows, pages;
+    int32_t *new_slots, *missing;
+    PlanSpace w;   // head[0]: pages to copy, rank[p]: the first row that continues row p, list: pages that no row continues
+};
+__device__ __forceinline__ int32_t reorder_parent(const ReorderArgs &a, long long i) {   // -1 for none that has a page
+    const int32_t p = a.parents[i];
+    return p >= 0 && p < a.rows && valid_page(a.slots[p], a.pages) >= 0 ? p : -1;
+}
+__global__ void __launch_bounds__(kPlanThreads) pages_reorder_plan_kernel(const ReorderArgs a) {
+    __shared__ int warps[32];
+    for (long long i = threadIdx.x; i < a.rows; i += kPlanThreads) a.w.rank[i] = INT_MAX;
+    __syncthreads();
+    for (long long i = threadIdx.x; i < a.rows; i += kPlanThreads) {
+        const int32_t p = reorder_parent(a, i);
+        if (p >= 0) atomicMin(a.w.rank + p, (int32_t)i);
+    }
+    __syncthreads();
+    // pages that no row continues, and how many rows have to copy (a page named twice could make more of the first than pages)
+    long long spare = 0, copies = 0;
+    for (long long base = 0; base < a.rows; base += kPlanThreads) {
+        const long long i = base + threadIdx.x;
+        const bool in = i < a.rows;
+        const int32_t page = in ? valid_page(a.slots[i], a.pages) : -1, p = in ? reorder_parent(a, i) : -1;
+        const bool free_page = page >= 0 && __ldcg(a.w.rank + i) == INT_MAX;
+        const bool copied = p >= 0 && __ldcg(a.w.rank + p) != i;
+        int total;
+        const long long at = spare + block_exclusive(free_page, warps, total);
+        if (free_page && at < a.pages) a.w.list[at] = page;
+        spare += total;
+        block_exclusive(copied, warps, total);
+        copies += total;
+    }
+    spare = min(spare, a.pages);
+    __syncthreads();
+    long long copy = 0, rest = copies;   // rows that copy come first, then those that continue none
+    for (long long base = 0; base < a.rows; base += kPlanThreads) {
+        const long long i = base + threadIdx.x;
+        const bool in = i < a.rows;
+        const int32_t p = in ? reorder_parent(a, i) : -1;
+        const bool copied = p >= 0 && __ldcg(a.w.rank + p) != i, orphan = in && p < 0;
+        int n_copied, n_orphan;
+        const long long at_copy = copy + block_exclusive(copied, warps, n_copied);
+        const long long at_rest = rest + block_exclusive(orphan, warps, n_orphan);
+        if (in) {
+            const long long at = copied ? at_copy : at_rest;
+            const int32_t to = !copied && !orphan ? a.slots[p] : at < spare ? a.w.list[at] : -1;
+            if (copied && to >= 0) {
+                a.w.from[at] = a.slots[p];
+                a.w.to[at] = to;
+            }
+            a.new_slots[i] = to;
+        }
+        copy += n_copied;
+        rest += n_orphan;
+    }
+    if (threadIdx.x == 0) {
+        a.w.head[0] = (int32_t)min(copies, spare);
+        if (a.missing) *a.missing = (int32_t)max(copies - spare, 0ll);
+    }
+}
+__global__ void __launch_bounds__(kMoveThreads) pages_reorder_kernel(const PlanSpace w, const Pools pools) {
+    const long long tasks = (long long)w.head[0] * pools.pieces;
+    for (long long t = blockIdx.x; t < tasks; t += gridDim.x) {
+        const long long i = t / pools.pieces;
+        move_piece(pools, (int)(t % pools.pieces), w.from[i], w.to[i]);
     }
 }
 
@@ -484,6 +556,32 @@ extern "C" ps_status ps_pages_fork(const int32_t *table, const int32_t *lengths,
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && new_rows > 0) {
         pages_fork_kernel<<<move_grid(new_rows * (p.pieces + 1)), kMoveThreads, 0, s>>>(a, p);
+        e = cudaGetLastError();
+    }
+    return done(e);
+}
+
+extern "C" ps_status ps_pages_reorder(const int32_t *slots, const int32_t *parents, int64_t rows, const ps_page_pool *pools,
+                                      int npools, int64_t pages, int32_t *new_slots, int32_t *missing, void *ws, size_t ws_bytes,
+                                      ps_stream_t stream) {
+    Pools p{};
+    if (!sizes_ok(rows, 1, pages)) return PS_ERR_INVALID_ARG;
+    const ps_status st = pools_of(pools, npools, pages, p);
+    if (st != PS_OK) return st;
+    if (!aligned4(slots) || !aligned4(parents) || !aligned4(new_slots) || !aligned4(missing) || reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+        return PS_ERR_INVALID_ARG;
+    if ((rows > 0 && (slots == nullptr || parents == nullptr || new_slots == nullptr)) || ws == nullptr) return PS_ERR_INVALID_ARG;
+    const size_t need = ps_pages_workspace_size(rows, pages);
+    if (ws_bytes < need) return PS_ERR_WORKSPACE_TOO_SMALL;
+    const Bytes list[] = {bytes_of(slots, (size_t)rows * 4), bytes_of(parents, (size_t)rows * 4), bytes_of(new_slots, (size_t)rows * 4),
+                          bytes_of(missing, 4), bytes_of(ws, need)};
+    if (arrays_meet(list, p, pages)) return PS_ERR_OVERLAP;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const ReorderArgs a{slots, parents, rows, pages, new_slots, missing, plan_space(ws, rows, pages)};
+    pages_reorder_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && rows > 1 && p.pieces > 0) {   // at least one row keeps its page or has none
+        pages_reorder_kernel<<<move_grid((rows < pages ? rows : pages) * p.pieces), kMoveThreads, 0, s>>>(a.w, p);
         e = cudaGetLastError();
     }
     return done(e);

@@ -107,6 +107,41 @@ def pages_fork(table: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor
     return out_table, out_lengths, missing
 
 
+def pages_reorder(slots: torch.Tensor, parents: torch.Tensor, pools, *, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Branches of rows in place, for states that fill a page each: ``(new_slots, missing)``, row i a branch of row ``parents[i]``.
+
+    ``slots`` (int32, all different, -1 for none): each row's page, which no other row shares, so there are no counts.  The
+    lowest row of a parent takes over its page; the others get, in order, the pages that no row continues, and the parent's
+    page is copied there in every pool.  ``parents`` (int32, as many): as ``beam_select`` gives them, -1 for none; such rows
+    get what pages are left, as they are.  ``missing`` (int32, one entry): how many branches found no page; their places are
+    -1.  Any shapes go, as long as both are contiguous; the result has the shape of ``slots``, or is ``out``, another tensor.
+    """
+    fn = "pages_reorder"
+    device = slots.device
+    _check_ints(fn, device, slots=(slots, slots.dim()), parents=(parents, parents.dim()))
+    rows = slots.numel()
+    if parents.numel() != rows:
+        raise ValueError(f"{fn}: one parent per row is needed")
+    pools = [pools] if isinstance(pools, torch.Tensor) else pools
+    pages = pools[0].shape[0] if len(pools) else 0
+    arr, n = _pools(fn, pools, pages, device)
+    lib = _lib.load()
+    s, ctx = enter(device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(slots.shape, dtype=torch.int32, device=device)
+        _check_ints(fn, device, out=(out, slots.dim()))
+        if out.shape != slots.shape:
+            raise ValueError(f"{fn}: out must have the shape of slots")
+        missing = torch.empty(1, dtype=torch.int32, device=device)
+        workspace = _workspace(fn, lib, workspace, rows, pages, device)
+        st = lib.ps_pages_reorder(slots.data_ptr(), parents.data_ptr(), rows, arr, n, pages, out.data_ptr(), missing.data_ptr(),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    _lib.check("ps_pages_reorder", st)
+    return out, missing
+
+
 def pages_grow(table: torch.Tensor, lengths: torch.Tensor, new_lengths: torch.Tensor, refcount: torch.Tensor, *,
                page_tokens: int, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gives each row the pages it needs for ``new_lengths`` tokens instead of ``lengths`` (``table`` and ``refcount``
