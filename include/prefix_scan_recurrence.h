@@ -14,7 +14,7 @@
  * gradient of that type or f32; states, their gradients and all sums are f32.
  * Results repeat bit for bit from call to call.
  *
- * Log decays are at most 0 as a rule.  Above 0 states grow; sums of g over 256
+ * Log decays are at most 0 as a rule.  Above 0 states grow; sums of g over 512
  * tokens then have to stay below 80.  -infinity forgets the state: what follows
  * does not depend on it, unless it was not finite.  NaN and infinities reach the
  * channel's later outputs in their own sequence (and earlier tokens' gradients),
@@ -61,7 +61,7 @@ typedef struct ps_linrec_tensor {
  *            clamped into [0, tokens]; an end before its start is an empty
  *            sequence.  They must not fall: results are then unspecified for
  *            all sequences; no access leaves the tensors.
- * All sequences together have at most 2^31 - 129 tokens.
+ * All sequences together have at most 2^31 - 513 tokens.
  */
 typedef struct ps_linrec_shape {
     int64_t num_seqs;

@@ -17,7 +17,7 @@ size_t real_bytes(int t) { return t == PS_REAL_F32 ? 4 : 2; }
 bool known(int t) { return t == PS_REAL_F32 || t == PS_REAL_BF16 || t == PS_REAL_F16; }
 long long total_tokens(const ps_linrec_shape *d) { return d->cu_seqlens ? d->tokens : d->num_seqs * d->tokens; }
 long long tiles_of(const ps_linrec_shape *d) { return (total_tokens(d) + ps::kLinrecTile - 1) / ps::kLinrecTile; }
-long long blocks_of(const ps_linrec_shape *d) { return (d->channels + 63) / 64; }
+long long blocks_of(const ps_linrec_shape *d) { return (d->channels + ps::kLinrecWide - 1) / ps::kLinrecWide; }
 
 bool valid(const ps_linrec_shape *d) {
     if (d == nullptr || !known(d->type)) return false;
@@ -25,7 +25,7 @@ bool valid(const ps_linrec_shape *d) {
     if (d->num_seqs < 0 || d->tokens < 0 || d->num_seqs > INT_MAX || d->tokens > INT_MAX) return false;
     if (d->channels < 1 || d->channels > INT_MAX) return false;
     if (reinterpret_cast<uintptr_t>(d->cu_seqlens) % 4 != 0) return false;
-    if (total_tokens(d) > INT_MAX - 128) return false;
+    if (total_tokens(d) > INT_MAX - 512) return false;
     // a ticket a tile, and in steps a CTA a sequence and part of the channels
     if (blocks_of(d) * (tiles_of(d) > 1 ? tiles_of(d) : 1) > INT_MAX) return false;
     return (d->channels + 127) / 128 * (d->num_seqs > 1 ? d->num_seqs : 1) <= INT_MAX;
@@ -81,33 +81,23 @@ bool outputs_meet(const Range (&out)[NO], const Range (&in)[NI]) {
 // Ticket, maps, states, a copy of the states at the start for calls in place, and in training the states before
 // the backward pass's tiles.
 struct Parts {
-    size_t map, state, copy, start, total;
+    size_t copy, start, total;
 };
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 Parts parts_of(const ps_linrec_shape *d, int train) {
     Parts p{};
-    const size_t tiles = (size_t)tiles_of(d), places = tiles * (size_t)blocks_of(d);
-    const bool chained = tiles > 1;
-    p.map = chained ? 256 : 0;
-    p.state = p.map + (chained ? places * 64 * 8 : 0);
-    p.copy = p.state + (chained ? places * 64 * 4 : 0);
+    const size_t tiles = (size_t)tiles_of(d), places = (tiles + ps::kLinrecSlack) * (size_t)blocks_of(d) * ps::kLinrecWide;
+    p.copy = tiles > 1 ? up(256 + places * 12) : 0;
     p.start = p.copy + up((size_t)d->num_seqs * (size_t)d->channels * 4);
-    const size_t tokens = ps::linrec_start_tokens(real_bytes(d->type));
+    const size_t tokens = ps::linrec_start_tokens(real_bytes(d->type), real_bytes(d->gate_type));
     p.total = p.start + (train ? up(((size_t)total_tokens(d) + tokens - 1) / tokens * (size_t)d->channels * 4) : 0);
     return p;
 }
-// The chain's parts of the workspace, prepared.
-cudaError_t place(ps::LinrecArgs &a, const ps_linrec_shape *d, int train, void *ws, cudaStream_t s) {
-    const Parts p = parts_of(d, train);
-    unsigned char *w = static_cast<unsigned char *>(ws);
+void place(ps::LinrecArgs &a, const ps_linrec_shape *d, int train, void *ws) {
     a.blocks = (int)blocks_of(d);
-    a.start_tokens = ps::linrec_start_tokens(real_bytes(d->type));
-    a.ticket = reinterpret_cast<unsigned *>(w);
-    a.map = reinterpret_cast<float4 *>(w + p.map);
-    a.state = reinterpret_cast<float2 *>(w + p.state);
-    a.start = train ? reinterpret_cast<float *>(w + p.start) : nullptr;
-    if (tiles_of(d) < 2) return cudaSuccess;
-    return cudaMemsetAsync(ws, 0xff, p.copy, s);
+    a.start_tokens = ps::linrec_start_tokens(real_bytes(d->type), real_bytes(d->gate_type));
+    a.ticket = static_cast<unsigned *>(ws);
+    a.start = train ? reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + parts_of(d, train).start) : nullptr;
 }
 // Tiles read the states at the start while others write those at the end: where both have one place, the first are read
 // from a copy.
@@ -126,7 +116,7 @@ cudaError_t hand_on(const float *from, float *to, size_t bytes, cudaStream_t s) 
 
 }  // namespace
 
-bool ps::linrec_tensor_map(CUtensorMap &map, const LinrecTensor &x, const LinrecArgs &a, size_t bytes, bool f16, int tokens) {
+bool ps::linrec_tensor_map(CUtensorMap &map, const LinrecTensor &x, const LinrecArgs &a, size_t bytes, bool f16, int runs, int run) {
     typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -139,13 +129,15 @@ bool ps::linrec_tensor_map(CUtensorMap &map, const LinrecTensor &x, const Linrec
         return reinterpret_cast<Encode>(f);
     }();
     const long long row = x.tok * (long long)bytes;
-    if (encode == nullptr || !x.flat || row % 16 != 0 || row <= 0 || row >= 1ll << 40 || !on(x.p, 16)) return false;
-    const cuuint64_t sizes[2] = {(cuuint64_t)a.channels, (cuuint64_t)a.total}, strides[1] = {(cuuint64_t)row};
-    const cuuint32_t box[2] = {64, (cuuint32_t)tokens}, steps[2] = {1, 1};
+    if (encode == nullptr || !x.flat || row % 16 != 0 || row <= 0 || row * run >= 1ll << 40 || !on(x.p, 16) || a.total < run)
+        return false;
+    const cuuint64_t sizes[3] = {(cuuint64_t)a.channels, (cuuint64_t)(a.total / run), (cuuint64_t)run};
+    const cuuint64_t strides[2] = {(cuuint64_t)(row * run), (cuuint64_t)row};
+    const cuuint32_t box[3] = {(cuuint32_t)kLinrecWide, (cuuint32_t)runs, (cuuint32_t)run}, steps[3] = {1, 1, 1};
     const CUtensorMapDataType type = bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : f16      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return encode(&map, type, 2, const_cast<void *>(x.p), sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return encode(&map, type, 3, const_cast<void *>(x.p), sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -189,8 +181,8 @@ extern "C" ps_status ps_linrec_forward(const ps_linrec_shape *d, const ps_linrec
     a.h0 = h0;
     a.ht = ht;
     a.h = h;
-    cudaError_t e = place(a, d, train, ws, s);
-    if (e == cudaSuccess) e = apart(a.h0, ht, d, train, ws, s);
+    place(a, d, train, ws);
+    cudaError_t e = apart(a.h0, ht, d, train, ws, s);
     if (e == cudaSuccess) e = ps::launch_linrec_forward(a, d->type, d->gate_type, d->tied != 0, s);
     return done(e);
 }
@@ -233,8 +225,8 @@ extern "C" ps_status ps_linrec_backward(const ps_linrec_shape *d, const ps_linre
     a.dh0 = dh0;
     a.dx = dx;
     a.dg = dg;
-    cudaError_t e = place(a, d, 1, ws, s);
-    if (e == cudaSuccess) e = apart(a.dht, dh0, d, 1, ws, s);
+    place(a, d, 1, ws);
+    cudaError_t e = apart(a.dht, dh0, d, 1, ws, s);
     if (e == cudaSuccess) e = ps::launch_linrec_backward(a, d->type, d->gate_type, d->tied != 0, s);
     return done(e);
 }

@@ -14,67 +14,69 @@ namespace ps {
 namespace {
 
 template <typename TX, typename TG, int R> struct BackwardSpace {
-    alignas(128) TG g[kLrWarps * R * kLrWide];
-    alignas(128) TX x[kLrWarps * R * kLrWide];
-    alignas(128) TX dh[2][kLrWarps * R * kLrWide];   // the next tile's while this one's second pass is to come
+    alignas(128) TG g[2][kLrRuns * R * kLrWide];   // the next tile's are on their way
+    alignas(128) TX x[2][kLrRuns * R * kLrWide], dh[2][kLrRuns * R * kLrWide];
+    float2 add[kLrWarps][kLrPairs];                // what the warps' runs add to h
     Shared<R> shared;
-    float2 add[kLrWarps][32];                        // what the runs add to h
 };
 
 template <typename TX, typename TG, bool TIED, int R>
-__global__ void __launch_bounds__(kLrThreads, 2) linrec_backward_kernel(const LinrecArgs a, const __grid_constant__ LinrecMaps maps) {
+__global__ void __launch_bounds__(kLrThreads, kLinrecCtasPerSm) linrec_backward_kernel(const LinrecArgs a, const __grid_constant__ LinrecMaps maps) {
     typedef BackwardSpace<TX, TG, R> Space;
-    constexpr int TOKENS = kLrWarps * R;
+    constexpr int TOKENS = kLrRuns * R;
     extern __shared__ __align__(128) unsigned char raw[];
     Space &space = *reinterpret_cast<Space *>(raw);
     Shared<R> &sm = space.shared;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned all = (unsigned)a.tiles * (unsigned)a.blocks;
     const bool tensor_copies = a.tensor_copies;
     if (tid == 0) {
-        mbar_init(&sm.landed, 1);
+        mbar_init(&sm.landed[0], 1);
+        mbar_init(&sm.landed[1], 1);
         mbar_init(&sm.summed, kLrWarps);
-        mbar_init(&sm.read, kLrWarps);
+        mbar_init(&sm.done, kLrWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
 
     if (warp == kLrWarps) {
-        int stage = 0;
-        ninth_warp<R, true>(a, sm, a.dht, a.dh0, tensor_copies, [&](unsigned k, unsigned block) {
-            const uint32_t n = (a.tiles - 1 - k) * TOKENS;
-            const int c = (int)(block * kLrWide);
-            mbar_arrive_expect_tx(&sm.landed, sizeof(space.g) + 2 * sizeof(space.x));
-            tile_copy(space.g, maps.g, n, c, &sm.landed);
-            tile_copy(space.x, maps.x, n, c, &sm.landed);
-            tile_copy(space.dh[stage], maps.d, n, c, &sm.landed);
-            stage ^= 1;
+        ninth_warp<R, true>(a, sm, a.dht, a.dh0, tensor_copies, [&](const Place &at, int stage) {
+            const int n = at.tile * kLrRuns, c = at.block * kLrWide;
+            mbar_arrive_expect_tx(&sm.landed[stage], sizeof(space.g[0]) + 2 * sizeof(space.x[0]));
+            tile_copy(space.g[stage], maps.g, n, c, &sm.landed[stage]);
+            tile_copy(space.x[stage], maps.x, n, c, &sm.landed[stage]);
+            tile_copy(space.dh[stage], maps.d, n, c, &sm.landed[stage]);
         });
         return;
     }
 
-    auto load = [&](unsigned ticket, int stage) {
-        const uint32_t n = (a.tiles - 1 - ticket / (unsigned)a.blocks) * TOKENS;
-        const long long c = (long long)(ticket % (unsigned)a.blocks) * kLrWide;
-        load_tile<TG, TOKENS>(space.g, a.g, a, n, c);
-        load_tile<TX, TOKENS>(space.x, a.x, a, n, c);
-        load_tile<TX, TOKENS>(space.dh[stage], a.dout, a, n, c);
+    auto load = [&](const Place &at, int stage) {
+        const uint32_t n = (uint32_t)at.tile * TOKENS;
+        const long long c = (long long)at.block * kLrWide;
+        load_tile<TG, R>(space.g[stage], a.g, a, n, c);
+        load_tile<TX, R>(space.x[stage], a.x, a, n, c);
+        load_tile<TX, R>(space.dh[stage], a.dout, a, n, c);
     };
     meet(2);
-    unsigned ticket = sm.ticket[0];
-    if (!tensor_copies && ticket < all) load(ticket, 0);
-    for (int turn = 0; ticket < all; turn ^= 1) {
+    Place place = sm.place[0];
+    if (!tensor_copies && place.tile >= 0) load(place, 0);
+    for (int turn = 0, phase = 0; place.tile >= 0; phase ^= turn, turn ^= 1) {
         const Marks<TOKENS> &m = sm.marks[turn];
-        const int tile = a.tiles - 1 - (int)(ticket / (unsigned)a.blocks);
-        const long long ch = (long long)(ticket % (unsigned)a.blocks) * kLrWide + 2 * lane;
-        float2 h = get_f32(a.start + (long long)tile * a.channels + ch, ch < a.channels, ch + 1 < a.channels);
+        const float2 first = get_f32(a.start + (long long)place.tile * a.channels + (long long)place.block * kLrWide + 2 * lr_pair(),
+                                     place.block * kLrWide + 2 * lr_pair() < a.channels, place.block * kLrWide + 2 * lr_pair() + 1 < a.channels);
         bool whole_tile = true;
-        if (tensor_copies) whole_tile = mbar_wait(&sm.landed, turn);
+        if (tensor_copies) whole_tile = mbar_wait(&sm.landed[turn], phase);
         else copies_landed();
         meet(1);
-        const Run<R> r(a, m, ticket, tile, warp);
-        const TG *gs = space.g + warp * R * kLrWide;
-        const TX *xs = space.x + warp * R * kLrWide, *ds = space.dh[turn] + warp * R * kLrWide;
+        const Place next_place = sm.place[turn ^ 1];
+        if (!tensor_copies && next_place.tile >= 0) load(next_place, turn ^ 1);
+        const Run<R> r(a, m, place);
+        TG *gs = space.g[turn];
+        TX *xs = space.x[turn], *ds = space.dh[turn];
+        if (tensor_copies && r.first < (uint32_t)a.total && r.first + R > (uint32_t)a.total) {
+            load_last_run<TG, R>(gs, a.g, a, r.first, r.ch);
+            load_last_run<TX, R>(xs, a.x, a, r.first, r.ch);
+            load_last_run<TX, R>(ds, a.dout, a, r.first, r.ch);
+        }
         float2 f[R], was[R], add = both(0.f), s = both(whole_tile ? 0.f : __uint_as_float(0x7fffffffu)), mu = both(0.f);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_backward_kernel(const Li
             f[i] = factor(g);
             s = add2(s, g);
         }
-        if ((r.starts | r.ends) == 0) {
+        if (!r.marked) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const float2 x = pair_at(xs, i);
@@ -104,18 +106,15 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_backward_kernel(const Li
                 if (r.starts >> i & 1) mu = both(0.f);   // dh0 takes it
             }
         }
-        sm.sums.s[warp][lane] = s;
-        sm.sums.f[warp][lane] = factor_of_sum(s);
-        sm.sums.b[warp][lane] = mu;
-        space.add[warp][lane] = add;
+        const float2 own = factor_of_sum(s);
+        const Ahead behind = join_runs<true>(s, own, mu, (r.starts | r.ends) != 0, (m.starts | m.ends) != 0, sm.sums[turn].s,
+                                             sm.sums[turn].f, sm.sums[turn].b);
+        const Ahead ahead = join_runs<false>(s, own, add, r.starts != 0, m.starts != 0, nullptr, nullptr, space.add);
         __syncwarp();
-        if (lane == 0 && tensor_copies) mbar_arrive(&sm.summed);
+        if (lane == 0) mbar_arrive(&sm.summed);
         named_barrier(4, kLrCompute);
         // the states before each token; with tied inputs less the token's x, as the gradient of g needs them
-        for (int w = 0; w < warp; ++w) {
-            const float2 b = space.add[w][lane];
-            h = m.starts && run_bits<R>(m.start, w) != 0 ? b : apply(sm.sums.f[w][lane], h, b);
-        }
+        float2 h = before_run<false>(first, ahead, sm.sums[turn].f, space.add, m.starts != 0, [&](int w) { return warp_cut<R, false>(m, w); });
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const float2 x = pair_at(xs, i);
@@ -123,22 +122,9 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_backward_kernel(const Li
             was[i] = TIED ? make_float2(h.x - x.x, h.y - x.y) : h;
             h = apply(f[i], h, TIED ? mul2(forgotten(f[i]), x) : x);
         }
-        __syncwarp();
-        if (tensor_copies) {
-            if (lane == 0) mbar_arrive(&sm.read);
-        } else {
-            meet(2);   // before the ninth warp may come to its next ticket
-            if (lane == 0) mbar_arrive(&sm.summed);
-            if (sm.ticket[turn ^ 1] < all) load(sm.ticket[turn ^ 1], turn ^ 1);
-        }
-
         meet(3);
-        mu = sm.before[lane];
-        for (int w = kLrWarps - 1; w > warp; --w) {
-            const float2 b = sm.sums.b[w][lane];
-            const bool cut = (m.starts | m.ends) && (run_bits<R>(m.start, w) | run_bits<R>(m.end, w)) != 0;
-            mu = cut ? b : apply(sm.sums.f[w][lane], mu, b);
-        }
+        mu = before_run<true>(sm.before[lr_pair()], behind, sm.sums[turn].f, sm.sums[turn].b, (m.starts | m.ends) != 0,
+                              [&](int w) { return warp_cut<R, true>(m, w); });
         TX *dx = static_cast<TX *>(a.dx) + (long long)(r.first + R - 1) * a.channels + r.ch;
         TG *dg = static_cast<TG *>(a.dg) + (long long)(r.first + R - 1) * a.channels + r.ch;
         if (r.plain) {
@@ -165,26 +151,29 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_backward_kernel(const Li
                     put_pair<TG>(dg, counts ? mul2(mu, was[i]) : both(0.f), r.whole, r.in0, r.in1);
                 }
                 if (r.starts >> i & 1) {
-                    if (a.dh0 != nullptr) put_f32(a.dh0 + m.start_seq[warp * R + i] * a.channels + r.ch, mu, r.in0, r.in1);
+                    if (a.dh0 != nullptr) put_f32(a.dh0 + m.start_seq[lr_run() * R + i] * a.channels + r.ch, mu, r.in0, r.in1);
                     mu = both(0.f);
                 }
                 dx -= a.channels;
                 dg -= a.channels;
             }
         }
-        ticket = sm.ticket[turn ^ 1];
-        named_barrier(4, kLrCompute);   // all have read the sums
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.done);
+        place = next_place;
     }
 }
 
 template <typename TX, typename TG, bool TIED> cudaError_t launch(LinrecArgs a, cudaStream_t s) {
-    constexpr int R = linrec_start_tokens(sizeof(TX)) / kLrWarps;
+    constexpr int R = linrec_start_tokens(sizeof(TX), sizeof(TG)) / kLrRuns;
     typedef BackwardSpace<TX, TG, R> Space;
-    a.tiles = (int)((a.total + kLrWarps * R - 1) / (kLrWarps * R));
+    static_assert(sizeof(Space) <= 113 * 1024, "two CTAs an SM");
+    const cudaError_t e0 = linrec_prepare(a, kLrRuns * R, s);
+    if (e0 != cudaSuccess) return e0;
     LinrecMaps maps{};
-    a.tensor_copies = linrec_tensor_map(maps.g, a.g, a, sizeof(TG), std::is_same<TG, __half>::value, kLrWarps * R) &&
-                      linrec_tensor_map(maps.x, a.x, a, sizeof(TX), std::is_same<TX, __half>::value, kLrWarps * R) &&
-                      linrec_tensor_map(maps.d, a.dout, a, sizeof(TX), std::is_same<TX, __half>::value, kLrWarps * R);
+    a.tensor_copies = linrec_tensor_map(maps.g, a.g, a, sizeof(TG), std::is_same<TG, __half>::value, kLrRuns, R) &&
+                      linrec_tensor_map(maps.x, a.x, a, sizeof(TX), std::is_same<TX, __half>::value, kLrRuns, R) &&
+                      linrec_tensor_map(maps.d, a.dout, a, sizeof(TX), std::is_same<TX, __half>::value, kLrRuns, R);
     const auto kernel = linrec_backward_kernel<TX, TG, TIED, R>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Space));
     if (e != cudaSuccess) return e;

@@ -6,8 +6,10 @@
 //     backward, from the last token:  lam_t = dh_t + mu_{t+1},  mu_t = a_t lam_t,
 //     dx_t = w_t lam_t,  dg_t = mu_t (h_{t-1} - [tied] x_t),  dh0 = mu_1
 //
-// A tile is 8 R tokens by 64 channels.  Warp w of eight has tokens R w ... R w + R - 1 of it (a run), a lane two neighbouring
-// channels.  Sequences are cut out of the flat index over all tokens: where one starts the state is set, not multiplied, so
+// A tile is 512 tokens (256 where inputs are wide) by 16 channels, in 32 runs of R tokens.  A lane has a run and two neighbouring
+// channels; a warp of eight has four runs, one after the other, of all 16 channels.  Tiles are long and narrow so that of the
+// tiles under way at a time few are of one chain: with 64 channels by 128 tokens, four times as many waited for
+// one another.  Sequences are cut out of the flat index over all tokens: where one starts the state is set, not multiplied, so
 // short sequences fill tiles as long ones do.
 //
 // Each tile tells the ones behind it its map h -> a h + b, and the state behind it once it knows that.  A tile that
@@ -17,7 +19,7 @@
 // composed in the order of arrival would not.
 //
 // CTAs stay and take tiles by ticket, in the order of the recurrence.  Eight warps compute; a ninth takes tickets, has
-// tiles loaded, finds starts and ends, and looks back, which it begins while the tile's first pass still runs.
+// tiles loaded one ahead, finds starts and ends, and looks back, which it begins while the tile's first pass still runs.
 //
 // Factors.  exp(g) of a slow decay rounds to 2^-24 of 1, and what a state forgets in a token, 1 - exp(g), may be not much
 // more than that: an error to one side adds up over the state's whole memory (a thousand tokens and more).  So a factor
@@ -37,9 +39,15 @@ namespace ps {
 
 namespace {
 
-constexpr int kLrWarps = 8;
+constexpr int kLrWarps = kLinrecWarps;
 constexpr int kLrCompute = 32 * kLrWarps, kLrThreads = kLrCompute + 32;
-constexpr int kLrWide = 64;   // channels of a tile
+constexpr int kLrWide = kLinrecWide, kLrPairs = kLrWide / 2;   // channels of a tile, and pairs of them
+constexpr int kLrGroups = 32 / kLrPairs;                       // runs of a warp
+constexpr int kLrRuns = kLrWarps * kLrGroups;                  // of a tile
+
+__device__ __forceinline__ int lr_pair() { return threadIdx.x % kLrPairs; }
+__device__ __forceinline__ int lr_group() { return threadIdx.x % 32 / kLrPairs; }
+__device__ __forceinline__ int lr_run() { return threadIdx.x / kLrPairs; }   // of a compute warp's lane
 
 // ---- pairs of f32 ------------------------------------------------------------------------
 
@@ -139,9 +147,13 @@ template <> struct Pair<__half> {
         return *reinterpret_cast<const uint32_t *>(&y);
     }
 };
-// A lane's two channels of a row of a tile in shared memory.
-template <typename T> __device__ __forceinline__ float2 pair_at(const T *tile, int row) {
-    return Pair<T>::get(reinterpret_cast<const typename Pair<T>::type *>(tile)[row * (kLrWide / 2) + (threadIdx.x & 31)]);
+// Token i of a lane's run in a tile in shared memory: there the runs' first tokens come first, then their second ones, and so
+// on, so that a warp reads neighbouring words.
+template <typename T> __device__ __forceinline__ float2 pair_at(const T *tile, int i) {
+    return Pair<T>::get(reinterpret_cast<const typename Pair<T>::type *>(tile)[i * kLrCompute + threadIdx.x]);
+}
+template <typename T> __device__ __forceinline__ void set_pair_at(T *tile, int i, float2 x) {
+    reinterpret_cast<typename Pair<T>::type *>(tile)[i * kLrCompute + threadIdx.x] = Pair<T>::put(x);
 }
 // A lane's two channels of a row in global memory; `whole`: both are there and the row starts on a multiple of two.
 template <typename T> __device__ __forceinline__ void put_pair(T *p, float2 x, bool whole, bool in0, bool in1) {
@@ -168,11 +180,11 @@ template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, co
 }
 __device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Rows n0 ... n0 + ROWS - 1 of a tensor, channels c0 ... c0 + 63, to a tile in shared memory, in pieces of N numbers, by the
-// threads of the compute warps; 0 past the ends.
-template <typename T, int ROWS, int N, int UNROLL>
+// The tokens from n0 on of a tensor, channels from c0 on, to a tile in shared memory, in pieces of N numbers, by the threads of
+// the compute warps; 0 past the ends.
+template <typename T, int R, int N, int UNROLL>
 __device__ __forceinline__ void load_pieces(T *tile, const LinrecTensor &x, const LinrecArgs &a, uint32_t n0, long long c0) {
-    constexpr int PER = kLrWide / N, STEP = kLrCompute / PER;   // pieces of a row, rows at a time
+    constexpr int PER = kLrWide / N, STEP = kLrCompute / PER, ROWS = kLrRuns * R;   // pieces of a row, rows at a time
     const int col = threadIdx.x % PER * N, row0 = threadIdx.x / PER;
     const bool in = c0 + col < a.channels;
     const T *base = static_cast<const T *>(x.p), *src = base + c0 + col;
@@ -185,51 +197,48 @@ __device__ __forceinline__ void load_pieces(T *tile, const LinrecTensor &x, cons
         src += seq * x.seq + (long long)t * x.tok;
     }
     const long long step = STEP * x.tok;
-    T *dst = tile + row0 * kLrWide + col;
 #pragma unroll(UNROLL)
     for (int row = row0; row < ROWS; row += STEP) {
         const bool there = in && n < (uint32_t)a.total;
+        T *dst = tile + (row % R * kLrRuns + row / R) * kLrWide + col;
         if constexpr (N * sizeof(T) == 2) *dst = there ? *src : from_f32<T>(0.f);
         else copy_async<N * sizeof(T)>(smem_u32(dst), there ? src : base, there);
         n += STEP;
         src += step;
-        dst += STEP * kLrWide;
         if (!x.flat) {
             for (t += STEP; t >= (uint32_t)a.tokens; t -= (uint32_t)a.tokens) src += x.seq - (long long)a.tokens * x.tok;
         }
     }
 }
-template <typename T, int ROWS>
+template <typename T, int R>
 __device__ __forceinline__ void load_tile(T *tile, const LinrecTensor &x, const LinrecArgs &a, uint32_t n0, long long c0) {
-    if (x.piece == 16) {
-        if (x.flat) {
-            LinrecTensor y = x;
-            y.flat = true;
-            load_pieces<T, ROWS, 16 / sizeof(T), 8>(tile, y, a, n0, c0);
-        } else {
-            load_pieces<T, ROWS, 16 / sizeof(T), 1>(tile, x, a, n0, c0);
-        }
-    } else if (sizeof(T) == 4 || x.piece == 4) {
-        load_pieces<T, ROWS, 4 / sizeof(T), 1>(tile, x, a, n0, c0);
-    } else {
-        load_pieces<T, ROWS, 1, 1>(tile, x, a, n0, c0);
-    }
+    if (x.piece == 16) load_pieces<T, R, 16 / sizeof(T), 1>(tile, x, a, n0, c0);
+    else if (sizeof(T) == 4 || x.piece == 4) load_pieces<T, R, 4 / sizeof(T), 2>(tile, x, a, n0, c0);
+    else load_pieces<T, R, 1, 4>(tile, x, a, n0, c0);
 }
 
-// Inputs whose rows are evenly spaced, on multiples of 16 bytes, come by tensor copies of whole tiles, one thread's doing;
+// Inputs whose rows are evenly spaced, on multiples of 16 bytes, come by tensor copies of whole tiles, one thread's doing
+// (their maps count channels, runs and tokens of a run; a last run that is not whole is left out, and read by its own lanes);
 // others in pieces of 16, 4 or 2 bytes by all compute warps.
 struct LinrecMaps {
     CUtensorMap g, x, d;
 };
-__device__ __forceinline__ void tile_copy(void *tile, const CUtensorMap &map, uint32_t n0, int c0, uint64_t *bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(smem_u32(tile)), "l"(&map), "r"(c0), "r"((int)n0), "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void tile_copy(void *tile, const CUtensorMap &map, int run, int c0, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(smem_u32(tile)), "l"(&map), "r"(c0), "r"(run), "r"(0), "r"(smem_u32(bar)) : "memory");
+}
+// The last run's tokens, if it is not whole (a lane of the run; it alone reads them).
+template <typename T, int R>
+__device__ __forceinline__ void load_last_run(T *tile, const LinrecTensor &x, const LinrecArgs &a, uint32_t first, long long ch) {
+    const T *p = static_cast<const T *>(x.p) + first * x.tok + ch;
+    for (int i = 0; first + i < (uint32_t)a.total; ++i, p += x.tok)
+        set_pair_at(tile, i, make_float2(ch < a.channels ? to_f32<T>(p[0]) : 0.f, ch + 1 < a.channels ? to_f32<T>(p[1]) : 0.f));
 }
 
 // ---- starts and ends -------------------------------------------------------------------
 
 template <int TOKENS> struct Marks {
-    uint32_t start[TOKENS / 32], end[TOKENS / 32];      // bits of tokens that are a sequence's first, its last
+    uint32_t start[TOKENS / 32], end[TOKENS / 32];      // bits of tokens that are a sequence's first, its last (if there is any)
     int32_t start_seq[TOKENS], end_seq[TOKENS];         // whose
     uint32_t lo, held;                                  // tokens lo ... lo + held - 1 are sequences'
     int starts, ends;                                   // whether there is any
@@ -261,21 +270,18 @@ __device__ __forceinline__ void mark_tile(Marks<TOKENS> &m, const LinrecArgs &a,
     if (a.cu == nullptr) {
         const uint32_t tokens = (uint32_t)a.tokens, first = n0 / tokens, t0 = n0 - first * tokens;
         uint32_t any_s = 0, any_e = 0;
-        const bool inside = t0 > 0 && t0 + TOKENS < tokens;   // of one sequence
-        for (int i = 0; i < TOKENS / 32; ++i) {
-            uint32_t s = 0, e = 0;
-            if (!inside) {
+        if (t0 == 0 || t0 + TOKENS >= tokens) {   // not inside of one sequence
+            for (int i = 0; i < TOKENS / 32; ++i) {
                 const uint32_t n = n0 + 32 * i + lane, seq = n / tokens, t = n - seq * tokens;
                 const bool in = n < (uint32_t)a.total;
-                s = __ballot_sync(0xffffffffu, in && t == 0);
-                e = __ballot_sync(0xffffffffu, in && t == tokens - 1);
+                const uint32_t s = __ballot_sync(0xffffffffu, in && t == 0), e = __ballot_sync(0xffffffffu, in && t == tokens - 1);
                 m.start_seq[32 * i + lane] = m.end_seq[32 * i + lane] = (int32_t)seq;
-            }
-            any_s |= s;
-            any_e |= e;
-            if (lane == 0) {
-                m.start[i] = s;
-                m.end[i] = e;
+                any_s |= s;
+                any_e |= e;
+                if (lane == 0) {
+                    m.start[i] = s;
+                    m.end[i] = e;
+                }
             }
         }
         if (lane == 0) {
@@ -310,7 +316,7 @@ __device__ __forceinline__ void mark_tile(Marks<TOKENS> &m, const LinrecArgs &a,
                     any_e = true;
                 }
             } else if (to != nullptr && s >= n0 && (s < n1 || last_tile)) {
-                for (long long c = c0; c < min(c0 + kLrWide, a.channels); ++c)
+                for (long long c = c0; c < min(c0 + (long long)kLrWide, a.channels); ++c)
                     to[i * a.channels + c] = from ? from[i * a.channels + c] : 0.f;
             }
         }
@@ -327,35 +333,48 @@ __device__ __forceinline__ void mark_tile(Marks<TOKENS> &m, const LinrecArgs &a,
     }
     __syncwarp();
 }
-// The bits of the tokens of warp w's run.
-template <int R, int N> __device__ __forceinline__ uint32_t run_bits(const uint32_t (&bits)[N], int w) {
-    static_assert(N * 32 == kLrWarps * R, "a bit a token");
-    return bits[w * R / 32] >> (w * R % 32) & (R == 32 ? 0xffffffffu : (1u << (R % 32)) - 1);
+// The bits of a run's tokens.
+template <int R, int N> __device__ __forceinline__ uint32_t run_bits(const uint32_t (&bits)[N], int run) {
+    static_assert(N * 32 == kLrRuns * R && 32 % R == 0, "a bit a token");
+    return bits[run * R / 32] >> (run * R % 32) & (R == 32 ? 0xffffffffu : (1u << (R % 32)) - 1);
 }
 
-// A warp's run of the tile of a ticket, and a lane's channels.
+// Whether one of warp w's runs forgets what came before.
+template <int R, bool BACKWARD, int TOKENS> __device__ __forceinline__ bool warp_cut(const Marks<TOKENS> &m, int w) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int g = 0; g < kLrGroups; ++g) {
+        x |= m.starts ? run_bits<R>(m.start, w * kLrGroups + g) : 0u;
+        if (BACKWARD) x |= m.ends ? run_bits<R>(m.end, w * kLrGroups + g) : 0u;
+    }
+    return x != 0;
+}
+// Where a tile is: the tile of tokens (-1: there is none) and the block of channels.
+struct Place {
+    int tile, block;
+};
+// A lane's run of a tile, and its channels.
 template <int R> struct Run {
     uint32_t first, starts, ends;
     long long ch;
-    bool in0, in1, whole;   // whether the lane's channels are there; whether outputs' pairs are, and on multiples of two numbers
-    bool plain;             // no start or end, all tokens held, all pairs whole
-    int warp;
-    template <int TOKENS>
-    __device__ __forceinline__ Run(const LinrecArgs &a, const Marks<TOKENS> &m, unsigned ticket, int k, int warp_) : warp(warp_) {
-        first = (uint32_t)k * TOKENS + warp * R;
-        ch = (long long)(ticket % (unsigned)a.blocks) * kLrWide + 2 * (threadIdx.x & 31);
+    bool in0, in1, whole;   // whether the channels are there; whether outputs' pairs are, and on multiples of two numbers
+    bool marked, plain;     // of any run of the warp: has a start or end; neither, all tokens held and all pairs whole
+    template <int TOKENS> __device__ __forceinline__ Run(const LinrecArgs &a, const Marks<TOKENS> &m, const Place &at) {
+        first = (uint32_t)at.tile * TOKENS + lr_run() * R;
+        ch = (long long)at.block * kLrWide + 2 * lr_pair();
         in0 = ch < a.channels;
         in1 = ch + 1 < a.channels;
         whole = in1 && a.pairs;
-        starts = run_bits<R>(m.start, warp);
-        ends = run_bits<R>(m.end, warp);
-        plain = (starts | ends) == 0 && __all_sync(0xffffffffu, whole || !in0) && first - m.lo < m.held && first - m.lo + R <= m.held;
+        starts = m.starts ? run_bits<R>(m.start, lr_run()) : 0u;
+        ends = m.ends ? run_bits<R>(m.end, lr_run()) : 0u;
+        marked = __any_sync(0xffffffffu, (starts | ends) != 0);
+        plain = !marked && __all_sync(0xffffffffu, (whole || !in0) && first - m.lo < m.held && first - m.lo + R <= m.held);
     }
     template <int TOKENS> __device__ __forceinline__ float2 start(const LinrecArgs &a, const Marks<TOKENS> &m, int i) const {
-        return get_f32(a.h0 ? a.h0 + m.start_seq[warp * R + i] * a.channels + ch : nullptr, in0, in1);
+        return get_f32(a.h0 ? a.h0 + m.start_seq[lr_run() * R + i] * a.channels + ch : nullptr, in0, in1);
     }
     template <int TOKENS> __device__ __forceinline__ float2 end(const LinrecArgs &a, const Marks<TOKENS> &m, int i) const {
-        return get_f32(a.dht ? a.dht + m.end_seq[warp * R + i] * a.channels + ch : nullptr, in0, in1);
+        return get_f32(a.dht ? a.dht + m.end_seq[lr_run() * R + i] * a.channels + ch : nullptr, in0, in1);
     }
 };
 
@@ -389,145 +408,244 @@ __device__ __forceinline__ float4 ask(const float4 *p) {
                  : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p) : "memory");
     return x;
 }
-// Of a lane's two channels of the k-th tile of a block of channels.
-__device__ __forceinline__ size_t tile_at(const LinrecArgs &a, int k, int block) {
-    return ((size_t)k * a.blocks + block) * 32 + (threadIdx.x & 31);
+// What the warps' runs come to together.
+struct Sums {
+    float2 s[kLrWarps][kLrPairs], f[kLrWarps][kLrPairs];   // sums of log decays, their factors
+    float2 b[kLrWarps][kLrPairs];                          // what the runs add
+};
+// What a warp's runs before a lane's come to (the state before the run is a h + b of the one before the warp's first), in the
+// direction of the recurrence.  `cut`: whether one of them forgets what came before.
+struct Ahead {
+    float2 f, b;
+    bool cut;
+};
+__device__ __forceinline__ float2 from_group(float2 x, int group) {
+    return make_float2(__shfl_sync(0xffffffffu, x.x, group * kLrPairs + lr_pair()), __shfl_sync(0xffffffffu, x.y, group * kLrPairs + lr_pair()));
+}
+// A warp joins its runs, of which a lane knows its own: the sum of log decays s, its factor f, the addend b, whether it is
+// `cut`; and leaves the whole's in the places [warp][pair] that are given.
+template <bool BACKWARD>
+__device__ __forceinline__ Ahead join_runs(float2 s, float2 f, float2 b, bool cut, bool any, float2 (*sum)[kLrPairs],
+                                           float2 (*factors)[kLrPairs], float2 (*adds)[kLrPairs]) {
+    const int warp = threadIdx.x >> 5, nth = BACKWARD ? kLrGroups - 1 - lr_group() : lr_group();
+    Ahead a{both(0.f), both(0.f), false};
+    float2 as = both(0.f);
+#pragma unroll
+    for (int q = 0; q < kLrGroups - 1; ++q) {
+        const int g = BACKWARD ? kLrGroups - 1 - q : q;
+        const float2 gs = from_group(s, g), gf = from_group(f, g), gb = from_group(b, g);
+        const bool gc = any && __shfl_sync(0xffffffffu, (int)cut, g * kLrPairs);
+        if (q < nth) {
+            a.b = gc ? gb : apply(gf, a.b, gb);
+            a.cut |= gc;
+            as = add2(as, gs);
+            if (kLrGroups == 2) a.f = gf;
+        }
+    }
+    if (kLrGroups > 2) a.f = factor_of_sum(as);
+    if (kLrGroups > 1) {
+        b = cut || nth == 0 ? b : apply(f, a.b, b);
+        s = add2(as, s);
+        f = factor_of_sum(s);
+    }
+    if (nth == kLrGroups - 1) {
+        if (sum != nullptr) sum[warp][lr_pair()] = s;
+        if (factors != nullptr) factors[warp][lr_pair()] = f;
+        adds[warp][lr_pair()] = b;
+    }
+    return a;
+}
+// The state before a lane's run from the one before the tile.  `cut(w)`: whether warp w's runs forget what came before.
+template <bool BACKWARD, typename Cut>
+__device__ __forceinline__ float2 before_run(float2 h, const Ahead &a, const float2 (*factors)[kLrPairs], const float2 (*adds)[kLrPairs],
+                                             bool any, Cut cut) {
+    const int warp = threadIdx.x >> 5, nth = BACKWARD ? kLrGroups - 1 - lr_group() : lr_group();
+    for (int i = 0; i < (BACKWARD ? kLrWarps - 1 - warp : warp); ++i) {
+        const int w = BACKWARD ? kLrWarps - 1 - i : i;
+        const float2 b = adds[w][lr_pair()];
+        h = any && cut(w) ? b : apply(factors[w][lr_pair()], h, b);
+    }
+    return nth == 0 ? h : a.cut ? a.b : apply(a.f, h, a.b);
 }
 
-// What the runs of a tile come to.
-struct Sums {
-    float2 s[kLrWarps][32];   // sums of log decays
-    float2 f[kLrWarps][32];   // their factors
-    float2 b[kLrWarps][32];   // what the run adds
-};
-
 // What a CTA's warps share beside its tiles.
+constexpr int kLrWindow = 8;   // tiles that a round of the look-back reads
+static_assert(kLrWindow <= kLinrecSlack, "a round stays in the workspace");
 template <int R> struct Shared {
-    static constexpr int TOKENS = kLrWarps * R;
-    Sums sums;
-    float2 before[32];           // the state before the tile, in the direction of the recurrence
+    static constexpr int TOKENS = kLrRuns * R;
+    Sums sums[2];
+    float2 before[kLrPairs];     // the state before the tile, in the direction of the recurrence
+    float4 maps[kLrWindow][kLrPairs];
+    float2 states[kLrWindow][kLrPairs];
     Marks<TOKENS> marks[2];
-    unsigned ticket[2];
-    uint64_t landed, summed;     // the tile's inputs are there; all runs are summed
-    uint64_t read;               // and g and x no longer needed (backward; forward they are not when runs are summed)
+    Place place[2];
+    uint64_t landed[2];          // a tile's inputs are there
+    uint64_t summed, done;       // all runs are summed; backward: the tile's inputs have been read
 };
-// Barriers by number.  1: marks are set, and pieces of tiles have landed; 2: the next ticket is known (tiles in pieces);
-// 3: the state before the tile is known; 4: among the compute warps.  The ninth warp never waits at 1 to 3.
+// Barriers by number.  1: marks are set, the next tile is known, pieces of tiles have landed; 2: the first tile is known;
+// 3: the state before the tile is known; 4: among the compute warps.  The ninth warp never waits at them.
+// Whether a phase is over, without waiting (try_wait may hold the warp for some time).
+__device__ __forceinline__ bool mbar_over(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void pass_by(int id) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(kLrThreads) : "memory"); }
 __device__ __forceinline__ void meet(int id) { named_barrier(id, kLrThreads); }
 
-// The ninth warp.  `issue(k, block)` has a tile loaded (one lane), where tensor copies do.
+// The ninth warp.  `issue(place, stage)` has a tile loaded (one lane), where tensor copies do.
 //
-// Look-back: `at` is the last tile before this one whose state, h, is known (-1: none yet).  A round reads what eight tiles
-// have told, from at + 1 on, or, with nothing known, further and further back; a state told replaces h, a map is
-// applied to the state before it.  (Lanes go on by themselves: each has its own two channels.)  Rounds begin while the
-// tile's inputs are summed; if the state before it is not known when they are, the tile's map is told at once, for others
-// to pass over it.  The first tile always tells its state.  Waits end after about two seconds, with NaN.
+// Tiles have positions in the order of the recurrence: the tile before position p is at p - 1.  Tickets go up the positions, or,
+// where equal sequences take turns, up each sequence's; a chain starts at position 0, or at its sequence's first.
+//
+// Look-back: `at` is the last position before this tile's whose state, h, is known (-1: none yet).  A round reads what a window of
+// tiles has told, from at + 1 on, or, with nothing known, further and further back in the chain; the last state told
+// replaces h, the maps behind it are applied.  Rounds begin while the tile's inputs are summed; if the state before it is not
+// known when they are, the tile's map is told at once, for others to pass over it.  A chain's first tile always tells its
+// state.  Waits end after about two seconds, with NaN.
 template <int R, bool BACKWARD, typename Issue>
 __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, const float *from, float *to, bool tensor_copies,
                                            Issue issue) {
-    constexpr int TOKENS = Shared<R>::TOKENS, AT_ONCE = 8;
-    const int lane = threadIdx.x & 31;
+    constexpr int TOKENS = Shared<R>::TOKENS, AT_ONCE = kLrWindow / kLrGroups;
+    constexpr uint32_t FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, pair = lr_pair(), group = lr_group();
     const unsigned all = (unsigned)a.tiles * (unsigned)a.blocks;
     const bool chained = a.tiles > 1;
-    unsigned mine = blockIdx.x;
-    if (chained && lane == 0) mine = atomicAdd(a.ticket, 1u) + 1;   // from -1 on
-    unsigned ticket = __shfl_sync(0xffffffffu, mine, 0);
+    const size_t stride = (size_t)a.blocks * kLrPairs;
+    auto place_of = [&](unsigned ticket) {
+        if (ticket >= all) return Place{-1, 0};
+        const unsigned k = ticket / (unsigned)a.blocks;
+        const int p = (int)(a.steps ? k % (unsigned)a.seqs * (unsigned)a.steps + k / (unsigned)a.seqs : k);
+        return Place{BACKWARD ? a.tiles - 1 - p : p, (int)(ticket % (unsigned)a.blocks)};
+    };
+    auto take = [&]() { return chained ? atomicAdd(a.ticket, 1u) + 1 : all; };   // from -1 on
+    unsigned ticket = blockIdx.x, next = all;
+    if (chained && lane == 0) ticket = take();
+    Place place = place_of(__shfl_sync(FULL, ticket, 0));
     if (lane == 0) {
-        sm.ticket[0] = ticket;
-        if (tensor_copies && ticket < all) issue(ticket / (unsigned)a.blocks, ticket % (unsigned)a.blocks);
+        sm.place[0] = place;
+        if (tensor_copies && place.tile >= 0) issue(place, 0);
+        next = take();
     }
     __syncwarp();
     pass_by(2);
-    for (int turn = 0; ticket < all; turn ^= 1) {
-        const int k = (int)(ticket / (unsigned)a.blocks), block = (int)(ticket % (unsigned)a.blocks);
-        const int tile = BACKWARD ? a.tiles - 1 - k : k;
+    Place next_place = place_of(__shfl_sync(FULL, next, 0));
+    for (int turn = 0, first = 1; place.tile >= 0; turn ^= 1, first = 0) {
         Marks<TOKENS> &m = sm.marks[turn];
-        mark_tile(m, a, (uint32_t)tile * TOKENS, tile == a.tiles - 1, from, to, (long long)block * kLrWide);
+        const Sums &sums = sm.sums[turn];
+        bool issued = !tensor_copies || next_place.tile < 0;
+        if (!issued && (!BACKWARD || first)) {   // forward, the runs of the tile that had the place before are summed
+            issued = true;
+            if (lane == 0) issue(next_place, turn ^ 1);
+        }
+        mark_tile(m, a, (uint32_t)place.tile * TOKENS, place.tile == a.tiles - 1, from, to, (long long)place.block * kLrWide);
+        if (lane == 0) sm.place[turn ^ 1] = next_place;
+        __syncwarp();
         pass_by(1);
-        unsigned next = all;
-        if (chained && lane == 0) next = atomicAdd(a.ticket, 1u) + 1;
+        if (lane == 0) next = take();
 
+        const int p = BACKWARD ? a.tiles - 1 - place.tile : place.tile;
+        const int chain = a.steps ? p - p % a.steps : 0;
         const bool any = BACKWARD ? (m.starts | m.ends) != 0 : m.starts != 0;   // a run forgets what came before the tile
-        const bool known = k == 0 || any;                                       // so does the state behind it
-        const bool needs = k > 0 && (BACKWARD ? m.end[TOKENS / 32 - 1] >> 31 == 0 : (m.start[0] & 1) == 0);
-        const size_t stride = (size_t)a.blocks * 32, place = (size_t)block * 32 + lane;
-        float2 *const states = a.state + place;
-        float4 *const maps = a.map + place;
+        const bool known = p == 0 || any;                                       // so does the state behind it
+        const bool needs = p > 0 && (BACKWARD ? !m.ends || m.end[TOKENS / 32 - 1] >> 31 == 0 : !m.starts || (m.start[0] & 1) == 0);
+        float2 *const states = a.state + (size_t)place.block * kLrPairs + pair;
+        float4 *const maps = a.map + (size_t)place.block * kLrPairs + pair;
         float2 h = both(0.f), f = both(0.f), b = both(0.f);
-        int at = needs ? -1 : k - 1, back = k - AT_ONCE;
-        bool have_next = false, have_sums = false, issued = !tensor_copies;
+        int at = needs ? -1 : p - 1, back = max(p - kLrWindow, chain);
+        bool have_sums = false, passed = false;
         uint32_t polls = 0;
         unsigned long long t0 = 0;
         while (true) {
-            const bool found = __all_sync(0xffffffffu, at == k - 1);
-            if (have_next && !have_sums && (found ? mbar_wait(&sm.summed, turn) || true : mbar_try_wait(&sm.summed, turn))) {
-                have_sums = true;
+            const bool found = at == p - 1;
+            bool just = false;
+            if (!have_sums && (found && issued ? mbar_wait_suspend(&sm.summed, turn, 2000) || true : mbar_over(&sm.summed, turn)))
+                have_sums = just = true;
+            if (found && have_sums && !passed) {   // not before all have their sums: some may still wait for the last tile's state
+                passed = true;
+                if (group == 0) sm.before[pair] = h;
+                __syncwarp();
+                pass_by(3);
+            }
+            if (just) {
                 if (chained) {
                     float2 s = both(0.f);
 #pragma unroll 4
                     for (int i = 0; i < kLrWarps; ++i) {
                         const int w = BACKWARD ? kLrWarps - 1 - i : i;
-                        const bool reset = any && (run_bits<R>(m.start, w) | (BACKWARD ? run_bits<R>(m.end, w) : 0u)) != 0;
-                        const float2 bw = sm.sums.b[w][lane];
-                        b = reset ? bw : apply(sm.sums.f[w][lane], b, bw);
-                        s = add2(s, sm.sums.s[w][lane]);
+                        const float2 bw = sums.b[w][pair];
+                        b = any && warp_cut<R, BACKWARD>(m, w) ? bw : apply(sums.f[w][pair], b, bw);
+                        s = add2(s, sums.s[w][pair]);
                     }
                     f = factor_of_sum(s);
-                    if (known) tell(states + k * stride, b);
-                    else if (!found) tell(maps + k * stride, f, b);
+                    if (group == 0) {
+                        if (known) tell(states + p * stride, b);
+                        else if (found) tell(states + p * stride, apply(f, h, b));
+                        else tell(maps + p * stride, f, b);
+                    }
                 }
             }
-            if (have_sums && !issued && (!BACKWARD || (found ? mbar_wait(&sm.read, turn) || true : mbar_try_wait(&sm.read, turn)))) {
+            if (!issued && (passed ? mbar_wait_suspend(&sm.done, turn ^ 1, 2000) || true : mbar_over(&sm.done, turn ^ 1))) {
                 issued = true;
-                if (lane == 0 && next < all) issue(next / (unsigned)a.blocks, next % (unsigned)a.blocks);
+                if (lane == 0) issue(next_place, turn ^ 1);
                 __syncwarp();
             }
-            if (found && have_sums && issued) break;
+            if (passed && issued) break;
             if (!found) {
-                const int j = at >= 0 ? at + 1 : back;
+                const int j = at >= 0 ? at + 1 : back, n = min(p - j, kLrWindow);
                 float2 st[AT_ONCE];
                 float4 mp[AT_ONCE];
 #pragma unroll
-                for (int i = 0; i < AT_ONCE; ++i)
-                    if (j + i >= 0 && j + i < k) {
-                        st[i] = ask(states + (j + i) * stride);
-                        mp[i] = ask(maps + (j + i) * stride);
-                    }
+                for (int i = 0; i < AT_ONCE; ++i) {   // past the tile's own, places are of later tiles, or slack
+                    st[i] = ask(states + (j + i * kLrGroups + group) * stride);
+                    mp[i] = ask(maps + (j + i * kLrGroups + group) * stride);
+                }
+                uint32_t told_state = 0, told_map = 0;   // a bit a tile
 #pragma unroll
-                for (int i = 0; i < AT_ONCE; ++i)
-                    if (j + i >= 0 && j + i < k) {
-                        if (told(st[i])) {
-                            h = st[i];
-                            at = j + i;
-                        } else if (at == j + i - 1 && at >= 0 && told(mp[i])) {
-                            h = apply(make_float2(mp[i].x, mp[i].y), h, make_float2(mp[i].z, mp[i].w));
-                            at = j + i;
-                        }
+                for (int i = 0; i < AT_ONCE; ++i) {
+                    const uint32_t s = ~__ballot_sync(FULL, told(st[i])), q = ~__ballot_sync(FULL, told(mp[i]));
+#pragma unroll
+                    for (int g = 0; g < kLrGroups; ++g) {
+                        constexpr uint32_t LANES = kLrPairs == 32 ? FULL : (1u << (kLrPairs % 32)) - 1;
+                        told_state |= (uint32_t)((s >> (g * kLrPairs) & LANES) == 0) << (i * kLrGroups + g);
+                        told_map |= (uint32_t)((q >> (g * kLrPairs) & LANES) == 0) << (i * kLrGroups + g);
                     }
-                if (at < 0) back = back > 0 ? back - AT_ONCE : k - AT_ONCE;
+                    sm.states[i * kLrGroups + group][pair] = st[i];
+                    sm.maps[i * kLrGroups + group][pair] = mp[i];
+                }
+                __syncwarp();
+                told_state &= FULL >> (32 - n);
+                if (told_state) {
+                    const int last = 31 - __clz(told_state);
+                    h = sm.states[last][pair];
+                    at = j + last;
+                }
+                if (at >= 0) {
+                    for (int i = at + 1 - j; i < n && (told_map >> i & 1); ++i) {
+                        const float4 x = sm.maps[i][pair];
+                        h = apply(make_float2(x.x, x.y), h, make_float2(x.z, x.w));
+                        at = j + i;
+                    }
+                } else {
+                    back = back > chain ? max(back - kLrWindow, chain) : max(p - kLrWindow, chain);
+                }
+                __syncwarp();
                 if (have_sums && ++polls > 4) {
                     if (polls == 5) t0 = global_ns();
-                    const bool late = global_ns() - t0 > kMbarWaitLimitNs;
-                    if (__shfl_sync(0xffffffffu, (int)late, 0)) {
+                    if (__shfl_sync(FULL, (int)(global_ns() - t0 > kMbarWaitLimitNs), 0)) {
                         h = both(__uint_as_float(0x7fffffffu));
-                        at = k - 1;
+                        at = p - 1;
                     }
                 }
-            }
-            if (!have_next) {   // the atomic has had the time of a round
-                next = __shfl_sync(0xffffffffu, next, 0);
-                if (lane == 0) sm.ticket[turn ^ 1] = next;
-                have_next = true;
-                __syncwarp();
-                if (!tensor_copies) pass_by(2);
+                if (have_sums && at == p - 1 && !known && group == 0) tell(states + p * stride, apply(f, h, b));
             }
         }
-        if (chained && !known) tell(states + k * stride, apply(f, h, b));
-        sm.before[lane] = h;
-        __syncwarp();
-        pass_by(3);
-        ticket = next;
+        place = next_place;
+        next_place = place_of(__shfl_sync(FULL, next, 0));
     }
 }
 

@@ -14,56 +14,59 @@ namespace ps {
 namespace {
 
 template <typename TX, typename TG, int R> struct ForwardSpace {
-    alignas(128) TG g[kLrWarps * R * kLrWide];
-    alignas(128) TX x[kLrWarps * R * kLrWide];
+    alignas(128) TG g[2][kLrRuns * R * kLrWide];   // the next tile's are on their way
+    alignas(128) TX x[2][kLrRuns * R * kLrWide];
     Shared<R> shared;
 };
 
 template <typename TX, typename TG, bool TIED, int R>
-__global__ void __launch_bounds__(kLrThreads, 2) linrec_forward_kernel(const LinrecArgs a, const __grid_constant__ LinrecMaps maps) {
+__global__ void __launch_bounds__(kLrThreads, kLinrecCtasPerSm) linrec_forward_kernel(const LinrecArgs a, const __grid_constant__ LinrecMaps maps) {
     typedef ForwardSpace<TX, TG, R> Space;
-    constexpr int TOKENS = kLrWarps * R;
+    constexpr int TOKENS = kLrRuns * R;
     extern __shared__ __align__(128) unsigned char raw[];
     Space &space = *reinterpret_cast<Space *>(raw);
     Shared<R> &sm = space.shared;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned all = (unsigned)a.tiles * (unsigned)a.blocks;
     const bool tensor_copies = a.tensor_copies;
     if (tid == 0) {
-        mbar_init(&sm.landed, 1);
+        mbar_init(&sm.landed[0], 1);
+        mbar_init(&sm.landed[1], 1);
         mbar_init(&sm.summed, kLrWarps);
-        mbar_init(&sm.read, kLrWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
 
     if (warp == kLrWarps) {
-        ninth_warp<R, false>(a, sm, a.h0, a.ht, tensor_copies, [&](unsigned k, unsigned block) {
-            mbar_arrive_expect_tx(&sm.landed, sizeof(space.g) + sizeof(space.x));
-            tile_copy(space.g, maps.g, k * TOKENS, (int)(block * kLrWide), &sm.landed);
-            tile_copy(space.x, maps.x, k * TOKENS, (int)(block * kLrWide), &sm.landed);
+        ninth_warp<R, false>(a, sm, a.h0, a.ht, tensor_copies, [&](const Place &at, int stage) {
+            mbar_arrive_expect_tx(&sm.landed[stage], sizeof(space.g[0]) + sizeof(space.x[0]));
+            tile_copy(space.g[stage], maps.g, at.tile * kLrRuns, at.block * kLrWide, &sm.landed[stage]);
+            tile_copy(space.x[stage], maps.x, at.tile * kLrRuns, at.block * kLrWide, &sm.landed[stage]);
         });
         return;
     }
 
-    auto load = [&](unsigned ticket) {
-        const uint32_t n = ticket / (unsigned)a.blocks * TOKENS;
-        const long long c = (long long)(ticket % (unsigned)a.blocks) * kLrWide;
-        load_tile<TG, TOKENS>(space.g, a.g, a, n, c);
-        load_tile<TX, TOKENS>(space.x, a.x, a, n, c);
+    auto load = [&](const Place &at, int stage) {
+        load_tile<TG, R>(space.g[stage], a.g, a, (uint32_t)at.tile * TOKENS, (long long)at.block * kLrWide);
+        load_tile<TX, R>(space.x[stage], a.x, a, (uint32_t)at.tile * TOKENS, (long long)at.block * kLrWide);
     };
     meet(2);
-    unsigned ticket = sm.ticket[0];
-    if (!tensor_copies && ticket < all) load(ticket);
-    for (int turn = 0; ticket < all; turn ^= 1) {
+    Place place = sm.place[0];
+    if (!tensor_copies && place.tile >= 0) load(place, 0);
+    for (int turn = 0, phase = 0; place.tile >= 0; phase ^= turn, turn ^= 1) {
         const Marks<TOKENS> &m = sm.marks[turn];
         bool whole_tile = true;
-        if (tensor_copies) whole_tile = mbar_wait(&sm.landed, turn);
+        if (tensor_copies) whole_tile = mbar_wait(&sm.landed[turn], phase);
         else copies_landed();
         meet(1);
-        const Run<R> r(a, m, ticket, (int)(ticket / (unsigned)a.blocks), warp);
-        const TX *xs = space.x + warp * R * kLrWide;
-        const TG *gs = space.g + warp * R * kLrWide;
+        const Place next_place = sm.place[turn ^ 1];
+        if (!tensor_copies && next_place.tile >= 0) load(next_place, turn ^ 1);
+        const Run<R> r(a, m, place);
+        TX *xs = space.x[turn];
+        TG *gs = space.g[turn];
+        if (tensor_copies && r.first < (uint32_t)a.total && r.first + R > (uint32_t)a.total) {
+            load_last_run<TG, R>(gs, a.g, a, r.first, r.ch);
+            load_last_run<TX, R>(xs, a.x, a, r.first, r.ch);
+        }
         float2 hs[R], ps[R], h = both(0.f), p = both(1.f), s = both(whole_tile ? 0.f : __uint_as_float(0x7fffffffu));
         auto token = [&](int i) {
             const float2 g = pair_at(gs, i), x = pair_at(xs, i), f = factor(g);
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_forward_kernel(const Lin
             hs[i] = h;
             ps[i] = p;
         };
-        if (r.starts == 0) {
+        if (!r.marked) {
 #pragma unroll
             for (int i = 0; i < R; ++i) token(i);
         } else {
@@ -88,21 +91,14 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_forward_kernel(const Lin
                 token(i);
             }
         }
-        sm.sums.s[warp][lane] = s;
-        sm.sums.f[warp][lane] = factor_of_sum(s);
-        sm.sums.b[warp][lane] = h;
+        const Ahead ahead = join_runs<false>(s, factor_of_sum(s), h, r.starts != 0, m.starts != 0, sm.sums[turn].s, sm.sums[turn].f,
+                                             sm.sums[turn].b);
         __syncwarp();
-        if (!tensor_copies) meet(2);   // before the ninth warp may come to its next ticket
         if (lane == 0) mbar_arrive(&sm.summed);
-        if (!tensor_copies && sm.ticket[turn ^ 1] < all) load(sm.ticket[turn ^ 1]);
-
         meet(3);
-        float2 H = sm.before[lane];
-        for (int w = 0; w < warp; ++w) {
-            const float2 b = sm.sums.b[w][lane];
-            H = m.starts && run_bits<R>(m.start, w) != 0 ? b : apply(sm.sums.f[w][lane], H, b);
-        }
-        if (a.start != nullptr && warp * R % a.start_tokens == 0 && r.first < (uint32_t)a.total)
+        float2 H = before_run<false>(sm.before[lr_pair()], ahead, sm.sums[turn].f, sm.sums[turn].b, m.starts != 0,
+                                     [&](int w) { return warp_cut<R, false>(m, w); });
+        if (a.start != nullptr && r.first % a.start_tokens == 0 && r.first < (uint32_t)a.total)
             put_f32(a.start + r.first / a.start_tokens * a.channels + r.ch, H, r.in0, r.in1);
         TX *out = static_cast<TX *>(a.h) + (long long)r.first * a.channels + r.ch;
         if (r.plain) {
@@ -118,22 +114,24 @@ __global__ void __launch_bounds__(kLrThreads, 2) linrec_forward_kernel(const Lin
                 const float2 y = fma2(ps[i], H, hs[i]);
                 if (r.first + i - m.lo < m.held) put_pair<TX>(out, y, r.whole, r.in0, r.in1);
                 if ((r.ends >> i & 1) && a.ht != nullptr)
-                    put_f32(a.ht + m.end_seq[warp * R + i] * a.channels + r.ch, y, r.in0, r.in1);
+                    put_f32(a.ht + m.end_seq[lr_run() * R + i] * a.channels + r.ch, y, r.in0, r.in1);
                 out += a.channels;
             }
         }
-        ticket = sm.ticket[turn ^ 1];
-        named_barrier(4, kLrCompute);   // all have read the sums
+        place = next_place;
     }
 }
 
 template <typename TX, typename TG, bool TIED> cudaError_t launch(LinrecArgs a, cudaStream_t s) {
-    constexpr int R = 16;
+    // runs of 8 tokens where 16 of them, twice, leave no room for a second CTA
+    constexpr int R = sizeof(TX) + sizeof(TG) <= 6 ? 16 : 8;
     typedef ForwardSpace<TX, TG, R> Space;
-    a.tiles = (int)((a.total + kLrWarps * R - 1) / (kLrWarps * R));
+    static_assert(sizeof(Space) <= 113 * 1024, "two CTAs an SM");
+    const cudaError_t e0 = linrec_prepare(a, kLrRuns * R, s);
+    if (e0 != cudaSuccess) return e0;
     LinrecMaps maps{};
-    a.tensor_copies = linrec_tensor_map(maps.g, a.g, a, sizeof(TG), std::is_same<TG, __half>::value, kLrWarps * R) &&
-                      linrec_tensor_map(maps.x, a.x, a, sizeof(TX), std::is_same<TX, __half>::value, kLrWarps * R);
+    a.tensor_copies = linrec_tensor_map(maps.g, a.g, a, sizeof(TG), std::is_same<TG, __half>::value, kLrRuns, R) &&
+                      linrec_tensor_map(maps.x, a.x, a, sizeof(TX), std::is_same<TX, __half>::value, kLrRuns, R);
     const auto kernel = linrec_forward_kernel<TX, TG, TIED, R>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Space));
     if (e != cudaSuccess) return e;

@@ -12,10 +12,20 @@
 
 namespace ps {
 
-constexpr int kLinrecTile = 64;       // tokens of the smallest tile
-constexpr int kLinrecCtas = 152 * 2;  // two CTAs stay on each SM
+#ifndef W_
+#define W_ 32
+#endif
+constexpr int kLinrecWide = W_;       // channels of a tile
+#ifndef NW_
+#define NW_ 8
+#endif
+constexpr int kLinrecWarps = NW_;     // warps of a CTA that compute
+constexpr int kLinrecCtasPerSm = 16 / NW_, kLinrecCtas = 152 * kLinrecCtasPerSm;   // CTAs that stay on an SM, and on all
+constexpr int kLinrecTile = 512 * kLinrecWarps / kLinrecWide;   // tokens of the smallest tile
 // How many tokens are between the states that training keeps: the backward pass's tile.
-constexpr int linrec_start_tokens(size_t type_bytes) { return type_bytes == 4 ? 64 : 128; }
+constexpr int linrec_start_tokens(size_t type_bytes, size_t gate_bytes) {
+    return kLinrecTile * (2 * type_bytes + gate_bytes > 6 ? 1 : 2);
+}
 
 struct LinrecTensor {                 // element strides; channels are contiguous
     const void *p;
@@ -24,8 +34,7 @@ struct LinrecTensor {                 // element strides; channels are contiguou
     int piece;                        // rows start on multiples of so many bytes, and hold a multiple of them: 16, 4 or 2
 };
 
-// Workspace.  A ticket counter and what tiles tell one another, for each (tile of tokens, block of 64 channels, lane of two
-// channels):
+// Workspace.  A ticket counter and what tiles tell one another, for each (tile of tokens, block of 16 channels, pair of channels):
 //   map    the tile's factors, encoded as in linrec_common.cuh, and what it adds
 //   state  the state (backward: the state's gradient) behind the tile
 // (set by each call to 0xff bytes, which stands for nothing told yet), and in training `start`, the state before each tile
@@ -35,6 +44,7 @@ struct LinrecArgs {
     const int32_t *cu;
     long long channels;
     int tiles, blocks;                // tiles of tokens (set by the launchers), blocks of channels
+    int steps;                        // tiles of a sequence where equal sequences take turns (set by the launchers), else 0
     int start_tokens;
     bool tensor_copies;               // inputs come by tensor copies (set by the launchers)
     bool pairs;                       // outputs' rows start on multiples of two numbers
@@ -47,6 +57,21 @@ struct LinrecArgs {
     float2 *state;
     float *start;                     // nullptr outside of training
 };
+constexpr int kLinrecSlack = 16;      // tiles' places behind the last one that a look-back's round may read
+// Equal sequences of whole tiles take turns, so that the tiles under way at a time are of many chains and few wait for one another.
+inline int linrec_steps(const LinrecArgs &a, int tokens) {
+    return a.cu == nullptr && a.seqs > 1 && a.tokens % tokens == 0 ? (int)(a.tokens / tokens) : 0;
+}
+// Tiles of `tokens`: how many, in which order, and where they tell one another what; sets that to nothing told.
+inline cudaError_t linrec_prepare(LinrecArgs &a, int tokens, cudaStream_t s) {
+    a.tiles = (int)((a.total + tokens - 1) / tokens);
+    a.steps = linrec_steps(a, tokens);
+    if (a.tiles < 2) return cudaSuccess;
+    const size_t places = ((size_t)a.tiles + kLinrecSlack) * (size_t)a.blocks * (kLinrecWide / 2);
+    a.map = reinterpret_cast<float4 *>(a.ticket + 64);
+    a.state = reinterpret_cast<float2 *>(a.map + places);
+    return cudaMemsetAsync(a.ticket, 0xff, 256 + places * 24, s);
+}
 inline unsigned linrec_grid(const LinrecArgs &a) {
     const long long all = (long long)a.tiles * a.blocks;
     return (unsigned)(a.tiles == 1 || all < kLinrecCtas ? all : kLinrecCtas);
@@ -61,9 +86,9 @@ struct LinrecStepArgs {
     void *h;
 };
 
-// Describes tiles of `tokens` by 64 channels of an input for tensor copies; false where its rows are not evenly spaced on
-// multiples of 16 bytes, or the driver declines.
-bool linrec_tensor_map(CUtensorMap &map, const LinrecTensor &x, const LinrecArgs &a, size_t bytes, bool f16, int tokens);
+// Describes tiles of an input for tensor copies, token by token of `runs` runs of `run` tokens; false where its rows are not
+// evenly spaced on multiples of 16 bytes, no run is whole, or the driver declines.
+bool linrec_tensor_map(CUtensorMap &map, const LinrecTensor &x, const LinrecArgs &a, size_t bytes, bool f16, int runs, int run);
 
 cudaError_t launch_linrec_forward(const LinrecArgs &a, int type, int gate_type, bool tied, cudaStream_t s);
 cudaError_t launch_linrec_backward(const LinrecArgs &a, int type, int gate_type, bool tied, cudaStream_t s);

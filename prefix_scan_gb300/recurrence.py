@@ -92,9 +92,10 @@ def _check_no_graph(fn, tensors):
                          "and linear_recurrence_backward, or call it under torch.no_grad()")
 
 
-def linear_recurrence_workspace_size(x: torch.Tensor, cu_seqlens: torch.Tensor | None = None, *, train: bool = False) -> int:
-    """Bytes of workspace :func:`linear_recurrence` needs for such inputs (``train``: the buffer that
-    :func:`linear_recurrence_forward` leaves for the backward pass)."""
+def linear_recurrence_workspace_size(x: torch.Tensor, cu_seqlens: torch.Tensor | None = None, *, train: bool = False,
+                                     gate_dtype: torch.dtype = torch.float32) -> int:
+    """Bytes of workspace :func:`linear_recurrence` needs for such inputs, log decays of ``gate_dtype`` (``train``: the buffer
+    that :func:`linear_recurrence_forward` leaves for the backward pass)."""
     if x.dtype not in REAL_CODES:
         raise TypeError(f"linear_recurrence_workspace_size supports float32, bfloat16 and float16, not {x.dtype}")
     packed = cu_seqlens is not None
@@ -102,7 +103,8 @@ def linear_recurrence_workspace_size(x: torch.Tensor, cu_seqlens: torch.Tensor |
         raise ValueError("linear_recurrence_workspace_size: x is [sequences, tokens, channels], or [tokens, channels] packed")
     code = REAL_CODES[x.dtype]
     shape = _lib.LINREC_SHAPE.pack(cu_seqlens.numel() - 1 if packed else x.shape[0], x.shape[0] if packed else x.shape[1],
-                                   cu_seqlens.data_ptr() if packed else 0, x.shape[-1], code, code, 0)
+                                   cu_seqlens.data_ptr() if packed else 0, x.shape[-1], code,
+                                   REAL_CODES.get(gate_dtype, -1), 0)
     return int(_lib.load().ps_linrec_workspace_size(shape, int(train)))
 
 

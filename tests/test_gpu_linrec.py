@@ -159,6 +159,34 @@ def strided(t, how):
     return big[:n, ::2]
 
 
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, F32)], ids=str)
+@pytest.mark.parametrize("seqs,tokens,d", [(3, 1024, 40), (5, 512, 16), (2, 4096, 30), (7, 1536, 300)])
+def test_equal_sequences_that_take_turns(types, seqs, tokens, d):
+    # of whole tiles: those of one sequence are not next to one another in the order of work
+    x, g, dh = make(seqs * tokens, d, *types, 35)
+    h0, dht = states(seqs, d, 36)
+    view = lambda t: t.view(seqs, tokens, d).to(DEV)  # noqa: E731
+    for _ in range(3):
+        h, state, saved = api.linear_recurrence_forward(view(x), view(g), tied=True, initial_state=h0.to(DEV), output_final_state=True)
+        dx, dg, dh0 = api.linear_recurrence_backward(saved, view(dh), d_final_state=dht.to(DEV))
+    got = {"h": h.flatten(0, 1), "state": state, "dx": dx.flatten(0, 1), "dg": dg.flatten(0, 1), "dh0": dh0}
+    check_packed(got, x, g, [tokens] * seqs, dh, h0, dht, True)
+
+
+def test_many_chains_under_way_at_once():
+    # more tiles than run at once, of many chains, alone and one call after another: every result the same, and finite
+    x, g, dh = (t.to(DEV).view(8, 2048, 1024) for t in make(8 * 2048, 1024, BF16, BF16, 37))
+    want = None
+    for i in range(30):
+        h, state, saved = api.linear_recurrence_forward(x, g, output_final_state=True)
+        got = (h, state, *api.linear_recurrence_backward(saved, dh)[:2])
+        if i % 3 == 0:
+            torch.cuda.synchronize()
+        want = got if want is None else want
+        for a, b in zip(got, want):
+            assert torch.equal(a, b) and a.isfinite().all()
+
+
 @pytest.mark.parametrize("how", ["projection", "odd", "tokens first", "every other"])
 @pytest.mark.parametrize("types", TYPES, ids=str)
 def test_strides(types, how):

@@ -46,13 +46,13 @@ def test_workspace_size(lib):
     f = lib.ps_linrec_workspace_size
     assert f(shape(seqs=0), 0) == 0 and f(shape(tokens=0), 0) % 256 == 0
     for bad in (dict(channels=0), dict(code=7), dict(gate=F16), dict(seqs=-1), dict(tokens=-1), dict(tokens=1 << 32), dict(cu=FAKE + 2),
-                dict(seqs=1 << 20, tokens=1 << 11), dict(tokens=(1 << 31) - 128, seqs=1), dict(channels=1 << 31),
-                dict(channels=1 << 30, tokens=1 << 14), dict(seqs=1 << 30, tokens=1, channels=1 << 10)):
+                dict(seqs=1 << 20, tokens=1 << 11), dict(tokens=(1 << 31) - 512, seqs=1), dict(channels=1 << 31),
+                dict(channels=1 << 30, tokens=1 << 15), dict(seqs=1 << 30, tokens=1, channels=1 << 10)):
         assert f(shape(**bad), 0) == 0, bad
     for d in (1, 63, 64, 65, 4096):
         for tokens in (1, 128, 129, 4096):
             infer, train = f(shape(seqs=1, tokens=tokens, channels=d), 0), f(shape(seqs=1, tokens=tokens, channels=d), 1)
-            tiles = -(-tokens // 128)
+            tiles = -(-tokens // 512)
             assert infer % 256 == 0 and train % 256 == 0
             assert infer >= 4 * d + (tiles * d * 12 + 256 if tiles > 1 else 0)   # a copy of the states; maps and states of tiles
             assert train >= infer + tiles * d * 4                                # the states before the tiles
