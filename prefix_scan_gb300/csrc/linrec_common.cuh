@@ -86,14 +86,27 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ bool just_below_zero(float g, float bound) { return __float_as_int(g) < __float_as_int(bound); }
 // The factors exp(g) of one token.  Above -1/16 the series up to g^4 / 24 leaves less than 2^-22.9 of the distance; the
 // hardware's 2^x, off by some 2^-22 of 1, serves elsewhere: there a state's memory is at most 16 tokens (and 2^0 is 1).
-__device__ __forceinline__ float2 factor(float2 g) {
-    const float2 y = mul2(g, both(1.44269504088896341f));
-    float2 d = fma2(g, both(1.f / 24.f), both(1.f / 6.f));
-    d = fma2(g, d, both(0.5f));
-    d = fma2(g, d, both(1.f));
-    d = mul2(g, d);
-    return make_float2(just_below_zero(g.x, -0.0625f) ? d.x : exp2_fast(y.x), just_below_zero(g.y, -0.0625f) ? d.y : exp2_fast(y.y));
-}
+// `one`: 1 where the factor is near one, 0 elsewhere.
+struct Token {
+    float2 f, one;
+    __device__ __forceinline__ static Token of(float2 g) {
+        const float2 y = mul2(g, both(1.44269504088896341f));
+        float2 d = fma2(g, both(1.f / 24.f), both(1.f / 6.f));
+        d = fma2(g, d, both(0.5f));
+        d = fma2(g, d, both(1.f));
+        d = mul2(g, d);
+        const bool x = just_below_zero(g.x, -0.0625f), z = just_below_zero(g.y, -0.0625f);
+        return {make_float2(x ? d.x : exp2_fast(y.x), z ? d.y : exp2_fast(y.y)), make_float2(x ? 1.f : 0.f, z ? 1.f : 0.f)};
+    }
+    __device__ __forceinline__ static Token from(float2 f) {
+        return {f, make_float2(near_one(f.x) ? 1.f : 0.f, near_one(f.y) ? 1.f : 0.f)};
+    }
+    __device__ __forceinline__ float2 weigh(float2 x, bool tied) const {   // x, or (1 - a) x
+        return tied ? mul2(make_float2(1.f - one.x - f.x, 1.f - one.y - f.y), x) : x;
+    }
+    __device__ __forceinline__ float2 apply(float2 h, float2 b) const { return fma2(one, h, fma2(f, h, b)); }   // a h + b
+    __device__ __forceinline__ float2 decayed(float2 h) const { return fma2(one, h, mul2(f, h)); }              // a h
+};
 // The factors of many tokens from the sums of their log decays: the same with a series up to s^8 / 8! above -1/2, because
 // errors add up over the factors of a state's memory in runs and tiles.
 __device__ __forceinline__ float2 factor_of_sum(float2 s) {
@@ -113,16 +126,6 @@ __device__ __forceinline__ float2 apply(float2 f, float2 h, float2 b) {
     const float2 t = fma2(f, h, b);
     return add2(t, make_float2(near_one(f.x) ? h.x : 0.f, near_one(f.y) ? h.y : 0.f));
 }
-// a h
-__device__ __forceinline__ float2 decayed(float2 f, float2 h) {
-    const float2 t = mul2(f, h);
-    return add2(t, make_float2(near_one(f.x) ? h.x : 0.f, near_one(f.y) ? h.y : 0.f));
-}
-// 1 - a
-__device__ __forceinline__ float2 forgotten(float2 f) {
-    return make_float2((near_one(f.x) ? 0.f : 1.f) - f.x, (near_one(f.y) ? 0.f : 1.f) - f.y);
-}
-
 // ---- numbers in memory -------------------------------------------------------------------
 
 template <typename T> struct Pair;
@@ -154,6 +157,12 @@ template <typename T> __device__ __forceinline__ float2 pair_at(const T *tile, i
 }
 template <typename T> __device__ __forceinline__ void set_pair_at(T *tile, int i, float2 x) {
     reinterpret_cast<typename Pair<T>::type *>(tile)[i * kLrCompute + threadIdx.x] = Pair<T>::put(x);
+}
+// Log decays of 32 bits give their place to the token's factor once that is known, for the second pass.
+template <typename TG> __device__ __forceinline__ Token token_at(const TG *gs, int i) { return Token::of(pair_at(gs, i)); }
+template <> __device__ __forceinline__ Token token_at<float>(const float *gs, int i) { return Token::from(pair_at(gs, i)); }
+template <typename TG> __device__ __forceinline__ void keep(TG *gs, int i, const Token &t) {
+    if (sizeof(TG) == 4) set_pair_at(gs, i, t.f);
 }
 // A lane's two channels of a row in global memory; `whole`: both are there and the row starts on a multiple of two.
 template <typename T> __device__ __forceinline__ void put_pair(T *p, float2 x, bool whole, bool in0, bool in1) {
@@ -239,7 +248,7 @@ __device__ __forceinline__ void load_last_run(T *tile, const LinrecTensor &x, co
 
 template <int TOKENS> struct Marks {
     uint32_t start[TOKENS / 32], end[TOKENS / 32];      // bits of tokens that are a sequence's first, its last (if there is any)
-    int32_t start_seq[TOKENS], end_seq[TOKENS];         // whose
+    int32_t seq[TOKENS];                                // whose they are
     uint32_t lo, held;                                  // tokens lo ... lo + held - 1 are sequences'
     int starts, ends;                                   // whether there is any
 };
@@ -275,7 +284,7 @@ __device__ __forceinline__ void mark_tile(Marks<TOKENS> &m, const LinrecArgs &a,
                 const uint32_t n = n0 + 32 * i + lane, seq = n / tokens, t = n - seq * tokens;
                 const bool in = n < (uint32_t)a.total;
                 const uint32_t s = __ballot_sync(0xffffffffu, in && t == 0), e = __ballot_sync(0xffffffffu, in && t == tokens - 1);
-                m.start_seq[32 * i + lane] = m.end_seq[32 * i + lane] = (int32_t)seq;
+                m.seq[32 * i + lane] = (int32_t)seq;
                 any_s |= s;
                 any_e |= e;
                 if (lane == 0) {
@@ -307,12 +316,12 @@ __device__ __forceinline__ void mark_tile(Marks<TOKENS> &m, const LinrecArgs &a,
             if (e > s) {
                 if (s >= n0 && s < n1) {
                     atomicOr(&m.start[(s - n0) / 32], 1u << ((s - n0) & 31));
-                    m.start_seq[s - n0] = (int32_t)i;
+                    m.seq[s - n0] = (int32_t)i;
                     any_s = true;
                 }
                 if (e > n0 && e <= n1) {
                     atomicOr(&m.end[(e - 1 - n0) / 32], 1u << ((e - 1 - n0) & 31));
-                    m.end_seq[e - 1 - n0] = (int32_t)i;
+                    m.seq[e - 1 - n0] = (int32_t)i;
                     any_e = true;
                 }
             } else if (to != nullptr && s >= n0 && (s < n1 || last_tile)) {
@@ -371,10 +380,10 @@ template <int R> struct Run {
         plain = !marked && __all_sync(0xffffffffu, (whole || !in0) && first - m.lo < m.held && first - m.lo + R <= m.held);
     }
     template <int TOKENS> __device__ __forceinline__ float2 start(const LinrecArgs &a, const Marks<TOKENS> &m, int i) const {
-        return get_f32(a.h0 ? a.h0 + m.start_seq[lr_run() * R + i] * a.channels + ch : nullptr, in0, in1);
+        return get_f32(a.h0 ? a.h0 + m.seq[lr_run() * R + i] * a.channels + ch : nullptr, in0, in1);
     }
     template <int TOKENS> __device__ __forceinline__ float2 end(const LinrecArgs &a, const Marks<TOKENS> &m, int i) const {
-        return get_f32(a.dht ? a.dht + m.end_seq[lr_run() * R + i] * a.channels + ch : nullptr, in0, in1);
+        return get_f32(a.dht ? a.dht + m.seq[lr_run() * R + i] * a.channels + ch : nullptr, in0, in1);
     }
 };
 
@@ -473,14 +482,13 @@ constexpr int kLrWindow = 8;   // tiles that a round of the look-back reads
 static_assert(kLrWindow <= kLinrecSlack, "a round stays in the workspace");
 template <int R> struct Shared {
     static constexpr int TOKENS = kLrRuns * R;
-    Sums sums[2];
+    Sums sums;
     float2 before[kLrPairs];     // the state before the tile, in the direction of the recurrence
     float4 maps[kLrWindow][kLrPairs];
     float2 states[kLrWindow][kLrPairs];
     Marks<TOKENS> marks[2];
     Place place[2];
-    uint64_t landed[2];          // a tile's inputs are there
-    uint64_t summed, done;       // all runs are summed; backward: the tile's inputs have been read
+    uint64_t landed, summed, done;   // the tile's inputs are there; all runs are summed; the inputs are no longer needed
 };
 // Barriers by number.  1: marks are set, the next tile is known, pieces of tiles have landed; 2: the first tile is known;
 // 3: the state before the tile is known; 4: among the compute warps.  The ninth warp never waits at them.
@@ -497,7 +505,7 @@ __device__ __forceinline__ bool mbar_over(uint64_t *bar, uint32_t parity) {
 __device__ __forceinline__ void pass_by(int id) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(kLrThreads) : "memory"); }
 __device__ __forceinline__ void meet(int id) { named_barrier(id, kLrThreads); }
 
-// The ninth warp.  `issue(place, stage)` has a tile loaded (one lane), where tensor copies do.
+// The ninth warp.  `issue(place)` has a tile loaded (one lane), where tensor copies do.
 //
 // Tiles have positions in the order of the recurrence: the tile before position p is at p - 1.  Tickets go up the positions, or,
 // where equal sequences take turns, up each sequence's; a chain starts at position 0, or at its sequence's first.
@@ -528,24 +536,24 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
     Place place = place_of(__shfl_sync(FULL, ticket, 0));
     if (lane == 0) {
         sm.place[0] = place;
-        if (tensor_copies && place.tile >= 0) issue(place, 0);
+        if (tensor_copies && place.tile >= 0) issue(place);
         next = take();
     }
     __syncwarp();
     pass_by(2);
-    Place next_place = place_of(__shfl_sync(FULL, next, 0));
     for (int turn = 0, first = 1; place.tile >= 0; turn ^= 1, first = 0) {
         Marks<TOKENS> &m = sm.marks[turn];
-        const Sums &sums = sm.sums[turn];
-        bool issued = !tensor_copies || next_place.tile < 0;
-        if (!issued && (!BACKWARD || first)) {   // forward, the runs of the tile that had the place before are summed
-            issued = true;
-            if (lane == 0) issue(next_place, turn ^ 1);
-        }
+        const Sums &sums = sm.sums;
         mark_tile(m, a, (uint32_t)place.tile * TOKENS, place.tile == a.tiles - 1, from, to, (long long)place.block * kLrWide);
+        const Place next_place = place_of(__shfl_sync(FULL, next, 0));
         if (lane == 0) sm.place[turn ^ 1] = next_place;
         __syncwarp();
         pass_by(1);
+        if (!first && tensor_copies) {
+            mbar_wait_suspend(&sm.done, turn ^ 1, 1000);   // with the tile before
+            if (lane == 0) issue(place);
+            __syncwarp();
+        }
         if (lane == 0) next = take();
 
         const int p = BACKWARD ? a.tiles - 1 - place.tile : place.tile;
@@ -563,7 +571,7 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
         while (true) {
             const bool found = at == p - 1;
             bool just = false;
-            if (!have_sums && (found && issued ? mbar_wait_suspend(&sm.summed, turn, 2000) || true : mbar_over(&sm.summed, turn)))
+            if (!have_sums && (found ? mbar_wait_suspend(&sm.summed, turn, 2000) || true : mbar_over(&sm.summed, turn)))
                 have_sums = just = true;
             if (found && have_sums && !passed) {   // not before all have their sums: some may still wait for the last tile's state
                 passed = true;
@@ -589,12 +597,7 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
                     }
                 }
             }
-            if (!issued && (passed ? mbar_wait_suspend(&sm.done, turn ^ 1, 2000) || true : mbar_over(&sm.done, turn ^ 1))) {
-                issued = true;
-                if (lane == 0) issue(next_place, turn ^ 1);
-                __syncwarp();
-            }
-            if (passed && issued) break;
+            if (passed) break;
             if (!found) {
                 const int j = at >= 0 ? at + 1 : back, n = min(p - j, kLrWindow);
                 float2 st[AT_ONCE];
@@ -634,6 +637,7 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
                     back = back > chain ? max(back - kLrWindow, chain) : max(p - kLrWindow, chain);
                 }
                 __syncwarp();
+                if (!have_sums && at < p - 1) mbar_try_wait_for(&sm.summed, turn, 300);   // others may tell more meanwhile
                 if (have_sums && ++polls > 4) {
                     if (polls == 5) t0 = global_ns();
                     if (__shfl_sync(FULL, (int)(global_ns() - t0 > kMbarWaitLimitNs), 0)) {
@@ -645,7 +649,6 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
             }
         }
         place = next_place;
-        next_place = place_of(__shfl_sync(FULL, next, 0));
     }
 }
 

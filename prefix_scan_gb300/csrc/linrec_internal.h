@@ -20,11 +20,10 @@ constexpr int kLinrecWide = W_;       // channels of a tile
 #define NW_ 8
 #endif
 constexpr int kLinrecWarps = NW_;     // warps of a CTA that compute
-constexpr int kLinrecCtasPerSm = 16 / NW_, kLinrecCtas = 152 * kLinrecCtasPerSm;   // CTAs that stay on an SM, and on all
 constexpr int kLinrecTile = 512 * kLinrecWarps / kLinrecWide;   // tokens of the smallest tile
 // How many tokens are between the states that training keeps: the backward pass's tile.
 constexpr int linrec_start_tokens(size_t type_bytes, size_t gate_bytes) {
-    return kLinrecTile * (2 * type_bytes + gate_bytes > 6 ? 1 : 2);
+    return kLinrecTile * (2 * type_bytes + gate_bytes > 8 ? 1 : 2);
 }
 
 struct LinrecTensor {                 // element strides; channels are contiguous
@@ -72,9 +71,9 @@ inline cudaError_t linrec_prepare(LinrecArgs &a, int tokens, cudaStream_t s) {
     a.state = reinterpret_cast<float2 *>(a.map + places);
     return cudaMemsetAsync(a.ticket, 0xff, 256 + places * 24, s);
 }
-inline unsigned linrec_grid(const LinrecArgs &a) {
+inline unsigned linrec_grid(const LinrecArgs &a, int ctas_per_sm) {
     const long long all = (long long)a.tiles * a.blocks;
-    return (unsigned)(a.tiles == 1 || all < kLinrecCtas ? all : kLinrecCtas);
+    return (unsigned)(a.tiles == 1 || all < 152 * ctas_per_sm ? all : 152 * ctas_per_sm);
 }
 
 struct LinrecStepArgs {

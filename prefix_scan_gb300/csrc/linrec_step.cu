@@ -35,9 +35,9 @@ __global__ void __launch_bounds__(kStepThreads) linrec_step_kernel(const LinrecS
 #pragma unroll
             for (int v = 0; v < V; v += 2) {
                 constexpr int N = V > 1;   // a channel alone takes the place of both
-                const float2 f = factor(make_float2(to_f32<TG>(gi.v[v]), to_f32<TG>(gi.v[v + N])));
+                const Token t = Token::of(make_float2(to_f32<TG>(gi.v[v]), to_f32<TG>(gi.v[v + N])));
                 const float2 y = make_float2(to_f32<TX>(xi.v[v]), to_f32<TX>(xi.v[v + N]));
-                const float2 next = apply(f, make_float2(h.v[v], h.v[v + N]), TIED ? mul2(forgotten(f), y) : y);
+                const float2 next = t.apply(make_float2(h.v[v], h.v[v + N]), t.weigh(y, TIED));
                 h.v[v] = next.x;
                 h.v[v + N] = next.y;
                 o.v[v] = from_f32<TX>(next.x);
