@@ -39,6 +39,10 @@ def _check(fn, logits, scores, width, ended, eos_token):
 _plans: dict = {}   # packed shapes and workspace sizes by what they follow from: kept from call to call (never data)
 
 
+def _goes_with(plan, t, dtype, device) -> bool:
+    return t.dtype == dtype and t.shape == plan[2] and t.device == device and t.is_contiguous()
+
+
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, width: int | None = None, ended: torch.Tensor | None = None,
                 eos_token: int = -1, workspace: torch.Tensor | None = None, stream=None) -> BeamChoice:
     """The best continuations of an item's beams: ``(scores, parents, tokens, ended)``, each [batch, width], best first.
@@ -52,34 +56,31 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, width: int | None
     the chosen are at theirs (None without).  Where candidates run out: score -infinity, parent and token -1.
     """
     fn = "beam_select"
-    if torch.is_grad_enabled() and (logits.requires_grad or scores.requires_grad):
+    if (logits.requires_grad or scores.requires_grad) and torch.is_grad_enabled():
         raise ValueError(f"{fn}: an input requires gradients, which do not pass through this call; call it under torch.no_grad()")
-    lib = _lib.load()
-    key = (logits.shape, logits.stride(), logits.dtype, logits.device, width, eos_token)
+    device = logits.device
+    key = (logits.shape, logits.stride(), logits.dtype, device, width, eos_token)
     plan = _plans.get(key)
-    if plan is None or scores.dtype != torch.float32 or scores.shape != logits.shape[:2] or scores.device != logits.device \
-            or not scores.is_contiguous() or ended is not None:
+    if plan is None or not _goes_with(plan, scores, torch.float32, device) \
+            or ended is not None and (eos_token < 0 or not _goes_with(plan, ended, torch.uint8, device)):
         w = logits.shape[1] if width is None and logits.dim() == 3 else width
         _check(fn, logits, scores, w if w is not None else 1, ended, eos_token)
-    if plan is None:
         st = logits.stride()
         shape = _lib.BEAM_SHAPE.pack(logits.shape[0], logits.shape[1], w, logits.shape[2], st[0], st[1], REAL_CODES[logits.dtype], eos_token)
         if len(_plans) >= 4096:
             _plans.clear()
-        plan = _plans[key] = (shape, lib.ps_beam_workspace_size(shape), w)
-    shape, need, w = plan
-    device = logits.device
+        plan = _plans[key] = (shape, _lib.load().ps_beam_workspace_size(shape), logits.shape[:2], (logits.shape[0], w))
+    shape, need, _, picks = plan
     s, ctx = enter(device, stream)
     with ctx:
-        batch = logits.shape[0]
-        out = torch.empty((3, batch, w), dtype=torch.int32, device=device)
-        out_scores, parents, tokens = out[0].view(torch.float32), out[1], out[2]
-        out_ended = torch.empty((batch, w), dtype=torch.uint8, device=device) if ended is not None else None
+        out_scores = torch.empty(picks, dtype=torch.float32, device=device)
+        parents, tokens = torch.empty((2, *picks), dtype=torch.int32, device=device).unbind()
+        out_ended = torch.empty(picks, dtype=torch.uint8, device=device) if ended is not None else None
         workspace = _workspace(fn, workspace, need, device)
-        st = lib.ps_beam_select(shape, logits.data_ptr(), scores.data_ptr(), ended.data_ptr() if ended is not None else None,
-                                out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
-                                out_ended.data_ptr() if ended is not None else None, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), s)
+        st = _lib.load().ps_beam_select(shape, logits.data_ptr(), scores.data_ptr(), ended.data_ptr() if ended is not None else None,
+                                        out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                                        out_ended.data_ptr() if ended is not None else None, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), s)
     _lib.check("ps_beam_select", st)
     return BeamChoice(out_scores, parents, tokens, out_ended)
 

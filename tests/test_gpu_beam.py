@@ -170,6 +170,20 @@ def test_large_logits():
     assert c.parents.cpu().tolist() == [[0, 1]] and c.tokens.cpu().tolist() == [[3, 5]] and c.scores.cpu().tolist() == [[0.0, 0.0]]
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("exponent", [10, 18, 20, 22, 24, 31, 40, 64, 99, 101, 126])
+def test_logits_of_any_size(exponent, sign):
+    # numbers a few steps of their type around one size, and a few far below
+    g = torch.Generator().manual_seed(exponent)
+    for dtype, bits, vocab in ((F32, 23, 5000), (F32, 23, 333), (BF16, 7, 20000)):
+        steps = torch.randint(-6, 7, (2, 3, vocab), generator=g)
+        x = (sign * 2.0 ** exponent * (1 + steps.double() * 2.0 ** -bits)).to(dtype)
+        x[:, :, ::7] = -(2.0 ** exponent)
+        x[1, 1] = (-(2.0 ** exponent) * (1 + steps[1, 1].double() * 2.0 ** -bits)).to(dtype)
+        s = torch.randn(2, 3, generator=g)
+        check(api.beam_select(x.to(DEV), s.to(DEV), width=5), x, s, 5)
+
+
 @pytest.mark.parametrize("dtype", [F32, F16])
 def test_masks_and_what_offers_nothing(dtype):
     logits, scores = make(8, 4, 5000, dtype, 11)
