@@ -74,7 +74,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, width: int | None
     s, ctx = enter(device, stream)
     with ctx:
         out_scores = torch.empty(picks, dtype=torch.float32, device=device)
-        parents, tokens = torch.empty((2, *picks), dtype=torch.int32, device=device).unbind()
+        parents = torch.empty(picks, dtype=torch.int32, device=device)
+        tokens = torch.empty(picks, dtype=torch.int32, device=device)
         out_ended = torch.empty(picks, dtype=torch.uint8, device=device) if ended is not None else None
         workspace = _workspace(fn, workspace, need, device)
         st = _lib.load().ps_beam_select(shape, logits.data_ptr(), scores.data_ptr(), ended.data_ptr() if ended is not None else None,

@@ -2,12 +2,19 @@
 //
 // Two kernels.  The first reads each row of logits once, a part of it a CTA, into registers: the part's maximum and sum of
 // exponentials, and its `width` best tokens in order.  The second, a CTA an item, joins the sums of each row's parts, and
-// chooses among what the parts' lists offer.  Bound by memory: a logit is read once and costs an exponential.
+// chooses among what the parts' lists offer.
 //
-// The best of many, in both: some numbers are ranked (of a part's the maxima of 32 groups, 128 where the width is above 32; of
-// the lists' entries those of 256); at least `width` numbers reach the width-th largest of these, T, and as a rule few more
+// The best of many, in both: some numbers are ranked (of a part's the maxima of 32 groups, 128 where the width is above 16; of
+// the lists' entries those of 512); at least `width` numbers reach the width-th largest of these, T, and as a rule few more
 // do.  Those are gathered and ranked one against all.  Where more reach T than there is room for (many equal numbers, say), the
 // best are taken one after the other instead.
+//
+// Memory bounds it from below (a logit is read once), instructions in fact: a pair of 16-bit logits takes six for its
+// exponentials, two for the maximum and three to see whether it reaches T, and a warp some 250 besides, for its 1024
+// logits.  64 x 8 beams over 128000 bf16 logits (131 MB, a fifth at their end): parts 35 us (3 TB/s; with five CTAs
+// an SM instead of the six that 40 registers allow 41), items 9 us; 12 x 16 beams over 50021 f16 logits with 32 candidates: 14
+// and 15 us (128 groups against 32: 14 us against 25, as 37 instead of 110 numbers reach T; 512 threads an item against 256: 15
+// against 17).
 //
 // How a row is cut into parts, threads and sums goes by places in the row alone, so that equal rows have equal sums.
 #include <cfloat>
@@ -23,14 +30,27 @@ namespace ps {
 
 namespace {
 
-constexpr int kPartThreads = 256, kPartWarps = kPartThreads / 32, kItemThreads = 256, kItemWarps = kItemThreads / 32;
+constexpr int kPartThreads = 256, kPartWarps = kPartThreads / 32, kItemThreads = 512, kItemWarps = kItemThreads / 32;
+
 constexpr int kRoom = 512;                             // candidates that are ranked one against all
 constexpr int kFewGroups = 32, kMostGroups = 128;      // of numbers: as many as the width at least
 typedef unsigned long long u64;
 
+// Division of numbers below 2^31: a multiplication, as divisions would be a tenth of a part's instructions.
+struct Divisor {
+    uint32_t factor, shift;
+};
+Divisor divisor(uint32_t d) {   // d < 2^31: s the least with 2^s >= d, then factor = ceil(2^(31 + s) / d) < 2^32 is off by less than
+    uint32_t s = 0;             // 2^s / d parts in 2^31 of what it should be, and x < 2^31
+    while ((1ull << s) < d) ++s;
+    return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s};
+}
+__device__ __forceinline__ uint32_t operator/(uint32_t x, Divisor d) { return (uint32_t)((u64)x * d.factor >> 31 >> d.shift); }
+
 struct BeamArgs {
     long long batch, vocab, item_stride, beam_stride, part_tokens;
     int beams, width, eos, parts;
+    Divisor by_parts, by_beams, by_list;   // by_list: parts * width
     const void *logits;
     const float *scores;
     const uint8_t *ended;
@@ -56,36 +76,22 @@ __device__ __forceinline__ u64 rising(double x) {
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
-// The k-th largest of 32 numbers, one a lane.
-__device__ __forceinline__ float kth_of_lanes(float x, int k) {
-    const int lane = threadIdx.x & 31;
+// The largest number that k of a warp's numbers (above -infinity), G a lane, are at least; -infinity if they are fewer.  BITS:
+// how many of its leading bits can differ from zeros.
+template <int BITS, int G> __device__ __forceinline__ float reached_by(const float (&x)[G], int k) {
+    uint32_t order[G], reach = 0;
 #pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int d = size / 2; d > 0; d >>= 1) {   // a bitonic sort, rising
-            const float y = __shfl_xor_sync(0xffffffffu, x, d);
-            x = ((lane & d) == 0) == ((lane & size) == 0) ? fminf(x, y) : fmaxf(x, y);
-        }
-    return __shfl_sync(0xffffffffu, x, 32 - k);
-}
-// The k-th largest of the 128 groups' maxima: every warp finds it for itself.
-__device__ __forceinline__ float kth_of_groups(const float (&groups)[kMostGroups], int k) {
-    const int lane = threadIdx.x & 31;
-    float t = __int_as_float(0xff800000);
+    for (int g = 0; g < G; ++g) order[g] = x[g] >= -FLT_MAX ? rising(x[g]) : 0;
 #pragma unroll 1
-    for (int j = 0; j < kMostGroups; j += 32) {
-        const float mine = groups[j + lane];
-        int above = 0, reach = 0;
-#pragma unroll 4
-        for (int i = 0; i < kMostGroups; i += 4) {
-            const float4 g = *reinterpret_cast<const float4 *>(&groups[i]);
-            above += (g.x > mine) + (g.y > mine) + (g.z > mine) + (g.w > mine);
-            reach += (g.x >= mine) + (g.y >= mine) + (g.z >= mine) + (g.w >= mine);
-        }
-        const uint32_t is = __ballot_sync(0xffffffffu, above < k && k <= reach);
-        if (is) t = __shfl_sync(0xffffffffu, mine, __ffs(is) - 1);
+    for (uint32_t bit = 1u << 31; bit != 0 && bit >= 1u << (32 - BITS); bit >>= 1) {
+        int n = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) n += order[g] >= (reach | bit);
+        n = G == 1 ? __popc(__ballot_sync(0xffffffffu, n)) : __reduce_add_sync(0xffffffffu, n);
+        if (n >= k) reach |= bit;
     }
-    return t;
+    if (reach == 0) return __int_as_float(0xff800000);
+    return number_of(reach >> 31 ? reach : reach | ((1ull << (32 - BITS)) - 1));   // a negative number's zeros are ones here
 }
 
 // ---- a part of a row ---------------------------------------------------------------------
@@ -169,16 +175,20 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
     return d;
 }
 
+template <typename T> constexpr bool kBf16 = false;
+template <> constexpr bool kBf16<__nv_bfloat16> = true;
+
 template <typename T, int N, int VEC>
-__global__ void __launch_bounds__(kPartThreads, 5) beam_part_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kPartThreads, 6) beam_part_kernel(const BeamArgs a) {
     __shared__ float tops[kPartWarps], sums[kPartWarps];
     __shared__ __align__(16) float groups[kMostGroups];
     __shared__ u64 found[kRoom];
     __shared__ int count;
+    __shared__ float reach;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t row = blockIdx.x / (uint32_t)a.parts, part = blockIdx.x % (uint32_t)a.parts;
+    const uint32_t row = blockIdx.x / a.by_parts, part = blockIdx.x - row * a.parts, item = row / a.by_beams;
     if ((a.ended != nullptr && a.ended[row] != 0) || !finite(a.scores[row])) return;   // nothing of it is read
-    const T *x = static_cast<const T *>(a.logits) + row / (uint32_t)a.beams * a.item_stride + row % (uint32_t)a.beams * a.beam_stride;
+    const T *x = static_cast<const T *>(a.logits) + item * a.item_stride + (row - item * a.beams) * a.beam_stride;
     const float none = __int_as_float(0xff800000);
 
     constexpr int WORDS = N * (int)sizeof(T) / 4;
@@ -217,6 +227,7 @@ __global__ void __launch_bounds__(kPartThreads, 5) beam_part_kernel(const BeamAr
     }
     if (tid == 0) count = 0;
     again(v);
+    const bool many = a.width > kFewGroups / 2;
     float top;
     {
         uint32_t w = v[0];
@@ -231,10 +242,10 @@ __global__ void __launch_bounds__(kPartThreads, 5) beam_part_kernel(const BeamAr
     }
     {
         float w = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        if (a.width > kFewGroups && (lane & 1) == 0) groups[tid / 2] = w;
+        if (many && (lane & 1) == 0) groups[tid / 2] = w;
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 2));
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 4));
-        if (a.width <= kFewGroups && (lane & 7) == 0) groups[tid / 8] = w;
+        if (!many && (lane & 7) == 0) groups[tid / 8] = w;
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 8));
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
         if (lane == 0) tops[warp] = w;
@@ -243,10 +254,20 @@ __global__ void __launch_bounds__(kPartThreads, 5) beam_part_kernel(const BeamAr
     float m = tops[lane % kPartWarps];
 #pragma unroll
     for (int d = 1; d < kPartWarps; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float t = a.width <= kFewGroups ? kth_of_lanes(groups[lane], a.width) : kth_of_groups(groups, a.width);
+    if (warp == 0) {
+        constexpr int BITS = sizeof(T) == 4 ? 32 : kBf16<T> ? 16 : 19;
+        float x;
+        if (many) {
+            const float4 g = *reinterpret_cast<const float4 *>(&groups[lane * 4]);
+            x = reached_by<BITS, 4>({g.x, g.y, g.z, g.w}, a.width);
+        } else {
+            x = reached_by<BITS, 1>({groups[lane]}, a.width);
+        }
+        if (lane == 0) reach = x;
+    }
 
     // The sum of exponentials, in a tree of 32-bit sums: 17 additions deep for 32 numbers a thread.  64 bits would cost more than
-    // all else here, as the machine adds two such numbers a cycle and SM (8192 parts of 8000 numbers: 57 us instead of ...).
+    // all else here, as the machine adds two such numbers a cycle and SM (8192 parts of 8000 numbers: 57 us, against 40).
     float sum = 0.f;
     if (base_is_used(m)) {
         const float base = base_of(m);
@@ -266,6 +287,8 @@ __global__ void __launch_bounds__(kPartThreads, 5) beam_part_kernel(const BeamAr
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    const float t = reach;
 
     again(v);
     uint32_t low = 0xffffffffu - (uint32_t)(first + place_in_part<VEC>(0));
@@ -379,6 +402,7 @@ constexpr int kLists = 4;   // of a lane
 __global__ void __launch_bounds__(kItemThreads) beam_item_kernel(const BeamArgs a) {
     __shared__ double shift[PS_BEAM_MAX_BEAMS];     // score - log sum exp(logit - largest)
     __shared__ float largest[PS_BEAM_MAX_BEAMS], score[PS_BEAM_MAX_BEAMS];
+    __shared__ float2 near[PS_BEAM_MAX_BEAMS];      // largest and shift in 32 bits; (0, -infinity) of a beam that offers no tokens
     __shared__ uint8_t state[PS_BEAM_MAX_BEAMS];    // 0: offers nothing, 1: tokens, 2: itself, ended
     __shared__ Candidate chosen[kItemWarps + 1][PS_BEAM_MAX_WIDTH];   // by warp, and of all so far; total 0 where there is none
     static_assert(sizeof(chosen) >= sizeof(Candidate) * kRoom, "one place for both ways");
@@ -416,10 +440,13 @@ __global__ void __launch_bounds__(kItemThreads) beam_item_kernel(const BeamArgs 
         if (lane == 0) {
             // the 32-bit logarithm, and once Newton's step from it: off by what expf is, 2^-23
             const float y = logf((float)all);
-            shift[b] = (double)sc - ((double)y + (all * (double)expf(-y) - 1.0));
+            const double sh = (double)sc - ((double)y + (all * (double)expf(-y) - 1.0));
+            const int st = !finite(sc) ? 0 : end ? 2 : all == all && m > none ? 1 : 0;   // NaN: NaN or +infinity among the logits
+            shift[b] = sh;
             largest[b] = m;
             score[b] = sc;
-            state[b] = !finite(sc) ? 0 : end ? 2 : all == all && m > none ? 1 : 0;   // NaN: NaN or +infinity among the logits
+            state[b] = st;
+            near[b] = st == 1 ? make_float2(m, (float)sh) : make_float2(0.f, none);
         }
     }
     __syncthreads();
@@ -442,41 +469,49 @@ __global__ void __launch_bounds__(kItemThreads) beam_item_kernel(const BeamArgs 
     };
     const uint32_t lists = (uint32_t)a.beams * a.parts;
     const u64 *best = a.best + item * lists * a.width;
-    // Totals of 32 bits: T is the width-th largest of the maxima of 256 groups.  A total near T is made of a score, a distance
-    // from the row's largest and a logarithm that are no larger than `size`; 32 bits lose less than 2^-20 of it.
-    auto near_total = [&](uint32_t i, u64 key) {
-        const uint32_t b = i / ((uint32_t)a.parts * a.width);
-        if (state[b] == 2) return i == b * a.parts * a.width ? score[b] : none;   // an ended beam is the head of its first list
-        return state[b] == 1 && key != 0 ? fmaxf(number_of((uint32_t)(key >> 32)) - largest[b] + (float)shift[b], -FLT_MAX) : none;
-    };
+    // Totals of 32 bits: T is the width-th largest of the maxima of 512 groups.  A total near T is made of a score, a distance
+    // from the row's largest and a logarithm that are no larger than `size`; 32 bits lose less than 2^-20 of it.  Distances
+    // beyond 2^126 are taken for that, of which no T above -2^124 with scores below 2^120 knows; else all are gathered.
     const uint32_t keys = (uint32_t)min((u64)lists * a.width, 1ull << 31);   // of more, those behind are left to the other way
+    auto near_total = [&](uint32_t i) {
+        const float2 c = near[i / a.by_list];
+        const uint32_t hi = reinterpret_cast<const uint32_t *>(best)[2 * (size_t)i + 1];
+        return hi != 0 ? fmaxf(number_of(hi) - c.x, -0x1p126f) + c.y : none;
+    };
     float mine = none, size = 0.f;
 #pragma unroll 4
-    for (uint32_t i = tid; i < keys; i += kItemThreads) mine = fmaxf(mine, near_total(i, best[i]));
+    for (uint32_t i = tid; i < keys; i += kItemThreads) mine = fmaxf(mine, near_total(i));
+    for (int b = tid; b < a.beams; b += kItemThreads)
+        if (state[b] == 2) mine = fmaxf(mine, score[b]);
     for (int b = lane; b < a.beams; b += 32)
-        if (state[b] != 0) size = fmaxf(size, fabsf(score[b]) + fabsf((float)shift[b]));
+        if (state[b] != 0) size = fmaxf(size, fabsf(score[b]) + (state[b] == 1 ? fabsf(near[b].y) : 0.f));
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, d));
-    uint32_t reach = 0;   // the largest number that `width` of them reach
-    const uint32_t order = mine > none ? rising(mine) : 0;
+    uint32_t reach = 0;   // its leading 24 bits: somewhat more than `width` may reach it
+    const uint32_t order = mine >= -FLT_MAX ? rising(mine) : 0;
 #pragma unroll 1
-    for (uint32_t bit = 1u << 31; bit != 0; bit >>= 1)
+    for (uint32_t bit = 1u << 31; bit >= 1u << 8; bit >>= 1)
         if (__syncthreads_count(order >= (reach | bit)) >= a.width) reach |= bit;
     float t = none;
     if (reach != 0) {
         t = number_of(reach);
         t -= (2.f * size + fabsf(t)) * 0x1p-20f;
+        if (!(t > -0x1p124f && size < 0x1p120f)) t = none;
     }
 #pragma unroll 4
     for (uint32_t i = tid; i < keys; i += kItemThreads) {
-        u64 key = best[i];
-        const float y = near_total(i, key);
+        const float y = near_total(i);
         if (!(y >= t) || y == none) continue;
-        const int at = atomicAdd(&count, 1), b = (int)(i / ((uint32_t)a.parts * a.width));
+        const int at = atomicAdd(&count, 1), b = (int)(i / a.by_list);
         if (at >= kRoom) continue;
-        if (state[b] == 2) found[at] = {rising((double)score[b]), 0, b};
-        else found[at] = {rising(((double)number_of((uint32_t)(key >> 32)) - (double)largest[b]) + shift[b]), key, b};
+        const u64 key = best[i];
+        found[at] = {rising(((double)number_of((uint32_t)(key >> 32)) - (double)largest[b]) + shift[b]), key, b};
     }
+    for (int b = tid; b < a.beams; b += kItemThreads)
+        if (state[b] == 2) {
+            const int at = atomicAdd(&count, 1);
+            if (at < kRoom) found[at] = {rising((double)score[b]), 0, b};
+        }
     __syncthreads();
     const int n = count;
     if (n <= kRoom && keys < 1u << 31) {
@@ -492,7 +527,7 @@ __global__ void __launch_bounds__(kItemThreads) beam_item_kernel(const BeamArgs 
         }
         return;
     }
-    // More than there is room for: the lists' heads one after the other, of 1024 lists at a time.  A warp merges 128 of them, four
+    // More than there is room for: the lists' heads one after the other, of 2048 lists at a time.  A warp merges 128 of them, four
     // a lane; then one warp those of all, and of the lists before.
     for (uint32_t base = 0; base < lists; base += kItemThreads * kLists) {
         Candidate head[kLists];
@@ -703,6 +738,9 @@ extern "C" ps_status ps_beam_select(const ps_beam_shape *d, const void *logits, 
     a.eos = d->eos_token;
     a.parts = (int)p.parts;
     a.part_tokens = cut_of(d).tokens;
+    a.by_parts = divisor((uint32_t)a.parts);
+    a.by_beams = divisor((uint32_t)a.beams);
+    a.by_list = divisor((uint32_t)a.parts * (uint32_t)a.width);
     a.logits = logits;
     a.scores = scores;
     a.ended = ended;

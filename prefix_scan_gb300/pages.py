@@ -28,13 +28,17 @@ def _pools(fn, pools, pages, device):
         pools = [pools]
     if len(pools) > _lib.PS_PAGES_MAX_POOLS:
         raise ValueError(f"{fn}: at most {_lib.PS_PAGES_MAX_POOLS} pools in one call")
-    out = []
+    out, like, dtype, size = [], None, None, 0
     for p in pools:
-        if p.device != device or p.dim() < 1 or p.shape[0] != pages or not p.is_contiguous():
+        shape = p.shape
+        if shape != like or p.dtype is not dtype:   # pools are often of one shape and type
+            if p.dim() < 1 or shape[0] != pages:
+                raise ValueError(f"{fn}: pools must be contiguous CUDA tensors of {pages} pages on one device")
+            like, dtype, size = shape, p.dtype, p.numel() // pages * p.element_size() if pages else 1
+            if size == 0:
+                raise ValueError(f"{fn}: pages must not be empty")
+        if p.device != device or not p.is_contiguous():
             raise ValueError(f"{fn}: pools must be contiguous CUDA tensors of {pages} pages on one device")
-        size = p.numel() // pages * p.element_size() if pages else 1
-        if size == 0:
-            raise ValueError(f"{fn}: pages must not be empty")
         out += (p.data_ptr(), size)
     return struct.pack("@" + "Pq" * len(pools), *out), len(pools)   # ps_page_pool
 
@@ -131,9 +135,10 @@ def pages_reorder(slots: torch.Tensor, parents: torch.Tensor, pools, *, out: tor
     with ctx:
         if out is None:
             out = torch.empty(slots.shape, dtype=torch.int32, device=device)
-        _check_ints(fn, device, out=(out, slots.dim()))
-        if out.shape != slots.shape:
-            raise ValueError(f"{fn}: out must have the shape of slots")
+        else:
+            _check_ints(fn, device, out=(out, slots.dim()))
+            if out.shape != slots.shape:
+                raise ValueError(f"{fn}: out must have the shape of slots")
         missing = torch.empty(1, dtype=torch.int32, device=device)
         workspace = _workspace(fn, lib, workspace, rows, pages, device)
         st = lib.ps_pages_reorder(slots.data_ptr(), parents.data_ptr(), rows, arr, n, pages, out.data_ptr(), missing.data_ptr(),
