@@ -1,14 +1,17 @@
 // linrec_backward.cu -- gradients of the gated linear recurrence (notation and
 // tiles in linrec_common.cuh).
 //
-// Bound by memory: x, g and dh are read once, dx and dg are written once.  The states are not read: the forward pass keeps
-// the one before each tile (in 32 bits), and the tile is scanned again from there, so that 16-bit types, too, get the
-// gradient of g from states of 32 bits.  What runs backward is mu, a state's gradient handed to the token before; its
+// Memory bounds it from below (x, g and dh are read once, dx and dg are written once), instructions in fact: 58 a number.  The
+// states are not read: the forward pass keeps the one before each tile (in 32 bits), and the tile is scanned again from there,
+// so that 16-bit types, too, get the gradient of g from states of 32 bits.  What runs backward is mu, a state's gradient handed to the token before; its
 // look-back goes over the tiles from the last one.
 //
 // A run's first scan is forward only: what it adds to mu is the sum of P_i dh_i, P_i the product of its factors up to token i.
 // The second takes eight tokens at a time, the last ones first: forward for the states before them, from what the first
-// scan kept there (a state from 0, and P), then backward.
+// scan kept there (a state from 0, and P), then backward: a step back from a state would divide by factors near 0.
+//
+// 4 sequences of 8192 tokens by 4096 bf16 channels, forward and backward: 495 us, of which this is 320; 65536 tokens by 512 f32
+// channels, tied: 281 us.
 #include <type_traits>
 
 #include "linrec_common.cuh"

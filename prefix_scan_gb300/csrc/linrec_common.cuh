@@ -6,11 +6,15 @@
 //     backward, from the last token:  lam_t = dh_t + mu_{t+1},  mu_t = a_t lam_t,
 //     dx_t = w_t lam_t,  dg_t = mu_t (h_{t-1} - [tied] x_t),  dh0 = mu_1
 //
-// A tile is 512 tokens (256 where inputs are wide) by 16 channels, in 32 runs of R tokens.  A lane has a run and two neighbouring
-// channels; a warp of eight has four runs, one after the other, of all 16 channels.  Tiles are long and narrow so that of the
-// tiles under way at a time few are of one chain: with 64 channels by 128 tokens, four times as many waited for
-// one another.  Sequences are cut out of the flat index over all tokens: where one starts the state is set, not multiplied, so
-// short sequences fill tiles as long ones do.
+// A tile is 32 channels by 512, 256 or 128 tokens, as much as three CTAs an SM can hold, in 16 runs of R = 32, 16 or 8 tokens.  A
+// lane has a run and two neighbouring channels; a warp of eight has two runs of all 32 channels.  What a run costs beside its
+// tokens (joining, the look-back's share) is some 300 instructions a lane, so longer runs are better (32 tokens instead of 16,
+// forward, one sequence of 131072 tokens by 512 bf16 channels: 143 us instead of 170); shared memory bounds them, as two CTAs an
+// SM with runs twice as long are slower (backward, 4 x 8192 tokens by 4096 bf16 channels, trained: 546 us instead of 495).  Wide tiles have long rows in
+// memory (copies of 32 and 64 bf16 channels run at 5.9 and 6.0 TB/s, of 16 at 5.0), narrow ones make more chains, so that
+// fewer of the tiles under way wait for one another: with 16, 32 and 64 channels 48 ragged prompts (24571 tokens by 4096
+// channels) took 283, 265 and 254 us, the long one 180, 189 and 210, training 733, 630 and 615.  Sequences are cut out of the flat index over all tokens: where one
+// starts the state is set, not multiplied, so short sequences fill tiles as long ones do.
 //
 // Each tile tells the ones behind it its map h -> a h + b, and the state behind it once it knows that.  A tile that
 // needs the state before it takes the nearest state that is known and applies the maps since then in order
@@ -19,7 +23,7 @@
 // composed in the order of arrival would not.
 //
 // CTAs stay and take tiles by ticket, in the order of the recurrence.  Eight warps compute; a ninth takes tickets, has
-// tiles loaded one ahead, finds starts and ends, and looks back, which it begins while the tile's first pass still runs.
+// tiles loaded as soon as the one before is done with, finds starts and ends, and looks back, which it begins while the tile's first pass still runs.
 //
 // Factors.  exp(g) of a slow decay rounds to 2^-24 of 1, and what a state forgets in a token, 1 - exp(g), may be not much
 // more than that: an error to one side adds up over the state's whole memory (a thousand tokens and more).  So a factor
@@ -43,6 +47,7 @@ constexpr int kLrWarps = kLinrecWarps;
 constexpr int kLrCompute = 32 * kLrWarps, kLrThreads = kLrCompute + 32;
 constexpr int kLrWide = kLinrecWide, kLrPairs = kLrWide / 2;   // channels of a tile, and pairs of them
 constexpr int kLrGroups = 32 / kLrPairs;                       // runs of a warp
+static_assert(kLrGroups == 2, "as joining assumes");
 constexpr int kLrRuns = kLrWarps * kLrGroups;                  // of a tile
 
 __device__ __forceinline__ int lr_pair() { return threadIdx.x % kLrPairs; }
@@ -206,16 +211,29 @@ __device__ __forceinline__ void load_pieces(T *tile, const LinrecTensor &x, cons
         src += seq * x.seq + (long long)t * x.tok;
     }
     const long long step = STEP * x.tok;
-#pragma unroll(UNROLL)
-    for (int row = row0; row < ROWS; row += STEP) {
-        const bool there = in && n < (uint32_t)a.total;
-        T *dst = tile + (row % R * kLrRuns + row / R) * kLrWide + col;
-        if constexpr (N * sizeof(T) == 2) *dst = there ? *src : from_f32<T>(0.f);
-        else copy_async<N * sizeof(T)>(smem_u32(dst), there ? src : base, there);
+    auto next = [&] {
         n += STEP;
         src += step;
         if (!x.flat) {
             for (t += STEP; t >= (uint32_t)a.tokens; t -= (uint32_t)a.tokens) src += x.seq - (long long)a.tokens * x.tok;
+        }
+    };
+    auto place = [&](int row) { return tile + (row % R * kLrRuns + row / R) * kLrWide + col; };
+    if constexpr (N * sizeof(T) == 2) {   // 16 under way at a time (3001 tokens by 1001 f16 channels, trained: 63 us; 8: 66, 4: 80)
+        static_assert(ROWS / STEP % UNROLL == 0, "whole rounds");
+#pragma unroll 1
+        for (int row = row0; row < ROWS; row += STEP * UNROLL) {
+            T y[UNROLL];
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k, next()) y[k] = in && n < (uint32_t)a.total ? *src : from_f32<T>(0.f);
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k) *place(row + k * STEP) = y[k];
+        }
+    } else {
+#pragma unroll(UNROLL)
+        for (int row = row0; row < ROWS; row += STEP, next()) {
+            const bool there = in && n < (uint32_t)a.total;
+            copy_async<N * sizeof(T)>(smem_u32(place(row)), there ? src : base, there);
         }
     }
 }
@@ -223,7 +241,7 @@ template <typename T, int R>
 __device__ __forceinline__ void load_tile(T *tile, const LinrecTensor &x, const LinrecArgs &a, uint32_t n0, long long c0) {
     if (x.piece == 16) load_pieces<T, R, 16 / sizeof(T), 1>(tile, x, a, n0, c0);
     else if (sizeof(T) == 4 || x.piece == 4) load_pieces<T, R, 4 / sizeof(T), 2>(tile, x, a, n0, c0);
-    else load_pieces<T, R, 1, 4>(tile, x, a, n0, c0);
+    else load_pieces<T, R, 1, 16>(tile, x, a, n0, c0);
 }
 
 // Inputs whose rows are evenly spaced, on multiples of 16 bytes, come by tensor copies of whole tiles, one thread's doing
@@ -436,28 +454,16 @@ __device__ __forceinline__ float2 from_group(float2 x, int group) {
 template <bool BACKWARD>
 __device__ __forceinline__ Ahead join_runs(float2 s, float2 f, float2 b, bool cut, bool any, float2 (*sum)[kLrPairs],
                                            float2 (*factors)[kLrPairs], float2 (*adds)[kLrPairs]) {
-    const int warp = threadIdx.x >> 5, nth = BACKWARD ? kLrGroups - 1 - lr_group() : lr_group();
+    const int warp = threadIdx.x >> 5, first = BACKWARD ? 1 : 0;   // the run that comes first
+    const float2 fs = from_group(s, first), ff = from_group(f, first), fb = from_group(b, first);
+    const bool fc = any && __shfl_sync(0xffffffffu, (int)cut, first * kLrPairs);
+    const bool second = lr_group() != first;
     Ahead a{both(0.f), both(0.f), false};
-    float2 as = both(0.f);
-#pragma unroll
-    for (int q = 0; q < kLrGroups - 1; ++q) {
-        const int g = BACKWARD ? kLrGroups - 1 - q : q;
-        const float2 gs = from_group(s, g), gf = from_group(f, g), gb = from_group(b, g);
-        const bool gc = any && __shfl_sync(0xffffffffu, (int)cut, g * kLrPairs);
-        if (q < nth) {
-            a.b = gc ? gb : apply(gf, a.b, gb);
-            a.cut |= gc;
-            as = add2(as, gs);
-            if (kLrGroups == 2) a.f = gf;
-        }
-    }
-    if (kLrGroups > 2) a.f = factor_of_sum(as);
-    if (kLrGroups > 1) {
-        b = cut || nth == 0 ? b : apply(f, a.b, b);
-        s = add2(as, s);
+    if (second) {
+        a = {ff, fb, fc};
+        if (!cut) b = apply(f, a.b, b);
+        s = add2(fs, s);
         f = factor_of_sum(s);
-    }
-    if (nth == kLrGroups - 1) {
         if (sum != nullptr) sum[warp][lr_pair()] = s;
         if (factors != nullptr) factors[warp][lr_pair()] = f;
         adds[warp][lr_pair()] = b;
@@ -468,13 +474,13 @@ __device__ __forceinline__ Ahead join_runs(float2 s, float2 f, float2 b, bool cu
 template <bool BACKWARD, typename Cut>
 __device__ __forceinline__ float2 before_run(float2 h, const Ahead &a, const float2 (*factors)[kLrPairs], const float2 (*adds)[kLrPairs],
                                              bool any, Cut cut) {
-    const int warp = threadIdx.x >> 5, nth = BACKWARD ? kLrGroups - 1 - lr_group() : lr_group();
+    const int warp = threadIdx.x >> 5;
     for (int i = 0; i < (BACKWARD ? kLrWarps - 1 - warp : warp); ++i) {
         const int w = BACKWARD ? kLrWarps - 1 - i : i;
         const float2 b = adds[w][lr_pair()];
         h = any && cut(w) ? b : apply(factors[w][lr_pair()], h, b);
     }
-    return nth == 0 ? h : a.cut ? a.b : apply(a.f, h, a.b);
+    return lr_group() == (BACKWARD ? 1 : 0) ? h : a.cut ? a.b : apply(a.f, h, a.b);
 }
 
 // What a CTA's warps share beside its tiles.
@@ -613,7 +619,7 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
                     const uint32_t s = ~__ballot_sync(FULL, told(st[i])), q = ~__ballot_sync(FULL, told(mp[i]));
 #pragma unroll
                     for (int g = 0; g < kLrGroups; ++g) {
-                        constexpr uint32_t LANES = kLrPairs == 32 ? FULL : (1u << (kLrPairs % 32)) - 1;
+                        constexpr uint32_t LANES = (1u << kLrPairs) - 1;
                         told_state |= (uint32_t)((s >> (g * kLrPairs) & LANES) == 0) << (i * kLrGroups + g);
                         told_map |= (uint32_t)((q >> (g * kLrPairs) & LANES) == 0) << (i * kLrGroups + g);
                     }

@@ -12,15 +12,9 @@
 
 namespace ps {
 
-#ifndef W_
-#define W_ 32
-#endif
-constexpr int kLinrecWide = W_;       // channels of a tile
-#ifndef NW_
-#define NW_ 8
-#endif
-constexpr int kLinrecWarps = NW_;     // warps of a CTA that compute
-constexpr int kLinrecTile = 512 * kLinrecWarps / kLinrecWide;   // tokens of the smallest tile
+constexpr int kLinrecWide = 32;       // channels of a tile
+constexpr int kLinrecWarps = 8;       // warps of a CTA that compute
+constexpr int kLinrecTile = 512 * kLinrecWarps / kLinrecWide;   // tokens of the smallest tile: 128
 // How many tokens are between the states that training keeps: the backward pass's tile.
 constexpr int linrec_start_tokens(size_t type_bytes, size_t gate_bytes) {
     return kLinrecTile * (2 * type_bytes + gate_bytes > 8 ? 1 : 2);
@@ -33,7 +27,7 @@ struct LinrecTensor {                 // element strides; channels are contiguou
     int piece;                        // rows start on multiples of so many bytes, and hold a multiple of them: 16, 4 or 2
 };
 
-// Workspace.  A ticket counter and what tiles tell one another, for each (tile of tokens, block of 16 channels, pair of channels):
+// Workspace.  A ticket counter and what tiles tell one another, for each (tile of tokens, block of 32 channels, pair of channels):
 //   map    the tile's factors, encoded as in linrec_common.cuh, and what it adds
 //   state  the state (backward: the state's gradient) behind the tile
 // (set by each call to 0xff bytes, which stands for nothing told yet), and in training `start`, the state before each tile
