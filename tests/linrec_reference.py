@@ -9,9 +9,14 @@ Tolerance, with u = 2^-24 and M_t the same recurrence over absolute values, whic
 - Each token's factor is off to one side by at most 2^-22.5 of 1 - a where -1/16 < g <= 0 (a series cut at 2^-22.9, and its
   rounding) and 2^-21.5 of a elsewhere (the hardware's 2^x within 2^-22, its argument within u of itself, of which
   |g| exp(g) <= 0.37 remains; 1 - a of tied inputs within as much): L_t = a_t L_{t-1} + that times (M_{t-1} + |x_t| if tied).
-- What a run of 16 tokens and a tile of 128 hand on is multiplied by exp of a sum of up to 128 log decays.  A sum of n numbers
-  added in order is off by n u |s|, and |s| exp(s) <= 0.37; runs are added in order too: (16 + 8) 0.37 u < 9 u, exp itself 2 u,
-  two roundings 2 u; a token sees a run's and a tile's: 26 u M_t.
+- What a run of up to 32 tokens and a tile of 16 runs hand on is multiplied by exp of the sum of their log decays.  A sum of n
+  numbers is off by n roundings of at most u |s|, uniform and independent, with a deviation of (n / 3)^0.5 u |s|, and
+  |s| exp(s) <= 0.37: 32 of a run, 1 of a pair of them, 8 of the pairs, 3.7 u |s|, six times and by 0.37 less than 9 u; exp itself
+  2 u, two roundings 2 u; a token sees a run's and a tile's: 26 u M_t.
+- Backward, what a run of up to 16 tokens adds is the sum of P_i dh_i, P_i the product of its factors so far: 16 additions and as
+  many roundings of P, each of at most u M, with a deviation of (32 / 3)^0.5 u M, six times 20 u M.  It takes the place of the
+  first point's roundings, which are 24 u M where the run decays little and 6 u M at least; where it decays much |s| exp(s) is
+  near 0 and the sums' 18 u of the third point are free.
 Outputs of fewer bits are off by half a step more, and f16 by half its smallest step."""
 from __future__ import annotations
 
