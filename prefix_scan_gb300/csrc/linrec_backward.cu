@@ -186,10 +186,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
             if (r.plain) part(q, h, std::false_type{});
             else part(q, h, std::true_type{});
         }
-        if (tensor_copies) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.done);
-        }
+        if (tensor_copies) sm.release();
         named_barrier(4, kLrCompute);   // all have read what the warps' runs add
         place = next_place;
     }

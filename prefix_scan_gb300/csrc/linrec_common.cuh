@@ -495,6 +495,12 @@ template <int R> struct Shared {
     Marks<TOKENS> marks[2];
     Place place[2];
     uint64_t landed, summed, done;   // the tile's inputs are there; all runs are summed; the inputs are no longer needed
+    // Of a whole warp: it needs its inputs no longer, and what it wrote in their place comes before the next copies.
+    __device__ __forceinline__ void release() {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&done);
+    }
 };
 // Barriers by number.  1: marks are set, the next tile is known, pieces of tiles have landed; 2: the first tile is known;
 // 3: the state before the tile is known; 4: among the compute warps.  The ninth warp never waits at them.

@@ -121,12 +121,8 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
                 out += a.channels;
             }
         }
-        if (tensor_copies) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.done);
-        } else {
-            named_barrier(4, kLrCompute);
-        }
+        if (tensor_copies) sm.release();
+        else named_barrier(4, kLrCompute);
         place = next_place;
     }
 }
