@@ -9,12 +9,13 @@
 // do.  Those are gathered and ranked one against all.  Where more reach T than there is room for (many equal numbers, say), the
 // best are taken one after the other instead.
 //
-// Memory bounds it from below (a logit is read once), instructions in fact: a pair of 16-bit logits takes six for its
-// exponentials, two for the maximum and three to see whether it reaches T, and a warp some 250 besides, for its 1024
-// logits.  64 x 8 beams over 128000 bf16 logits (131 MB, a fifth at their end): parts 35 us (3 TB/s; with five CTAs
-// an SM instead of the six that 40 registers allow 41), items 9 us; 12 x 16 beams over 50021 f16 logits with 32 candidates: 14
-// and 15 us (128 groups against 32: 14 us against 25, as 37 instead of 110 numbers reach T; 512 threads an item against 256: 15
-// against 17).
+// Memory bounds it from below (a logit is read once); in fact a part's chain of loads, barriers and shuffles does, which five
+// other CTAs on its SM cover in part.  A pair of 16-bit logits takes six instructions for its exponentials, two for the maximum
+// and three to see whether it reaches T, and a warp some 250 besides for its 1024 logits.  64 x 8 beams over 128000 bf16 logits
+// (131 MB, a fifth at their end): parts 33 us (3.1 TB/s; five CTAs an SM instead of the six that 40 registers allow: 41 instead of
+// 35; T found by one warp in steps of a bit: 35; parts twice as long, on four CTAs: 37; parts to come fetched into L2: no
+// difference), items 9 us.  12 x 16 beams over 50021 f16 logits with 32 candidates: 14 and 15 us (128 groups against 32: 14 us
+// against 25, as 37 instead of 110 numbers reach T; 512 threads an item against 256: 15 against 17).
 //
 // How a row is cut into parts, threads and sums goes by places in the row alone, so that equal rows have equal sums.
 #include <cfloat>
@@ -76,22 +77,21 @@ __device__ __forceinline__ u64 rising(double x) {
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
-// The largest number that k of a warp's numbers (above -infinity), G a lane, are at least; -infinity if they are fewer.  BITS:
-// how many of its leading bits can differ from zeros.
-template <int BITS, int G> __device__ __forceinline__ float reached_by(const float (&x)[G], int k) {
-    uint32_t order[G], reach = 0;
+// Of a warp's share of N numbers in shared memory (a WARPS-th), the least that fewer than k of all N exceed, as an integer that
+// rises with it; ~0 if there is none.  The least of all warps' is the k-th largest number.
+template <int N, int WARPS> __device__ __forceinline__ uint32_t reached_by(const float *x, int k) {
+    constexpr int LANES = 32 * WARPS / N;   // that compare a number with all
+    const int lane = threadIdx.x & 31;
+    const float mine = x[(threadIdx.x >> 5) * (N / WARPS) + lane / LANES];
+    int above = 0;
 #pragma unroll
-    for (int g = 0; g < G; ++g) order[g] = x[g] >= -FLT_MAX ? rising(x[g]) : 0;
-#pragma unroll 1
-    for (uint32_t bit = 1u << 31; bit != 0 && bit >= 1u << (32 - BITS); bit >>= 1) {
-        int n = 0;
-#pragma unroll
-        for (int g = 0; g < G; ++g) n += order[g] >= (reach | bit);
-        n = G == 1 ? __popc(__ballot_sync(0xffffffffu, n)) : __reduce_add_sync(0xffffffffu, n);
-        if (n >= k) reach |= bit;
+    for (int i = 0; i < N; i += 4 * LANES) {
+        const float4 y = *reinterpret_cast<const float4 *>(&x[i + lane % LANES * 4]);
+        above += (y.x > mine) + (y.y > mine) + (y.z > mine) + (y.w > mine);
     }
-    if (reach == 0) return __int_as_float(0xff800000);
-    return number_of(reach >> 31 ? reach : reach | ((1ull << (32 - BITS)) - 1));   // a negative number's zeros are ones here
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) above += __shfl_xor_sync(0xffffffffu, above, d);
+    return __reduce_min_sync(0xffffffffu, above < k ? rising(mine) : 0xffffffffu);
 }
 
 // ---- a part of a row ---------------------------------------------------------------------
@@ -175,16 +175,13 @@ __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
     return d;
 }
 
-template <typename T> constexpr bool kBf16 = false;
-template <> constexpr bool kBf16<__nv_bfloat16> = true;
-
 template <typename T, int N, int VEC>
 __global__ void __launch_bounds__(kPartThreads, 6) beam_part_kernel(const BeamArgs a) {
     __shared__ float tops[kPartWarps], sums[kPartWarps];
     __shared__ __align__(16) float groups[kMostGroups];
     __shared__ u64 found[kRoom];
     __shared__ int count;
-    __shared__ float reach;
+    __shared__ uint32_t reach[kPartWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t row = blockIdx.x / a.by_parts, part = blockIdx.x - row * a.parts, item = row / a.by_beams;
     if ((a.ended != nullptr && a.ended[row] != 0) || !finite(a.scores[row])) return;   // nothing of it is read
@@ -254,17 +251,8 @@ __global__ void __launch_bounds__(kPartThreads, 6) beam_part_kernel(const BeamAr
     float m = tops[lane % kPartWarps];
 #pragma unroll
     for (int d = 1; d < kPartWarps; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (warp == 0) {
-        constexpr int BITS = sizeof(T) == 4 ? 32 : kBf16<T> ? 16 : 19;
-        float x;
-        if (many) {
-            const float4 g = *reinterpret_cast<const float4 *>(&groups[lane * 4]);
-            x = reached_by<BITS, 4>({g.x, g.y, g.z, g.w}, a.width);
-        } else {
-            x = reached_by<BITS, 1>({groups[lane]}, a.width);
-        }
-        if (lane == 0) reach = x;
-    }
+    const uint32_t least = many ? reached_by<kMostGroups, kPartWarps>(groups, a.width) : reached_by<kFewGroups, kPartWarps>(groups, a.width);
+    if (lane == 0) reach[warp] = least;
 
     // The sum of exponentials, in a tree of 32-bit sums: 17 additions deep for 32 numbers a thread.  64 bits would cost more than
     // all else here, as the machine adds two such numbers a cycle and SM (8192 parts of 8000 numbers: 57 us, against 40).
@@ -288,7 +276,7 @@ __global__ void __launch_bounds__(kPartThreads, 6) beam_part_kernel(const BeamAr
     for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) sums[warp] = sum;
     __syncthreads();
-    const float t = reach;
+    const float t = number_of(__reduce_min_sync(0xffffffffu, reach[lane % kPartWarps]));
 
     again(v);
     uint32_t low = 0xffffffffu - (uint32_t)(first + place_in_part<VEC>(0));
