@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kItemThreads) beam_item_kernel(const BeamArgs 
     auto near_total = [&](uint32_t i) {
         const float2 c = near[i / a.by_list];
         const uint32_t hi = reinterpret_cast<const uint32_t *>(best)[2 * (size_t)i + 1];
-        return hi != 0 ? fmaxf(number_of(hi) - c.x, -0x1p126f) + c.y : none;
+        return hi != 0 && c.y > none ? fmaxf(fmaxf(number_of(hi) - c.x, -0x1p126f) + c.y, -FLT_MAX) : none;
     };
     float mine = none, size = 0.f;
 #pragma unroll 4

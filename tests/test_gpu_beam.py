@@ -184,6 +184,39 @@ def test_logits_of_any_size(exponent, sign):
         check(api.beam_select(x.to(DEV), s.to(DEV), width=5), x, s, 5)
 
 
+@pytest.mark.parametrize("width", [3, 17, 64])
+@pytest.mark.parametrize("vocab", [700, 40000])
+def test_scores_of_any_size(width, vocab):
+    # one beam has them all; beams far apart; scores at the end of their type
+    for row in ([0.0, -1e4, -1e4, -1e4], [-50.0, -50.5, -2e30, -3e38], [3.4e38, 3.4e38, 1e38, -3e38], [-3e38] * 4, [2e36, 0.0, -2e36, -INF]):
+        logits, _ = make(2, 4, vocab, F32, width)
+        logits[1] *= 1e36
+        scores = torch.tensor([row] * 2, device=DEV)
+        check(api.beam_select(logits, scores, width=width), logits, scores, width)
+
+
+def test_totals_beyond_32_bits_are_chosen_last():
+    logits = torch.tensor([[[0.0, -3e38, -INF]]], device=DEV)
+    c = api.beam_select(logits, torch.tensor([[-3e38]], device=DEV), width=3)
+    assert c.parents.cpu().tolist() == [[0, 0, -1]] and c.tokens.cpu().tolist() == [[0, 1, -1]]
+    assert c.scores.cpu().tolist() == [[torch.tensor(-3e38).item(), -INF, -INF]]
+
+
+def test_many_lists_with_equal_numbers():
+    # 256 beams of 10 parts each, more equal totals than there is room for
+    gen = torch.Generator(device=DEV).manual_seed(23)
+    logits = torch.randint(0, 2, (1, 256, 80000), device=DEV, generator=gen).to(BF16)
+    logits[0, 17, 79999] = 2
+    scores = torch.zeros(1, 256, device=DEV)
+    scores[0, ::3] = -INF
+    # every row's sum is another, so beams differ; equal rows are equal
+    logits[0, 40:60] = logits[0, 40]
+    check(api.beam_select(logits, scores, width=64), logits, scores, 64)
+    logits[:] = 1
+    c = api.beam_select(logits, scores, width=64)
+    assert c.parents.cpu().tolist() == [[1] * 64] and c.tokens.cpu().tolist() == [list(range(64))]
+
+
 @pytest.mark.parametrize("dtype", [F32, F16])
 def test_masks_and_what_offers_nothing(dtype):
     logits, scores = make(8, 4, 5000, dtype, 11)
