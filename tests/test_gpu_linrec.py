@@ -313,6 +313,26 @@ def test_step(types, d, t):
         assert torch.equal(state.cpu()[left], pool[left])
 
 
+@pytest.mark.parametrize("n,d", [(3000, 1), (1111, 12), (700, 104), (130, 255), (129, 256), (65, 257), (30, 704), (20, 1001), (9, 1024), (9, 1028),
+                                 (5, 2052), (3, 5000)])
+@pytest.mark.parametrize("types", TYPES, ids=str)
+def test_step_of_many_sequences_and_of_many_channels(types, n, d):
+    t = 2
+    x, g, _ = make(n * t, d, *types, n)
+    pool, _ = states(n + 3, d, 30)
+    slots = torch.randperm(n + 3, generator=torch.Generator().manual_seed(d))[:n].to(torch.int32)
+    state = pool.to(DEV)
+    h = api.linear_recurrence_step(x.view(n, t, d).to(DEV), g.view(n, t, d).to(DEV), state, tied=True, slots=slots.to(DEV)).cpu()
+    # a sequence's channels are as other channels
+    flat = lambda y: y.view(n, t, d).transpose(0, 1).reshape(t, n * d)  # noqa: E731
+    want = ref.sequence(flat(x), flat(g), pool[slots.long()].reshape(n * d), True)
+    ref.check(flat(h), want["h"])
+    ref.check(state.cpu()[slots.long()].reshape(n * d), want["state"])
+    rest = torch.ones(n + 3, dtype=torch.bool)
+    rest[slots.long()] = False
+    assert torch.equal(state.cpu()[rest], pool[rest])
+
+
 def test_step_takes_whole_prompts():
     x, g, _ = make(2 * 500, 64, F32, F32, 29)
     state = torch.zeros(2, 64, device=DEV)
