@@ -140,8 +140,9 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
         TX *dx = static_cast<TX *>(a.dx) + (long long)(r.first + R - 1) * a.channels + r.ch;
         TG *dg = static_cast<TG *>(a.dg) + (long long)(r.first + R - 1) * a.channels + r.ch;
         auto part = [&](int q, float2 h, auto marked) {
+            constexpr int UNROLL = decltype(marked)::value ? 1 : kPart;
             float2 f[kPart], was[kPart];   // the states before each token; with tied inputs less the token's x, as dg needs them
-#pragma unroll
+#pragma unroll UNROLL
             for (int i = 0; i < kPart; ++i) {
                 const Token t = token_at(gs, q * kPart + i);
                 const float2 x = pair_at(xs, q * kPart + i);
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
                 was[i] = TIED ? make_float2(h.x - x.x, h.y - x.y) : h;
                 h = t.apply(h, t.weigh(x, TIED));
             }
-#pragma unroll
+#pragma unroll UNROLL
             for (int i = kPart - 1; i >= 0; --i) {
                 if (marked && (r.ends >> (q * kPart + i) & 1)) mu = r.end(a, m, q * kPart + i);
                 const float2 lam = add2(pair_at(ds, q * kPart + i), mu);

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
                 h = t.apply(h, t.weigh(pair_at(xs, i), TIED));
             }
         } else {
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < R; ++i) {
                 const float2 g = pair_at(gs, i);
                 const Token t = Token::of(g);
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
                 out += a.channels;
             }
         } else {
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < R; ++i) {
                 const Token t = token_at(gs, i);
                 if (r.starts >> i & 1) h = r.start(a, m, i);
