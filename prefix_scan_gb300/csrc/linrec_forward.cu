@@ -7,7 +7,7 @@
 // other's waits (issue slots 38 instead of 56% in use): one sequence of 131072 tokens 185 us instead of 170 (with runs of 16).  Factors of 32-bit log
 // decays take their place in shared memory; those of 16 bits are computed again, as they would be rounded there.
 //
-// 48 ragged prompts, 24571 tokens by 4096 bf16 channels with f32 log decays: 217 us, 3.7 TB/s.  One sequence of 131072 tokens by
+// 48 ragged prompts, 24571 tokens by 4096 bf16 channels with f32 log decays: 212 us, 3.8 TB/s.  One sequence of 131072 tokens by
 // 512 bf16 channels: 142 us, 2.8 TB/s (its 16 blocks of channels are one chain of 256 tiles each).
 #include <type_traits>
 
