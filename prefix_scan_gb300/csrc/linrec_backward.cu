@@ -3,8 +3,8 @@
 //
 // Memory bounds it from below (x, g and dh are read once, dx and dg are written once), instructions in fact: 58 a number.  The
 // states are not read: the forward pass keeps the one before each tile (in 32 bits), and the tile is scanned again from there,
-// so that 16-bit types, too, get the gradient of g from states of 32 bits.  What runs backward is mu, a state's gradient handed to the token before; its
-// look-back goes over the tiles from the last one.
+// so that 16-bit types, too, get the gradient of g from states of 32 bits.  What runs backward is mu, a state's gradient
+// handed to the token before; its look-back goes over the tiles from the last one.
 //
 // A run's first scan is forward only: what it adds to mu is the sum of P_i dh_i, P_i the product of its factors up to token i.
 // The second takes eight tokens at a time, the last ones first: forward for the states before them, from what the first
