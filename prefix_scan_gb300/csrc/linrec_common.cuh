@@ -583,7 +583,8 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
         while (true) {
             const bool found = at == p - 1;
             bool just = false;
-            if (!have_sums && (found ? mbar_wait_suspend(&sm.summed, turn, 2000) || true : mbar_over(&sm.summed, turn)))
+            // Lanes may see a phase end at different times, and all of them shuffle below: so all have seen it, or none has.
+            if (!have_sums && (found ? mbar_wait_suspend(&sm.summed, turn, 2000) || true : __all_sync(FULL, mbar_over(&sm.summed, turn))))
                 have_sums = just = true;
             if (found && have_sums && !passed) {   // not before all have their sums: some may still wait for the last tile's state
                 passed = true;
