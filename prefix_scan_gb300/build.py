@@ -97,15 +97,16 @@ TINY_TILE_DEFINES = {"PS_ITEMS32": 4, "PS_ITEMS64": 4, "PS_LOOKBACK_K": 2, "PS_R
 
 
 def build_variant(name: str, defines: dict[str, int], exclude: tuple[str, ...] = ("scan_noalloc.cu",),
-                  force: bool = False) -> Path:
+                  force: bool = False, only: list[Path] | None = None) -> Path:
     """Build a second copy of the library with other geometry macros, for
     stress tests: ``_build/<name>/libprefixscan_<name>.so`` (not the
-    product library).  No-op when it is newer than every source."""
+    product library), of all sources but ``exclude`` or of ``only`` these.
+    No-op when it is newer than every source."""
     obj_dir = BUILD_DIR / name
     target = obj_dir / f"libprefixscan_{name}.so"
     if not force and target.exists() and all(p.stat().st_mtime <= target.stat().st_mtime for p in _deps()):
         return target
-    srcs = [p for p in sources() if p.name not in exclude]
+    srcs = only if only is not None else [p for p in sources() if p.name not in exclude]
     extra = [f"-D{k}={v}" for k, v in sorted(defines.items())]
     return _compile_and_link(srcs, obj_dir, target, extra, False)
 

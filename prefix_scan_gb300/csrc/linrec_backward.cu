@@ -39,15 +39,9 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
     extern __shared__ __align__(128) unsigned char raw[];
     Space &space = *reinterpret_cast<Space *>(raw);
     Shared<R> &sm = space.shared;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool tensor_copies = a.tensor_copies;
-    if (tid == 0) {
-        mbar_init(&sm.landed, 1);
-        mbar_init(&sm.summed, kLrWarps);
-        mbar_init(&sm.done, kLrWarps);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
+    sm.init();
 
     if (warp == kLrWarps) {
         ninth_warp<R, true>(a, sm, a.dht, a.dh0, tensor_copies, [&](const Place &at) {
@@ -68,9 +62,8 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
         const Marks<TOKENS> &m = sm.marks[turn];
         const long long ch = (long long)place.block * kLrWide + 2 * lr_pair();
         const float2 first = get_f32(a.start + (long long)place.tile * a.channels + ch, ch < a.channels, ch + 1 < a.channels);
-        bool whole_tile = true;
         if (tensor_copies) {
-            whole_tile = mbar_wait_suspend(&sm.landed, turn, 2000);
+            sm.wait_for_inputs(turn);
         } else {
             const uint32_t n = (uint32_t)place.tile * TOKENS;
             const long long c = (long long)place.block * kLrWide;
@@ -81,13 +74,13 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
         }
         meet(1);
         const Place next_place = sm.place[turn ^ 1];
-        const Run<R> r(a, m, place);
+        Run<R> r(a, m, place);
         if (tensor_copies && r.first < (uint32_t)a.total && r.first + R > (uint32_t)a.total) {
             load_last_run<TG, R>(gs, a.g, a, r.first, r.ch);
             load_last_run<TX, R>(xs, a.x, a, r.first, r.ch);
             load_last_run<TX, R>(ds, a.dout, a, r.first, r.ch);
         }
-        float2 add = both(0.f), s = both(whole_tile ? 0.f : __uint_as_float(0x7fffffffu)), mu = both(0.f), p = both(1.f);
+        float2 add = both(0.f), s = both(0.f), mu = both(0.f), p = both(1.f);
         float2 kept_h[R / kPart], kept_p[R / kPart];   // before each part
 #pragma unroll
         for (int q = 0; q < R / kPart; ++q) {
@@ -128,6 +121,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
                 if (r.starts >> i & 1) mu = both(0.f);   // dh0 takes it
             }
         }
+        if (sm.lost) s = mu = both(nan_f32());   // whatever was read, mu is NaN, and so is all that is made of it
         const float2 own = factor_of_sum(s);
         const Ahead behind = join_runs<true>(s, own, mu, (r.starts | r.ends) != 0, (m.starts | m.ends) != 0, sm.sums.s,
                                              sm.sums.f, sm.sums.b);
@@ -140,6 +134,10 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
                                            [&](int w) { return warp_cut<R, false>(m, w); });
         mu = before_run<true>(sm.before[lr_pair()], behind, sm.sums.f, sm.sums.b, (m.starts | m.ends) != 0,
                               [&](int w) { return warp_cut<R, true>(m, w); });
+        if (sm.lost) {
+            mu = both(nan_f32());
+            r.ends = 0;
+        }
         TX *dx = static_cast<TX *>(a.dx) + (long long)(r.first + R - 1) * a.channels + r.ch;
         TG *dg = static_cast<TG *>(a.dg) + (long long)(r.first + R - 1) * a.channels + r.ch;
         auto part = [&](int q, float2 h, auto marked) {
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
                     }
                     if (r.starts >> (q * kPart + i) & 1) {
                         if (a.dh0 != nullptr) put_f32(a.dh0 + m.seq[lr_run() * R + q * kPart + i] * a.channels + r.ch, mu, r.in0, r.in1);
-                        mu = both(0.f);
+                        mu = both(sm.lost ? nan_f32() : 0.f);
                     }
                 }
                 dx -= a.channels;

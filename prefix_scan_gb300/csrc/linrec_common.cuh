@@ -78,6 +78,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float nan_f32() { return __uint_as_float(0x7fffffffu); }
 
 // ---- factors ---------------------------------------------------------------------------
 
@@ -414,7 +415,7 @@ template <int R> struct Run {
 constexpr uint32_t kUntold = 0xffffffffu;
 
 __device__ __forceinline__ bool told(float x) { return __float_as_uint(x) != kUntold; }
-__device__ __forceinline__ float telling(float x) { return told(x) ? x : __uint_as_float(0x7fffffffu); }
+__device__ __forceinline__ float telling(float x) { return told(x) ? x : nan_f32(); }
 __device__ __forceinline__ bool told(float2 x) { return told(x.x) && told(x.y); }
 __device__ __forceinline__ bool told(float4 x) { return told(x.x) && told(x.y) && told(x.z) && told(x.w); }
 __device__ __forceinline__ void tell(float2 *p, float2 x) {
@@ -483,6 +484,22 @@ __device__ __forceinline__ float2 before_run(float2 h, const Ahead &a, const flo
     return lr_group() == (BACKWARD ? 1 : 0) ? h : a.cut ? a.b : apply(a.f, h, a.b);
 }
 
+// How long anything is waited for; two seconds, which no correct launch takes.  (Tests of what follows then set another limit.)
+#ifndef PS_LINREC_WAIT_LIMIT_NS
+#define PS_LINREC_WAIT_LIMIT_NS 2000000000ull
+#endif
+constexpr unsigned long long kLrWaitLimitNs = PS_LINREC_WAIT_LIMIT_NS;
+// Waits for a phase in tries of up to `ns` nanoseconds; false if that ran out.
+__device__ __forceinline__ bool mbar_wait_limited(uint64_t *bar, uint32_t parity, uint32_t ns, unsigned long long limit = kLrWaitLimitNs) {
+    if (mbar_try_wait_for(bar, parity, ns)) return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 0; i < kMbarSpinCap; ++i) {
+        if (mbar_try_wait_for(bar, parity, ns)) return true;
+        if ((i & 15u) == 15u && global_ns() - t0 > limit) break;
+    }
+    return false;
+}
+
 // What a CTA's warps share beside its tiles.
 constexpr int kLrWindow = 8;   // tiles that a round of the look-back reads
 static_assert(kLrWindow <= kLinrecSlack, "a round stays in the workspace");
@@ -495,6 +512,23 @@ template <int R> struct Shared {
     Marks<TOKENS> marks[2];
     Place place[2];
     uint64_t landed, summed, done;   // the tile's inputs are there; all runs are summed; the inputs are no longer needed
+    volatile int lost;               // a wait for inputs, or for their place, ran out: see wait_for_inputs
+    // All lanes, before barriers and anything else.
+    __device__ __forceinline__ void init() {
+        if (threadIdx.x == 0) {
+            mbar_init(&landed, 1);
+            mbar_init(&summed, kLrWarps);
+            mbar_init(&done, kLrWarps);
+            lost = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncthreads();
+    }
+    // Waits for a tile's inputs (a compute warp's lane).  Where that runs out, the tile and all that the CTA takes after it
+    // are lost: nothing is copied any more, what was not read is not written over, and the outputs are NaN.
+    __device__ __forceinline__ void wait_for_inputs(int turn) {
+        if (!mbar_try_wait_for(&landed, turn, 2000) && !lost && !mbar_wait_limited(&landed, turn, 2000)) lost = 1;
+    }
     // Of a whole warp: it needs its inputs no longer, and what it wrote in their place comes before the next copies.
     __device__ __forceinline__ void release() {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -526,7 +560,7 @@ __device__ __forceinline__ void meet(int id) { named_barrier(id, kLrThreads); }
 // tiles has told, from at + 1 on, or, with nothing known, further and further back in the chain; the last state told
 // replaces h, the maps behind it are applied.  Rounds begin while the tile's inputs are summed; if the state before it is not
 // known when they are, the tile's map is told at once, for others to pass over it.  A chain's first tile always tells its
-// state.  Waits end after about two seconds, with NaN.
+// state.  Waits end after kLrWaitLimitNs, with NaN.
 template <int R, bool BACKWARD, typename Issue>
 __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, const float *from, float *to, bool tensor_copies,
                                            Issue issue) {
@@ -543,14 +577,21 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
         return Place{BACKWARD ? a.tiles - 1 - p : p, (int)(ticket % (unsigned)a.blocks)};
     };
     auto take = [&]() { return chained ? atomicAdd(a.ticket, 1u) + 1 : all; };   // from -1 on
+    auto copy = [&](const Place &at) {
+#ifdef PS_TESTING_LOST_TILE   // of the first block: a tile that is never copied, so that the wait for it runs out
+        if (at.tile == PS_TESTING_LOST_TILE && at.block == 0) return;
+#endif
+        issue(at);
+    };
     unsigned ticket = blockIdx.x, next = all;
     if (chained && lane == 0) ticket = take();
     Place place = place_of(__shfl_sync(FULL, ticket, 0));
     if (lane == 0) {
         sm.place[0] = place;
-        if (tensor_copies && place.tile >= 0) issue(place);
+        if (tensor_copies && place.tile >= 0) copy(place);
         next = take();
     }
+    int last_turn = 0;   // whose inputs were copied last
     __syncwarp();
     pass_by(2);
     for (int turn = 0, first = 1; place.tile >= 0; turn ^= 1, first = 0) {
@@ -562,8 +603,12 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
         __syncwarp();
         pass_by(1);
         if (!first && tensor_copies) {
-            mbar_wait_suspend(&sm.done, turn ^ 1, 1000);   // with the tile before
-            if (lane == 0) issue(place);
+            if (!mbar_wait_limited(&sm.done, turn ^ 1, 1000)) sm.lost = 1;   // with the tile before
+            __syncwarp();
+            if (!sm.lost) {
+                if (lane == 0) copy(place);
+                last_turn = turn;
+            }
             __syncwarp();
         }
         if (lane == 0) next = take();
@@ -584,7 +629,9 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
             const bool found = at == p - 1;
             bool just = false;
             // Lanes may see a phase end at different times, and all of them shuffle below: so all have seen it, or none has.
-            if (!have_sums && (found ? mbar_wait_suspend(&sm.summed, turn, 2000) || true : __all_sync(FULL, mbar_over(&sm.summed, turn))))
+            // Sums come after the wait for inputs, and the limit of their wait after its.
+            if (!have_sums && (found ? mbar_wait_limited(&sm.summed, turn, 2000, 4 * kLrWaitLimitNs) || true
+                                     : __all_sync(FULL, mbar_over(&sm.summed, turn))))
                 have_sums = just = true;
             if (found && have_sums && !passed) {   // not before all have their sums: some may still wait for the last tile's state
                 passed = true;
@@ -653,8 +700,8 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
                 if (!have_sums && at < p - 1) mbar_try_wait_for(&sm.summed, turn, 300);   // others may tell more meanwhile
                 if (have_sums && ++polls > 4) {
                     if (polls == 5) t0 = global_ns();
-                    if (__shfl_sync(FULL, (int)(global_ns() - t0 > kMbarWaitLimitNs), 0)) {
-                        h = both(__uint_as_float(0x7fffffffu));
+                    if (__shfl_sync(FULL, (int)(global_ns() - t0 > kLrWaitLimitNs), 0)) {
+                        h = both(nan_f32());
                         at = p - 1;
                     }
                 }
@@ -663,6 +710,7 @@ __device__ __forceinline__ void ninth_warp(const LinrecArgs &a, Shared<R> &sm, c
         }
         place = next_place;
     }
+    if (tensor_copies && sm.lost) mbar_wait_limited(&sm.landed, last_turn, 2000);   // what is under way still writes to this CTA's memory
 }
 
 }  // namespace

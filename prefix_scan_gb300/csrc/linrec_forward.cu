@@ -30,15 +30,9 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
     extern __shared__ __align__(128) unsigned char raw[];
     Space &space = *reinterpret_cast<Space *>(raw);
     Shared<R> &sm = space.shared;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool tensor_copies = a.tensor_copies;
-    if (tid == 0) {
-        mbar_init(&sm.landed, 1);
-        mbar_init(&sm.summed, kLrWarps);
-        mbar_init(&sm.done, kLrWarps);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
+    sm.init();
 
     if (warp == kLrWarps) {
         ninth_warp<R, false>(a, sm, a.h0, a.ht, tensor_copies, [&](const Place &at) {
@@ -55,9 +49,8 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
     Place place = sm.place[0];
     for (int turn = 0; place.tile >= 0; turn ^= 1) {
         const Marks<TOKENS> &m = sm.marks[turn];
-        bool whole_tile = true;
         if (tensor_copies) {
-            whole_tile = mbar_wait_suspend(&sm.landed, turn, 2000);
+            sm.wait_for_inputs(turn);
         } else {
             load_tile<TG, R>(gs, a.g, a, (uint32_t)place.tile * TOKENS, (long long)place.block * kLrWide);
             load_tile<TX, R>(xs, a.x, a, (uint32_t)place.tile * TOKENS, (long long)place.block * kLrWide);
@@ -65,12 +58,12 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
         }
         meet(1);
         const Place next_place = sm.place[turn ^ 1];
-        const Run<R> r(a, m, place);
+        Run<R> r(a, m, place);
         if (tensor_copies && r.first < (uint32_t)a.total && r.first + R > (uint32_t)a.total) {
             load_last_run<TG, R>(gs, a.g, a, r.first, r.ch);
             load_last_run<TX, R>(xs, a.x, a, r.first, r.ch);
         }
-        float2 h = both(0.f), s = both(whole_tile ? 0.f : __uint_as_float(0x7fffffffu));
+        float2 h = both(0.f), s = both(0.f);
         if (!r.marked) {
 #pragma unroll 4
             for (int i = 0; i < R; ++i) {
@@ -91,6 +84,8 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
                 h = t.apply(h, t.weigh(pair_at(xs, i), TIED));
             }
         }
+        const bool lost = sm.lost;   // whatever was read, h is NaN
+        if (lost) h = s = both(nan_f32());
         const Ahead ahead = join_runs<false>(s, factor_of_sum(s), h, r.starts != 0, m.starts != 0, sm.sums.s, sm.sums.f,
                                              sm.sums.b);
         __syncwarp();
@@ -99,6 +94,10 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
         meet(3);
         h = before_run<false>(sm.before[lr_pair()], ahead, sm.sums.f, sm.sums.b, m.starts != 0,
                               [&](int w) { return warp_cut<R, false>(m, w); });
+        if (lost) {
+            h = both(nan_f32());
+            r.starts = 0;
+        }
         if (a.start != nullptr && (r.first & (a.start_tokens - 1)) == 0 && r.first < (uint32_t)a.total)
             put_f32(a.start + r.first / a.start_tokens * a.channels + r.ch, h, r.in0, r.in1);
         TX *out = static_cast<TX *>(a.h) + (long long)r.first * a.channels + r.ch;
