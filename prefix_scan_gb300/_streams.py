@@ -21,3 +21,12 @@ def enter(device: torch.device, stream):
     ctx.enter_context(torch.cuda.device(device))
     ctx.enter_context(torch.cuda.stream(s))
     return s.cuda_stream, ctx
+
+
+def read_here(device: torch.device, *tensors: torch.Tensor | None) -> None:
+    """Marks tensors of other streams as read by what the current stream (that of the call, inside its context) has enqueued:
+    their memory is not handed out before that is done, even if they are dropped as soon as the call returns."""
+    used = torch.cuda.current_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(used)

@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._streams import enter
+from ._streams import enter, read_here
 
 REAL_CODES = {torch.float32: _lib.PS_REAL_F32, torch.bfloat16: _lib.PS_REAL_BF16, torch.float16: _lib.PS_REAL_F16}
 
@@ -171,6 +171,8 @@ def _forward(fn, q, k, v, g, beta, scale, cu_seqlens, initial_state, output_fina
         st = lib.ps_delta_forward(shape, inputs, initial_state.data_ptr() if initial_state is not None else None,
                                   final_state.data_ptr() if final_state is not None else None, out.data_ptr(), train,
                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+        if train and stream is not None:   # what is saved may be dropped while the stream given still reads it
+            read_here(device, q, k, cu_seqlens, workspace)
     _lib.check("ps_delta_forward", st)
     return out, final_state, plan, shape, states, workspace, s
 
@@ -251,11 +253,8 @@ def delta_rule_backward(saved: DeltaRuleSaved, d_o: torch.Tensor, *, d_final_sta
         st = lib.ps_delta_backward(saved.shape, *ts, ptr(d_final_state), ptr(dq),
                                    ptr(dk), ptr(dv), ptr(dg), ptr(dbeta), ptr(dh0), saved.workspace.data_ptr(),
                                    saved.workspace.numel() * saved.workspace.element_size(), s)
-        if s != saved.stream:   # `saved` may be dropped while this stream still reads what it holds
-            used = torch.cuda.current_stream(q.device)
-            for t in (saved.workspace, q, k, saved.cu_seqlens, d_o, d_final_state):
-                if t is not None:
-                    t.record_stream(used)
+        if stream is not None or s != saved.stream:   # `saved` may be dropped while this stream still reads what it holds
+            read_here(q.device, saved.workspace, q, k, saved.cu_seqlens, d_o, d_final_state)
     _lib.check("ps_delta_backward", st)
     return dq, dk, dv, dg, dbeta, dh0
 

@@ -14,7 +14,7 @@ from dataclasses import dataclass, field
 import torch
 
 from . import _lib
-from ._streams import enter
+from ._streams import enter, read_here
 from .delta import REAL_CODES, _check_state, _workspace
 
 
@@ -147,6 +147,8 @@ def _forward(fn, x, g, tied, cu_seqlens, initial_state, output_final_state, out,
                                    initial_state.data_ptr() if initial_state is not None else None,
                                    final_state.data_ptr() if final_state is not None else None, out.data_ptr(), train,
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+        if train and stream is not None:   # what is saved may be dropped while the stream given still reads it
+            read_here(device, x, g, cu_seqlens, initial_state, workspace)
     _lib.check("ps_linrec_forward", st)
     return out, final_state, plan, shape, states, workspace, s
 
@@ -222,11 +224,8 @@ def linear_recurrence_backward(saved: LinearRecurrenceSaved, d_h: torch.Tensor, 
                                     d_final_state.data_ptr() if d_final_state is not None else None, dx.data_ptr(), dg.data_ptr(),
                                     dh0.data_ptr() if dh0 is not None else None, saved.workspace.data_ptr(),
                                     saved.workspace.numel() * saved.workspace.element_size(), s)
-        if s != saved.stream:   # `saved` may be dropped while this stream still reads what it holds
-            used = torch.cuda.current_stream(x.device)
-            for t in (saved.workspace, x, g, cu, h0, d_h, d_final_state):
-                if t is not None:
-                    t.record_stream(used)
+        if stream is not None or s != saved.stream:   # `saved` may be dropped while this stream still reads what it holds
+            read_here(x.device, saved.workspace, x, g, cu, h0, d_h, d_final_state)
     _lib.check("ps_linrec_backward", st)
     return dx, dg, dh0
 
