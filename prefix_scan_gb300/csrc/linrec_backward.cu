@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
 #pragma unroll 4
                 for (int i = q * kPart; i < (q + 1) * kPart; ++i) {
                     const float2 g = pair_at(gs, i);
-                    const Token t = Token::of(g);
+                    const Token t = Token::of<kWeights<TX, TIED>>(g);
                     keep(gs, i, t);
                     s = add2(s, g);
                     add = t.apply(add, t.weigh(pair_at(xs, i), TIED));
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
 #pragma unroll 1
                 for (int i = q * kPart; i < (q + 1) * kPart; ++i) {
                     const float2 g = pair_at(gs, i);
-                    const Token t = Token::of(g);
+                    const Token t = Token::of<kWeights<TX, TIED>>(g);
                     keep(gs, i, t);
                     s = add2(s, g);
                     if (r.starts >> i & 1) {
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
 #pragma unroll 1
             for (int i = R - 1; i >= 0; --i) {
                 if (r.ends >> i & 1) mu = r.end(a, m, i);
-                mu = token_at(gs, i).decayed(add2(pair_at(ds, i), mu));
+                mu = token_at<kWeights<TX, TIED>>(gs, i).decayed(add2(pair_at(ds, i), mu));
                 if (r.starts >> i & 1) mu = both(0.f);   // dh0 takes it
             }
         }
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_backward_kernel(const
             float2 f[kPart], was[kPart];   // the states before each token; with tied inputs less the token's x, as dg needs them
 #pragma unroll UNROLL
             for (int i = 0; i < kPart; ++i) {
-                const Token t = token_at(gs, q * kPart + i);
+                const Token t = token_at<kWeights<TX, TIED>>(gs, q * kPart + i);
                 const float2 x = pair_at(xs, q * kPart + i);
                 if (marked && (r.starts >> (q * kPart + i) & 1)) h = r.start(a, m, q * kPart + i);
                 f[i] = t.f;

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
 #pragma unroll 4
             for (int i = 0; i < R; ++i) {
                 const float2 g = pair_at(gs, i);
-                const Token t = Token::of(g);
+                const Token t = Token::of<kWeights<TX, TIED>>(g);
                 keep(gs, i, t);
                 s = add2(s, g);
                 h = t.apply(h, t.weigh(pair_at(xs, i), TIED));
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
 #pragma unroll 2
             for (int i = 0; i < R; ++i) {
                 const float2 g = pair_at(gs, i);
-                const Token t = Token::of(g);
+                const Token t = Token::of<kWeights<TX, TIED>>(g);
                 keep(gs, i, t);
                 s = add2(s, g);
                 if (r.starts >> i & 1) h = r.start(a, m, i);
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
         if (r.plain) {
 #pragma unroll 4
             for (int i = 0; i < R; ++i) {
-                const Token t = token_at(gs, i);
+                const Token t = token_at<kWeights<TX, TIED>>(gs, i);
                 h = t.apply(h, t.weigh(pair_at(xs, i), TIED));
                 if (r.in0) *reinterpret_cast<typename Pair<TX>::type *>(out) = Pair<TX>::put(h);
                 out += a.channels;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kLrThreads, CTAS) linrec_forward_kernel(const 
         } else {
 #pragma unroll 2
             for (int i = 0; i < R; ++i) {
-                const Token t = token_at(gs, i);
+                const Token t = token_at<kWeights<TX, TIED>>(gs, i);
                 if (r.starts >> i & 1) h = r.start(a, m, i);
                 h = t.apply(h, t.weigh(pair_at(xs, i), TIED));
                 if (r.first + i - m.lo < m.held) put_pair<TX>(out, h, r.whole, r.in0, r.in1);

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kStepThreads) linrec_step_kernel(const LinrecS
 #pragma unroll
                 for (int v = 0; v < V; v += 2) {
                     constexpr int N = V > 1;   // a channel alone takes the place of both
-                    const Token t = Token::of(make_float2(to_f32<TG>(gi[k].v[v]), to_f32<TG>(gi[k].v[v + N])));
+                    const Token t = Token::of<kWeights<TX, TIED>>(make_float2(to_f32<TG>(gi[k].v[v]), to_f32<TG>(gi[k].v[v + N])));
                     const float2 y = make_float2(to_f32<TX>(xi[k].v[v]), to_f32<TX>(xi[k].v[v + N]));
                     const float2 next = t.apply(make_float2(h[k].v[v], h[k].v[v + N]), t.weigh(y, TIED));
                     h[k].v[v] = next.x;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kStepThreads) linrec_step_narrow_kernel(const 
 #pragma unroll
                 for (int v = 0; v < V; v += 2) {
                     constexpr int N = V > 1;   // a channel alone takes the place of both
-                    const Token t = Token::of(make_float2(to_f32<TG>(gi[k].v[v]), to_f32<TG>(gi[k].v[v + N])));
+                    const Token t = Token::of<kWeights<TX, TIED>>(make_float2(to_f32<TG>(gi[k].v[v]), to_f32<TG>(gi[k].v[v + N])));
                     const float2 y = make_float2(to_f32<TX>(xi[k].v[v]), to_f32<TX>(xi[k].v[v + N]));
                     const float2 next = t.apply(make_float2(h[k].v[v], h[k].v[v + N]), t.weigh(y, TIED));
                     h[k].v[v] = next.x;
