@@ -74,6 +74,13 @@ def search(lens: list, beams: int, steps: int, vocab: int = 300, channels: int =
     return scores, off
 
 
+def gradients(x: torch.Tensor, g: torch.Tensor, cu: torch.Tensor, target: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The layer's outputs h over packed prompts, and the gradients of the loss |h - target|^2 / 2 of its inputs and log decays."""
+    h, _, saved = api.linear_recurrence_forward(x, g, tied=True, cu_seqlens=cu)
+    dx, dg, _ = api.linear_recurrence_backward(saved, h - target)
+    return h, dx, dg
+
+
 def train(lens: list, vocab: int = 300, channels: int = 96, seed: int = 2) -> tuple[float, float]:
     """The loss |h - target|^2 / 2 before and after a short step of the inputs and log decays against its gradient."""
     model = Model(vocab, channels, seed)
@@ -84,10 +91,8 @@ def train(lens: list, vocab: int = 300, channels: int = 96, seed: int = 2) -> tu
     target = torch.randn(x.shape, device="cuda", generator=gen)
     losses = []
     for _ in range(2):
-        h, _, saved = api.linear_recurrence_forward(x, g, tied=True, cu_seqlens=cu)
-        d = h - target
-        losses.append(float(d.square().sum() / 2))
-        dx, dg, _ = api.linear_recurrence_backward(saved, d)
+        h, dx, dg = gradients(x, g, cu, target)
+        losses.append(float((h - target).square().sum() / 2))
         x, g = x - 0.05 * dx, (g - 0.01 * dg).clamp(max=0)
     return losses[0], losses[1]
 
