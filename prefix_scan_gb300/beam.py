@@ -17,6 +17,11 @@ class BeamChoice(NamedTuple):
     ended: torch.Tensor | None
 
 
+def _check_sizes(fn, beams, width):
+    if beams > _lib.PS_BEAM_MAX_BEAMS or not 1 <= width <= _lib.PS_BEAM_MAX_WIDTH:
+        raise ValueError(f"{fn}: up to {_lib.PS_BEAM_MAX_BEAMS} beams and {_lib.PS_BEAM_MAX_WIDTH} candidates are supported")
+
+
 def _check(fn, logits, scores, width, ended, eos_token):
     device = logits.device
     if not logits.is_cuda:
@@ -27,8 +32,7 @@ def _check(fn, logits, scores, width, ended, eos_token):
         raise ValueError(f"{fn}: logits are [batch, beams, vocabulary]")
     if logits.shape[-1] > 1 and logits.numel() > 0 and logits.stride(-1) != 1:
         raise ValueError(f"{fn}: logits must be contiguous in their last dimension")
-    if logits.shape[1] > _lib.PS_BEAM_MAX_BEAMS or not 1 <= width <= _lib.PS_BEAM_MAX_WIDTH:
-        raise ValueError(f"{fn}: up to {_lib.PS_BEAM_MAX_BEAMS} beams and {_lib.PS_BEAM_MAX_WIDTH} candidates are supported")
+    _check_sizes(fn, logits.shape[1], width)
     for name, t, dtype in (("scores", scores, torch.float32), ("ended", ended, torch.uint8)):
         if t is not None and (t.dtype != dtype or t.shape != logits.shape[:2] or t.device != device or not t.is_contiguous()):
             raise ValueError(f"{fn}: {name} must be a contiguous {dtype} CUDA tensor [batch, beams]")
@@ -93,5 +97,6 @@ def beam_workspace_size(logits: torch.Tensor, *, width: int | None = None) -> in
     if logits.dim() != 3:
         raise ValueError("beam_workspace_size: logits are [batch, beams, vocabulary]")
     w = logits.shape[1] if width is None else width
+    _check_sizes("beam_workspace_size", logits.shape[1], w)
     return int(_lib.load().ps_beam_workspace_size(_lib.BEAM_SHAPE.pack(
         logits.shape[0], logits.shape[1], w, logits.shape[2], logits.stride(0), logits.stride(1), REAL_CODES[logits.dtype], -1)))

@@ -98,13 +98,15 @@ def linear_recurrence_workspace_size(x: torch.Tensor, cu_seqlens: torch.Tensor |
     that :func:`linear_recurrence_forward` leaves for the backward pass)."""
     if x.dtype not in REAL_CODES:
         raise TypeError(f"linear_recurrence_workspace_size supports float32, bfloat16 and float16, not {x.dtype}")
+    if gate_dtype not in (torch.float32, x.dtype):
+        raise TypeError(f"linear_recurrence_workspace_size supports log decays of x's type or float32, not {gate_dtype} with {x.dtype}")
     packed = cu_seqlens is not None
     if x.dim() != (2 if packed else 3):
         raise ValueError("linear_recurrence_workspace_size: x is [sequences, tokens, channels], or [tokens, channels] packed")
     code = REAL_CODES[x.dtype]
     shape = _lib.LINREC_SHAPE.pack(cu_seqlens.numel() - 1 if packed else x.shape[0], x.shape[0] if packed else x.shape[1],
                                    cu_seqlens.data_ptr() if packed else 0, x.shape[-1], code,
-                                   REAL_CODES.get(gate_dtype, -1), 0)
+                                   REAL_CODES[gate_dtype], 0)
     return int(_lib.load().ps_linrec_workspace_size(shape, int(train)))
 
 
