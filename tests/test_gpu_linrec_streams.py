@@ -35,3 +35,21 @@ def test_both_calls_on_a_stream_that_is_not_the_tensors():
     torch.cuda.synchronize()
     del new
     check_packed({"h": h, "state": state, "dx": dx, "dg": dg, "dh0": dh0}, *host[:2], lens, host[2], h0, dht, False)
+
+
+def test_two_calls_at_once():
+    # their tiles share the SMs, each call's wait for one another only
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    data = [[t.to(DEV).view(4, 2048, 700) for t in make(4 * 2048, 700, BF16, BF16, 50 + i)] for i in range(2)]
+
+    def run(x, g, dh, stream=None):
+        h, state, saved = api.linear_recurrence_forward(x, g, output_final_state=True, stream=stream)
+        return (h, state, *api.linear_recurrence_backward(saved, dh, stream=stream)[:2])
+
+    want = [run(*d) for d in data]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [run(*d, stream=s) for d, s in zip(data, sides)]
+        torch.cuda.synchronize()
+        for one, w in zip(got, want):
+            assert all(torch.equal(a, b) and a.isfinite().all() for a, b in zip(one, w))
