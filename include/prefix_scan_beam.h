@@ -7,16 +7,20 @@
  * What it returns is made for what comes after it: `parents` name the rows whose
  * pages ps_pages_fork or ps_pages_reorder (prefix_scan_pages.h) hand on.
  *
- * Order: by total, taken in 64 bits; equal totals by the lower beam, then, within
- * a beam, by the larger logit, then by the lower token.  (A beam's own candidates
- * are compared by their logits, exactly.)  Results do not depend on
+ * Order: by total; equal totals by the lower beam, then, within a beam, by the
+ * larger logit, then by the lower token.  A beam's own candidates are compared by
+ * their logits, exactly.  Totals of different beams are compared in 64 bits, but
+ * each row's log sum exp comes from exponentials and sums of 32 bits: it is off by
+ * 2^-19 at most, as a rule by 2^-22, so beams whose totals are closer than that may
+ * change places.  Equal rows have equal sums, and results do not depend on
  * scheduling.
  *
  * What offers nothing: a token whose logit is -infinity; a beam whose score is not
  * finite; a beam with a NaN or +infinity among its logits.  Where fewer than
  * `width` candidates are left, the rest of the item's results have score
  * -infinity, parent -1 and token -1 (which the page operations take as a row with
- * no parent).
+ * no parent).  A total below what f32 can hold is chosen in its order like any
+ * other; its score is returned as -infinity, with its parent and token.
  *
  * Beams at their end: where `ended` is not NULL and ended[row] != 0, the row's
  * logits are not read; it offers itself once, with its score as it is and

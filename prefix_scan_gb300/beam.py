@@ -53,8 +53,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, width: int | None
 
     ``logits``: [batch, beams, vocabulary], float32, bfloat16 or float16, of any strides with a contiguous last dimension;
     ``scores`` (float32, [batch, beams]): the beams' scores, -infinity for a beam that takes no part.  A continuation's total
-    is score + log_softmax(logits)[token], taken in 64 bits; equal totals go to the lower beam, then to the larger logit, then
-    to the lower token.  ``width`` (the number of beams if not given, at most 64): how many to choose.  ``parents`` (int32) are
+    is score + log_softmax(logits)[token]; equal totals go to the lower beam, then to the larger logit, then to the lower token.
+    A beam's own continuations are compared exactly, those of different beams in 64 bits from row sums of 32 bits (off by 2^-19 at
+    most, as a rule by 2^-22: closer totals may change places).  ``width`` (the number of beams if not given, at most 64): how many to choose.  ``parents`` (int32) are
     rows item * beams + beam, as :func:`pages_fork` and :func:`pages_reorder` take them.  With ``ended`` (uint8, [batch, beams])
     a beam at its end offers itself once, with its score as it is and ``eos_token``, and the ``ended`` returned says which of
     the chosen are at theirs (None without).  Where candidates run out: score -infinity, parent and token -1.

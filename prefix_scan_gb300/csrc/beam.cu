@@ -10,14 +10,17 @@
 // best are taken one after the other instead.
 //
 // Memory bounds it from below (a logit is read once); in fact a part's chain of loads, barriers and shuffles does, which five
-// other CTAs on its SM cover in part.  A pair of 16-bit logits takes six instructions for its exponentials, two for the maximum
+// other CTAs on its SM cover in part (two thirds of the issue slots are in use).  A pair of 16-bit logits takes six instructions for its exponentials, two for the maximum
 // and three to see whether it reaches T, and a warp some 250 besides for its 1024 logits.  64 x 8 beams over 128000 bf16 logits
-// (131 MB, a fifth at their end): parts 33 us (3.1 TB/s; five CTAs an SM instead of the six that 40 registers allow: 41 instead of
+// (131 MB, of which a fifth, at their end, is not read): parts 33 us (105 MB, 3.2 TB/s; five CTAs an SM instead of the six that 40 registers allow: 41 instead of
 // 35; T found by one warp in steps of a bit: 35; parts twice as long, on four CTAs: 37; parts to come fetched into L2: no
 // difference), items 9 us.  12 x 16 beams over 50021 f16 logits with 32 candidates: 14 and 15 us (128 groups against 32: 14 us
 // against 25, as 37 instead of 110 numbers reach T; 512 threads an item against 256: 15 against 17).
 //
-// How a row is cut into parts, threads and sums goes by places in the row alone, so that equal rows have equal sums.
+// How a row is cut into parts, threads and sums goes by places in the row alone, so that equal rows have equal sums.  A row's
+// logarithm of the sum of exponentials is off by 2^-19 at most and by 2^-22 or so as a rule: an exponential by 2^-22 of itself (and
+// 2^-25.4 by its argument), a part's sum by 17 roundings of 2^-24, its share in the row's by 2^-22, the logarithm by 2^-23; the
+// parts' shares are added, and totals compared, in 64 bits.
 #include <cfloat>
 #include <climits>
 #include <cmath>

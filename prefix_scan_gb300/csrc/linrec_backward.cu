@@ -1,8 +1,8 @@
 // linrec_backward.cu -- gradients of the gated linear recurrence (notation and
 // tiles in linrec_common.cuh).
 //
-// Memory bounds it from below (x, g and dh are read once, dx and dg are written once), instructions in fact: 58 a number.  The
-// states are not read: the forward pass keeps the one before each tile (in 32 bits), and the tile is scanned again from there,
+// Memory bounds it from below (x, g and dh are read once, dx and dg are written once).  In fact it is 54 instructions a number in
+// half of the issue slots, and waits at barriers for a tile's inputs and for what comes from the tile behind it.  The states are not read: the forward pass keeps the one before each tile (in 32 bits), and the tile is scanned again from there,
 // so that 16-bit types, too, get the gradient of g from states of 32 bits.  What runs backward is mu, a state's gradient
 // handed to the token before; its look-back goes over the tiles from the last one.
 //
@@ -11,10 +11,12 @@
 // scan kept there (a state from 0, and P), then backward: a step back from a state would divide by factors near 0.
 //
 // Runs with starts or ends, which are few as a rule, go backward in rolled loops (their arrays in local memory): the others' code
-// then stays in the instruction cache and in registers.
+// then stays in the instruction cache and in registers.  So do all runs of rows whose pairs are not whole or not on multiples of
+// two numbers, odd channel counts among them: 8192 tokens by 4097 bf16 channels take 206 us, by 4096 95 (forward 126 and 64, where
+// such rows are loaded number by number, too).
 //
-// 4 sequences of 8192 tokens by 4096 bf16 channels, forward and backward: 455 us, of which this is about 280 (all in unrolled loops:
-// 495; rolled by twos 465); 65536 tokens by 512 f32 channels, tied: 278 us.
+// 4 sequences of 8192 tokens by 4096 bf16 channels, forward and backward: 458 us, of which this is about 280 (earlier, all in unrolled
+// loops 495, rolled by twos 465); 65536 tokens by 512 f32 channels, tied: 278 us.
 #include <type_traits>
 
 #include "linrec_common.cuh"

@@ -10,10 +10,11 @@
 // lane has a run and two neighbouring channels; a warp of eight has two runs of all 32 channels.  What a run costs beside its
 // tokens (joining, the look-back's share) is some 300 instructions a lane, so longer runs are better (32 tokens instead of 16,
 // forward, one sequence of 131072 tokens by 512 bf16 channels: 143 us instead of 170); shared memory bounds them, as two CTAs an
-// SM with runs twice as long are slower (backward, 4 x 8192 tokens by 4096 bf16 channels, trained: 546 us instead of 495).  Wide tiles have long rows in
-// memory (copies of 32 and 64 bf16 channels run at 5.9 and 6.0 TB/s, of 16 at 5.0), narrow ones make more chains, so that
-// fewer of the tiles under way wait for one another: with 16, 32 and 64 channels 48 ragged prompts (24571 tokens by 4096
-// channels) took 283, 265 and 254 us, the long one 180, 189 and 210, training 733, 630 and 615.  Sequences are cut out of the flat index over all tokens: where one
+// SM with runs twice as long were slower (backward, 4 x 8192 tokens by 4096 bf16 channels, trained, now 458 us: 546 instead of 495
+// then).  Wide tiles have long rows in memory (copies of 32 and 64 bf16 channels run at 5.9 and 6.0 TB/s, of 16 at 5.0), narrow
+// ones make more chains, so that fewer of the tiles under way wait for one another: with 16, 32 and 64 channels earlier kernels
+// took 283, 265 and 254 us for 48 ragged prompts (24571 tokens by 4096 channels, now 214), 180, 189 and 210 for the long one (now
+// 141), 733, 630 and 615 for the training.  Sequences are cut out of the flat index over all tokens: where one
 // starts the state is set, not multiplied, so short sequences fill tiles as long ones do.
 //
 // Each tile tells the ones behind it its map h -> a h + b, and the state behind it once it knows that.  A tile that
@@ -90,12 +91,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 // Whether g is in (bound, -0]: the bits of negative numbers, as signed integers, rise with their magnitude.
 __device__ __forceinline__ bool just_below_zero(float g, float bound) { return __float_as_int(g) < __float_as_int(bound); }
-// The factors exp(g) of one token.  Above -1/16 the series up to g^4 / 24 leaves less than 2^-22.9 of the distance; the
-// hardware's 2^x, off by some 2^-22 of 1, serves elsewhere: there a state's memory is at most 16 tokens (and 2^0 is 1).
-// Tied inputs are weighted by 1 - exp(g), of which 2^-22 of 1 would be 2^-18 just below -1/16.  For them the distance is
-// g (1 + g q(g)), q such that the largest relative error is least: of degree 2 above -5/32 (with f32's roundings 2^-22.8) for
-// inputs of 16 bits, as many operations as the series, so that the weight is within 2^-19.4; of degree 3 above -7/16 (2^-22.7) for
-// inputs of 32 bits, within 2^-21 (degree 3 for all: one sequence of 131072 tokens by 512 bf16 channels 142 -> 149 us).
+// The factors exp(g) of one token.  Above -1/16 the series up to g^4 / 24 leaves less than 2^-22.9 of the distance (with f32's
+// roundings 2^-22.3); the hardware's 2^x, off by some 2^-22 of 1, serves elsewhere: there a state's memory is at most 16 tokens (and
+// 2^0 is 1).
+// Tied inputs are weighted by 1 - exp(g), of which 2^-22 of 1 would be 2^-18 just below -1/16 (with all roundings 2^-17.4).  For them
+// the distance is g (1 + g q(g)), q such that the largest relative error is least.  Inputs of 16 bits: q of degree 2 above -5/32
+// (with f32's roundings 2^-22.8), which is as many operations as the series; below, 2^x leaves 2^-19.4 of the weight (2^-18.7).
+// Inputs of 32 bits: of degree 3 above -7/16 (2^-22.7); below, 2^-20.9 (2^-20.2).  (Degree 3 for all: one sequence of 131072 tokens by
+// 512 bf16 channels 149 us instead of 141.)
 // `one`: 1 where the factor is near one, 0 elsewhere.
 enum class Weights { one, tied16, tied32 };   // 1, or tied inputs of 16 or 32 bits
 template <typename TX, bool TIED> constexpr Weights kWeights = !TIED ? Weights::one : sizeof(TX) == 4 ? Weights::tied32 : Weights::tied16;

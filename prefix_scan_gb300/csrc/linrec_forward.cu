@@ -1,14 +1,14 @@
 // linrec_forward.cu -- the gated linear recurrence over whole sequences
 // (notation and tiles in linrec_common.cuh).
 //
-// Memory bounds it from below (x and g are read once, h is written once), instructions in fact: every run is scanned twice
-// from shared memory, first from 0 for what it adds, then from the state before it, 33 instructions a number in all (16-bit
-// types).  Kept in registers in between, factors and inputs cost fewer, but so many registers that fewer warps hide each
+// Memory bounds it from below (x and g are read once, h is written once).  In fact half of the issue slots are in use, and warps
+// wait at barriers for a tile's inputs and for the state before it: every run is scanned twice from shared memory, first from 0
+// for what it adds, then from the state before it, 33 instructions a number in all (16-bit types).  Kept in registers in between, factors and inputs cost fewer, but so many registers that fewer warps hide each
 // other's waits (issue slots 38 instead of 56% in use): one sequence of 131072 tokens 185 us instead of 170 (with runs of 16).  Factors of 32-bit log
 // decays take their place in shared memory; those of 16 bits are computed again, as they would be rounded there.
 //
-// 48 ragged prompts, 24571 tokens by 4096 bf16 channels with f32 log decays: 212 us, 3.8 TB/s.  One sequence of 131072 tokens by
-// 512 bf16 channels: 142 us, 2.8 TB/s (its 16 blocks of channels are one chain of 256 tiles each).
+// 48 ragged prompts, 24571 tokens by 4096 bf16 channels with f32 log decays: 214 us, 3.8 TB/s.  One sequence of 131072 tokens by
+// 512 bf16 channels: 141 us, 2.9 TB/s (its 16 blocks of channels are one chain of 256 tiles each).
 #include <type_traits>
 
 #include "linrec_common.cuh"
